@@ -12,12 +12,15 @@ Tensors:
   q       torch.int8   [nvec, n] (or [n])
   d       torch.int16/uint16 [nvec, n/32] (fp16 bit patterns; torch.float16 accepted)
   out     torch.float32 [nvec, rows] (or [rows])
+The operators between the products (add_rms_norm, lora_add, rope_append,
+paged_attention) name their tensors in their own docstrings.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -34,7 +37,8 @@ EXPORTS = ("q1_last_error", "q1_0_packed_bytes", "q1_0_pack", "q1_0_unpack", "q8
            "q1_0_gemv", "q1_0_gemv_multi", "q1_0_gemv_multi_plan", "q1_0_gemm_small", "q1_0_verify",
            "q1_device_status", "q2_0_packed_bytes", "q2_0_pack", "q2_0_unpack", "q2_0_gemv", "q2_0_gemv_multi",
            "q2_0_gemv_multi_plan", "q1_gemm_small_kernel", "q1_0_gemm_small_noalloc",
-           "q1_0_gemv_multi_prefetch", "q2_0_gemv_multi_prefetch")
+           "q1_0_gemv_multi_prefetch", "q2_0_gemv_multi_prefetch", "q8_add_rms_norm", "q1_lora_add",
+           "q1_rope_append", "q1_paged_attention_workspace", "q1_paged_attention")
 
 MAX_PRODUCTS = 256
 
@@ -59,6 +63,16 @@ class MultiPlan(ctypes.Structure):
     _fields_ = [("rows_per_thread", ctypes.c_int), ("grid", ctypes.c_int), ("total_cost", ctypes.c_int64),
                 ("max_range_cost", ctypes.c_int64), ("panel_warps", ctypes.c_int),
                 ("panel_unit_blocks", ctypes.c_int), ("panel_panels", ctypes.c_int)]
+
+
+class PagedKV(ctypes.Structure):
+    """Mirror of q1_paged_kv (include/q1gemv.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
+                ("new_start", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("total_new", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
 class Q1Error(RuntimeError):
@@ -126,6 +140,17 @@ def load():
         lib.q1_gemm_small_kernel.restype = I
         lib.q1_device_status.argtypes = [I]
         lib.q1_device_status.restype = I
+        F = ctypes.c_float
+        lib.q8_add_rms_norm.argtypes = [P, I64, P, I64, P, F, I64, I64, I, P, I64, P, I64, P, P, P]
+        lib.q8_add_rms_norm.restype = I
+        lib.q1_lora_add.argtypes = [P, I64, I64, I64, I64, P, P, I, I64, I64, P, P, P, P, I64, P, I64, P]
+        lib.q1_lora_add.restype = I
+        lib.q1_rope_append.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, I, I64, P, ctypes.POINTER(PagedKV), P]
+        lib.q1_rope_append.restype = I
+        lib.q1_paged_attention_workspace.argtypes = [I64, I64, I64, I64]
+        lib.q1_paged_attention_workspace.restype = I64
+        lib.q1_paged_attention.argtypes = [P, I64, I64, I64, F, ctypes.POINTER(PagedKV), I64, P, I64, I64, P, I64, P]
+        lib.q1_paged_attention.restype = I
         lib.q1_0_verify.argtypes = [I, ctypes.c_char_p, ctypes.c_size_t]
         lib.q1_0_verify.restype = I
         _lib = lib
@@ -449,6 +474,209 @@ def verify(quick: bool = False, corrupt: bool = False, wait_probe: bool = False)
     flags = (1 if quick else 0) | (2 if corrupt else 0) | (4 if wait_probe else 0)
     rc = load().q1_0_verify(flags, buf, len(buf))
     return rc, buf.value.decode(errors="replace")
+
+
+# ------------------------------------ operators between the products --
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_HALF = (torch.bfloat16, torch.float16)
+
+
+class NormOut(NamedTuple):
+    """What add_rms_norm returns; None where an output was not asked for."""
+    residual: torch.Tensor | None
+    y: torch.Tensor | None
+    q: torch.Tensor | None
+    d: torch.Tensor | None
+
+
+def _cuda(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """Pointer of a CUDA tensor of one of dtypes, of the given shape, whose
+    last axis is contiguous (the other strides are the call's own matter)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stride(t: torch.Tensor, axis: int, least: int) -> int:
+    """Stride of an axis; an axis of one entry may have any (least is given)."""
+    return t.stride(axis) if t.shape[axis] > 1 else max(t.stride(axis), least)
+
+
+def _whole(t: torch.Tensor, name: str, shape) -> int:
+    p = _cuda(t, name, (torch.int32,), shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+                 residual_out: torch.Tensor | None = None, out: str = "q8", y: torch.Tensor | None = None,
+                 q: torch.Tensor | None = None, d: torch.Tensor | None = None, stream=None) -> NormOut:
+    """q8_add_rms_norm of x [nvec, n] (f32, bf16 or f16; rows may be strided):
+    h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight (f32 [n]).
+    out "q8" gives the q8_0 form of y (q int8 [nvec, n], d int16 fp16 bits
+    [nvec, n/32]), "y" y itself in x's type, "both" both.  With a residual, h
+    rounded to x's type is written to residual_out (which may be the residual
+    or x; allocated when not given)."""
+    if out not in ("q8", "y", "both"):
+        raise ValueError("out must be 'q8', 'y' or 'both'")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [nvec, n]")
+    nvec, n = x.shape
+    t = (x.dtype,)
+    if x.dtype not in DTYPES:
+        raise TypeError(f"x has dtype {x.dtype}, expected one of {tuple(DTYPES)}")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty((nvec, n), dtype=x.dtype, device=x.device)
+    if out != "q8" and y is None:
+        y = torch.empty((nvec, n), dtype=x.dtype, device=x.device)
+    if out != "y":
+        if n % 32:
+            raise ValueError("the q8_0 form needs n to be a multiple of 32")
+        if q is None:
+            q = torch.empty((nvec, n), dtype=torch.int8, device=x.device)
+        if d is None:
+            d = torch.empty((nvec, n // 32), dtype=torch.int16, device=x.device)
+        if q.numel() != nvec * n or d.numel() != nvec * (n // 32):
+            raise ValueError("q/d sizes do not match x")
+    s = (nvec, n)
+    _check(load().q8_add_rms_norm(
+        _cuda(x, "x", t), _stride(x, 0, n),
+        None if residual is None else _cuda(residual, "residual", t, s), 0 if residual is None else _stride(residual, 0, n),
+        _cuda(weight, "weight", (torch.float32,), (n,)), eps, nvec, n, DTYPES[x.dtype],
+        None if residual_out is None else _cuda(residual_out, "residual_out", t, s),
+        0 if residual_out is None else _stride(residual_out, 0, n),
+        None if out == "q8" else _cuda(y, "y", t, s), 0 if out == "q8" else _stride(y, 0, n),
+        None if out == "y" else _dev(q, "q", (torch.int8,)), None if out == "y" else _dev(d, "d", _SCALE_DTYPES),
+        _stream_ptr(stream)), "q8_add_rms_norm")
+    return NormOut(residual_out, None if out == "q8" else y, None if out == "y" else q, None if out == "y" else d)
+
+
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor, scale: torch.Tensor | None = None,
+             ranks: torch.Tensor | None = None, base: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """q1_lora_add: out[v] = base[v] + scale[i] * (b[i] @ (a[i] @ x[v])), i = index[v]
+    (-1: out[v] = base[v]).  x f32 [nvec, n], a [adapters, rank, n] and b [adapters,
+    rows, rank] bf16 or f16, index int32 [nvec], scale f32 and ranks int32
+    [adapters].  base f32 [nvec, rows] is the product the adapters stand
+    beside; without one, out is (it is added to in place)."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [nvec, n], a [adapters, rank, n], b [adapters, rows, rank]")
+    nvec, n = x.shape
+    adapters, rows, rank = b.shape
+    f32 = (torch.float32,)
+    if base is None:
+        if out is None:
+            raise ValueError("lora_add needs base, out or both")
+        base = out
+    if out is None:
+        out = torch.empty((nvec, rows), dtype=torch.float32, device=x.device)
+    pa, pb = _cuda(a, "a", _HALF, (adapters, rank, n)), _cuda(b, "b", (a.dtype,))
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous")
+    _check(load().q1_lora_add(
+        _cuda(x, "x", f32), _stride(x, 0, n), nvec, n, rows, pa, pb, DTYPES[a.dtype], adapters, rank,
+        _whole(index, "index", (nvec,)), None if ranks is None else _whole(ranks, "ranks", (adapters,)),
+        None if scale is None else _cuda(scale, "scale", f32, (adapters,)), _cuda(base, "base", f32, (nvec, rows)),
+        _stride(base, 0, rows), _cuda(out, "out", f32, (nvec, rows)), _stride(out, 0, rows), _stream_ptr(stream)),
+        "q1_lora_add")
+    return out
+
+
+def paged_kv(cache_k: torch.Tensor, cache_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
+             new_start: torch.Tensor, total_new: int) -> PagedKV:
+    """The q1_paged_kv of a cache [pages, page_size, kv_heads, dim] (bf16 or
+    f16; the first three axes in any order of storage, the same for both),
+    table int32 [batch, width], kv_len int32 [batch], new_start int32 [batch + 1]."""
+    if cache_k.dim() != 4:
+        raise ValueError("cache_k must be [pages, page_size, kv_heads, dim]")
+    shape = tuple(cache_k.shape)
+    pk, pv = _cuda(cache_k, "cache_k", _HALF), _cuda(cache_v, "cache_v", (cache_k.dtype,), shape)
+    if cache_k.stride() != cache_v.stride():
+        raise ValueError("cache_k and cache_v must have the same strides")
+    if table.dim() != 2:
+        raise ValueError("table must be [batch, width]")
+    batch, width = table.shape
+    st = [_stride(cache_k, i, shape[3]) for i in range(3)]
+    return PagedKV(pk, pv, st[0], st[1], st[2], _cuda(table, "table", (torch.int32,)), width, _stride(table, 0, width),
+                   _whole(kv_len, "kv_len", (batch,)), _whole(new_start, "new_start", (batch + 1,)), shape[0], shape[1],
+                   shape[2], shape[3], batch, total_new, DTYPES[cache_k.dtype])
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, cache_k: torch.Tensor,
+                cache_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, new_start: torch.Tensor,
+                q_out: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> torch.Tensor:
+    """q1_rope_append: the new tokens' q [tokens, heads * dim] turned to their
+    positions and returned as [tokens, heads, dim] in the cache's type; k
+    (turned) and v [tokens, kv_heads * dim] put into the cache (see paged_kv).
+    q, k and v are f32, their rows may be strided; cos_sin f32 [positions, rot]
+    holds rot/2 cosines, then rot/2 sines a position."""
+    total = q.shape[0]
+    kv = paged_kv(cache_k, cache_v, table, kv_len, new_start, total)
+    dim, width = kv.dim, kv.kv_heads * kv.dim
+    if q.dim() != 2 or cos_sin.dim() != 2 or q.shape[1] % dim:
+        raise ValueError("q must be [tokens, heads * dim] and cos_sin [positions, rot]")
+    heads = q.shape[1] // dim
+    f32 = (torch.float32,)
+    if q_out is None:
+        q_out = torch.empty((total, heads, dim), dtype=cache_k.dtype, device=q.device)
+    elif not q_out.is_contiguous():
+        raise ValueError("q_out must be contiguous")
+    if not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous")
+    _check(load().q1_rope_append(
+        _cuda(q, "q", f32), _stride(q, 0, heads * dim), _cuda(k, "k", f32, (total, width)), _stride(k, 0, width),
+        _cuda(v, "v", f32, (total, width)), _stride(v, 0, width), _cuda(cos_sin, "cos_sin", f32), cos_sin.shape[0],
+        cos_sin.shape[1], 1 if interleaved else 0, heads, _cuda(q_out, "q_out", (cache_k.dtype,), (total, heads, dim)),
+        ctypes.byref(kv), _stream_ptr(stream)), "q1_rope_append")
+    return q_out
+
+
+def paged_attention_workspace(max_new: int, heads: int, kv_heads: int, dim: int) -> int:
+    """Bytes of paged_attention's workspace on the current device."""
+    v = load().q1_paged_attention_workspace(int(max_new), int(heads), int(kv_heads), int(dim))
+    if v < 0:
+        raise Q1Error(int(v), last_error())
+    return int(v)
+
+
+def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tensor, table: torch.Tensor,
+                    kv_len: torch.Tensor, new_start: torch.Tensor, max_new: int, scale: float | None = None,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q1_paged_attention: the new tokens' q [tokens, heads, dim] (the cache's
+    type; tokens and heads may be strided) attend to their sequence's cache,
+    causally (see paged_kv; the new keys and values are in the cache already).
+    max_new is the most new tokens of any sequence; scale defaults to
+    dim ** -0.5.  A given workspace (uint8) must hold
+    paged_attention_workspace(...) bytes."""
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, dim]")
+    total, heads, dim = q.shape
+    kv = paged_kv(cache_k, cache_v, table, kv_len, new_start, total)
+    t = (cache_k.dtype,)
+    if kv.dim != dim:
+        raise ValueError(f"q has dim {dim}, the cache {kv.dim}")
+    if out is None:
+        out = torch.empty((total, heads, dim), dtype=q.dtype, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(paged_attention_workspace(max_new, heads, kv.kv_heads, dim), dtype=torch.uint8,
+                                device=q.device)
+        if stream is not None:  # it goes back to the allocator on return, while `stream` may still use it
+            workspace.record_stream(stream)
+    _check(load().q1_paged_attention(
+        _cuda(q, "q", t), _stride(q, 0, heads * dim), _stride(q, 1, dim), heads, dim ** -0.5 if scale is None else scale,
+        ctypes.byref(kv), max_new, _cuda(out, "out", t, (total, heads, dim)), _stride(out, 0, heads * dim),
+        _stride(out, 1, dim), _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream_ptr(stream)),
+        "q1_paged_attention")
+    return out
 
 
 class Q1Linear:

@@ -1,0 +1,339 @@
+// attend.cu -- q1_paged_attention: new tokens attend to their sequence's paged
+// cache, causal, grouped heads.  This file holds the kernel for few rows a key
+// head (single tokens and short chunks) and the entry points.
+//
+// For row r at position p: o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m) over
+// keys j <= p, s_j = scale log2(e) q.k_j, m the running maximum.  Keys and values
+// are read once in one pass; with up to 16 rows that is 2 D bytes and at most
+// 64 D operations a key and row tile, so bytes bound it: what counts is reads in
+// flight and equal shares for the SMs.  Each warp takes chunks of 16 keys on
+// its own: a private ring of kStages chunks in shared memory filled by 16-byte
+// asynchronous copies, scores and p v by m16n8k16 MMAs (16-bit operands, f32
+// sums), maximum, sum and output in registers, no barrier between warps until
+// an item ends.  p is rounded to the cache's type for its product with v (off
+// by 2^-8 or 2^-11 of a term at most, as the output's own rounding is); the sum of p
+// is taken in f32 before that.
+#include <cmath>
+#include <type_traits>
+
+#include "attend.cuh"
+
+namespace q1 {
+
+constexpr int kRowsS = 16;   // rows of a tile
+constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
+constexpr int kWarpsS = 4;
+constexpr int kStagesS = 3;  // 2 x 96 KB of reads in flight an SM at D = 128
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+template <int D>
+constexpr int attend_smem() {
+  return kWarpsS * kStagesS * 2 * 16 * D * 2;
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
+  using Tile = Tiling<kRowsS, kKeysS>;
+  constexpr int kRowBytes = D * 2, kChunkBytes = 16 * kRowBytes, kPieces = kRowBytes / 16;  // 16-byte pieces of a row
+  constexpr int kSteps = D / 16;       // k16 steps of q.k, and pairs of n8 tiles of p v
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ int64_t scratch[34];
+  __shared__ float ml[kWarpsS][16][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  Cursor cur = {};
+  int64_t u0, u1;
+  int ctas = a.ctas;
+  locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  const uint32_t ring = smem_addr(smem) + warp * (kStagesS * 2 * kChunkBytes);
+  const int page_mask = (1 << a.kv.page_shift) - 1;
+  int slot = 0;  // of a partial: 0 only for an item that began in an earlier CTA
+  for (int64_t u = u0; u < u1;) {
+    const int take = int(min(int64_t(cur.units - cur.unit), u1 - u));  // units of this item here
+    const int keys = Tile::keys(cur.s, a.group, cur.m);
+    const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
+    const T* kbase = static_cast<const T*>(a.kv.k) + cur.h * a.kv.head_stride;
+    const T* vbase = static_cast<const T*>(a.kv.v) + cur.h * a.kv.head_stride;
+
+    // Chunk i of this warp: keys j0 + 64 i .. +15.  Lane l < 16 finds row l's
+    // place; the copies then run over rows in pairs (or fours, D = 64).
+    const int j0 = cur.unit * kKeysS + warp * 16;
+    const auto fill = [&](int i) {
+      if (i < take) {
+        const int j = j0 + i * kKeysS + (lane & 15);
+        int64_t off = -1;
+        if (j < keys) {
+          const int page = table[j >> a.kv.page_shift];
+          if (page >= 0 && page < a.kv.pages)
+            off = int64_t(page) * a.kv.page_stride + int64_t(j & page_mask) * a.kv.slot_stride;
+          else
+            atomicOr(a.status, kStatusBadIndex);
+        }
+        constexpr int kRowsOnce = 32 / kPieces;
+        const int piece = lane % kPieces;
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
+          const int r = r0 + lane / kPieces;
+          const int64_t o = __shfl_sync(0xffffffffu, off, r);
+          const uint32_t dst = ring + (i % kStagesS) * 2 * kChunkBytes + r * kRowBytes + ((piece ^ (r & 7)) << 4);
+          const int64_t e = (o < 0 ? 0 : o) + piece * 8;  // rows that are not there read as zeros
+          cp_async16(dst, kbase + e, o < 0 ? 0 : 16);
+          cp_async16(dst + kChunkBytes, vbase + e, o < 0 ? 0 : 16);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStagesS - 1; ++i) fill(i);
+
+    // Q of the tile as A fragments: rows lane/4 and lane/4 + 8.
+    uint32_t qa[kSteps][4];
+    int limit[2];  // keys each of the two rows may see
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      int token, head;
+      const int r = cur.m * kRowsS + lane / 4 + half * 8;
+      const bool live = row_of(cur, a.group, r, token, head);
+      limit[half] = live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0;
+      const T* row = static_cast<const T*>(a.q) + (live ? token * a.q_token + head * a.q_head : 0) + (lane & 3) * 2;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qa[k][half] = live ? *reinterpret_cast<const uint32_t*>(row + k * 16) : 0u;
+        qa[k][half + 2] = live ? *reinterpret_cast<const uint32_t*>(row + k * 16 + 8) : 0u;
+      }
+    }
+    float o[2 * kSteps][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2 * kSteps; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+    for (int i = 0; i < take; ++i) {
+      cp_wait<kStagesS - 2>();
+      __syncwarp();
+      fill(i + kStagesS - 1);
+      const uint32_t kt = ring + (i % kStagesS) * 2 * kChunkBytes, vt = kt + kChunkBytes;
+      float s[2][4] = {};
+      {
+        // matrices: keys 0-7 and 8-15, each with the step's two groups of 8 dims
+        const int r = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t b[4];
+          ldsm4(kt + r * kRowBytes + (((k * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4), b);
+          mma16816<T>(s[0], qa[k], b[0], b[1]);
+          mma16816<T>(s[1], qa[k], b[2], b[3]);
+        }
+      }
+      // Scores to log2 units; keys a row may not see drop out by selection.
+      const int j = j0 + i * kKeysS + (lane & 3) * 2;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[t][e] = j + t * 8 + (e & 1) < limit[e >> 1] ? s[t][e] * a.scale_log2 : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
+        }
+      float base[2];
+      bool grown = false;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float m = fmaxf(mx[half], quad_max(top[half]));
+        base[half] = m == -INFINITY ? 0.f : m;  // a row that sees nothing yet
+        if (m > mx[half]) {
+          grown = true;
+          const float f = ex2(mx[half] - base[half]);
+          sum[half] *= f;
+          top[half] = f;
+        } else {
+          top[half] = 1.f;
+        }
+        mx[half] = m;
+      }
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int n = 0; n < 2 * kSteps; ++n) o[n][0] *= top[0], o[n][1] *= top[0], o[n][2] *= top[1], o[n][3] *= top[1];
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[t][e] = ex2(s[t][e] - base[e >> 1]);
+          sum[e >> 1] += s[t][e];
+        }
+      const uint32_t p[4] = {Elem<T>::pack2(s[0][0], s[0][1]), Elem<T>::pack2(s[0][2], s[0][3]),
+                             Elem<T>::pack2(s[1][0], s[1][1]), Elem<T>::pack2(s[1][2], s[1][3])};
+      const int r = lane & 15;
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n) {
+        uint32_t b[4];
+        ldsm4t(vt + r * kRowBytes + (((n * 2 + (lane >> 4)) ^ (r & 7)) << 4), b);
+        mma16816<T>(o[2 * n], p, b[0], b[1]);
+        mma16816<T>(o[2 * n + 1], p, b[2], b[3]);
+      }
+      __syncwarp();
+    }
+    cp_wait<0>();
+
+    // Join the warps: their maxima and sums, then their outputs (f32 over the
+    // ring, which is drained) scaled to the common maximum.
+    sum[0] = quad_sum(sum[0]);
+    sum[1] = quad_sum(sum[1]);
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ml[warp][lane / 4 + half * 8][0] = mx[half];
+        ml[warp][lane / 4 + half * 8][1] = sum[half];
+      }
+    }
+    __syncthreads();
+    float* joined = reinterpret_cast<float*>(smem);  // [warp][16][D + 4]
+    constexpr int kLd = D + 4;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = lane / 4 + half * 8;
+      float m = ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kWarpsS; ++w) m = fmaxf(m, ml[w][r][0]);
+      const float f = mx[half] == -INFINITY ? 0.f : ex2(mx[half] - m);
+#pragma unroll
+      for (int n = 0; n < 2 * kSteps; ++n) {
+        float2 v = make_float2(o[n][half * 2] * f, o[n][half * 2 + 1] * f);
+        *reinterpret_cast<float2*>(joined + (warp * 16 + r) * kLd + n * 8 + (lane & 3) * 2) = v;
+      }
+    }
+    __syncthreads();
+    const bool whole = cur.unit == 0 && take == cur.units;
+    slot = cur.unit == 0 ? 1 : 0;
+    for (int i = threadIdx.x; i < 16 * (D / 4); i += kWarpsS * 32) {
+      const int r = i / (D / 4), col = i % (D / 4) * 4;
+      int token, head;
+      if (!row_of(cur, a.group, cur.m * kRowsS + r, token, head)) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpsS; ++w) {
+        const float4 t = *reinterpret_cast<const float4*>(joined + (w * 16 + r) * kLd + col);
+        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+        m = fmaxf(m, ml[w][r][0]);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarpsS; ++w)
+        if (ml[w][r][1] != 0.f) l += ml[w][r][1] * ex2(ml[w][r][0] - m);
+      if (whole) {
+        const float inv = l > 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+        const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
+      } else {
+        float* row = a.part + (int64_t(2 * blockIdx.x + slot) * kRowsS + r) * (D + 2);
+        *reinterpret_cast<float2*>(row + col) = make_float2(v.x, v.y);
+        *reinterpret_cast<float2*>(row + col + 2) = make_float2(v.z, v.w);
+        if (col == 0) row[D] = m, row[D + 1] = l;
+      }
+    }
+    __syncthreads();  // the ring and ml are free again
+    u += take;
+    if (u < u1) next_item<Tile>(a, cur);
+  }
+}
+
+static int64_t workspace_rows() { return int64_t(2) * 2 * num_sms() * kRowsS; }
+
+template <class T, int D>
+static int launch_attend(AttendArgs& a, cudaStream_t s) {
+  const char* who = "q1_paged_attention launch";
+  static bool set[64] = {};
+  int dev = 0;
+  if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem<D>()),
+                            who))
+      return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  a.ctas = 2 * num_sms();
+  if (int e = launch_op(k_attend<T, D>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
+  return launch_op(k_attend_join<T, kRowsS, kKeysS, D>, dim3(unsigned(a.ctas)), 256, 0, 1, s, who, a);
+}
+
+}  // namespace q1
+
+using namespace q1;
+
+extern "C" int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_heads, int64_t dim) {
+  if (max_new < 1 || heads < 1 || kv_heads < 1 || heads > 4096 || heads % kv_heads || (dim != 64 && dim != 128))
+    return fail(Q1_ERR_ARG, "q1_paged_attention_workspace: bad shape max_new=%lld heads=%lld kv_heads=%lld dim=%lld",
+                (long long)max_new, (long long)heads, (long long)kv_heads, (long long)dim);
+  return workspace_rows() * (dim + 2) * 4;
+}
+
+extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
+                                  const q1_paged_kv* kv, int64_t max_new, void* out, int64_t out_token_stride,
+                                  int64_t out_head_stride, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* who = "q1_paged_attention";
+  AttendArgs a = {};
+  if (int e = check_paged(who, kv, a.kv)) return e;
+  if (heads < 1 || heads > 4096 || heads % kv->kv_heads)
+    return fail(Q1_ERR_ARG, "%s: heads=%lld is no multiple of kv_heads=%lld up to 4096", who, (long long)heads,
+                (long long)kv->kv_heads);
+  if (!q || !out || !workspace) return fail(Q1_ERR_ARG, "%s: null pointer", who);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || q_token_stride % 8 || q_head_stride % 8 ||
+      out_token_stride % 8 || out_head_stride % 8)
+    return fail(Q1_ERR_ARG, "%s: buffers must be 16-byte aligned, strides multiples of 8", who);
+  if (q_head_stride < kv->dim || q_token_stride < kv->dim || out_head_stride < kv->dim || out_token_stride < kv->dim)
+    return fail(Q1_ERR_ARG, "%s: a stride is less than dim", who);
+  if (!std::isfinite(scale)) return fail(Q1_ERR_ARG, "%s: scale must be finite", who);
+  if (max_new < 1) return fail(Q1_ERR_ARG, "%s: max_new must be positive", who);
+  const int64_t need = q1_paged_attention_workspace(max_new, heads, kv->kv_heads, kv->dim);
+  if (need < 0) return int(need);
+  if (workspace_bytes < need)
+    return fail(Q1_ERR_ARG, "%s: the workspace holds %lld bytes, %lld are needed", who, (long long)workspace_bytes,
+                (long long)need);
+  a.q = q, a.out = out, a.q_token = q_token_stride, a.q_head = q_head_stride;
+  a.o_token = out_token_stride, a.o_head = out_head_stride;
+  a.part = static_cast<float*>(workspace);
+  if (int e = ops_status_ptr(&a.status)) return e;
+  a.heads = int(heads), a.group = int(heads / kv->kv_heads);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = kv->dtype == Q1_BF16;
+  if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, s) : launch_attend<__half, 128>(a, s);
+  return bf ? launch_attend<__nv_bfloat16, 64>(a, s) : launch_attend<__half, 64>(a, s);
+}

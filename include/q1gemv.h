@@ -322,7 +322,9 @@ int q2_0_gemv_multi_plan(const q1_product *products, int count, int sms, q1_mult
 /* Device status word of the library's kernels on the current device.  A
  * kernel whose bounded internal wait gives up (it never should: every wait is
  * for work the same kernel issued) sets bit 0 instead of hanging, and skips
- * its remaining output.  Synchronous: copies the word to the host.
+ * its remaining output.  Bit 1 (2): an index on the device (an adapter, a
+ * page, a position, a length) lay outside what its call was given, see the
+ * operators below.  Synchronous: copies the word to the host.
  *   clear : nonzero resets the word to 0 after reading it.
  * Returns the status flags (0 = no event) or a negative Q1_ERR_CUDA. */
 int q1_device_status(int clear);
@@ -354,6 +356,122 @@ int q1_device_status(int clear);
  * Returns Q1_OK if every output is bit-identical, Q1_MISMATCH (2) if any
  * differs, or a negative error. */
 int q1_0_verify(int flags, char *report, size_t report_len);
+
+/* ---------------------------------------------------------------------------
+ * The operators between a decoder layer's products.  The pages name none of
+ * them; they are the formulas that any layer around the products computes:
+ * residual and root-mean-square norm with the next product's q8_0 activation,
+ * low-rank adapters beside a product, rotary positions with a paged cache of
+ * keys and values, and attention over that cache.
+ *
+ * Conventions of the calls above, except where a call says otherwise: element
+ * strides are given, and index arrays are read on the device.  An index that
+ * lies outside its range is never followed: the call says what happens to its
+ * rows, and q1_device_status bit 1 is set.  All sums, maxima and norms are f32.
+ * Like the products these launches start while the preceding kernel on the
+ * stream drains, and read nothing before it has finished.
+ * ------------------------------------------------------------------------- */
+
+/* Element types. */
+#define Q1_F32 0
+#define Q1_BF16 1
+#define Q1_F16 2
+
+/* Residual addition, root-mean-square norm and q8_0 quantization of nvec rows:
+ *   h = x + residual (x where residual is NULL), in f32;
+ *   residual_out = h rounded to the type;
+ *   y = (h * (1 / sqrt(mean(h^2) + eps))) * weight;  q, d = the q8_0 form of
+ *   y exactly as q8_quantize_act gives it (of y in f32, before any rounding).
+ *   x, residual, residual_out, y : [nvec][n] of `dtype` (Q1_F32, Q1_BF16,
+ *     Q1_F16), rows ldx, ldr, ldo, ldy elements apart; residual, residual_out
+ *     and y may be NULL.  residual_out may be x or residual itself, and y may be x.
+ *   weight : f32 [n].  q : int8 [nvec][n], d : fp16 bits [nvec][n/32], both or
+ *     neither (NULL); with them n is a multiple of 32, else any n >= 1.
+ * Alignment: q and d 16 bytes, the others their type's size (16-byte aligned
+ * rows are faster).  1 <= nvec <= 2^24, n <= 2^24.  A row's outputs do not
+ * depend on the number of rows, bit for bit. */
+int q8_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const float *weight, float eps,
+                    int64_t nvec, int64_t n, int dtype, void *residual_out, int64_t ldo, void *y, int64_t ldy,
+                    int8_t *q, uint16_t *d, void *stream);
+
+/* Low-rank adapters of many requests beside a product: for each vector v with
+ * adapter i = index[v],
+ *   out_v = base_v + scale[i] * (b_i (a_i x_v)),
+ * and out_v = base_v where index[v] is -1.
+ *   x : f32 [nvec][n], rows ldx apart.  base, out : f32 [nvec][rows], rows ldb
+ *     and ldo apart; base may be out (in place).  1 <= nvec <= 65535.
+ *   a : [adapters][rank][n], b : [adapters][rows][rank] of `dtype` (Q1_BF16 or
+ *     Q1_F16); n and rank multiples of 8, rank in 8..128.
+ *   index : int32 [nvec].  ranks : int32 [adapters] or NULL: the ranks in use
+ *     (0..rank) of each adapter; what lies past them is not used and may hold
+ *     anything.  scale : f32 [adapters] or NULL (1).
+ * x, a and b must be 16-byte aligned, ldx a multiple of 4.  An index outside
+ * -1..adapters-1 counts as -1 and sets the status bit. */
+int q1_lora_add(const float *x, int64_t ldx, int64_t nvec, int64_t n, int64_t rows, const void *a, const void *b,
+                int dtype, int64_t adapters, int64_t rank, const int32_t *index, const int32_t *ranks,
+                const float *scale, const float *base, int64_t ldb, float *out, int64_t ldo, void *stream);
+
+/* A paged cache of keys and values, and the sequences of one call.  Sequence b
+ * has its tokens 0 .. kv_len[b]-1 in the cache, the last new_start[b+1] -
+ * new_start[b] of them new in this call; token t lies in page
+ * table[b][t / page_size], slot t % page_size.  The new tokens of all
+ * sequences are packed: rows new_start[b] .. new_start[b+1]-1 of q, k, v, out. */
+typedef struct q1_paged_kv {
+  void *k, *v;              /* device [pages][page_size][kv_heads][dim] of dtype, in any
+                               order of the first three axes, the same for both        */
+  int64_t page_stride, slot_stride, head_stride; /* elements; multiples of 8, at least dim */
+  const int32_t *table;     /* device [batch][table_width], rows table_stride apart;
+                               entries past a sequence's length are not read           */
+  int64_t table_width, table_stride;
+  const int32_t *kv_len;    /* device [batch]: cached tokens, the new ones among them  */
+  const int32_t *new_start; /* device [batch + 1]: not falling                         */
+  int64_t pages, page_size; /* page_size a power of two in 8..4096                     */
+  int64_t kv_heads, dim;    /* dim 64 or 128                                           */
+  int64_t batch, total_new; /* total_new: rows of the packed tensors, >= new_start[batch];
+                               rows past new_start[batch] belong to no sequence        */
+  int dtype;                /* Q1_BF16 or Q1_F16                                       */
+} q1_paged_kv;
+
+/* Rotary positions and the cache's new entries, from the q, k and v products'
+ * outputs: each pair (e, f) of a head's first `rot` values at position p
+ * becomes (e cos - f sin, f cos + e sin); values past rot stay.  Row j of a
+ * sequence's new tokens has position kv_len - (new tokens) + j.
+ *   q : f32 [total_new][heads][dim], k, v : f32 [total_new][kv_heads][dim], rows
+ *     ldq, ldk, ldv elements apart (multiples of 4).
+ *   cos_sin : f32 [positions][rot]: rot/2 cosines, then rot/2 sines.  rot is a
+ *     multiple of 8 up to dim.
+ *   interleaved : 0 pairs value i with value i + rot/2, else 2i with 2i + 1.
+ *   q_out : [total_new][heads][dim] of the cache's type.
+ * k (turned) and v go to the cache.  Pointers 16-byte aligned.  A token whose
+ * position or page is out of range goes nowhere, its q_out row is zero, and
+ * the status bit is set; so is the q_out row of a token of no sequence
+ * (without the bit). */
+int q1_rope_append(const float *q, int64_t ldq, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                   const float *cos_sin, int64_t positions, int64_t rot, int interleaved, int64_t heads, void *q_out,
+                   const q1_paged_kv *kv, void *stream);
+
+/* Bytes of q1_paged_attention's workspace for sequences of up to max_new new
+ * tokens, on the current device; negative Q1_ERR_ARG for a bad shape. */
+int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_heads, int64_t dim);
+
+/* Causal attention of the new tokens over their sequence's cache: for a token
+ * at position p and query head h (key head h / (heads / kv_heads)),
+ *   out = sum_j w_j v_j / sum_j w_j over j = 0..p, w_j = exp(scale * q.k_j).
+ *   q, out : [total_new][heads][dim] of the cache's type, strides in elements
+ *     (multiples of 8).  A row that sees no key (p < 0) is zero; rows of no
+ *     sequence are left as they are.
+ *   max_new : the most new tokens any sequence has (it picks the kernel: a
+ *     larger or smaller number costs time, not correctness).
+ *   workspace : device, 16-byte aligned, q1_paged_attention_workspace bytes;
+ *     needs no initial value; calls that may overlap need one each.
+ * Keys and values of cached tokens must be finite; slots past a sequence's
+ * length may hold anything.  The weights w_j are rounded to the cache's type
+ * for their product with v (their sum is not).  A page out of range reads as
+ * zeros and sets the status bit, as does a kv_len outside the table (it is
+ * clamped). */
+int q1_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
+                       const q1_paged_kv *kv, int64_t max_new, void *out, int64_t out_token_stride,
+                       int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
