@@ -489,32 +489,48 @@ class NormOut(NamedTuple):
     d: torch.Tensor | None
 
 
-def _cuda(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
-    """Pointer of a CUDA tensor of one of dtypes, of the given shape, whose
-    last axis is contiguous (the other strides are the call's own matter)."""
+def _refuse(t, name: str, dtypes, shape):
+    """Raises for what is wrong with t."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"the last axis of {name} must be contiguous")
+
+
+def _cuda(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """Pointer of a CUDA tensor of one of dtypes, of the given shape, whose
+    last axis is contiguous (the other strides are the call's own matter).
+    The operators' calls are short, so what is right passes in one test."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and (shape is None or t.shape == shape) and
+            (t.is_contiguous() or t.stride(-1) == 1 or t.shape[-1] == 1)):
+        return t.data_ptr()
+    return _refuse(t, name, dtypes, shape)
 
 
 def _stride(t: torch.Tensor, axis: int, least: int) -> int:
     """Stride of an axis; an axis of one entry may have any (least is given)."""
-    return t.stride(axis) if t.shape[axis] > 1 else max(t.stride(axis), least)
+    s = t.stride(axis)
+    return s if s >= least or t.shape[axis] > 1 else least
 
 
 def _whole(t: torch.Tensor, name: str, shape) -> int:
-    p = _cuda(t, name, (torch.int32,), shape)
-    if not t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return p
+    return _refuse(t, name, (torch.int32,), shape)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The given stream, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
@@ -548,7 +564,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
         if q.numel() != nvec * n or d.numel() != nvec * (n // 32):
             raise ValueError("q/d sizes do not match x")
     s = (nvec, n)
-    _check(load().q8_add_rms_norm(
+    _check((_lib or load()).q8_add_rms_norm(
         _cuda(x, "x", t), _stride(x, 0, n),
         None if residual is None else _cuda(residual, "residual", t, s), 0 if residual is None else _stride(residual, 0, n),
         _cuda(weight, "weight", (torch.float32,), (n,)), eps, nvec, n, DTYPES[x.dtype],
@@ -556,7 +572,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
         0 if residual_out is None else _stride(residual_out, 0, n),
         None if out == "q8" else _cuda(y, "y", t, s), 0 if out == "q8" else _stride(y, 0, n),
         None if out == "y" else _dev(q, "q", (torch.int8,)), None if out == "y" else _dev(d, "d", _SCALE_DTYPES),
-        _stream_ptr(stream)), "q8_add_rms_norm")
+        _stream_of(x, stream)), "q8_add_rms_norm")
     return NormOut(residual_out, None if out == "q8" else y, None if out == "y" else q, None if out == "y" else d)
 
 
@@ -582,11 +598,11 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Ten
     pa, pb = _cuda(a, "a", _HALF, (adapters, rank, n)), _cuda(b, "b", (a.dtype,))
     if not a.is_contiguous() or not b.is_contiguous():
         raise ValueError("a and b must be contiguous")
-    _check(load().q1_lora_add(
+    _check((_lib or load()).q1_lora_add(
         _cuda(x, "x", f32), _stride(x, 0, n), nvec, n, rows, pa, pb, DTYPES[a.dtype], adapters, rank,
         _whole(index, "index", (nvec,)), None if ranks is None else _whole(ranks, "ranks", (adapters,)),
         None if scale is None else _cuda(scale, "scale", f32, (adapters,)), _cuda(base, "base", f32, (nvec, rows)),
-        _stride(base, 0, rows), _cuda(out, "out", f32, (nvec, rows)), _stride(out, 0, rows), _stream_ptr(stream)),
+        _stride(base, 0, rows), _cuda(out, "out", f32, (nvec, rows)), _stride(out, 0, rows), _stream_of(x, stream)),
         "q1_lora_add")
     return out
 
@@ -632,17 +648,17 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torc
         raise ValueError("q_out must be contiguous")
     if not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous")
-    _check(load().q1_rope_append(
+    _check((_lib or load()).q1_rope_append(
         _cuda(q, "q", f32), _stride(q, 0, heads * dim), _cuda(k, "k", f32, (total, width)), _stride(k, 0, width),
         _cuda(v, "v", f32, (total, width)), _stride(v, 0, width), _cuda(cos_sin, "cos_sin", f32), cos_sin.shape[0],
         cos_sin.shape[1], 1 if interleaved else 0, heads, _cuda(q_out, "q_out", (cache_k.dtype,), (total, heads, dim)),
-        ctypes.byref(kv), _stream_ptr(stream)), "q1_rope_append")
+        ctypes.byref(kv), _stream_of(q, stream)), "q1_rope_append")
     return q_out
 
 
 def paged_attention_workspace(max_new: int, heads: int, kv_heads: int, dim: int) -> int:
     """Bytes of paged_attention's workspace on the current device."""
-    v = load().q1_paged_attention_workspace(int(max_new), int(heads), int(kv_heads), int(dim))
+    v = (_lib or load()).q1_paged_attention_workspace(int(max_new), int(heads), int(kv_heads), int(dim))
     if v < 0:
         raise Q1Error(int(v), last_error())
     return int(v)
@@ -671,10 +687,10 @@ def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tenso
                                 device=q.device)
         if stream is not None:  # it goes back to the allocator on return, while `stream` may still use it
             workspace.record_stream(stream)
-    _check(load().q1_paged_attention(
+    _check((_lib or load()).q1_paged_attention(
         _cuda(q, "q", t), _stride(q, 0, heads * dim), _stride(q, 1, dim), heads, dim ** -0.5 if scale is None else scale,
         ctypes.byref(kv), max_new, _cuda(out, "out", t, (total, heads, dim)), _stride(out, 0, heads * dim),
-        _stride(out, 1, dim), _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream_ptr(stream)),
+        _stride(out, 1, dim), _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream_of(q, stream)),
         "q1_paged_attention")
     return out
 
