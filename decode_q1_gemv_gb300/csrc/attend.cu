@@ -274,6 +274,10 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   }
 }
 
+// Which kernel: the tensor-core one from more rows a key head on than one tile
+// of this file's has.
+static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kRowsS; }
+
 static int64_t workspace_rows() { return int64_t(2) * 2 * num_sms() * kRowsS; }
 
 template <class T, int D>
@@ -290,7 +294,7 @@ static int launch_attend(AttendArgs& a, cudaStream_t s) {
   }
   a.ctas = 2 * num_sms();
   if (int e = launch_op(k_attend<T, D>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
-  return launch_op(k_attend_join<T, kRowsS, kKeysS, D>, dim3(unsigned(a.ctas)), 256, 0, 1, s, who, a);
+  return launch_op(k_attend_join<T, kRowsS, kKeysS, D, false>, dim3(unsigned(a.ctas)), 256, 0, 1, s, who, a);
 }
 
 }  // namespace q1
@@ -301,7 +305,10 @@ extern "C" int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, 
   if (max_new < 1 || heads < 1 || kv_heads < 1 || heads > 4096 || heads % kv_heads || (dim != 64 && dim != 128))
     return fail(Q1_ERR_ARG, "q1_paged_attention_workspace: bad shape max_new=%lld heads=%lld kv_heads=%lld dim=%lld",
                 (long long)max_new, (long long)heads, (long long)kv_heads, (long long)dim);
-  return workspace_rows() * (dim + 2) * 4;
+  const int64_t few = workspace_rows() * (dim + 2) * 4;
+  if (!many_rows(max_new, heads / kv_heads)) return few;
+  const int64_t many = attend_tc_workspace(int(dim));
+  return few > many ? few : many;
 }
 
 extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
@@ -334,6 +341,11 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = kv->dtype == Q1_BF16;
+  if (many_rows(max_new, a.group)) {
+    bool ran = false;
+    if (int e = launch_attend_tc(a, bf, int(kv->dim), s, ran)) return e;
+    if (ran) return Q1_OK;
+  }
   if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, s) : launch_attend<__half, 128>(a, s);
   return bf ? launch_attend<__nv_bfloat16, 64>(a, s) : launch_attend<__half, 64>(a, s);
 }

@@ -147,7 +147,8 @@ __device__ __forceinline__ bool row_of(const Cursor& cur, int group, int r, int&
 // first item, when it began before, is in slot 0).  A partial is, per row,
 // dim sums of p v relative to the row's maximum, then the maximum (in log2
 // units) and the sum of p.  Parts are added in order.
-template <class T, int TM, int TK, int D>
+// Partials lie row by row, or (Turned) column by column, rows side by side.
+template <class T, int TM, int TK, int D, bool Turned>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a) {
   using Tile = Tiling<TM, TK>;
   __shared__ int64_t scratch[34];
@@ -172,17 +173,18 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a) {
   constexpr int kRow = D + 2, kLanes = D / 4;  // a thread takes four columns of a row
   const int rows = min(TM, cur.s.count * a.group - cur.m * TM);
   for (int i = threadIdx.x; i < rows * kLanes; i += 256) {
-    const int r = i / kLanes, col = i % kLanes * 4;
+    const int r = Turned ? i % rows : i / kLanes, col = (Turned ? i / rows : i % kLanes) * 4;
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int p = 0; p < parts; ++p) {
-      const float* row = a.part + (int64_t(2 * (c + p) + (p == 0)) * TM + r) * kRow;
-      const float pm = row[D], pl = row[D + 1];
+      const float* row = a.part + int64_t(2 * (c + p) + (p == 0)) * TM * kRow + (Turned ? r : r * kRow);
+      constexpr int kNext = Turned ? TM : 1;  // from one column to the next
+      const float pm = row[D * kNext], pl = row[(D + 1) * kNext];
       const float mx = fmaxf(m, pm);
       if (pl != 0.f) {  // a sum that is NaN counts
         const float f = ex2(m - mx), g = ex2(pm - mx);
         l = __fmaf_rn(l, f, pl * g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(o[k], f, row[col + k] * g);
+        for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(o[k], f, row[(col + k) * kNext] * g);
         m = mx;
       }
     }
@@ -193,5 +195,9 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a) {
     *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
   }
 }
+
+// attend_tc.cu: the kernel for many rows, its workspace in bytes.
+int64_t attend_tc_workspace(int dim);
+int launch_attend_tc(const AttendArgs& a, bool bf16, int dim, cudaStream_t s, bool& ran);
 
 }  // namespace q1

@@ -1,0 +1,585 @@
+// attend_tc.cu -- q1_paged_attention for many rows a key head: the tensor-core
+// kernel.
+//
+// The same formula as attend.cu, 4 D operations a (row, key) pair: from some
+// tens of rows on these bound it, so both products run on tcgen05 MMAs of 128
+// rows x 128 keys and the softmax between them on eight warps.
+//
+// An item is 256 rows (two tiles of 128) of one key head; a row is a new token
+// and one of the group's heads, so grouped heads share each key and value
+// tile.  Roles of the CTA's warps:
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row (its row of S lies
+//                   in its tensor-memory lane): maximum, p = 2^(s - m), P back
+//                   to tensor memory over S, the output at an item's end; they
+//                   also copy the rows of Q into shared memory.
+//   warp 8          issues the MMAs: S_w = Q_w K^T and O_w += P_w V, alternating between
+//                   the tiles, so that one tile's softmax runs under the
+//                   other's products.
+//   warp 9          TMA: one box a page and 64 dims, keys and values through one ring
+//                   of 128-key stages (128-byte swizzle; V is read as the
+//                   MN-major operand, so nothing is transposed).
+// Tensor memory: S_0, S_1 (128 columns each, P in the first 64 of them), O_0, O_1.
+// MMAs of one thread execute in order, so S_w of the next tile may be issued
+// behind the product that reads P_w, and S_w's completion implies that O_w holds
+// still: the softmax warps rescale O_w themselves, and only when a row's maximum
+// has grown by more than 2^8 (weights are then at most 2^8 relative to the
+// maximum in use, which f32 sums and both 16-bit types hold).
+//
+// Every wait is bounded; one that gives up raises the CTA's abort flag and the
+// device status word, and every role winds down.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <type_traits>
+
+#include "attend.cuh"
+#include "tc.cuh"
+
+namespace q1 {
+
+constexpr int kTcM = 128;            // rows of a tile
+constexpr int kTcItem = 2 * kTcM;    // rows of an item
+constexpr int kTcKeys = 128;         // keys of a unit
+constexpr int kTcAThreads = 384;     // three warpgroups (the last one's warps 10 and 11 have no role)
+// Registers a thread: 168 at launch, 384 threads; then 56 for the third
+// warpgroup and 224 for the two with the softmax, the same total.
+constexpr int kTcRegsLess = 56, kTcRegsMore = 224;
+static_assert(128 * (kTcRegsLess + 2 * kTcRegsMore) <= kTcAThreads * 168, "the block's registers at launch");
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr float kTcGrow = 8.f;       // log2 units a maximum may be behind
+
+struct AttendTcArgs {
+  AttendArgs a;
+  CUtensorMap k, v;   // boxes of 64 dims x box_keys slots
+  uint32_t q_sign;    // 0x80008000 where the scale is negative: -q and |scale| instead
+  int box_keys;
+  int axis_head, axis_slot, axis_page;  // positions (1..3) of the axes in the maps
+};
+
+template <int D>
+struct TcShape {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kTcKeys * D * 2;       // of K, V or a tile of Q
+  static constexpr int kHalfBytes = kTcKeys * 128;         // 64 dims of it
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kOffKV = 2 * kTileBytes;
+  static constexpr int kOffBars = kOffKV + kStages * kTileBytes;
+  static constexpr int kNumBars = 2 * kStages + 8;
+  static constexpr int kSmem = kOffBars + kNumBars * 8 + 16 + 1024;  // + alignment
+  static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
+};
+
+// K-major operand tile, 128-byte swizzle: 8-row groups of 1024 bytes.
+__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// MN-major operand tile, 128-byte swizzle: 8 rows of K are 1024 bytes, 64
+// columns further on is `chunk` bytes.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t chunk) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((chunk >> 4) & 0x3FFFu) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+template <class T>
+__host__ __device__ constexpr uint32_t idesc_attend(int N, bool b_mn_major) {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(kTcM >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] x B[smem], issued by one thread.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3,%4,%5,%6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A ring position: stage and parity of its current pass.
+struct RingPos {
+  int stage = 0;
+  uint32_t parity = 0;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++stage == N) stage = 0, parity ^= 1;
+  }
+};
+
+template <class T, int D>
+__global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_constant__ AttendTcArgs g) {
+  using Tile = Tiling<kTcItem, kTcKeys>;
+  using Shape = TcShape<D>;
+  constexpr int kStages = Shape::kStages;
+  const AttendArgs& a = g.a;
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ int64_t scratch[34];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile uint32_t abort_s;
+  unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  const uint32_t s0 = smem_addr(smem);
+  const uint32_t bars = s0 + Shape::kOffBars;
+  const auto full = [&](int s) { return bars + s * 8; };
+  const auto empty = [&](int s) { return bars + (kStages + s) * 8; };
+  const uint32_t qfull = bars + 2 * kStages * 8, sfull = qfull + 16, pfull = qfull + 32, ofull = qfull + 48;  // [2] each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(qfull + 8 * w, kTcM);
+      mbar_init(sfull + 8 * w, 1);
+      mbar_init(pfull + 8 * w, kTcM);
+      mbar_init(ofull + 8 * w, 1);
+    }
+    fence_barrier_init();
+    abort_s = 0;
+  }
+  if (warp == 8) tmem_alloc(smem_addr(&tmem_base_s), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  Cursor cur = {};
+  int64_t u0, u1;
+  int ctas = a.ctas;
+  locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+
+  // Whole warps wait, and agree on whether they may go on.  (Written out here:
+  // a call in the loops would keep the register split from taking effect.)
+  const auto wait = [&](uint32_t bar, uint32_t parity) {
+    bool done = mbar_try(bar, parity);
+    if (!done && !abort_s) {
+      const uint64_t t0 = globaltimer();
+      for (uint32_t i = 1; !(done = mbar_try(bar, parity)); ++i)
+        if ((i & 63) == 0 && (abort_s || globaltimer() - t0 > 1000000000ull)) break;
+      if (!done) {
+        abort_s = 1;
+        atomicOr(a.status, kStatusWaitTimeout);
+      }
+    }
+    return bool(__all_sync(0xffffffffu, done));
+  };
+  // Units of the current item that this CTA takes, and whether it has two tiles.
+  const auto part_of = [&](int64_t u) { return int(min(int64_t(cur.units - cur.unit), u1 - u)); };
+  const auto tiles_of = [&]() { return cur.s.count * a.group - cur.m * kTcItem > kTcM ? 2 : 1; };
+
+  if (warp >= 8) {
+   regs_down<kTcRegsLess>();
+   if (warp == 9) {
+    // ------------------------------------------------------------- TMA --
+    RingPos pos;
+    const int boxes_max = kTcKeys / g.box_keys, page_mask = (1 << a.kv.page_shift) - 1;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
+      const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
+      // The page of this lane's box, one unit ahead.
+      const auto page_at = [&](int unit) {
+        const int j = unit * kTcKeys + lane * g.box_keys;
+        return lane < boxes_max && j < keys ? table[j >> a.kv.page_shift] : 0;
+      };
+      int page = keys ? page_at(cur.unit) : 0;
+      for (int t = 0; t < take && keys && ok; ++t) {
+        const int unit = cur.unit + t, j = unit * kTcKeys + lane * g.box_keys;
+        const int boxes = min(boxes_max, (keys - unit * kTcKeys + g.box_keys - 1) / g.box_keys);
+        const int next = t + 1 < take ? page_at(unit + 1) : 0;
+        if (lane < boxes && (page < 0 || page >= a.kv.pages)) {
+          atomicOr(a.status, kStatusBadIndex);
+          page = a.kv.pages;  // past the map's end: the box reads as zeros
+        }
+        int c[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait(empty(pos.stage), pos.parity ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(pos.stage), uint32_t(boxes) * g.box_keys * D * 2);
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes + lane * g.box_keys * 128;
+#pragma unroll
+            for (int h = 0; h < Shape::kHalves; ++h)
+              tma_box(dst + h * Shape::kHalfBytes, kv ? &g.v : &g.k, full(pos.stage), h * 64, c[0], c[1], c[2]);
+          }
+          __syncwarp();
+          pos.next<kStages>();
+        }
+        page = next;
+      }
+      u += take;
+      if (u < u1) next_item<Tile>(a, cur);
+    }
+   } else if (warp == 8) {
+    // ------------------------------------------------------------- MMA --
+    constexpr uint32_t kIdS = idesc_attend<T>(kTcKeys, false), kIdO = idesc_attend<T>(D, true);
+    RingPos pos;              // of the next K or V tile
+    uint32_t qpar = 0, ppar[2] = {0, 0}, qpar2 = 0;
+    bool ok = true;
+    const auto scores = [&](int w, uint32_t kaddr) {  // S_w = Q_w K^T
+      if (lane == 0) {
+        const uint32_t q = s0 + w * Shape::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * Shape::kHalfBytes + (k % 4) * 32;
+          mma_f16_ss(tmem + w * 128, desc_k_sw128(q + off), desc_k_sw128(kaddr + off), kIdS, k > 0);
+        }
+        mma_commit(sfull + 8 * w);
+      }
+      __syncwarp();
+    };
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m), nw = tiles_of();
+      if (keys) {
+        ok = ok && wait(qfull, qpar);
+        qpar ^= 1;
+        if (nw == 2) {
+          ok = ok && wait(qfull + 8, qpar2);
+          qpar2 ^= 1;
+        }
+        ok = ok && wait(full(pos.stage), pos.parity);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t kaddr = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes;
+          for (int w = 0; w < nw; ++w) scores(w, kaddr);
+          if (lane == 0) mma_commit(empty(pos.stage));
+          __syncwarp();
+          pos.next<kStages>();
+        }
+        for (int t = 0; t < take && ok; ++t) {
+          const int unit = cur.unit + t, vstage = pos.stage;
+          ok = wait(full(vstage), pos.parity);
+          if (!ok) break;
+          const uint32_t vaddr = s0 + Shape::kOffKV + vstage * Shape::kTileBytes;
+          const int valid = keys - unit * kTcKeys;
+          if (valid < kTcKeys) {
+            // Rows past the keys hold whatever lay there: a weight of zero
+            // times that must be zero.
+            unsigned char* v = smem + Shape::kOffKV + vstage * Shape::kTileBytes;
+            for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
+#pragma unroll
+              for (int h = 0; h < Shape::kHalves; ++h)
+                *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          pos.next<kStages>();
+          const bool more = t + 1 < take;
+          const uint32_t kaddr = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes;
+          for (int w = 0; w < nw && ok; ++w) {
+            ok = wait(pfull + 8 * w, ppar[w]);
+            ppar[w] ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int k = 0; k < kTcKeys / 16; ++k)
+                mma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, desc_mn_sw128(vaddr + k * 2048, Shape::kHalfBytes), kIdO,
+                           t > 0 || k > 0);
+              if (!more) mma_commit(ofull + 8 * w);
+            }
+            __syncwarp();
+            if (more) {
+              if (w == 0) ok = wait(full(pos.stage), pos.parity);
+              if (ok) {
+                tc_fence_after();
+                scores(w, kaddr);
+              }
+            }
+          }
+          if (lane == 0) mma_commit(empty(vstage));
+          if (more && ok) {
+            if (lane == 0) mma_commit(empty(pos.stage));
+            pos.next<kStages>();
+          }
+          __syncwarp();
+        }
+      }
+      u += take;
+      if (u < u1) next_item<Tile>(a, cur);
+    }
+   }
+  } else {
+    // --------------------------------------------------------- softmax --
+    regs_up<kTcRegsMore>();
+    const int w = warp >> 2;                 // tile
+    const int row_in_tile = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t(warp & 3) * 32 << 16;
+    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * D;
+    uint32_t spar = 0, opar = 0;
+    bool ok = true;
+    const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
+      if (w < tiles_of()) {
+        const int row0 = cur.m * kTcItem + w * kTcM;
+        int token, head;
+        const bool live = row_of(cur, a.group, row0 + row_in_tile, token, head);
+        const int limit = live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0;
+        float o_scale = 0.f, mx = -INFINITY, sum = 0.f;
+        if (keys) {
+          // Q: this warp's 32 rows, 16 (8) lanes a row; rows past the last are zero.
+          {
+            constexpr int kLanes = D / 8, kOnce = 32 / kLanes;
+            const int piece = lane % kLanes;
+            unsigned char* q = smem + w * Shape::kTileBytes + (piece / 8) * Shape::kHalfBytes;
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += kOnce) {
+              const int r = (warp & 3) * 32 + r0 + lane / kLanes;
+              int qt, qh;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (row_of(cur, a.group, row0 + r, qt, qh))
+                v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
+              v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
+              *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(qfull + 8 * w);
+          }
+          float used = -INFINITY;  // the maximum that weights are relative to
+          uint64_t sum2 = f32x2(0.f, 0.f);
+          for (int t = 0; t < take; ++t) {
+            ok = wait(sfull + 8 * w, spar);
+            spar ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_wait_ld32(s[i]);
+            const int seen = limit - (cur.unit + t) * kTcKeys;
+            if (__any_sync(0xffffffffu, seen < kTcKeys)) {
+#pragma unroll
+              for (int i = 0; i < 128; ++i) s[i / 32][i % 32] = i < seen ? s[i / 32][i % 32] : 0xff800000u;
+            }
+            // Maximum in four chains.
+            float m4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              m4[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+              for (int j = 1; j < 32; ++j) m4[i] = fmaxf(m4[i], __uint_as_float(s[i][j]));
+            }
+            float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            const bool grown = top > used + kTcGrow || (used == -INFINITY && top > -INFINITY);
+            float f = 1.f;
+            if (grown) {
+              f = ex2(used - top);
+              used = top;
+              sum2 = mul2(sum2, f32x2(f, f));
+            }
+            if (t > 0 && __any_sync(0xffffffffu, grown)) {
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + c, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(to + c, o);
+              }
+            }
+            const float base = used == -INFINITY ? 0.f : -used;
+            const uint64_t base2 = f32x2(base, base);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t p[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int e = i * 32 + j * 2;
+                float x, y;
+                split2(fma2(f32x2(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1])), scale2, base2), x, y);
+                x = ex2(x), y = ex2(y);
+                sum2 = add2(sum2, f32x2(x, y));
+                p[j] = Elem<T>::pack2(x, y);
+              }
+              tmem_st16(ts + i * 16, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pfull + 8 * w);
+          }
+          if (!ok) break;
+          float sa, sb;
+          split2(sum2, sa, sb);
+          sum = sa + sb;
+          mx = used;
+          ok = wait(ofull + 8 * w, opar);
+          opar ^= 1;
+          if (!ok) break;
+          tc_fence_after();
+          o_scale = sum != 0.f ? 1.f : 0.f;
+        }
+        const bool whole = cur.unit == 0 && take == cur.units;
+        const int slot = cur.unit == 0 ? 1 : 0;
+        if (whole) o_scale = o_scale != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+        float* part = a.part + int64_t(2 * blockIdx.x + slot) * (D + 2) * kTcItem + w * kTcM + row_in_tile;
+        T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (keys) {
+            tmem_ld32(to + c, o);
+            tmem_wait_ld32(o);
+          }
+          if (whole) {
+            if (live) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  pk[e] = o_scale != 0.f ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * o_scale,
+                                                          __uint_as_float(o[j + 2 * e + 1]) * o_scale)
+                                         : 0u;
+                *reinterpret_cast<uint4*>(out + c + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) part[(c + j) * kTcItem] = __uint_as_float(o[j]);
+          }
+        }
+        if (!whole) {
+          part[D * kTcItem] = mx;
+          part[(D + 1) * kTcItem] = sum;
+        }
+        tc_fence_before();  // the next item's first product overwrites O after this thread's next arrival
+      }
+      u += take;
+      if (u < u1) next_item<Tile>(a, cur);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (abort_s) {
+    // Copies and products may still be under way: let them end first.
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base, int dim, int box_keys, int (&axis)[3]) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Encode fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess || !f) {
+      (void)cudaGetLastError();
+      return CUDA_ERROR_NOT_SUPPORTED;
+    }
+    fn = reinterpret_cast<Encode>(f);
+  }
+  // The axes head, slot, page in the order of their strides.
+  const int64_t stride[3] = {p.head_stride, p.slot_stride, p.page_stride};
+  const uint64_t size[3] = {uint64_t(p.kv_heads), uint64_t(1) << p.page_shift, uint64_t(p.pages)};
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[order[j]] > stride[order[j + 1]]) {
+        const int t = order[j];
+        order[j] = order[j + 1], order[j + 1] = t;
+      }
+  cuuint64_t dims[4] = {cuuint64_t(dim)}, strides[3];
+  cuuint32_t box[4] = {64}, ones[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = size[order[i]];
+    strides[i] = cuuint64_t(stride[order[i]]) * 2;
+    box[i + 1] = order[i] == 1 ? cuuint32_t(box_keys) : 1;
+    axis[order[i]] = i + 1;
+  }
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int64_t attend_tc_workspace(int dim) { return int64_t(2) * num_sms() * kTcItem * (dim + 2) * 4; }
+
+template <class T, int D>
+static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
+  const char* who = "q1_paged_attention launch";
+  static bool set[64] = {};
+  int dev = 0;
+  if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 TcShape<D>::kSmem), who))
+      return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  if (int e = launch_op<AttendTcArgs>(k_attend_tc<T, D>, dim3(unsigned(g.a.ctas)), kTcAThreads, TcShape<D>::kSmem, 1, s, who, g))
+    return e;
+  return launch_op(k_attend_join<T, kTcItem, kTcKeys, D, true>, dim3(unsigned(g.a.ctas)), 256, 0, 1, s, who, g.a);
+}
+
+// False in `ran` where no tensor map can describe the cache's strides.
+int launch_attend_tc(const AttendArgs& a, bool bf16, int dim, cudaStream_t s, bool& ran) {
+  AttendTcArgs g = {};
+  g.a = a;
+  g.a.ctas = num_sms();
+  // The largest score comes from the largest q.k, and a masked one stays -inf
+  // when scaled, where the scale is positive.
+  g.q_sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+  g.a.scale_log2 = std::max(std::fabs(a.scale_log2), FLT_MIN);
+  g.box_keys = a.kv.page_shift < 7 ? 1 << a.kv.page_shift : kTcKeys;
+  int axis[3] = {};
+  ran = encode_map(&g.k, bf16, a.kv, a.kv.k, dim, g.box_keys, axis) == CUDA_SUCCESS &&
+        encode_map(&g.v, bf16, a.kv, a.kv.v, dim, g.box_keys, axis) == CUDA_SUCCESS;
+  if (!ran) return Q1_OK;
+  g.axis_head = axis[0], g.axis_slot = axis[1], g.axis_page = axis[2];
+  if (dim == 128) return bf16 ? launch_tc_kernel<__nv_bfloat16, 128>(g, s) : launch_tc_kernel<__half, 128>(g, s);
+  return bf16 ? launch_tc_kernel<__nv_bfloat16, 64>(g, s) : launch_tc_kernel<__half, 64>(g, s);
+}
+
+}  // namespace q1
