@@ -8,17 +8,25 @@
 // An item is 256 rows (two tiles of 128) of one key head; a row is a new token
 // and one of the group's heads, so grouped heads share each key and value
 // tile.  Roles of the CTA's warps:
-//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row (its row of S lies
-//                   in its tensor-memory lane): maximum, p = 2^(s - m), P back
-//                   to tensor memory over S, the output at an item's end; they
-//                   also copy the rows of Q into shared memory.
-//   warp 8          issues the MMAs: S_w = Q_w K^T and O_w += P_w V, alternating between
-//                   the tiles, so that one tile's softmax runs under the
-//                   other's products.
-//   warp 9          TMA: one box a page and 64 dims, keys and values through one ring
+//   warps 0-7, 8-15 softmax of tile 0 and 1; warps q and q + 4 of a tile share rows
+//                   32q..32q+31 (tensor-memory lanes), one thread a row, the
+//                   first with keys 0-63 of a unit and the second with 64-127:
+//                   maximum, p = 2^(s - m), P back to tensor memory over its
+//                   own part of S, the output at an item's end.  They also
+//                   copy the rows of Q into shared memory.
+//   warps 16, 18    issue the MMAs of tile 0 and 1: O_w += P_w V and the next
+//                   S_w = Q_w K^T, in turns, so that one tile's softmax runs
+//                   under the other's products.  (Left to themselves the tiles
+//                   fall into step and the tensor core waits for both
+//                   softmaxes; with one warp for both, its waits, 150 cycles
+//                   each, lie bare.)
+//   warp 17         TMA: one box a page and 64 dims, keys and values through one ring
 //                   of 128-key stages (128-byte swizzle; V is read as the
 //                   MN-major operand, so nothing is transposed).
-// Tensor memory: S_0, S_1 (128 columns each, P in the first 64 of them), O_0, O_1.
+// A unit's weights are taken relative to the maximum in use before it, and its
+// own maximum, exchanged between a row's two threads meanwhile, is looked at
+// before P is stored: it rarely has grown by 2^8, and then they are taken again.
+// Tensor memory: S_0, S_1 (128 columns each, P in columns 0-31 and 64-95), O_0, O_1.
 // MMAs of one thread execute in order, so S_w of the next tile may be issued
 // behind the product that reads P_w, and S_w's completion implies that O_w holds
 // still: the softmax warps rescale O_w themselves, and only when a row's maximum
@@ -42,11 +50,12 @@ namespace q1 {
 constexpr int kTcM = 128;            // rows of a tile
 constexpr int kTcItem = 2 * kTcM;    // rows of an item
 constexpr int kTcKeys = 128;         // keys of a unit
-constexpr int kTcAThreads = 384;     // three warpgroups (the last one's warps 10 and 11 have no role)
-// Registers a thread: 168 at launch, 384 threads; then 56 for the third
-// warpgroup and 224 for the two with the softmax, the same total.
-constexpr int kTcRegsLess = 56, kTcRegsMore = 224;
-static_assert(128 * (kTcRegsLess + 2 * kTcRegsMore) <= kTcAThreads * 168, "the block's registers at launch");
+constexpr int kTcSoftWarps = 16;     // softmax warps: two a 32-row quarter of a tile
+constexpr int kTcAThreads = (kTcSoftWarps + 4) * 32;
+// Registers a thread: 96 at launch, then 64 for the last warpgroup and 104 for
+// the four with the softmax, the same total.
+constexpr int kTcRegsLess = 64, kTcRegsMore = 104;
+static_assert(128 * kTcRegsLess + 32 * kTcSoftWarps * kTcRegsMore <= kTcAThreads * 96, "the block's registers at launch");
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -73,7 +82,7 @@ struct TcShape {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffBars = kOffKV + kStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kStages + 8;
+  static constexpr int kNumBars = 2 * kStages + 18;
   static constexpr int kSmem = kOffBars + kNumBars * 8 + 16 + 1024;  // + alignment
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
 };
@@ -95,12 +104,28 @@ __host__ __device__ constexpr uint32_t idesc_attend(int N, bool b_mn_major) {
   return (1u << 4) | (f << 7) | (f << 10) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
          (uint32_t(kTcM >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] x B[smem], issued by one thread.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] x B[smem], issued by one elected lane of a converged warp.
+__device__ __forceinline__ void mma_f16_ss_elect(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
@@ -149,6 +174,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   const AttendArgs& a = g.a;
   extern __shared__ unsigned char raw_smem[];
   __shared__ int64_t scratch[34];
+  __shared__ float exchange[2][2][2][kTcM];  // [unit parity][tile][half][row]
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile uint32_t abort_s;
   unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -156,21 +182,25 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   const uint32_t bars = s0 + Shape::kOffBars;
   const auto full = [&](int s) { return bars + s * 8; };
   const auto empty = [&](int s) { return bars + (kStages + s) * 8; };
-  const uint32_t qfull = bars + 2 * kStages * 8, sfull = qfull + 16, pfull = qfull + 32, ofull = qfull + 48;  // [2] each
+  // Two of each (one a tile); pair: one for each two warps that share rows.
+  const uint32_t qfull = bars + 2 * kStages * 8, sfull = qfull + 16, ofull = qfull + 32, turn = qfull + 48,
+                 pfull = qfull + 64, pair = qfull + 80;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 2);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(qfull + 8 * w, kTcM);
+      mbar_init(qfull + 8 * w, 2 * kTcM);
       mbar_init(sfull + 8 * w, 1);
-      mbar_init(pfull + 8 * w, kTcM);
+      mbar_init(pfull + 8 * w, 2 * kTcM);
       mbar_init(ofull + 8 * w, 1);
+      mbar_init(turn + 8 * w, 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(pair + 8 * i, 2);
     fence_barrier_init();
     abort_s = 0;
   }
-  if (warp == 8) tmem_alloc(smem_addr(&tmem_base_s), 512);
+  if (warp == kTcSoftWarps) tmem_alloc(smem_addr(&tmem_base_s), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -202,153 +232,169 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   const auto part_of = [&](int64_t u) { return int(min(int64_t(cur.units - cur.unit), u1 - u)); };
   const auto tiles_of = [&]() { return cur.s.count * a.group - cur.m * kTcItem > kTcM ? 2 : 1; };
 
-  if (warp >= 8) {
-   regs_down<kTcRegsLess>();
-   if (warp == 9) {
-    // ------------------------------------------------------------- TMA --
-    RingPos pos;
-    const int boxes_max = kTcKeys / g.box_keys, page_mask = (1 << a.kv.page_shift) - 1;
-    bool ok = true;
-    for (int64_t u = u0; u < u1 && ok;) {
-      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
-      const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
-      // The page of this lane's box, one unit ahead.
-      const auto page_at = [&](int unit) {
-        const int j = unit * kTcKeys + lane * g.box_keys;
-        return lane < boxes_max && j < keys ? table[j >> a.kv.page_shift] : 0;
-      };
-      int page = keys ? page_at(cur.unit) : 0;
-      for (int t = 0; t < take && keys && ok; ++t) {
-        const int unit = cur.unit + t, j = unit * kTcKeys + lane * g.box_keys;
-        const int boxes = min(boxes_max, (keys - unit * kTcKeys + g.box_keys - 1) / g.box_keys);
-        const int next = t + 1 < take ? page_at(unit + 1) : 0;
-        if (lane < boxes && (page < 0 || page >= a.kv.pages)) {
-          atomicOr(a.status, kStatusBadIndex);
-          page = a.kv.pages;  // past the map's end: the box reads as zeros
-        }
-        int c[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!wait(empty(pos.stage), pos.parity ^ 1)) {
-            ok = false;
-            break;
+  if (warp >= kTcSoftWarps) {
+    regs_down<kTcRegsLess>();
+    if (warp == kTcSoftWarps + 1) {
+      // ------------------------------------------------------------- TMA --
+      RingPos pos;
+      const int boxes_max = kTcKeys / g.box_keys, page_mask = (1 << a.kv.page_shift) - 1;
+      bool ok = true;
+      for (int64_t u = u0; u < u1 && ok;) {
+        const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
+        const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
+        // The page of this lane's box, one unit ahead.
+        const auto page_at = [&](int unit) {
+          const int j = unit * kTcKeys + lane * g.box_keys;
+          return lane < boxes_max && j < keys ? table[j >> a.kv.page_shift] : 0;
+        };
+        int page = keys ? page_at(cur.unit) : 0;
+        for (int t = 0; t < take && keys && ok; ++t) {
+          const int unit = cur.unit + t, j = unit * kTcKeys + lane * g.box_keys;
+          const int boxes = min(boxes_max, (keys - unit * kTcKeys + g.box_keys - 1) / g.box_keys);
+          const int next = t + 1 < take ? page_at(unit + 1) : 0;
+          if (lane < boxes && (page < 0 || page >= a.kv.pages)) {
+            atomicOr(a.status, kStatusBadIndex);
+            page = a.kv.pages;  // past the map's end: the box reads as zeros
           }
-          if (lane == 0) mbar_arrive_expect_tx(full(pos.stage), uint32_t(boxes) * g.box_keys * D * 2);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes + lane * g.box_keys * 128;
+          int c[3];
 #pragma unroll
-            for (int h = 0; h < Shape::kHalves; ++h)
-              tma_box(dst + h * Shape::kHalfBytes, kv ? &g.v : &g.k, full(pos.stage), h * 64, c[0], c[1], c[2]);
-          }
-          __syncwarp();
-          pos.next<kStages>();
-        }
-        page = next;
-      }
-      u += take;
-      if (u < u1) next_item<Tile>(a, cur);
-    }
-   } else if (warp == 8) {
-    // ------------------------------------------------------------- MMA --
-    constexpr uint32_t kIdS = idesc_attend<T>(kTcKeys, false), kIdO = idesc_attend<T>(D, true);
-    RingPos pos;              // of the next K or V tile
-    uint32_t qpar = 0, ppar[2] = {0, 0}, qpar2 = 0;
-    bool ok = true;
-    const auto scores = [&](int w, uint32_t kaddr) {  // S_w = Q_w K^T
-      if (lane == 0) {
-        const uint32_t q = s0 + w * Shape::kTileBytes;
+          for (int i = 0; i < 3; ++i)
+            c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * Shape::kHalfBytes + (k % 4) * 32;
-          mma_f16_ss(tmem + w * 128, desc_k_sw128(q + off), desc_k_sw128(kaddr + off), kIdS, k > 0);
-        }
-        mma_commit(sfull + 8 * w);
-      }
-      __syncwarp();
-    };
-    for (int64_t u = u0; u < u1 && ok;) {
-      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m), nw = tiles_of();
-      if (keys) {
-        ok = ok && wait(qfull, qpar);
-        qpar ^= 1;
-        if (nw == 2) {
-          ok = ok && wait(qfull + 8, qpar2);
-          qpar2 ^= 1;
-        }
-        ok = ok && wait(full(pos.stage), pos.parity);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t kaddr = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes;
-          for (int w = 0; w < nw; ++w) scores(w, kaddr);
-          if (lane == 0) mma_commit(empty(pos.stage));
-          __syncwarp();
-          pos.next<kStages>();
-        }
-        for (int t = 0; t < take && ok; ++t) {
-          const int unit = cur.unit + t, vstage = pos.stage;
-          ok = wait(full(vstage), pos.parity);
-          if (!ok) break;
-          const uint32_t vaddr = s0 + Shape::kOffKV + vstage * Shape::kTileBytes;
-          const int valid = keys - unit * kTcKeys;
-          if (valid < kTcKeys) {
-            // Rows past the keys hold whatever lay there: a weight of zero
-            // times that must be zero.
-            unsigned char* v = smem + Shape::kOffKV + vstage * Shape::kTileBytes;
-            for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!wait(empty(pos.stage), pos.parity ^ 1)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full(pos.stage), uint32_t(boxes) * g.box_keys * D * 2);
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes + lane * g.box_keys * 128;
 #pragma unroll
               for (int h = 0; h < Shape::kHalves; ++h)
-                *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          pos.next<kStages>();
-          const bool more = t + 1 < take;
-          const uint32_t kaddr = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes;
-          for (int w = 0; w < nw && ok; ++w) {
-            ok = wait(pfull + 8 * w, ppar[w]);
-            ppar[w] ^= 1;
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int k = 0; k < kTcKeys / 16; ++k)
-                mma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, desc_mn_sw128(vaddr + k * 2048, Shape::kHalfBytes), kIdO,
-                           t > 0 || k > 0);
-              if (!more) mma_commit(ofull + 8 * w);
+                tma_box(dst + h * Shape::kHalfBytes, kv ? &g.v : &g.k, full(pos.stage), h * 64, c[0], c[1], c[2]);
             }
             __syncwarp();
-            if (more) {
-              if (w == 0) ok = wait(full(pos.stage), pos.parity);
-              if (ok) {
-                tc_fence_after();
-                scores(w, kaddr);
-              }
-            }
-          }
-          if (lane == 0) mma_commit(empty(vstage));
-          if (more && ok) {
-            if (lane == 0) mma_commit(empty(pos.stage));
             pos.next<kStages>();
           }
-          __syncwarp();
+          page = next;
         }
+        u += take;
+        if (u < u1) next_item<Tile>(a, cur);
       }
-      u += take;
-      if (u < u1) next_item<Tile>(a, cur);
+    } else if (warp != kTcSoftWarps + 3) {
+      // ------------------------------------------------------------- MMA --
+      constexpr uint32_t kIdS = idesc_attend<T>(kTcKeys, false), kIdO = idesc_attend<T>(D, true);
+      const int w = (warp - kTcSoftWarps) >> 1;  // tile
+      RingPos pos;                    // of the next K or V tile
+      uint32_t qpar = 0, ppar = 0, turnpar = 0;
+      bool ok = true;
+      const uint32_t ts = tmem + w * 128, to = tmem + 256 + w * D;
+      const uint64_t qdesc = desc_k_sw128(s0 + w * Shape::kTileBytes);
+      const auto tile_addr = [&](int stage) { return s0 + Shape::kOffKV + stage * Shape::kTileBytes; };
+      const auto hand_on = [&](bool hand) {
+        if (hand && lane == 0) mbar_arrive(turn + 8 * (w ^ 1));
+        __syncwarp();
+      };
+      const auto scores = [&](int stage, bool hand) {  // S_w = Q_w K^T
+        const uint64_t kdesc = desc_k_sw128(tile_addr(stage));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          constexpr int kHalf = Shape::kHalfBytes;
+          const int off = ((k / 4) * kHalf + (k % 4) * 32) >> 4;
+          if (k == D / 16 - 2) hand_on(hand);
+          mma_f16_ss_elect(ts, qdesc + off, kdesc + off, kIdS, k > 0);
+        }
+        mma_commit_elect(sfull + 8 * w);
+        mma_commit_elect(empty(stage));
+      };
+      for (int64_t u = u0; u < u1 && ok;) {
+        const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m), nw = tiles_of();
+        if (keys && w >= nw) {
+          // No rows for this tile: its share of releasing the stages.
+          for (int t = 0; t < 2 * take && ok; ++t) {
+            ok = wait(full(pos.stage), pos.parity);
+            if (ok && lane == 0) mbar_arrive(empty(pos.stage));
+            pos.next<kStages>();
+          }
+        } else if (keys) {
+          // This warp's turn: after the other tile's batch, if there is one.
+          const auto my_turn = [&](bool first) {
+            if (nw == 1 || (first && w == 0)) return true;
+            const bool done = wait(turn + 8 * w, turnpar);
+            turnpar ^= 1;
+            return done;
+          };
+          ok = wait(qfull + 8 * w, qpar) && wait(full(pos.stage), pos.parity) && my_turn(true);
+          qpar ^= 1;
+          if (ok) {
+            tc_fence_after();
+            scores(pos.stage, nw == 2);
+            pos.next<kStages>();
+          }
+          for (int t = 0; t < take && ok; ++t) {
+            const int vstage = pos.stage;
+            ok = wait(full(vstage), pos.parity);
+            if (!ok) break;
+            const int valid = keys - (cur.unit + t) * kTcKeys;
+            if (valid < kTcKeys) {
+              // Rows past the keys hold whatever lay there: a weight of zero
+              // times that must be zero.  (Both tiles' warps may write the same zeros.)
+              unsigned char* v = smem + Shape::kOffKV + vstage * Shape::kTileBytes;
+              for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
+#pragma unroll
+                for (int h = 0; h < Shape::kHalves; ++h)
+                  *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+            pos.next<kStages>();
+            const bool more = t + 1 < take;
+            const uint64_t vdesc = desc_mn_sw128(tile_addr(vstage), Shape::kHalfBytes);
+            if (more) ok = wait(full(pos.stage), pos.parity);
+            ok = ok && wait(pfull + 8 * w, ppar) && my_turn(false);
+            ppar ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ts_elect(to, ts + k / 4 * 64 + k % 4 * 8, vdesc + k * (2048 >> 4), kIdO, t > 0 || k > 0);
+            mma_commit_elect(empty(vstage));
+            if (more) {
+              scores(pos.stage, nw == 2);
+              pos.next<kStages>();
+            } else {
+              mma_commit_elect(ofull + 8 * w);
+              hand_on(nw == 2 && w == 0);
+            }
+          }
+        }
+        u += take;
+        if (u < u1) next_item<Tile>(a, cur);
+      }
     }
-   }
   } else {
     // --------------------------------------------------------- softmax --
     regs_up<kTcRegsMore>();
-    const int w = warp >> 2;                 // tile
-    const int row_in_tile = threadIdx.x & 127;
-    const uint32_t lanes = uint32_t(warp & 3) * 32 << 16;
-    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * D;
-    uint32_t spar = 0, opar = 0;
+    const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;  // tile, keys, rows
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = uint32_t(quarter) * 32 << 16;
+    constexpr int kCols = D / 2;  // columns of O that this warp rescales and writes
+    const uint32_t ts = tmem + lanes + w * 128 + half * 64, to = tmem + lanes + 256 + w * D + half * kCols;
+    const uint32_t pair_bar = pair + 8 * (w * 4 + quarter);
+    uint32_t spar = 0, opar = 0, xpar = 0;
+    // The value of the thread that shares the row (of the exchange whose parity is xpar).
+    const auto post = [&](float v) {
+      exchange[xpar][w][half][row] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_bar);
+    };
+    const auto fetch = [&](float& v) {
+      const bool done = wait(pair_bar, xpar);
+      v = exchange[xpar][w][half ^ 1][row];
+      xpar ^= 1;
+      return done;
+    };
     bool ok = true;
     const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
     for (int64_t u = u0; u < u1 && ok;) {
@@ -356,18 +402,19 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       if (w < tiles_of()) {
         const int row0 = cur.m * kTcItem + w * kTcM;
         int token, head;
-        const bool live = row_of(cur, a.group, row0 + row_in_tile, token, head);
-        const int limit = live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0;
-        float o_scale = 0.f, mx = -INFINITY, sum = 0.f;
+        const bool live = row_of(cur, a.group, row0 + row, token, head);
+        // Keys of this half of the CTA's first unit that the row may see.
+        int seen = (live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0) - cur.unit * kTcKeys - half * 64;
+        float used = -INFINITY, sum = 0.f;  // the maximum that weights are relative to
         if (keys) {
-          // Q: this warp's 32 rows, 16 (8) lanes a row; rows past the last are zero.
+          // Q: this warp's 16 rows, 16 (8) lanes a row; rows past the last are zero.
           {
             constexpr int kLanes = D / 8, kOnce = 32 / kLanes;
             const int piece = lane % kLanes;
             unsigned char* q = smem + w * Shape::kTileBytes + (piece / 8) * Shape::kHalfBytes;
 #pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += kOnce) {
-              const int r = (warp & 3) * 32 + r0 + lane / kLanes;
+            for (int r0 = 0; r0 < 16; r0 += kOnce) {
+              const int r = (warp & 7) * 16 + r0 + lane / kLanes;
               int qt, qh;
               uint4 v = make_uint4(0u, 0u, 0u, 0u);
               if (row_of(cur, a.group, row0 + r, qt, qh))
@@ -378,113 +425,130 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(qfull + 8 * w);
           }
-          float used = -INFINITY;  // the maximum that weights are relative to
-          uint64_t sum2 = f32x2(0.f, 0.f);
+          uint64_t sum2 = 0, base2 = 0;  // two partial sums; minus the maximum in use, twice
           for (int t = 0; t < take; ++t) {
             ok = wait(sfull + 8 * w, spar);
             spar ^= 1;
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[4][32];
+            uint32_t p[32];
+            const auto scores = [&](uint32_t (&s)[2][32]) {
+              tmem_ld32(ts, s[0]);
+              tmem_ld32(ts + 32, s[1]);
+              tmem_wait_ld32(s[0]);
+              tmem_wait_ld32(s[1]);
+              if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_wait_ld32(s[i]);
-            const int seen = limit - (cur.unit + t) * kTcKeys;
-            if (__any_sync(0xffffffffu, seen < kTcKeys)) {
-#pragma unroll
-              for (int i = 0; i < 128; ++i) s[i / 32][i % 32] = i < seen ? s[i / 32][i % 32] : 0xff800000u;
-            }
-            // Maximum in four chains.
-            float m4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              m4[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-              for (int j = 1; j < 32; ++j) m4[i] = fmaxf(m4[i], __uint_as_float(s[i][j]));
-            }
-            float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-            const bool grown = top > used + kTcGrow || (used == -INFINITY && top > -INFINITY);
-            float f = 1.f;
-            if (grown) {
-              f = ex2(used - top);
-              used = top;
-              sum2 = mul2(sum2, f32x2(f, f));
-            }
-            if (t > 0 && __any_sync(0xffffffffu, grown)) {
-#pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(to + c, o);
-                tmem_wait_ld16(o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(to + c, o);
+                for (int i = 0; i < 64; ++i) s[i / 32][i % 32] = i < seen ? s[i / 32][i % 32] : 0xff800000u;
               }
-            }
-            const float base = used == -INFINITY ? 0.f : -used;
-            const uint64_t base2 = f32x2(base, base);
+            };
+            const auto weights = [&](uint32_t (&s)[2][32]) {  // p, and their sums
+              uint64_t sum_a = 0, sum_b = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t p[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int e = i * 32 + j * 2;
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t(&v)[32] = s[j / 16];
                 float x, y;
-                split2(fma2(f32x2(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1])), scale2, base2), x, y);
+                split2(fma2(f32x2(__uint_as_float(v[j % 16 * 2]), __uint_as_float(v[j % 16 * 2 + 1])), scale2, base2), x, y);
                 x = ex2(x), y = ex2(y);
-                sum2 = add2(sum2, f32x2(x, y));
+                (j & 1 ? sum_b : sum_a) = add2(j & 1 ? sum_b : sum_a, f32x2(x, y));
                 p[j] = Elem<T>::pack2(x, y);
               }
-              tmem_st16(ts + i * 16, p);
+              return add2(sum_a, sum_b);
+            };
+            uint64_t part;
+            float mine, other;
+            {
+              uint32_t s[2][32];
+              scores(s);
+              float m[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t(&v)[32] = s[i / 2];
+                const int j0 = i % 2 * 16;
+                m[i] = fmaxf(__uint_as_float(v[j0]), __uint_as_float(v[j0 + 1]));
+#pragma unroll
+                for (int j = 2; j < 16; j += 2) m[i] = max3(m[i], __uint_as_float(v[j0 + j]), __uint_as_float(v[j0 + j + 1]));
+              }
+              mine = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+              post(mine);
+              part = weights(s);
             }
+            ok = fetch(other);
+            if (!ok) break;
+            const float top = fmaxf(mine, other) * a.scale_log2;
+            const bool grown = top > used + kTcGrow || (used == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, grown)) {
+              float f = 1.f;
+              if (grown) {
+                f = ex2(used - top);
+                used = top;
+                base2 = f32x2(-used, -used);
+                sum2 = mul2(sum2, f32x2(f, f));
+              }
+              if (t > 0) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(to + c, o);
+                  tmem_wait_ld16(o);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                  tmem_st16(to + c, o);
+                }
+              }
+              uint32_t s[2][32];
+              scores(s);
+              part = weights(s);
+            }
+            tmem_st32(ts, p);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(pfull + 8 * w);
+            sum2 = add2(sum2, part);
+            seen -= kTcKeys;
           }
           if (!ok) break;
-          float sa, sb;
+          float sa, sb, other;
           split2(sum2, sa, sb);
-          sum = sa + sb;
-          mx = used;
-          ok = wait(ofull + 8 * w, opar);
+          sa += sb;
+          post(sa);
+          ok = fetch(other) && wait(ofull + 8 * w, opar);
           opar ^= 1;
           if (!ok) break;
+          sum = sa + other;
           tc_fence_after();
-          o_scale = sum != 0.f ? 1.f : 0.f;
         }
         const bool whole = cur.unit == 0 && take == cur.units;
         const int slot = cur.unit == 0 ? 1 : 0;
-        if (whole) o_scale = o_scale != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
-        float* part = a.part + int64_t(2 * blockIdx.x + slot) * (D + 2) * kTcItem + w * kTcM + row_in_tile;
-        T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0);
+        const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+        float* part = a.part + int64_t(2 * blockIdx.x + slot) * (D + 2) * kTcItem + w * kTcM + row;
+        T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
+        for (int c = 0; c < kCols; c += 16) {
+          uint32_t o[16];
           if (keys) {
-            tmem_ld32(to + c, o);
-            tmem_wait_ld32(o);
+            tmem_ld16(to + c, o);
+            tmem_wait_ld16(o);
           }
           if (whole) {
             if (live) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
+              for (int j = 0; j < 16; j += 8) {
                 uint32_t pk[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  pk[e] = o_scale != 0.f ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * o_scale,
-                                                          __uint_as_float(o[j + 2 * e + 1]) * o_scale)
-                                         : 0u;
+                for (int e = 0; e < 4; ++e)  // a row that saw nothing is zero, whatever O holds
+                  pk[e] = sum != 0.f ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv)
+                                     : 0u;
                 *reinterpret_cast<uint4*>(out + c + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) part[(c + j) * kTcItem] = __uint_as_float(o[j]);
+            for (int j = 0; j < 16; ++j) part[(half * kCols + c + j) * kTcItem] = __uint_as_float(o[j]);
           }
         }
-        if (!whole) {
-          part[D * kTcItem] = mx;
+        if (!whole && half == 0) {
+          part[D * kTcItem] = used;
           part[(D + 1) * kTcItem] = sum;
         }
         tc_fence_before();  // the next item's first product overwrites O after this thread's next arrival
@@ -503,7 +567,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     }
   }
   __syncthreads();
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kTcSoftWarps) tmem_free(tmem, 512);
 }
 
 static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base, int dim, int box_keys, int (&axis)[3]) {
