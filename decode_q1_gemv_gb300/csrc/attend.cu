@@ -23,6 +23,7 @@ namespace q1 {
 constexpr int kRowsS = 16;   // rows of a tile
 constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
 constexpr int kWarpsS = 4;
+constexpr int kJoinSlices = 4;   // CTAs that join an item
 constexpr int kStagesS = 3;  // 2 x 96 KB of reads in flight an SM at D = 128
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -80,10 +81,10 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
-  locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  const int64_t total = locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
   const uint32_t ring = smem_addr(smem) + warp * (kStagesS * 2 * kChunkBytes);
   const int page_mask = (1 << a.kv.page_shift) - 1;
-  int slot = 0;  // of a partial: 0 only for an item that began in an earlier CTA
   for (int64_t u = u0; u < u1;) {
     const int take = int(min(int64_t(cur.units - cur.unit), u1 - u));  // units of this item here
     const int keys = Tile::keys(cur.s, a.group, cur.m);
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     }
     __syncthreads();
     const bool whole = cur.unit == 0 && take == cur.units;
-    slot = cur.unit == 0 ? 1 : 0;
+    if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
+    float* part = partial<kRowsS, D>(a, blockIdx.x, cur.unit == 0);
     for (int i = threadIdx.x; i < 16 * (D / 4); i += kWarpsS * 32) {
       const int r = i / (D / 4), col = i % (D / 4) * 4;
       int token, head;
@@ -262,10 +264,8 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
       } else {
-        float* row = a.part + (int64_t(2 * blockIdx.x + slot) * kRowsS + r) * (D + 2);
-        *reinterpret_cast<float2*>(row + col) = make_float2(v.x, v.y);
-        *reinterpret_cast<float2*>(row + col + 2) = make_float2(v.z, v.w);
-        if (col == 0) row[D] = m, row[D + 1] = l;
+        *reinterpret_cast<float4*>(part + r * D + col) = v;
+        if (col == 0) part[kRowsS * D + r] = m, part[kRowsS * (D + 1) + r] = l;
       }
     }
     __syncthreads();  // the ring and ml are free again
@@ -278,10 +278,10 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
 // of this file's has.
 static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kRowsS; }
 
-static int64_t workspace_rows() { return int64_t(2) * 2 * num_sms() * kRowsS; }
+static int attend_ctas() { return 2 * num_sms(); }
 
 template <class T, int D>
-static int launch_attend(AttendArgs& a, cudaStream_t s) {
+static int launch_attend(AttendArgs& a, void* workspace, cudaStream_t s) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
@@ -292,9 +292,10 @@ static int launch_attend(AttendArgs& a, cudaStream_t s) {
       return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  a.ctas = 2 * num_sms();
+  a.ctas = attend_ctas();
+  place_workspace(a, workspace);
   if (int e = launch_op(k_attend<T, D>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
-  return launch_op(k_attend_join<T, kRowsS, kKeysS, D, false>, dim3(unsigned(a.ctas)), 256, 0, 1, s, who, a);
+  return launch_op(k_attend_join<T, kRowsS, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
 }
 
 }  // namespace q1
@@ -305,7 +306,7 @@ extern "C" int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, 
   if (max_new < 1 || heads < 1 || kv_heads < 1 || heads > 4096 || heads % kv_heads || (dim != 64 && dim != 128))
     return fail(Q1_ERR_ARG, "q1_paged_attention_workspace: bad shape max_new=%lld heads=%lld kv_heads=%lld dim=%lld",
                 (long long)max_new, (long long)heads, (long long)kv_heads, (long long)dim);
-  const int64_t few = workspace_rows() * (dim + 2) * 4;
+  const int64_t few = attend_workspace(attend_ctas(), kRowsS, int(dim));
   if (!many_rows(max_new, heads / kv_heads)) return few;
   const int64_t many = attend_tc_workspace(int(dim));
   return few > many ? few : many;
@@ -335,7 +336,6 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
                 (long long)need);
   a.q = q, a.out = out, a.q_token = q_token_stride, a.q_head = q_head_stride;
   a.o_token = out_token_stride, a.o_head = out_head_stride;
-  a.part = static_cast<float*>(workspace);
   if (int e = ops_status_ptr(&a.status)) return e;
   a.heads = int(heads), a.group = int(heads / kv->kv_heads);
   a.scale_log2 = scale * 1.4426950408889634f;
@@ -343,9 +343,9 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   const bool bf = kv->dtype == Q1_BF16;
   if (many_rows(max_new, a.group)) {
     bool ran = false;
-    if (int e = launch_attend_tc(a, bf, int(kv->dim), s, ran)) return e;
+    if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
     if (ran) return Q1_OK;
   }
-  if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, s) : launch_attend<__half, 128>(a, s);
-  return bf ? launch_attend<__nv_bfloat16, 64>(a, s) : launch_attend<__half, 64>(a, s);
+  if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, workspace, s) : launch_attend<__half, 128>(a, workspace, s);
+  return bf ? launch_attend<__nv_bfloat16, 64>(a, workspace, s) : launch_attend<__half, 64>(a, workspace, s);
 }

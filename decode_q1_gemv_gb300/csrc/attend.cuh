@@ -11,7 +11,8 @@ struct AttendArgs {
   const void* q;           // [total_new][heads][dim], strides below
   void* out;
   int64_t q_token, q_head, o_token, o_head;  // elements
-  float* part;             // partial results: [2 * CTAs][rows of a tile][dim + 2]
+  float* part;             // partial results: two slots a CTA, see Partial
+  struct JoinItem* joins;  // [CTAs]
   unsigned* status;
   int heads, group;        // query heads, and of one key head
   float scale_log2;        // scale * log2(e)
@@ -141,63 +142,123 @@ __device__ __forceinline__ bool row_of(const Cursor& cur, int group, int r, int&
   return t < cur.s.count;
 }
 
-// Joins the items that were split over several CTAs.  CTA c of the launch
-// takes the item whose first unit is CTA c's and whose last is not: its
-// partials lie in slot 1 of CTA c and slot 0 of the CTAs after it (a CTA's
-// first item, when it began before, is in slot 0).  A partial is, per row,
-// dim sums of p v relative to the row's maximum, then the maximum (in log2
-// units) and the sum of p.  Parts are added in order.
-// Partials lie row by row, or (Turned) column by column, rows side by side.
-template <class T, int TM, int TK, int D, bool Turned>
-__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a) {
-  using Tile = Tiling<TM, TK>;
-  __shared__ int64_t scratch[34];
+// An item that begins in a CTA and ends in a later one: what the join has to
+// know of it, left by that CTA (parts = 0: none begins there).
+struct JoinItem {
+  int parts;              // CTAs with a part, from this one on
+  int first, count;       // the sequence's new tokens
+  int head, tile;         // key head and tile
+  int pad[3];
+};
+
+// Left by one thread of every CTA: first with no item, then for the one item
+// that it begins and does not end (its units begin at u, cut at u1).
+__device__ __forceinline__ void leave_join(const AttendArgs& a, const Cursor& cur, int64_t u, int64_t total, int ctas) {
+  const int64_t end = u + cur.units;
+  int parts = 1;
+  while (total * (int(blockIdx.x) + parts) / ctas < end) ++parts;
+  a.joins[blockIdx.x] = {parts, cur.s.first, cur.s.count, cur.h, cur.m, {0, 0, 0}};
+}
+
+// A partial result of TM rows: dim sums of p v relative to the row's maximum,
+// row by row or (Turned) column by column with the rows side by side, then
+// the maxima (log2 units), then the sums of p.  Slot 1 of a CTA holds the item
+// that it begins, slot 0 the one that began before it.
+template <int TM, int D>
+__device__ __forceinline__ float* partial(const AttendArgs& a, int cta, int slot) {
+  return a.part + int64_t(2 * cta + slot) * (TM * (D + 2));
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = 8;   // threads that share a value's parts, at most
+
+// Joins the items that were split: blockIdx.x is the CTA where the item
+// begins, the y CTAs share its values.  A thread takes four columns of a row;
+// up to eight of them share out the parts, so that a long row of parts (one
+// token over a long cache) costs few dependent reads.  Parts are added in a fixed order.
+template <class T, int TM, int D, bool Turned>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
+  __shared__ float sh[kJoinThreads][6];
   pdl_launch_dependents();
   pdl_wait();
-  Cursor cur = {};
-  int64_t u0, u1;
-  const int c = blockIdx.x;
-  int ctas = a.ctas;
-  const int64_t total = locate<Tile>(a, c, ctas, scratch, cur, u0, u1);
-  if (u0 >= u1) return;
-  // The last item of CTA c.
-  int64_t at = u0 - cur.unit;
-  while (at + cur.units < u1) {
-    at += cur.units;
-    next_item<Tile>(a, cur);
-  }
-  const int64_t end = at + cur.units;
-  if (end == u1 || at < u0) return;  // not split after c, or begun before c
-  int parts = 1;
-  while (total * (c + parts) / ctas < end) ++parts;
-  constexpr int kRow = D + 2, kLanes = D / 4;  // a thread takes four columns of a row
-  const int rows = min(TM, cur.s.count * a.group - cur.m * TM);
-  for (int i = threadIdx.x; i < rows * kLanes; i += 256) {
-    const int r = Turned ? i % rows : i / kLanes, col = (Turned ? i / rows : i % kLanes) * 4;
+  const JoinItem it = a.joins[blockIdx.x];
+  if (it.parts == 0) return;
+  int groups = 1;
+  while (groups < kJoinGroups && groups * 2 <= it.parts) groups *= 2;
+  const int width = kJoinThreads / groups, g = threadIdx.x / width;
+  const int rows = min(TM, it.count * a.group - it.tile * TM), values = rows * (D / 4);
+  for (int base = blockIdx.y * width; base < values; base += gridDim.y * width) {
+    const int e = base + threadIdx.x % width;
+    const int r = Turned ? e % rows : e / (D / 4), col = (Turned ? e / rows : e % (D / 4)) * 4;
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < parts; ++p) {
-      const float* row = a.part + int64_t(2 * (c + p) + (p == 0)) * TM * kRow + (Turned ? r : r * kRow);
-      constexpr int kNext = Turned ? TM : 1;  // from one column to the next
-      const float pm = row[D * kNext], pl = row[(D + 1) * kNext];
-      const float mx = fmaxf(m, pm);
-      if (pl != 0.f) {  // a sum that is NaN counts
-        const float f = ex2(m - mx), g = ex2(pm - mx);
-        l = __fmaf_rn(l, f, pl * g);
+    const auto add = [&](float pm, float pl, const float (&po)[4]) {
+      if (pl == 0.f) return;  // a sum that is NaN counts
+      const float mx = fmaxf(m, pm), f = ex2(m - mx), h = ex2(pm - mx);
+      l = __fmaf_rn(l, f, pl * h);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(o[k], f, row[(col + k) * kNext] * g);
-        m = mx;
+      for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(o[k], f, po[k] * h);
+      m = mx;
+    };
+    if (e < values) {
+      for (int p0 = g; p0 < it.parts; p0 += 4 * groups) {  // four parts' reads at a time
+        float pm[4], pl[4], po[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * groups;
+          pm[i] = -INFINITY, pl[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) po[i][k] = 0.f;
+          if (p < it.parts) {
+            const float* src = partial<TM, D>(a, blockIdx.x + p, p == 0);
+            pm[i] = src[TM * D + r], pl[i] = src[TM * (D + 1) + r];
+            if constexpr (Turned) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) po[i][k] = src[(col + k) * TM + r];
+            } else {
+              const float4 v = *reinterpret_cast<const float4*>(src + r * D + col);
+              po[i][0] = v.x, po[i][1] = v.y, po[i][2] = v.z, po[i][3] = v.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add(pm[i], pl[i], po[i]);
       }
     }
-    int token, head;
-    if (!row_of(cur, a.group, cur.m * TM + r, token, head)) continue;
-    const float inv = l > 0.f ? __fdiv_rn(1.0f, l) : 0.f;
-    uint2 w = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
+    if (groups > 1) {
+      __syncthreads();
+      float* mine = sh[threadIdx.x];
+      mine[0] = m, mine[1] = l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine[2 + k] = o[k];
+      __syncthreads();
+      if (g == 0)
+        for (int i = 1; i < groups; ++i) {
+          const float* his = sh[threadIdx.x + i * width];
+          const float po[4] = {his[2], his[3], his[4], his[5]};
+          add(his[0], his[1], po);
+        }
+    }
+    const int row = it.tile * TM + r, t = row / a.group;
+    if (g == 0 && e < values) {
+      const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+      const uint2 w = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
+      const int head = it.head * a.group + row - t * a.group;
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.first + t) * a.o_token + head * a.o_head + col) = w;
+    }
   }
+}
+
+// Bytes of a call's workspace: the join items, then two partials a CTA.
+inline int64_t attend_workspace(int ctas, int tm, int dim) {
+  return int64_t(ctas) * sizeof(JoinItem) + int64_t(2) * ctas * tm * (dim + 2) * 4;
+}
+inline void place_workspace(AttendArgs& a, void* workspace) {
+  a.joins = static_cast<JoinItem*>(workspace);
+  a.part = reinterpret_cast<float*>(a.joins + a.ctas);
 }
 
 // attend_tc.cu: the kernel for many rows, its workspace in bytes.
 int64_t attend_tc_workspace(int dim);
-int launch_attend_tc(const AttendArgs& a, bool bf16, int dim, cudaStream_t s, bool& ran);
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran);
 
 }  // namespace q1

@@ -64,6 +64,7 @@ template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+constexpr int kTcJoinSlices = 16;    // CTAs that join an item
 constexpr float kTcGrow = 8.f;       // log2 units a maximum may be behind
 
 struct AttendTcArgs {
@@ -211,7 +212,8 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
-  locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  const int64_t total = locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
 
   // Whole warps wait, and agree on whether they may go on.  (Written out here:
   // a call in the loops would keep the register split from taking effect.)
@@ -519,9 +521,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           tc_fence_after();
         }
         const bool whole = cur.unit == 0 && take == cur.units;
-        const int slot = cur.unit == 0 ? 1 : 0;
         const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
-        float* part = a.part + int64_t(2 * blockIdx.x + slot) * (D + 2) * kTcItem + w * kTcM + row;
+        if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
+        float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
         T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
@@ -608,7 +610,7 @@ static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-int64_t attend_tc_workspace(int dim) { return int64_t(2) * num_sms() * kTcItem * (dim + 2) * 4; }
+int64_t attend_tc_workspace(int dim) { return attend_workspace(num_sms(), kTcItem, dim); }
 
 template <class T, int D>
 static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
@@ -624,14 +626,16 @@ static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
   }
   if (int e = launch_op<AttendTcArgs>(k_attend_tc<T, D>, dim3(unsigned(g.a.ctas)), kTcAThreads, TcShape<D>::kSmem, 1, s, who, g))
     return e;
-  return launch_op(k_attend_join<T, kTcItem, kTcKeys, D, true>, dim3(unsigned(g.a.ctas)), 256, 0, 1, s, who, g.a);
+  return launch_op(k_attend_join<T, kTcItem, D, true>, dim3(unsigned(g.a.ctas), kTcJoinSlices), kJoinThreads, 0, 1, s, who,
+                   g.a);
 }
 
 // False in `ran` where no tensor map can describe the cache's strides.
-int launch_attend_tc(const AttendArgs& a, bool bf16, int dim, cudaStream_t s, bool& ran) {
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran) {
   AttendTcArgs g = {};
   g.a = a;
   g.a.ctas = num_sms();
+  place_workspace(g.a, workspace);
   // The largest score comes from the largest q.k, and a masked one stays -inf
   // when scaled, where the scale is positive.
   g.q_sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
