@@ -34,23 +34,28 @@ struct LoraArgs {
   unsigned* status;
   int64_t ldx, ldb, ldo;
   int nvec, n, rows, rank, adapters;
-  int vec_out;             // base and out rows allow 16-byte access
 };
 
 constexpr int kLoraTokens = 8;    // vectors of a bucket
 constexpr int kLoraWindow = 64;   // vectors among which buckets form
-constexpr int kLoraThreads = 256;
-constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kLoraLogThreads = 8, kLoraThreads = 1 << kLoraLogThreads;
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraRowsWarp = 4;  // rank rows a warp takes at a time
+constexpr int kLoraStages = 4;    // chunks of 16 KB in flight: 64 KB a CTA, two CTAs an SM
+constexpr int kLoraRing = kLoraStages * 4 * kLoraThreads * 16;
+constexpr int kLoraX = 8192;      // values of x in shared memory: of all vectors of the bucket
+constexpr int kLoraSmem = kLoraRing + kLoraX * 4;
 
 struct LoraShared {
-  float part[kLoraWarps][kLoraRowsWarp][kLoraTokens];  // a warp's sums
+  float part[kLoraThreads / 8][4 * kLoraTokens];       // (quad, warp of it): the sums of four rank rows
   float mine[kLoraMaxRank][kLoraTokens];               // this CTA's slice of n
   float t[kLoraMaxRank][kLoraTokens];                  // all slices, scaled
   int token[kLoraTokens];
   int count;
 };
+
+__device__ __forceinline__ void lora_copy(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
 
 // Sums of v over the lanes of aligned groups of `width` lanes, where each
 // halving step gives a lane half of the values it still has: afterwards lane
@@ -76,149 +81,252 @@ __device__ __forceinline__ void fold(float (&v)[N], int width, int lane) {
   }
 }
 
+// What a CTA has to do for a bucket: a slice of n of the first product, then a
+// slice of the rows of the second, both cut into chunks in which every thread
+// has four 16-byte pieces of weights:
+//   first:  four rank rows (quad) at one piece of n (part); parts * 8 values of
+//           n a chunk, parts a power of two;
+//   second: four rows at one piece of the rank; `width` (a power of two) lanes
+//           share a row.
+struct LoraSplit {
+  int rank, r0, r1, slice;   // rank in use; rows; values of n
+  int quads;                 // of four rank rows: a power of two, as are
+  int parts, width;          // parts = 1 << lparts and width = 1 << lwidth
+  int lparts, lwidth;
+  int down, up;              // chunks of each product
+  // The calling thread's place: in the first product its quad and part, in the
+  // second the first row of a chunk and its piece.
+  int quad, part, row, piece;
+  const void* a0;            // its first piece in A (row quad * 4), chunks parts * 8 values apart
+  const void* b0;            // its first piece in B (row r0 + row), chunks 4 * 256 / width rows apart
+  int b_step;                // values of B from one chunk to the next
+};
+
+// The least k with 2^k >= v, v >= 0 (0 for 0 and 1).
+__device__ __forceinline__ int log2_from(int v) { return v <= 1 ? 0 : 32 - __clz(v - 1); }
+
+// Asynchronous copies of chunk c (of both products in turn) into the calling
+// thread's own places of the ring; what lies past an end reads as zero.
+template <class T>
+__device__ __forceinline__ void lora_fetch(const LoraArgs& a, const LoraSplit& s, uint32_t ring, int c) {
+  const uint32_t dst = ring + (c % kLoraStages) * (4 * kLoraThreads * 16) + threadIdx.x * 16;
+  if (c < s.down) {
+    const T* src = static_cast<const T*>(s.a0) + c * s.parts * 8;
+    const bool inside = (c * s.parts + s.part) * 8 < s.slice;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool live = inside && s.quad * 4 + r < s.rank;
+      lora_copy(dst + r * (kLoraThreads * 16), live ? src : static_cast<const T*>(a.wa), live);
+      src += a.n;
+    }
+  } else if (c < s.down + s.up) {
+    const int k = c - s.down, left = s.r1 - s.r0 - s.row - k * (4 * kLoraThreads >> s.lwidth);
+    const T* src = static_cast<const T*>(s.b0) + int64_t(k) * s.b_step;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool live = r < left && s.piece * 8 < s.rank;
+      lora_copy(dst + r * (kLoraThreads * 16), live ? src : static_cast<const T*>(a.wb), live);
+      src += a.rank;
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The thread's four pieces of chunk c, and the copies of the chunk that takes
+// the place of the one before it.
+template <class T>
+__device__ __forceinline__ void lora_pieces(const LoraArgs& a, const LoraSplit& s, unsigned char* ring, int c, float (&w)[4][8]) {
+  lora_fetch<T>(a, s, smem_addr(ring), c + kLoraStages - 1);
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    Elem<T>::unpack(*reinterpret_cast<const uint4*>(ring + (((c % kLoraStages) * 4 + r) * kLoraThreads + threadIdx.x) * 16), w[r]);
+}
+
+// Copies x from element j0 on (`count` of them, a multiple of 8) of the
+// bucket's vectors into shared memory, 16-byte pieces of even and odd number
+// apart ([vector][2][window / 8]), so that neighbouring lanes read
+// neighbouring pieces.
+template <int M>
+__device__ __forceinline__ void lora_fetch_x(const LoraArgs& a, const LoraShared& sh, uint32_t xs, int j0, int count) {
+  constexpr int kWindow = kLoraX / M;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const float* x = a.x + sh.token[i] * a.ldx + j0;
+#pragma unroll 1
+    for (int p = threadIdx.x; p < count / 4; p += kLoraThreads)
+      lora_copy(xs + (i * (kWindow / 4) + (p & 1) * (kWindow / 8) + p / 2) * 16, x + p * 4, true);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
 // First product: mine[k][i] = sum over this CTA's slice of A[k] x_i, k < rank.
+// The first window of x is under way (before the ring's first chunks).
 template <class T, int M>
-__device__ __forceinline__ void lora_down(const LoraArgs& a, LoraShared& sh, const T* A, int rank, int j0, int j1) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* x[M];
+__device__ __forceinline__ void lora_down(const LoraArgs& a, LoraShared& sh, const LoraSplit& s, unsigned char* ring, int j0) {
+  constexpr int kWindow = kLoraX / M;  // at least parts * 8: a window is whole chunks
+  constexpr int kLog4M = M == 1 ? 2 : M == 2 ? 3 : M == 4 ? 4 : 5;
+  static_assert(kLoraX / kLoraTokens >= 1024, "a chunk of rank 8 (parts * 8 = 1024) fits the smallest window");
+  const int lane = threadIdx.x & 31;
+  const float4* xs = reinterpret_cast<const float4*>(ring + kLoraRing);
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
+  __syncthreads();
+  float acc[4 * M];
 #pragma unroll
-  for (int i = 0; i < M; ++i) x[i] = a.x + sh.token[i] * a.ldx;
-  // Warps share out (rank rows in fours) x (parts of the slice).
-  const int quads = (rank + kLoraRowsWarp - 1) / kLoraRowsWarp;
-  if (quads == 0) return;  // an adapter of rank 0 (the whole cluster agrees)
-  int parts = 1;
-  while (parts * 2 * quads <= kLoraWarps) parts *= 2;
-  const int step = kLoraWarps / parts;  // quads at a time
-  for (int q0 = 0; q0 < quads; q0 += step) {
-    const int quad = q0 + warp / parts, part = warp % parts;
-    float acc[kLoraRowsWarp * M];
-#pragma unroll
-    for (int i = 0; i < kLoraRowsWarp * M; ++i) acc[i] = 0.f;
-    if (quad < quads) {
-      const T* row[kLoraRowsWarp];
-#pragma unroll
-      for (int r = 0; r < kLoraRowsWarp; ++r) row[r] = A + int64_t(min(quad * kLoraRowsWarp + r, rank - 1)) * a.n;
-      for (int j = j0 + (part * 32 + lane) * 8; j < j1; j += parts * 256) {
-        float w[kLoraRowsWarp][8];
-#pragma unroll
-        for (int r = 0; r < kLoraRowsWarp; ++r) Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(row[r] + j)), w[r]);
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-          const float4 lo = *reinterpret_cast<const float4*>(x[i] + j), hi = *reinterpret_cast<const float4*>(x[i] + j + 4);
-          const float xv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int r = 0; r < kLoraRowsWarp; ++r) acc[r * M + i] = __fmaf_rn(w[r][e], xv[e], acc[r * M + i]);
-        }
-      }
+  for (int i = 0; i < 4 * M; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < s.down; ++c) {
+    const int j = (c * s.parts + s.part) * 8;
+    if (c > 0 && c * s.parts * 8 % kWindow == 0) {  // the next window of x
+      __syncthreads();
+      lora_fetch_x<M>(a, sh, smem_addr(xs), j0 + c * s.parts * 8, min(kWindow, s.slice - c * s.parts * 8));
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
     }
-    fold<kLoraRowsWarp * M>(acc, 32, lane);
-    // A lane holds kLoraRowsWarp * M / 32 sums, or one that 32 / that many lanes share.
-    constexpr int kSums = kLoraRowsWarp * M;
-    static_assert(kSums <= 32, "one sum a lane at most");
-    if (lane % (32 / kSums) == 0) (&sh.part[warp][0][0])[lane / (32 / kSums)] = acc[0];
-    __syncthreads();
-    for (int i = threadIdx.x; i < step * kSums; i += kLoraThreads) {
-      const int qd = i / kSums, k = (q0 + qd) * kLoraRowsWarp + i % kSums / M;
-      if (k < rank) {
-        float s = 0.f;
-        for (int p = 0; p < parts; ++p) s = __fadd_rn(s, (&sh.part[qd * parts + p][0][0])[i % kSums]);
-        sh.mine[k][i % M] = s;
-      }
+    float w[4][8];
+    lora_pieces<T>(a, s, ring, c, w);
+    if (j >= s.slice) continue;
+    const float4* xj = xs + j % kWindow / 8;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float4 lo = xj[i * (kWindow / 4)], hi = xj[i * (kWindow / 4) + kWindow / 8];
+      const float xv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r * M + i] = __fmaf_rn(w[r][e], xv[e], acc[r * M + i]);
     }
-    __syncthreads();
+  }
+  // Over the parts: the lanes of a quad, then (more than 32 parts) its warps.
+  const int width = s.parts < 32 ? s.parts : 32, lwarps = s.parts < 32 ? 0 : s.lparts - 5;
+  fold<4 * M>(acc, width, lane);
+  // A lane holds 4 M / width sums, or one that width / (4 M) lanes share.
+  const int at = lane & (width - 1), lshare = s.parts < 32 ? s.lparts - kLog4M : 5 - kLog4M;
+  const int keep = lshare > 0 ? 1 : 1 << -lshare;
+  if ((at & ((1 << (lshare > 0 ? lshare : 0)) - 1)) == 0) {
+    float* dst = sh.part[(s.quad << lwarps) + s.part / 32] + (lshare > 0 ? at >> lshare : at << -lshare);
+#pragma unroll
+    for (int i = 0; i < 4 * M; ++i)
+      if (i < keep) dst[i] = acc[i];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < s.quads * 4 * M; i += kLoraThreads) {
+    float v = 0.f;
+#pragma unroll 1
+    for (int p = 0; p < 1 << lwarps; ++p) v = __fadd_rn(v, sh.part[(i / (4 * M) << lwarps) + p][i % (4 * M)]);
+    sh.mine[i / M][i % M] = v;
   }
 }
 
-// Second product: rows [r0, r1) of B t for the bucket's vectors.  `width`
-// neighbouring lanes take the 16-byte pieces of a row of B, four rows at a
-// time.
-template <class T, int M>
-__device__ __forceinline__ void lora_up(const LoraArgs& a, const LoraShared& sh, const T* B, int rank, int r0, int r1) {
-  const int pieces = (rank + 7) / 8;
-  int width = 2;
-  while (width < pieces) width *= 2;
-  const int lane = threadIdx.x & 31, piece = lane & (width - 1);
+// Second product: rows [r0, r1) of B t for the bucket's vectors.
+template <class T, int M, bool VEC>
+__device__ __forceinline__ void lora_up(const LoraArgs& a, const LoraShared& sh, const LoraSplit& s, unsigned char* ring) {
+  const int lane = threadIdx.x & 31, piece = s.piece;
+  // A row's lanes share out the vectors to write: `keep` each, from `first` on.
+  constexpr int kLogM = M == 1 ? 0 : M == 2 ? 1 : M == 4 ? 2 : 3;
+  const int lshare = s.lwidth - kLogM, keep = lshare > 0 ? 1 : 1 << -lshare;
+  const int first = lshare > 0 ? piece >> lshare : piece << -lshare;
+  const bool writes = (piece & ((1 << (lshare > 0 ? lshare : 0)) - 1)) == 0;
   float t[8][M];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
 #pragma unroll
-    for (int i = 0; i < M; ++i) t[e][i] = piece * 8 + e < rank ? sh.t[piece * 8 + e][i] : 0.f;
-  const int rows_pass = kLoraThreads / width * 4;
-  for (int base = r0; base < r1; base += rows_pass) {  // whole warps stay together
-    const int row = base + threadIdx.x / width * 4;
-    float acc[M][4];
+    for (int i = 0; i < M; ++i) t[e][i] = piece * 8 + e < s.rank ? sh.t[piece * 8 + e][i] : 0.f;
+  // The values that the chunk's results are added to, read one chunk ahead.
+  constexpr int kKeep = M > 1 ? M / 2 : 1;
+  float4 next[kKeep];
+  const int step = 4 * kLoraThreads >> s.lwidth;  // rows of a chunk
+  const auto fetch_base = [&](int row) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (piece < pieces && row + k < r1) raw = __ldg(reinterpret_cast<const uint4*>(B + int64_t(row + k) * a.rank) + piece);
-      float w[8];
-      Elem<T>::unpack(raw, w);
-      if (piece * 8 + 8 > rank) {  // values past the adapter's rank may be anything
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = piece * 8 + e < rank ? w[e] : 0.f;
+    for (int i = 0; i < kKeep; ++i) {
+      next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!writes || i >= keep || first + i >= sh.count) continue;
+      const float* in = a.base + sh.token[first + i] * a.ldb + row;
+      if constexpr (VEC) {  // rows is a multiple of four
+        if (row < s.r1) next[i] = *reinterpret_cast<const float4*>(in);
+      } else {
+        if (row < s.r1) next[i].x = in[0];
+        if (row + 1 < s.r1) next[i].y = in[1];
+        if (row + 2 < s.r1) next[i].z = in[2];
+        if (row + 3 < s.r1) next[i].w = in[3];
       }
+    }
+  };
+  int row = s.r0 + s.row;
+  fetch_base(row);
+#pragma unroll 1
+  for (int c = 0; c < s.up; ++c, row += step) {  // whole warps stay together
+    float4 base[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) base[i] = next[i];
+    if (c + 1 < s.up) fetch_base(row + step);
+    float w[4][8], f[4][M];
+    lora_pieces<T>(a, s, ring, s.down + c, w);
+    if (piece * 8 + 8 > s.rank) {  // values past the adapter's rank may be anything
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r][e] = piece * 8 + e < s.rank ? w[r][e] : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
 #pragma unroll
       for (int i = 0; i < M; ++i) {
-        acc[i][k] = 0.f;
+        f[r][i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][k] = __fmaf_rn(w[e], t[e][i], acc[i][k]);
+        for (int e = 0; e < 8; ++e) f[r][i] = __fmaf_rn(w[r][e], t[e][i], f[r][i]);
       }
+      fold<M>(f[r], s.width, lane);
     }
-    // Fold over the lanes of a row; each lane ends with the vectors it writes.
-    float f[4][M];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-      for (int i = 0; i < M; ++i) f[k][i] = acc[i][k];
-      fold<M>(f[k], width, lane);
-    }
-    const int shared_by = width > M ? width / M : 1, keep = width > M ? 1 : M / width;
-    if (piece % shared_by) continue;
-    const int first = piece / shared_by * keep;
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      if (i >= keep || first + i >= sh.count) continue;
-      const int64_t v = sh.token[first + i];
-      const float* in = a.base + v * a.ldb + row;
-      float* out = a.out + v * a.ldo + row;
-      if (a.vec_out && row + 4 <= r1) {
-        float4 b = *reinterpret_cast<const float4*>(in);
-        b.x = __fadd_rn(b.x, f[0][i]), b.y = __fadd_rn(b.y, f[1][i]), b.z = __fadd_rn(b.z, f[2][i]), b.w = __fadd_rn(b.w, f[3][i]);
-        *reinterpret_cast<float4*>(out) = b;
+    for (int i = 0; i < kKeep; ++i) {
+      if (!writes || i >= keep || first + i >= sh.count) continue;
+      float* out = a.out + sh.token[first + i] * a.ldo + row;
+      const float4 v = make_float4(__fadd_rn(base[i].x, f[0][i]), __fadd_rn(base[i].y, f[1][i]), __fadd_rn(base[i].z, f[2][i]),
+                                   __fadd_rn(base[i].w, f[3][i]));
+      if constexpr (VEC) {
+        if (row < s.r1) *reinterpret_cast<float4*>(out) = v;
       } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (row + k < r1) out[k] = __fadd_rn(in[k], f[k][i]);
+        if (row < s.r1) out[0] = v.x;
+        if (row + 1 < s.r1) out[1] = v.y;
+        if (row + 2 < s.r1) out[2] = v.z;
+        if (row + 3 < s.r1) out[3] = v.w;
       }
     }
   }
 }
 
-template <class T, int M>
-__device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, int adapter, cg::cluster_group& cluster) {
-  const int c = int(cluster.block_rank()), C = int(cluster.num_blocks());
-  const int rank = a.ranks ? max(0, min(a.ranks[adapter], a.rank)) : a.rank;
-  const int per_n = (a.n / 8 + C - 1) / C * 8;
-  lora_down<T, M>(a, sh, static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n, rank, min(a.n, c * per_n),
-                  min(a.n, (c + 1) * per_n));
+template <class T, int M, bool VEC>
+__device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, const LoraSplit& s, unsigned char* ring,
+                                            int j0, float scale, cg::cluster_group& cluster) {
+  const int C = int(cluster.num_blocks());
+  lora_fetch_x<M>(a, sh, smem_addr(ring + kLoraRing), j0, min(kLoraX / M, s.slice));
+#pragma unroll 1
+  for (int i = 0; i < kLoraStages - 1; ++i) lora_fetch<T>(a, s, smem_addr(ring), i);
+  lora_down<T, M>(a, sh, s, ring, j0);
   cluster.sync();
-  const float scale = a.scale ? a.scale[adapter] : 1.f;
-  for (int i = threadIdx.x; i < rank * M; i += kLoraThreads) {
-    float s = 0.f;
-    for (int p = 0; p < C; ++p) s = __fadd_rn(s, cluster.map_shared_rank(&sh.mine[0][0], p)[i / M * kLoraTokens + i % M]);
-    sh.t[i / M][i % M] = __fmul_rn(s, scale);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < s.rank * M; i += kLoraThreads) {
+    float v = 0.f;
+    for (int p = 0; p < C; p += 4) {  // four reads at a time; a cluster has 4, 8 or 16 CTAs
+      float part[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part[k] = cluster.map_shared_rank(&sh.mine[0][0], p + k)[i / M * kLoraTokens + i % M];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v = __fadd_rn(v, part[k]);
+    }
+    sh.t[i / M][i % M] = __fmul_rn(v, scale);
   }
   cluster.sync();  // every CTA has read `mine`, and t is complete
-  const int per_r = ((a.rows + 3) / 4 + C - 1) / C * 4;
-  lora_up<T, M>(a, sh, static_cast<const T*>(a.wb) + int64_t(adapter) * a.rows * a.rank, rank, min(a.rows, c * per_r),
-                min(a.rows, (c + 1) * per_r));
+  lora_up<T, M, VEC>(a, sh, s, ring);
 }
 
-template <class T>
-__global__ void __launch_bounds__(kLoraThreads) k_lora_add(LoraArgs a) {
+// VEC: base and out rows allow 16-byte accesses, and rows is a multiple of 4.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
   __shared__ LoraShared sh;
+  extern __shared__ __align__(16) unsigned char ring[];
   cg::cluster_group cluster = cg::this_cluster();
   pdl_launch_dependents();
   pdl_wait();
@@ -254,19 +362,66 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_add(LoraArgs a) {
     if (count && adapter < 0) {
       if (a.out != a.base) {
         const int c = int(cluster.block_rank());
+#pragma unroll 1
         for (int i = 0; i < count; ++i)
+#pragma unroll 1
           for (int r = c * kLoraThreads + threadIdx.x; r < a.rows; r += C * kLoraThreads)
             a.out[sh.token[i] * a.ldo + r] = a.base[sh.token[i] * a.ldb + r];
       }
-    } else if (count == 1) {
-      lora_bucket<T, 1>(a, sh, adapter, cluster);
-    } else if (count && count <= 4) {
-      lora_bucket<T, 4>(a, sh, adapter, cluster);
     } else if (count) {
-      lora_bucket<T, 8>(a, sh, adapter, cluster);
+      LoraSplit s;
+      s.rank = a.ranks ? max(0, min(a.ranks[adapter], a.rank)) : a.rank;
+      const int c = int(cluster.block_rank());
+      const int per_n = (a.n / 8 + C - 1) / C * 8, per_r = ((a.rows + 3) / 4 + C - 1) / C * 4;
+      const int j0 = min(a.n, c * per_n);
+      s.slice = min(a.n, j0 + per_n) - j0;
+      s.r0 = min(a.rows, c * per_r), s.r1 = min(a.rows, s.r0 + per_r);
+      const int lquads = max(1, log2_from((s.rank + 3) / 4));
+      s.quads = 1 << lquads, s.lparts = kLoraLogThreads - lquads, s.parts = 1 << s.lparts;
+      s.lwidth = max(1, log2_from((s.rank + 7) / 8)), s.width = 1 << s.lwidth;
+      s.down = s.rank ? (s.slice + s.parts * 8 - 1) >> (s.lparts + 3) : 0;
+      s.up = (((s.r1 - s.r0) << s.lwidth) + 4 * kLoraThreads - 1) / (4 * kLoraThreads);
+      s.quad = threadIdx.x >> s.lparts, s.part = threadIdx.x & (s.parts - 1);
+      s.row = (threadIdx.x >> s.lwidth) * 4, s.piece = threadIdx.x & (s.width - 1);
+      s.a0 = static_cast<const T*>(a.wa) + (int64_t(adapter) * a.rank + s.quad * 4) * a.n + j0 + s.part * 8;
+      s.b0 = static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + s.r0 + s.row) * a.rank + s.piece * 8;
+      s.b_step = (4 * kLoraThreads >> s.lwidth) * a.rank;
+      const float scale = a.scale ? a.scale[adapter] : 1.f;
+      if (count == 1)
+        lora_bucket<T, 1, VEC>(a, sh, s, ring, j0, scale, cluster);
+      else if (count == 2)
+        lora_bucket<T, 2, VEC>(a, sh, s, ring, j0, scale, cluster);
+      else if (count <= 4)
+        lora_bucket<T, 4, VEC>(a, sh, s, ring, j0, scale, cluster);
+      else
+        lora_bucket<T, 8, VEC>(a, sh, s, ring, j0, scale, cluster);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();  // sh is free again
   }
+}
+
+template <class T, bool VEC>
+static int launch_lora(const LoraArgs& g, cudaStream_t s) {
+  const char* who = "q1_lora_add launch";
+  static bool set[64] = {};
+  int dev = 0;
+  if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    if (int e = cuda_status(cudaFuncSetAttribute(k_lora_add<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLoraSmem), who))
+      return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(k_lora_add<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
+      return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  // Clusters of 16 while all of them run at once (13 vectors of one adapter,
+  // n 8120: 12.8 us against 15.5 with 8), of 8 beyond (64 vectors, rank 64: 28.7 us
+  // against 47).  Their number is odd: the vectors that lead buckets are every
+  // eighth in a prompt, and a cluster takes every so many-th vector.
+  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : 8;
+  const int64_t most = (num_sms() - 1) | 1;
+  const dim3 grid(unsigned((g.nvec < most ? g.nvec : most) * cluster));
+  return launch_op(k_lora_add<T, VEC>, grid, kLoraThreads, kLoraSmem, cluster, s, who, g);
 }
 
 }  // namespace q1
@@ -290,13 +445,10 @@ extern "C" int q1_lora_add(const float* x, int64_t ldx, int64_t nvec, int64_t n,
   if (ldx < n || ldb < rows || ldo < rows) return fail(Q1_ERR_ARG, "%s: a row stride is less than its row", who);
   if (base == out && ldb != ldo) return fail(Q1_ERR_ARG, "%s: in place, base and out need the same stride", who);
   LoraArgs g = {x, a, b, index, ranks, scale, base, out, nullptr, ldx, ldb, ldo, int(nvec), int(n), int(rows), int(rank),
-                int(adapters), 0};
+                int(adapters)};
   if (int e = ops_status_ptr(&g.status)) return e;
-  g.vec_out = aligned16(base) && aligned16(out) && ldb % 4 == 0 && ldo % 4 == 0;
-  const int cluster = 8;
-  const int64_t most = int64_t(num_sms()) * 4 / cluster;
-  const dim3 grid(unsigned((nvec < most ? nvec : most) * cluster));
+  const bool vec = aligned16(base) && aligned16(out) && ldb % 4 == 0 && ldo % 4 == 0 && rows % 4 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == Q1_BF16) return launch_op(k_lora_add<__nv_bfloat16>, grid, kLoraThreads, 0, cluster, s, who, g);
-  return launch_op(k_lora_add<__half>, grid, kLoraThreads, 0, cluster, s, who, g);
+  if (dtype == Q1_BF16) return vec ? launch_lora<__nv_bfloat16, true>(g, s) : launch_lora<__nv_bfloat16, false>(g, s);
+  return vec ? launch_lora<__half, true>(g, s) : launch_lora<__half, false>(g, s);
 }
