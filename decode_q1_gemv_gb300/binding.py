@@ -3,7 +3,8 @@
 Argument marshalling only: every function checks tensor dtypes, devices and
 shapes, passes raw device pointers and the current CUDA stream to the C ABI,
 and raises ``Q1Error`` with the library's message when a call fails.  All
-arithmetic runs in the library's CUDA kernels; there is no fallback.
+arithmetic runs in the library's CUDA kernels; there is no fallback.  The
+operators between the products are marshalled natively (csrc/marshal.cpp).
 
 Tensors:
   blocks  torch.uint8  [rows, n/128, 18]  Q1_0 blocks (see q1_0_pack)
@@ -18,6 +19,7 @@ paged_attention) name their tensors in their own docstrings.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import NamedTuple
@@ -83,6 +85,7 @@ class Q1Error(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
 
 
 def library_path() -> str:
@@ -91,7 +94,7 @@ def library_path() -> str:
 
 def load():
     """Load libq1gemv.so (building it first if it is missing or stale)."""
-    global _lib
+    global _lib, _marshal
     with _lock:
         if _lib is not None:
             return _lib
@@ -153,8 +156,20 @@ def load():
         lib.q1_paged_attention.restype = I
         lib.q1_0_verify.argtypes = [I, ctypes.c_char_p, ctypes.c_size_t]
         lib.q1_0_verify.restype = I
+        spec = importlib.util.spec_from_file_location("decode_q1_gemv_gb300._marshal", _build.MARSHAL)
+        marshal = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(marshal)
+        marshal.set_error(Q1Error)
+        _marshal = marshal
         _lib = lib
         return lib
+
+
+def _native():
+    """The operators' calls (csrc/marshal.cpp), loaded with the library."""
+    if _marshal is None:
+        load()
+    return _marshal
 
 
 def last_error() -> str:
@@ -477,10 +492,6 @@ def verify(quick: bool = False, corrupt: bool = False, wait_probe: bool = False)
 
 
 # ------------------------------------ operators between the products --
-DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_HALF = (torch.bfloat16, torch.float16)
-
-
 class NormOut(NamedTuple):
     """What add_rms_norm returns; None where an output was not asked for."""
     residual: torch.Tensor | None
@@ -489,47 +500,12 @@ class NormOut(NamedTuple):
     d: torch.Tensor | None
 
 
-def _refuse(t, name: str, dtypes, shape):
-    """Raises for what is wrong with t."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    raise ValueError(f"the last axis of {name} must be contiguous")
-
-
-def _cuda(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
-    """Pointer of a CUDA tensor of one of dtypes, of the given shape, whose
-    last axis is contiguous (the other strides are the call's own matter).
-    The operators' calls are short, so what is right passes in one test."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and (shape is None or t.shape == shape) and
-            (t.is_contiguous() or t.stride(-1) == 1 or t.shape[-1] == 1)):
-        return t.data_ptr()
-    return _refuse(t, name, dtypes, shape)
-
-
-def _stride(t: torch.Tensor, axis: int, least: int) -> int:
-    """Stride of an axis; an axis of one entry may have any (least is given)."""
-    s = t.stride(axis)
-    return s if s >= least or t.shape[axis] > 1 else least
-
-
-def _whole(t: torch.Tensor, name: str, shape) -> int:
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if isinstance(t, torch.Tensor) and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _refuse(t, name, (torch.int32,), shape)
-
-
-def _stream_of(t: torch.Tensor, stream) -> int:
+def _stream_of(t, stream) -> int:
     """The given stream, or the current one of t's device."""
     if stream is not None:
         return stream.cuda_stream
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return 0  # the call refuses t
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
@@ -544,36 +520,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
     or x; allocated when not given)."""
     if out not in ("q8", "y", "both"):
         raise ValueError("out must be 'q8', 'y' or 'both'")
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be [nvec, n]")
-    nvec, n = x.shape
-    t = (x.dtype,)
-    if x.dtype not in DTYPES:
-        raise TypeError(f"x has dtype {x.dtype}, expected one of {tuple(DTYPES)}")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty((nvec, n), dtype=x.dtype, device=x.device)
-    if out != "q8" and y is None:
-        y = torch.empty((nvec, n), dtype=x.dtype, device=x.device)
-    if out != "y":
-        if n % 32:
-            raise ValueError("the q8_0 form needs n to be a multiple of 32")
-        if q is None:
-            q = torch.empty((nvec, n), dtype=torch.int8, device=x.device)
-        if d is None:
-            d = torch.empty((nvec, n // 32), dtype=torch.int16, device=x.device)
-        if q.numel() != nvec * n or d.numel() != nvec * (n // 32):
-            raise ValueError("q/d sizes do not match x")
-    s = (nvec, n)
-    _check((_lib or load()).q8_add_rms_norm(
-        _cuda(x, "x", t), _stride(x, 0, n),
-        None if residual is None else _cuda(residual, "residual", t, s), 0 if residual is None else _stride(residual, 0, n),
-        _cuda(weight, "weight", (torch.float32,), (n,)), eps, nvec, n, DTYPES[x.dtype],
-        None if residual_out is None else _cuda(residual_out, "residual_out", t, s),
-        0 if residual_out is None else _stride(residual_out, 0, n),
-        None if out == "q8" else _cuda(y, "y", t, s), 0 if out == "q8" else _stride(y, 0, n),
-        None if out == "y" else _dev(q, "q", (torch.int8,)), None if out == "y" else _dev(d, "d", _SCALE_DTYPES),
-        _stream_of(x, stream)), "q8_add_rms_norm")
-    return NormOut(residual_out, None if out == "q8" else y, None if out == "y" else q, None if out == "y" else d)
+    return NormOut(*(_marshal or _native()).add_rms_norm(x, weight, eps, residual, residual_out, out != "y", out != "q8", y, q, d,
+                                                         _stream_of(x, stream)))
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor, scale: torch.Tensor | None = None,
@@ -584,47 +532,14 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Ten
     rows, rank] bf16 or f16, index int32 [nvec], scale f32 and ranks int32
     [adapters].  base f32 [nvec, rows] is the product the adapters stand
     beside; without one, out is (it is added to in place)."""
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
-        raise ValueError("x must be [nvec, n], a [adapters, rank, n], b [adapters, rows, rank]")
-    nvec, n = x.shape
-    adapters, rows, rank = b.shape
-    f32 = (torch.float32,)
-    if base is None:
-        if out is None:
-            raise ValueError("lora_add needs base, out or both")
-        base = out
-    if out is None:
-        out = torch.empty((nvec, rows), dtype=torch.float32, device=x.device)
-    pa, pb = _cuda(a, "a", _HALF, (adapters, rank, n)), _cuda(b, "b", (a.dtype,))
-    if not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b must be contiguous")
-    _check((_lib or load()).q1_lora_add(
-        _cuda(x, "x", f32), _stride(x, 0, n), nvec, n, rows, pa, pb, DTYPES[a.dtype], adapters, rank,
-        _whole(index, "index", (nvec,)), None if ranks is None else _whole(ranks, "ranks", (adapters,)),
-        None if scale is None else _cuda(scale, "scale", f32, (adapters,)), _cuda(base, "base", f32, (nvec, rows)),
-        _stride(base, 0, rows), _cuda(out, "out", f32, (nvec, rows)), _stride(out, 0, rows), _stream_of(x, stream)),
-        "q1_lora_add")
-    return out
+    return (_marshal or _native()).lora_add(x, a, b, index, scale, ranks, base, out, _stream_of(x, stream))
 
 
 def paged_kv(cache_k: torch.Tensor, cache_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
              new_start: torch.Tensor, total_new: int) -> PagedKV:
-    """The q1_paged_kv of a cache [pages, page_size, kv_heads, dim] (bf16 or
-    f16; the first three axes in any order of storage, the same for both),
-    table int32 [batch, width], kv_len int32 [batch], new_start int32 [batch + 1]."""
-    if cache_k.dim() != 4:
-        raise ValueError("cache_k must be [pages, page_size, kv_heads, dim]")
-    shape = tuple(cache_k.shape)
-    pk, pv = _cuda(cache_k, "cache_k", _HALF), _cuda(cache_v, "cache_v", (cache_k.dtype,), shape)
-    if cache_k.stride() != cache_v.stride():
-        raise ValueError("cache_k and cache_v must have the same strides")
-    if table.dim() != 2:
-        raise ValueError("table must be [batch, width]")
-    batch, width = table.shape
-    st = [_stride(cache_k, i, shape[3]) for i in range(3)]
-    return PagedKV(pk, pv, st[0], st[1], st[2], _cuda(table, "table", (torch.int32,)), width, _stride(table, 0, width),
-                   _whole(kv_len, "kv_len", (batch,)), _whole(new_start, "new_start", (batch + 1,)), shape[0], shape[1],
-                   shape[2], shape[3], batch, total_new, DTYPES[cache_k.dtype])
+    """The q1_paged_kv that rope_append and paged_attention make of these
+    tensors, for callers of the C ABI."""
+    return PagedKV.from_buffer_copy((_marshal or _native()).paged_kv(cache_k, cache_v, table, kv_len, new_start, total_new))
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, cache_k: torch.Tensor,
@@ -632,33 +547,22 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torc
                 q_out: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> torch.Tensor:
     """q1_rope_append: the new tokens' q [tokens, heads * dim] turned to their
     positions and returned as [tokens, heads, dim] in the cache's type; k
-    (turned) and v [tokens, kv_heads * dim] put into the cache (see paged_kv).
+    (turned) and v [tokens, kv_heads * dim] put into the cache.
     q, k and v are f32, their rows may be strided; cos_sin f32 [positions, rot]
-    holds rot/2 cosines, then rot/2 sines a position."""
-    total = q.shape[0]
-    kv = paged_kv(cache_k, cache_v, table, kv_len, new_start, total)
-    dim, width = kv.dim, kv.kv_heads * kv.dim
-    if q.dim() != 2 or cos_sin.dim() != 2 or q.shape[1] % dim:
-        raise ValueError("q must be [tokens, heads * dim] and cos_sin [positions, rot]")
-    heads = q.shape[1] // dim
-    f32 = (torch.float32,)
-    if q_out is None:
-        q_out = torch.empty((total, heads, dim), dtype=cache_k.dtype, device=q.device)
-    elif not q_out.is_contiguous():
-        raise ValueError("q_out must be contiguous")
-    if not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous")
-    _check((_lib or load()).q1_rope_append(
-        _cuda(q, "q", f32), _stride(q, 0, heads * dim), _cuda(k, "k", f32, (total, width)), _stride(k, 0, width),
-        _cuda(v, "v", f32, (total, width)), _stride(v, 0, width), _cuda(cos_sin, "cos_sin", f32), cos_sin.shape[0],
-        cos_sin.shape[1], 1 if interleaved else 0, heads, _cuda(q_out, "q_out", (cache_k.dtype,), (total, heads, dim)),
-        ctypes.byref(kv), _stream_of(q, stream)), "q1_rope_append")
-    return q_out
+    holds rot/2 cosines, then rot/2 sines a position.
+
+    The cache: cache_k and cache_v [pages, page_size, kv_heads, dim] (bf16 or
+    f16; the first three axes in any order of storage, the same for both),
+    table int32 [batch, width] of page numbers, kv_len int32 [batch] the cached
+    tokens of each sequence, the new ones among them, new_start int32 [batch +
+    1] where each sequence's new tokens begin in q, k and v."""
+    return (_marshal or _native()).rope_append(q, k, v, cos_sin, cache_k, cache_v, table, kv_len, new_start, q_out,
+                                               bool(interleaved), _stream_of(q, stream))
 
 
 def paged_attention_workspace(max_new: int, heads: int, kv_heads: int, dim: int) -> int:
     """Bytes of paged_attention's workspace on the current device."""
-    v = (_lib or load()).q1_paged_attention_workspace(int(max_new), int(heads), int(kv_heads), int(dim))
+    v = load().q1_paged_attention_workspace(int(max_new), int(heads), int(kv_heads), int(dim))
     if v < 0:
         raise Q1Error(int(v), last_error())
     return int(v)
@@ -669,30 +573,16 @@ def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tenso
                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q1_paged_attention: the new tokens' q [tokens, heads, dim] (the cache's
     type; tokens and heads may be strided) attend to their sequence's cache,
-    causally (see paged_kv; the new keys and values are in the cache already).
+    causally (the cache as in rope_append; the new keys and values are in it).
     max_new is the most new tokens of any sequence; scale defaults to
     dim ** -0.5.  A given workspace (uint8) must hold
     paged_attention_workspace(...) bytes."""
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, dim]")
-    total, heads, dim = q.shape
-    kv = paged_kv(cache_k, cache_v, table, kv_len, new_start, total)
-    t = (cache_k.dtype,)
-    if kv.dim != dim:
-        raise ValueError(f"q has dim {dim}, the cache {kv.dim}")
-    if out is None:
-        out = torch.empty((total, heads, dim), dtype=q.dtype, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(paged_attention_workspace(max_new, heads, kv.kv_heads, dim), dtype=torch.uint8,
+    if stream is not None and workspace is None and isinstance(q, torch.Tensor) and q.dim() == 3:
+        workspace = torch.empty(paged_attention_workspace(max_new, q.shape[1], cache_k.shape[2], q.shape[2]), dtype=torch.uint8,
                                 device=q.device)
-        if stream is not None:  # it goes back to the allocator on return, while `stream` may still use it
-            workspace.record_stream(stream)
-    _check((_lib or load()).q1_paged_attention(
-        _cuda(q, "q", t), _stride(q, 0, heads * dim), _stride(q, 1, dim), heads, dim ** -0.5 if scale is None else scale,
-        ctypes.byref(kv), max_new, _cuda(out, "out", t, (total, heads, dim)), _stride(out, 0, heads * dim),
-        _stride(out, 1, dim), _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream_of(q, stream)),
-        "q1_paged_attention")
-    return out
+        workspace.record_stream(stream)  # it goes back to the allocator on return, while `stream` may still use it
+    return (_marshal or _native()).paged_attention(q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace,
+                                                   _stream_of(q, stream))
 
 
 class Q1Linear:
