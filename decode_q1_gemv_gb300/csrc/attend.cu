@@ -13,6 +13,7 @@
 // an item ends.  p is rounded to the cache's type for its product with v (off
 // by 2^-8 or 2^-11 of a term at most, as the output's own rounding is); the sum of p
 // is taken in f32 before that.
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   const int page_mask = (1 << a.kv.page_shift) - 1;
   for (int64_t u = u0; u < u1;) {
     const int take = int(min(int64_t(cur.units - cur.unit), u1 - u));  // units of this item here
-    const int keys = Tile::keys(cur.s, a.group, cur.m);
+    const int keys = Tile::keys(a, cur.s, cur.m);
     const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
     const T* kbase = static_cast<const T*>(a.kv.k) + cur.h * a.kv.head_stride;
     const T* vbase = static_cast<const T*>(a.kv.v) + cur.h * a.kv.head_stride;
@@ -276,6 +277,8 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
 
 // Which kernel: the tensor-core one from more rows a key head on than one tile
 // of this file's has.
+// (Sequences of few rows among others with many are this kernel's too, in a launch of
+// their own: a tile of 128 rows costs the same however few are in use.)
 static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kRowsS; }
 
 static int attend_ctas() { return 2 * num_sms(); }
@@ -341,11 +344,20 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = kv->dtype == Q1_BF16;
-  if (many_rows(max_new, a.group)) {
-    bool ran = false;
-    if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
-    if (ran) return Q1_OK;
+  a.least_rows = 0, a.most_rows = INT_MAX;
+  const auto few = [&] {
+    if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, workspace, s) : launch_attend<__half, 128>(a, workspace, s);
+    return bf ? launch_attend<__nv_bfloat16, 64>(a, workspace, s) : launch_attend<__half, 64>(a, workspace, s);
+  };
+  if (!many_rows(max_new, a.group)) return few();
+  const bool both = kv->batch > 1;
+  if (both) a.least_rows = kRowsS + 1;
+  bool ran = false;
+  if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
+  if (!ran) a.least_rows = 0;
+  if (!ran || both) {
+    if (ran) a.least_rows = 0, a.most_rows = kRowsS;
+    return few();
   }
-  if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, workspace, s) : launch_attend<__half, 128>(a, workspace, s);
-  return bf ? launch_attend<__nv_bfloat16, 64>(a, workspace, s) : launch_attend<__half, 64>(a, workspace, s);
+  return Q1_OK;
 }

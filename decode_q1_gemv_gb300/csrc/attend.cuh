@@ -17,6 +17,7 @@ struct AttendArgs {
   int heads, group;        // query heads, and of one key head
   float scale_log2;        // scale * log2(e)
   int ctas;                // CTAs the units are split over
+  int least_rows, most_rows;  // of a sequence that this launch takes (its new tokens times the group)
 };
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 at -inf
@@ -33,16 +34,19 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 at -inf
 // are.  An item that no CTA has to itself is joined by k_attend_join.
 template <int TM, int TK>
 struct Tiling {
-  __device__ static int tiles(const SeqSpan& s, int group) { return (s.count * group + TM - 1) / TM; }
+  __device__ static int tiles(const AttendArgs& a, const SeqSpan& s) {
+    const int rows = s.count * a.group;
+    return rows >= a.least_rows && rows <= a.most_rows ? (rows + TM - 1) / TM : 0;
+  }
   // Keys that tile m of s may see: those of its last row.
-  __device__ static int keys(const SeqSpan& s, int group, int m) {
-    const int last = min(s.count - 1, (m * TM + TM - 1) / group);
+  __device__ static int keys(const AttendArgs& a, const SeqSpan& s, int m) {
+    const int last = min(s.count - 1, (m * TM + TM - 1) / a.group);
     return max(0, s.len - s.count + last + 1);
   }
-  __device__ static int units(const SeqSpan& s, int group, int m) { return max(1, (keys(s, group, m) + TK - 1) / TK); }
-  __device__ static int64_t seq_units(const SeqSpan& s, int group) {  // of one key head
+  __device__ static int units(const AttendArgs& a, const SeqSpan& s, int m) { return max(1, (keys(a, s, m) + TK - 1) / TK); }
+  __device__ static int64_t seq_units(const AttendArgs& a, const SeqSpan& s) {  // of one key head
     int64_t u = 0;
-    for (int m = 0, n = tiles(s, group); m < n; ++m) u += units(s, group, m);
+    for (int m = 0, n = tiles(a, s); m < n; ++m) u += units(a, s, m);
     return u;
   }
 };
@@ -66,7 +70,7 @@ __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, in
   const int b0 = min(a.kv.batch, int(threadIdx.x) * per), b1 = min(a.kv.batch, b0 + per);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
-    mine += Tile::seq_units(seq_span(a.kv, b), a.group) * a.kv.kv_heads;
+    mine += Tile::seq_units(a, seq_span(a.kv, b)) * a.kv.kv_heads;
     if (a.kv.kv_len[b] < 0 || a.kv.kv_len[b] > a.kv.table_tokens || a.kv.new_start[b] < 0 ||
         a.kv.new_start[b + 1] < a.kv.new_start[b] || a.kv.new_start[b + 1] > a.kv.total_new)
       atomicOr(a.status, kStatusBadIndex);
@@ -95,7 +99,7 @@ __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, in
     SeqSpan s;
     for (;; ++b) {
       s = seq_span(a.kv, b);
-      su = Tile::seq_units(s, a.group);
+      su = Tile::seq_units(a, s);
       if (u0 < at + su * a.kv.kv_heads || b + 1 >= b1) break;
       at += su * a.kv.kv_heads;
     }
@@ -103,7 +107,7 @@ __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, in
     int64_t left = (u0 - at) - h * su;
     int m = 0, un;
     for (;; ++m) {
-      un = Tile::units(s, a.group, m);
+      un = Tile::units(a, s, m);
       if (left < un || left < 0) break;
       left -= un;
     }
@@ -123,15 +127,15 @@ __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, in
 template <class Tile>
 __device__ __forceinline__ void next_item(const AttendArgs& a, Cursor& cur) {
   cur.unit = 0;
-  if (++cur.m >= Tile::tiles(cur.s, a.group)) {
+  if (++cur.m >= Tile::tiles(a, cur.s)) {
     cur.m = 0;
     if (++cur.h >= a.kv.kv_heads) {
       cur.h = 0;
       do cur.s = seq_span(a.kv, ++cur.b);
-      while (cur.s.count == 0 && cur.b + 1 < a.kv.batch);
+      while (Tile::tiles(a, cur.s) == 0 && cur.b + 1 < a.kv.batch);
     }
   }
-  cur.units = Tile::units(cur.s, a.group, cur.m);
+  cur.units = Tile::units(a, cur.s, cur.m);
 }
 
 // Row r of a tile: its token and query head; false past the last row.

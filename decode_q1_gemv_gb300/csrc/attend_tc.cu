@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   };
   // Units of the current item that this CTA takes, and whether it has two tiles.
   const auto part_of = [&](int64_t u) { return int(min(int64_t(cur.units - cur.unit), u1 - u)); };
-  const auto tiles_of = [&]() { return cur.s.count * a.group - cur.m * kTcItem > kTcM ? 2 : 1; };
+  const auto tiles_of = [&](const Cursor& it) { return it.s.count * a.group - it.m * kTcItem > kTcM ? 2 : 1; };
 
   if (warp >= kTcSoftWarps) {
     regs_down<kTcRegsLess>();
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       const int boxes_max = kTcKeys / g.box_keys, page_mask = (1 << a.kv.page_shift) - 1;
       bool ok = true;
       for (int64_t u = u0; u < u1 && ok;) {
-        const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
+        const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m);
         const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
         // The page of this lane's box, one unit ahead.
         const auto page_at = [&](int unit) {
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       const int w = (warp - kTcSoftWarps) >> 1;  // tile
       RingPos pos;                    // of the next K or V tile
       uint32_t qpar = 0, ppar = 0, turnpar = 0;
-      bool ok = true;
+      bool ok = true, handed = false;
       const uint32_t ts = tmem + w * 128, to = tmem + 256 + w * D;
       const uint64_t qdesc = desc_k_sw128(s0 + w * Shape::kTileBytes);
       const auto tile_addr = [&](int stage) { return s0 + Shape::kOffKV + stage * Shape::kTileBytes; };
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         mma_commit_elect(empty(stage));
       };
       for (int64_t u = u0; u < u1 && ok;) {
-        const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m), nw = tiles_of();
+        const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m), nw = tiles_of(cur);
         if (keys && w >= nw) {
           // No rows for this tile: its share of releasing the stages.
           for (int t = 0; t < 2 * take && ok; ++t) {
@@ -320,15 +320,18 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             pos.next<kStages>();
           }
         } else if (keys) {
-          // This warp's turn: after the other tile's batch, if there is one.
-          const auto my_turn = [&](bool first) {
-            if (nw == 1 || (first && w == 0)) return true;
+          // This warp's turn: after the other tile's batch before, if there was one
+          // (of this item or of the last one with two tiles: neither warp may be
+          // two batches ahead, its barrier would pass two phases).
+          const auto my_turn = [&]() {
+            if (nw == 1 || (w == 0 && !handed)) return true;
             const bool done = wait(turn + 8 * w, turnpar);
             turnpar ^= 1;
             return done;
           };
-          ok = wait(qfull + 8 * w, qpar) && wait(full(pos.stage), pos.parity) && my_turn(true);
+          ok = wait(qfull + 8 * w, qpar) && wait(full(pos.stage), pos.parity) && my_turn();
           qpar ^= 1;
+          handed |= nw == 2;
           if (ok) {
             tc_fence_after();
             scores(pos.stage, nw == 2);
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             const bool more = t + 1 < take;
             const uint64_t vdesc = desc_mn_sw128(tile_addr(vstage), Shape::kHalfBytes);
             if (more) ok = wait(full(pos.stage), pos.parity);
-            ok = ok && wait(pfull + 8 * w, ppar) && my_turn(false);
+            ok = ok && wait(pfull + 8 * w, ppar) && my_turn();
             ppar ^= 1;
             if (!ok) break;
             tc_fence_after();
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               pos.next<kStages>();
             } else {
               mma_commit_elect(ofull + 8 * w);
-              hand_on(nw == 2 && w == 0);
+              hand_on(nw == 2);
             }
           }
         }
@@ -399,9 +402,41 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     };
     bool ok = true;
     const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+    // Q of an item, if this tile has rows of it that see keys: this warp's 16
+    // rows, 16 (8) lanes a row; rows past the last are zero.
+    const auto load_q = [&](const Cursor& it) {
+      if (w >= tiles_of(it) || Tile::keys(a, it.s, it.m) == 0) return;
+      constexpr int kLanes = D / 8, kOnce = 32 / kLanes;
+      const int piece = lane % kLanes;
+      unsigned char* q = smem + w * Shape::kTileBytes + (piece / 8) * Shape::kHalfBytes;
+#pragma unroll
+      for (int r0 = 0; r0 < 16; r0 += kOnce) {
+        const int r = (warp & 7) * 16 + r0 + lane / kLanes;
+        int qt, qh;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row_of(it, a.group, it.m * kTcItem + w * kTcM + r, qt, qh))
+          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
+        v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
+        *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(qfull + 8 * w);
+    };
+    if (u0 < u1) load_q(cur);
     for (int64_t u = u0; u < u1 && ok;) {
-      const int take = part_of(u), keys = Tile::keys(cur.s, a.group, cur.m);
-      if (w < tiles_of()) {
+      const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m);
+      Cursor next = cur;
+      bool have_next = false;
+      // The next item and its Q: its last reader here, the scores of this
+      // item's last unit, is done, so they are under way during the output.
+      const auto advance = [&]() {
+        have_next = u + take < u1;
+        if (have_next) {
+          next_item<Tile>(a, next);
+          load_q(next);
+        }
+      };
+      if (w < tiles_of(cur)) {
         const int row0 = cur.m * kTcItem + w * kTcM;
         int token, head;
         const bool live = row_of(cur, a.group, row0 + row, token, head);
@@ -409,24 +444,6 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         int seen = (live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0) - cur.unit * kTcKeys - half * 64;
         float used = -INFINITY, sum = 0.f;  // the maximum that weights are relative to
         if (keys) {
-          // Q: this warp's 16 rows, 16 (8) lanes a row; rows past the last are zero.
-          {
-            constexpr int kLanes = D / 8, kOnce = 32 / kLanes;
-            const int piece = lane % kLanes;
-            unsigned char* q = smem + w * Shape::kTileBytes + (piece / 8) * Shape::kHalfBytes;
-#pragma unroll 4
-            for (int r0 = 0; r0 < 16; r0 += kOnce) {
-              const int r = (warp & 7) * 16 + r0 + lane / kLanes;
-              int qt, qh;
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (row_of(cur, a.group, row0 + r, qt, qh))
-                v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
-              v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
-              *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(qfull + 8 * w);
-          }
           uint64_t sum2 = 0, base2 = 0;  // two partial sums; minus the maximum in use, twice
           for (int t = 0; t < take; ++t) {
             ok = wait(sfull + 8 * w, spar);
@@ -510,6 +527,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             seen -= kTcKeys;
           }
           if (!ok) break;
+          advance();
           float sa, sb, other;
           split2(sum2, sa, sb);
           sa += sb;
@@ -519,6 +537,8 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           if (!ok) break;
           sum = sa + other;
           tc_fence_after();
+        } else {
+          advance();
         }
         const bool whole = cur.unit == 0 && take == cur.units;
         const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
@@ -554,9 +574,11 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           part[(D + 1) * kTcItem] = sum;
         }
         tc_fence_before();  // the next item's first product overwrites O after this thread's next arrival
+      } else {
+        advance();
       }
       u += take;
-      if (u < u1) next_item<Tile>(a, cur);
+      cur = next;
     }
   }
   tc_fence_before();

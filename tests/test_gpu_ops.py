@@ -266,6 +266,7 @@ def check_attend(c, heads, dtype, dim, max_new=None, scale=None, seed=70):
     got = binding.paged_attention(q, *c.args(), max_new=max_new or max(c.new), scale=scale)
     want = attend_reference(c, q, dim ** -0.5 if scale is None else scale)
     within(got, want[0], attend_tol(c, q, *want))
+    assert binding.device_status() == 0  # no wait ran into its limit
     return q, got
 
 
@@ -294,6 +295,16 @@ def test_attend_ragged_batch(page, dim, dtype):
 @pytest.mark.parametrize("new,length", [(15, 200), (64, 64), (65, 700), (127, 129), (128, 128), (129, 1025), (257, 300)])
 def test_attend_chunk(new, length, heads, kv_heads, dim, dtype):
     check_attend(Cache([(new, length)], heads, kv_heads, dim, 32, dtype), heads, dtype, dim)
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 16, 16), (128, 16, 4)])
+def test_attend_many_items_a_cta(dim, heads, kv_heads):
+    """More items than CTAs, of one and two tiles and of few rows in turn: the kernels' barriers pass
+    from item to item.  No wait may have run into its limit."""
+    rng = np.random.default_rng(5)
+    seqs = [(int(n), int(n + rng.integers(0, 300))) for n in np.exp(rng.uniform(0, np.log(300), 40))]
+    check_attend(Cache(seqs, heads, kv_heads, dim, 32, torch.float16), heads, torch.float16, dim)
+    assert binding.device_status() == 0
 
 
 @pytest.mark.parametrize("new,length", [(1, 0), (4, 2), (40, 10), (300, 1), (130, 129)])
