@@ -24,6 +24,7 @@ namespace q1 {
 constexpr int kRowsS = 16;   // rows of a tile
 constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
 constexpr int kWarpsS = 4;
+constexpr int kWholeS = 4;       // units of an item that is not split
 constexpr int kJoinSlices = 4;   // CTAs that join an item
 constexpr int kStagesS = 3;  // 2 x 96 KB of reads in flight an SM at D = 128
 
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   constexpr int kRowBytes = D * 2, kChunkBytes = 16 * kRowBytes, kPieces = kRowBytes / 16;  // 16-byte pieces of a row
   constexpr int kSteps = D / 16;       // k16 steps of q.k, and pairs of n8 tiles of p v
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ int64_t scratch[34];
+  __shared__ LocateScratch scratch;
   __shared__ float ml[kWarpsS][16][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
-  const int64_t total = locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  const int64_t total = locate<Tile, kWholeS>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
   if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
   const uint32_t ring = smem_addr(smem) + warp * (kStagesS * 2 * kChunkBytes);
   const int page_mask = (1 << a.kv.page_shift) - 1;
@@ -94,14 +95,18 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     const T* vbase = static_cast<const T*>(a.kv.v) + cur.h * a.kv.head_stride;
 
     // Chunk i of this warp: keys j0 + 64 i .. +15.  Lane l < 16 finds row l's
-    // place; the copies then run over rows in pairs (or fours, D = 64).
+    // place (its page well before it is needed); the copies then run over
+    // rows in pairs (or fours, D = 64).
     const int j0 = cur.unit * kKeysS + warp * 16;
-    const auto fill = [&](int i) {
+    const auto page_of = [&](int i) {  // of this lane's row; -1 past the keys
+      const int j = j0 + i * kKeysS + (lane & 15);
+      return i < take && j < keys ? table[j >> a.kv.page_shift] : -1;
+    };
+    const auto fill = [&](int i, int page) {
       if (i < take) {
         const int j = j0 + i * kKeysS + (lane & 15);
         int64_t off = -1;
         if (j < keys) {
-          const int page = table[j >> a.kv.page_shift];
           if (page >= 0 && page < a.kv.pages)
             off = int64_t(page) * a.kv.page_stride + int64_t(j & page_mask) * a.kv.slot_stride;
           else
@@ -121,8 +126,14 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
       }
       cp_commit();
     };
+    int page[kStagesS];  // of the chunks that are filled next
 #pragma unroll
-    for (int i = 0; i < kStagesS - 1; ++i) fill(i);
+    for (int i = 0; i < kStagesS; ++i) page[i] = page_of(i);
+#pragma unroll
+    for (int i = 0; i < kStagesS; ++i) {
+      fill(i, page[i]);
+      page[i] = page_of(i + kStagesS);
+    }
 
     // Q of the tile as A fragments: rows lane/4 and lane/4 + 8.
     uint32_t qa[kSteps][4];
@@ -147,9 +158,8 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
     for (int i = 0; i < take; ++i) {
-      cp_wait<kStagesS - 2>();
+      cp_wait<kStagesS - 1>();
       __syncwarp();
-      fill(i + kStagesS - 1);
       const uint32_t kt = ring + (i % kStagesS) * 2 * kChunkBytes, vt = kt + kChunkBytes;
       float s[2][4] = {};
       {
@@ -211,6 +221,10 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         mma16816<T>(o[2 * n + 1], p, b[2], b[3]);
       }
       __syncwarp();
+      fill(i + kStagesS, page[0]);
+#pragma unroll
+      for (int k = 0; k < kStagesS - 1; ++k) page[k] = page[k + 1];
+      page[kStagesS - 1] = page_of(i + 2 * kStagesS);
     }
     cp_wait<0>();
 

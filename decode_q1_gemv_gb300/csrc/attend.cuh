@@ -58,22 +58,40 @@ struct Cursor {
   SeqSpan s;
 };
 
+// total * c / n, in 32 bits where that suffices (the usual case; a 64-bit
+// division takes some hundred instructions).
+__device__ __forceinline__ int64_t share(int64_t total, int c, int n) {
+  if (total < (int64_t(1) << 31) / n) return uint32_t(total) * uint32_t(c) / uint32_t(n);
+  return total * c / n;
+}
+
+struct LocateScratch {
+  int64_t sums[32];
+  int64_t cut[2];
+  Cursor at;
+};
+
 // Total units of the call, the number n of CTAs that have a share (n as given
 // or the units, if fewer), CTA c's share [u0, u1) and the cursor at its start.
-// Every thread of the CTA calls; `scratch` is 34 int64 in shared memory.
-template <class Tile>
-__device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, int64_t* scratch, Cursor& cur, int64_t& u0,
+// A cut within an item of at most kWhole units moves to the item's start:
+// splitting it would cost more than the balance gains.  Every thread of the
+// CTA calls.
+template <class Tile, int kWhole>
+__device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, LocateScratch& sh, Cursor& cur, int64_t& u0,
                                           int64_t& u1) {
   const int threads = blockDim.x, warps = threads / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Each thread takes a run of consecutive sequences.
   const int per = (a.kv.batch + threads - 1) / threads;
   const int b0 = min(a.kv.batch, int(threadIdx.x) * per), b1 = min(a.kv.batch, b0 + per);
-  int64_t mine = 0;
+  SeqSpan first = {0, 0, 0};
+  int64_t mine = 0, first_units = 0;
   for (int b = b0; b < b1; ++b) {
-    mine += Tile::seq_units(a, seq_span(a.kv, b)) * a.kv.kv_heads;
-    if (a.kv.kv_len[b] < 0 || a.kv.kv_len[b] > a.kv.table_tokens || a.kv.new_start[b] < 0 ||
-        a.kv.new_start[b + 1] < a.kv.new_start[b] || a.kv.new_start[b + 1] > a.kv.total_new)
-      atomicOr(a.status, kStatusBadIndex);
+    bool bad;
+    const SeqSpan s = seq_span(a.kv, b, &bad);
+    const int64_t su = Tile::seq_units(a, s);
+    if (b == b0) first = s, first_units = su;
+    mine += su * a.kv.kv_heads;
+    if (bad) atomicOr(a.status, kStatusBadIndex);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -81,45 +99,46 @@ __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, in
     const int64_t t = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += t;
   }
-  if (lane == 31) scratch[warp] = incl;
+  if (lane == 31) sh.sums[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+    if (w < warp) before += sh.sums[w];
+    total += sh.sums[w];
   }
   if (n > total) n = int(total);  // so that no share between two others is empty
-  u0 = c < n ? total * c / n : total;
-  u1 = c < n ? total * (c + 1) / n : total;
   const int64_t lo = before + incl - mine;
-  __syncthreads();
-  if (u0 >= lo && u0 < lo + mine) {  // the run that holds u0: one thread's
-    int64_t at = lo, su;
-    int b = b0;
-    SeqSpan s;
-    for (;; ++b) {
-      s = seq_span(a.kv, b);
-      su = Tile::seq_units(a, s);
-      if (u0 < at + su * a.kv.kv_heads || b + 1 >= b1) break;
-      at += su * a.kv.kv_heads;
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {  // where the share begins, and where it ends
+    const int64_t u = c + end < n ? share(total, c + end, n) : total;
+    if (u == total) {
+      if (threadIdx.x == 0) sh.cut[end] = total;
+    } else if (u >= lo && u < lo + mine) {  // the run that holds u: one thread's
+      int64_t at = lo, su = first_units;
+      SeqSpan s = first;
+      int b = b0;
+      while (u >= at + su * a.kv.kv_heads && b + 1 < b1) {
+        at += su * a.kv.kv_heads;
+        s = seq_span(a.kv, ++b);
+        su = Tile::seq_units(a, s);
+      }
+      const int h = u - at < (int64_t(1) << 31) && su < (int64_t(1) << 31) ? int(uint32_t(u - at) / uint32_t(su)) : int((u - at) / su);
+      int64_t left = (u - at) - h * su;
+      int m = 0, un;
+      for (;; ++m) {
+        un = Tile::units(a, s, m);
+        if (left < un || left < 0) break;
+        left -= un;
+      }
+      if (un <= kWhole) left = 0;
+      sh.cut[end] = at + h * su + left;
+      for (int i = 0; i < m; ++i) sh.cut[end] += Tile::units(a, s, i);
+      if (end == 0) sh.at = {b, h, m, int(left), un, s};
     }
-    const int h = int((u0 - at) / su);
-    int64_t left = (u0 - at) - h * su;
-    int m = 0, un;
-    for (;; ++m) {
-      un = Tile::units(a, s, m);
-      if (left < un || left < 0) break;
-      left -= un;
-    }
-    scratch[0] = b, scratch[1] = h, scratch[2] = m, scratch[3] = left, scratch[4] = un;
   }
   __syncthreads();
-  if (u0 < u1) {
-    cur.b = int(scratch[0]), cur.h = int(scratch[1]), cur.m = int(scratch[2]);
-    cur.unit = int(scratch[3]), cur.units = int(scratch[4]);
-    cur.s = seq_span(a.kv, cur.b);
-  }
-  __syncthreads();
+  u0 = sh.cut[0], u1 = sh.cut[1];
+  cur = sh.at;
   return total;
 }
 
@@ -158,10 +177,12 @@ struct JoinItem {
 // Left by one thread of every CTA: first with no item, then for the one item
 // that it begins and does not end (its units begin at u, cut at u1).
 __device__ __forceinline__ void leave_join(const AttendArgs& a, const Cursor& cur, int64_t u, int64_t total, int ctas) {
+  // The first cut at or past the item's end: the least k with total * k / ctas >= end.
   const int64_t end = u + cur.units;
-  int parts = 1;
-  while (total * (int(blockIdx.x) + parts) / ctas < end) ++parts;
-  a.joins[blockIdx.x] = {parts, cur.s.first, cur.s.count, cur.h, cur.m, {0, 0, 0}};
+  const bool small = total < (int64_t(1) << 31) / ctas;
+  const int k = small ? int((uint32_t(end) * uint32_t(ctas) + uint32_t(total) - 1) / uint32_t(total))
+                      : int((end * ctas + total - 1) / total);
+  a.joins[blockIdx.x] = {k - int(blockIdx.x), cur.s.first, cur.s.count, cur.h, cur.m, {0, 0, 0}};
 }
 
 // A partial result of TM rows: dim sums of p v relative to the row's maximum,

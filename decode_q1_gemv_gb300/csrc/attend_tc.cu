@@ -64,6 +64,7 @@ template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+constexpr int kTcWhole = 4;           // units of an item that is not split
 constexpr int kTcJoinSlices = 16;    // CTAs that join an item
 constexpr float kTcGrow = 8.f;       // log2 units a maximum may be behind
 
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   constexpr int kStages = Shape::kStages;
   const AttendArgs& a = g.a;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ int64_t scratch[34];
+  __shared__ LocateScratch scratch;
   __shared__ float exchange[2][2][2][kTcM];  // [unit parity][tile][half][row]
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile uint32_t abort_s;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
-  const int64_t total = locate<Tile>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+  const int64_t total = locate<Tile, kTcWhole>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
   if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
 
   // Whole warps wait, and agree on whether they may go on.  (Written out here:

@@ -23,14 +23,17 @@ struct Paged {
 int check_paged(const char* who, const q1_paged_kv* kv, Paged& p);
 
 // New tokens [first, first + count) of sequence b and its cached length, held
-// within what the call was given.
+// within what the call was given; `bad`: whether that changed them.
 struct SeqSpan {
   int first, count, len;
 };
-__device__ __forceinline__ SeqSpan seq_span(const Paged& p, int b) {
-  const int lo = max(0, min(p.new_start[b], p.total_new));
-  const int hi = max(lo, min(p.new_start[b + 1], p.total_new));
-  return {lo, hi - lo, max(0, min(p.kv_len[b], p.table_tokens))};
+__device__ __forceinline__ SeqSpan seq_span(const Paged& p, int b, bool* bad = nullptr) {
+  const int begin = p.new_start[b], end = p.new_start[b + 1], length = p.kv_len[b];
+  const int lo = max(0, min(begin, p.total_new));
+  const int hi = max(lo, min(end, p.total_new));
+  const int len = max(0, min(length, p.table_tokens));
+  if (bad) *bad = lo != begin || hi != end || len != length;
+  return {lo, hi - lo, len};
 }
 
 }  // namespace q1
