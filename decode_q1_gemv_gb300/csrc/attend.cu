@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     for (int half = 0; half < 2; ++half) {
       int token, head;
       const int r = cur.m * kRowsS + lane / 4 + half * 8;
-      const bool live = row_of(cur, a.group, r, token, head);
+      const bool live = row_of(a, cur, r, token, head);
       limit[half] = live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0;
       const T* row = static_cast<const T*>(a.q) + (live ? token * a.q_token + head * a.q_head : 0) + (lane & 3) * 2;
 #pragma unroll
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     for (int i = threadIdx.x; i < 16 * (D / 4); i += kWarpsS * 32) {
       const int r = i / (D / 4), col = i % (D / 4) * 4;
       int token, head;
-      if (!row_of(cur, a.group, cur.m * kRowsS + r, token, head)) continue;
+      if (!row_of(a, cur, cur.m * kRowsS + r, token, head)) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -355,6 +355,7 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   a.o_token = out_token_stride, a.o_head = out_head_stride;
   if (int e = ops_status_ptr(&a.status)) return e;
   a.heads = int(heads), a.group = int(heads / kv->kv_heads);
+  a.group_inverse = uint32_t((uint64_t(1) << 32) / uint64_t(a.group) + 1);
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = kv->dtype == Q1_BF16;

@@ -15,10 +15,19 @@ struct AttendArgs {
   struct JoinItem* joins;  // [CTAs]
   unsigned* status;
   int heads, group;        // query heads, and of one key head
+  uint32_t group_inverse;  // 2^32 / group + 1 (group > 1), see by_group
   float scale_log2;        // scale * log2(e)
   int ctas;                // CTAs the units are split over
   int least_rows, most_rows;  // of a sequence that this launch takes (its new tokens times the group)
 };
+
+// n / group, 0 <= n < 2^31: n * (2^32 / group + 1) / 2^32 is the quotient or
+// one more.  (A hardware division by a run-time value takes some forty instructions.)
+__device__ __forceinline__ int by_group(const AttendArgs& a, int n) {
+  if (a.group == 1) return n;  // (2^32 itself would not fit)
+  const int q = int(__umulhi(uint32_t(n), a.group_inverse));
+  return q - (q * a.group > n);
+}
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 at -inf
   float y;
@@ -40,7 +49,7 @@ struct Tiling {
   }
   // Keys that tile m of s may see: those of its last row.
   __device__ static int keys(const AttendArgs& a, const SeqSpan& s, int m) {
-    const int last = min(s.count - 1, (m * TM + TM - 1) / a.group);
+    const int last = min(s.count - 1, by_group(a, m * TM + TM - 1));
     return max(0, s.len - s.count + last + 1);
   }
   __device__ static int units(const AttendArgs& a, const SeqSpan& s, int m) { return max(1, (keys(a, s, m) + TK - 1) / TK); }
@@ -66,8 +75,7 @@ __device__ __forceinline__ int64_t share(int64_t total, int c, int n) {
 }
 
 struct LocateScratch {
-  int64_t sums[32];
-  int64_t cut[2];
+  int64_t total, cut[2];
   Cursor at;
 };
 
@@ -75,71 +83,66 @@ struct LocateScratch {
 // or the units, if fewer), CTA c's share [u0, u1) and the cursor at its start.
 // A cut within an item of at most kWhole units moves to the item's start:
 // splitting it would cost more than the balance gains.  Every thread of the
-// CTA calls.
+// CTA calls; the first warp looks, a run of consecutive sequences a lane.
 template <class Tile, int kWhole>
 __device__ __forceinline__ int64_t locate(const AttendArgs& a, int c, int& n, LocateScratch& sh, Cursor& cur, int64_t& u0,
                                           int64_t& u1) {
-  const int threads = blockDim.x, warps = threads / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Each thread takes a run of consecutive sequences.
-  const int per = (a.kv.batch + threads - 1) / threads;
-  const int b0 = min(a.kv.batch, int(threadIdx.x) * per), b1 = min(a.kv.batch, b0 + per);
-  SeqSpan first = {0, 0, 0};
-  int64_t mine = 0, first_units = 0;
-  for (int b = b0; b < b1; ++b) {
-    bool bad;
-    const SeqSpan s = seq_span(a.kv, b, &bad);
-    const int64_t su = Tile::seq_units(a, s);
-    if (b == b0) first = s, first_units = su;
-    mine += su * a.kv.kv_heads;
-    if (bad) atomicOr(a.status, kStatusBadIndex);
-  }
-  int64_t incl = mine;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (a.kv.batch + 31) / 32;
+    const int b0 = min(a.kv.batch, lane * per), b1 = min(a.kv.batch, b0 + per);
+    SeqSpan first = {0, 0, 0};
+    int64_t mine = 0, first_units = 0;
+    for (int b = b0; b < b1; ++b) {
+      bool bad;
+      const SeqSpan s = seq_span(a.kv, b, &bad);
+      const int64_t su = Tile::seq_units(a, s);
+      if (b == b0) first = s, first_units = su;
+      mine += su * a.kv.kv_heads;
+      if (bad) atomicOr(a.status, kStatusBadIndex);
+    }
+    int64_t incl = mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += t;
-  }
-  if (lane == 31) sh.sums[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += sh.sums[w];
-    total += sh.sums[w];
-  }
-  if (n > total) n = int(total);  // so that no share between two others is empty
-  const int64_t lo = before + incl - mine;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += t;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31), lo = incl - mine;
+    const int ctas = n < total ? n : int(total);  // so that no share between two others is empty
+    if (lane == 0) sh.total = total;
 #pragma unroll 1
-  for (int end = 0; end < 2; ++end) {  // where the share begins, and where it ends
-    const int64_t u = c + end < n ? share(total, c + end, n) : total;
-    if (u == total) {
-      if (threadIdx.x == 0) sh.cut[end] = total;
-    } else if (u >= lo && u < lo + mine) {  // the run that holds u: one thread's
-      int64_t at = lo, su = first_units;
-      SeqSpan s = first;
-      int b = b0;
-      while (u >= at + su * a.kv.kv_heads && b + 1 < b1) {
-        at += su * a.kv.kv_heads;
-        s = seq_span(a.kv, ++b);
-        su = Tile::seq_units(a, s);
+    for (int end = 0; end < 2; ++end) {  // where the share begins, and where it ends
+      const int64_t u = c + end < ctas ? share(total, c + end, ctas) : total;
+      if (u == total) {
+        if (lane == 0) sh.cut[end] = total;
+      } else if (u >= lo && u < lo + mine) {  // the run that holds u: one lane's
+        int64_t at = lo, su = first_units;
+        SeqSpan s = first;
+        int b = b0;
+        while (u >= at + su * a.kv.kv_heads && b + 1 < b1) {
+          at += su * a.kv.kv_heads;
+          s = seq_span(a.kv, ++b);
+          su = Tile::seq_units(a, s);
+        }
+        const bool small = u - at < (int64_t(1) << 31) && su < (int64_t(1) << 31);
+        const int h = small ? int(uint32_t(u - at) / uint32_t(su)) : int((u - at) / su);
+        int64_t start = at + h * su;  // of the item
+        int m = 0, un;
+        for (;; ++m) {
+          un = Tile::units(a, s, m);
+          if (u < start + un || u < start) break;
+          start += un;
+        }
+        const int64_t cut = un <= kWhole ? start : u;
+        sh.cut[end] = cut;
+        if (end == 0) sh.at = {b, h, m, int(cut - start), un, s};
       }
-      const int h = u - at < (int64_t(1) << 31) && su < (int64_t(1) << 31) ? int(uint32_t(u - at) / uint32_t(su)) : int((u - at) / su);
-      int64_t left = (u - at) - h * su;
-      int m = 0, un;
-      for (;; ++m) {
-        un = Tile::units(a, s, m);
-        if (left < un || left < 0) break;
-        left -= un;
-      }
-      if (un <= kWhole) left = 0;
-      sh.cut[end] = at + h * su + left;
-      for (int i = 0; i < m; ++i) sh.cut[end] += Tile::units(a, s, i);
-      if (end == 0) sh.at = {b, h, m, int(left), un, s};
     }
   }
   __syncthreads();
+  if (n > sh.total) n = int(sh.total);
   u0 = sh.cut[0], u1 = sh.cut[1];
   cur = sh.at;
-  return total;
+  return sh.total;
 }
 
 // The item after cur's (there is one).
@@ -158,10 +161,10 @@ __device__ __forceinline__ void next_item(const AttendArgs& a, Cursor& cur) {
 }
 
 // Row r of a tile: its token and query head; false past the last row.
-__device__ __forceinline__ bool row_of(const Cursor& cur, int group, int r, int& token, int& head) {
-  const int t = r / group;
+__device__ __forceinline__ bool row_of(const AttendArgs& a, const Cursor& cur, int r, int& token, int& head) {
+  const int t = by_group(a, r);
   token = cur.s.first + t;
-  head = cur.h * group + r - t * group;
+  head = cur.h * a.group + r - t * a.group;
   return t < cur.s.count;
 }
 
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
           add(his[0], his[1], po);
         }
     }
-    const int row = it.tile * TM + r, t = row / a.group;
+    const int row = it.tile * TM + r, t = by_group(a, row);
     if (g == 0 && e < values) {
       const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
       const uint2 w = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         const int r = (warp & 7) * 16 + r0 + lane / kLanes;
         int qt, qh;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row_of(it, a.group, row0 + r, qt, qh))
+        if (row_of(a, it, row0 + r, qt, qh))
           v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
         v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
         *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       if (own > 0) {
         const int row0 = cur.m * kTcItem + (one ? 0 : w * kTcM);
         int token, head;
-        const bool live = row_of(cur, a.group, row0 + row, token, head);
+        const bool live = row_of(a, cur, row0 + row, token, head);
         // Keys of this half of the CTA's first unit that the row may see.
         int seen = (live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0) - (cur.unit + (one ? w : 0)) * kTcKeys -
                    half * 64;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
                 sum2 = mul2(sum2, f32x2(f, f));
               }
               if (t > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kCols; c += 16) {
                   uint32_t o[16];
                   tmem_ld16(to + c, o);
@@ -535,11 +535,30 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
                   tmem_st16(to + c, o);
                 }
               }
-              uint32_t s[2][32];
-              scores(s);
-              part = weights(s);
+              // The weights once more, 16 keys at a time (compact code for a rare path;
+              // a chunk's weights take the place of scores that are read already).
+              part = 0;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t s[16], q[8];
+                tmem_ld16(ts + c * 16, s);
+                tmem_wait_ld16(s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const int e = c * 16 + 2 * j;
+                  float x, y;
+                  split2(fma2(f32x2(e < seen ? __uint_as_float(s[2 * j]) : -INFINITY,
+                                    e + 1 < seen ? __uint_as_float(s[2 * j + 1]) : -INFINITY), scale2, base2), x, y);
+                  x = ex2(x), y = ex2(y);
+                  part = add2(part, f32x2(x, y));
+                  q[j] = Elem<T>::pack2(x, y);
+                }
+                tmem_st8(ts + c * 8, q);
+                tmem_wait_st();
+              }
+            } else {
+              tmem_st32(ts, p);
             }
-            tmem_st32(ts, p);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(pfull + 8 * w);
@@ -583,7 +602,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
         float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
         T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kCols; c += 16) {
           if (one && w == 1) break;  // stream 0 writes
           uint32_t o[16];
