@@ -26,8 +26,6 @@
 // A unit's weights are taken relative to the maximum in use before it, and its
 // own maximum, exchanged between a row's two threads meanwhile, is looked at
 // before P is stored: it rarely has grown by 2^8, and then they are taken again.
-// An item of at most 128 rows has one tile; both streams then take its rows,
-// one the even and one the odd units, and stream 0 adds up their outputs.
 // Tensor memory: S_0, S_1 (128 columns each, P in columns 0-31 and 64-95), O_0, O_1.
 // MMAs of one thread execute in order, so S_w of the next tile may be issued
 // behind the product that reads P_w, and S_w's completion implies that O_w holds
@@ -86,7 +84,7 @@ struct TcShape {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffBars = kOffKV + kStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kStages + 20;
+  static constexpr int kNumBars = 2 * kStages + 18;
   static constexpr int kSmem = kOffBars + kNumBars * 8 + 16 + 1024;  // + alignment
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
 };
@@ -179,7 +177,6 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   extern __shared__ unsigned char raw_smem[];
   __shared__ LocateScratch scratch;
   __shared__ float exchange[2][2][2][kTcM];  // [unit parity][tile][half][row]
-  __shared__ float stat[2][kTcM];            // stream 1's maxima and sums, for stream 0
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile uint32_t abort_s;
   unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -187,10 +184,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   const uint32_t bars = s0 + Shape::kOffBars;
   const auto full = [&](int s) { return bars + s * 8; };
   const auto empty = [&](int s) { return bars + (kStages + s) * 8; };
-  // Two of each (one a tile); pair: one for each two warps that share rows;
-  // both, read: the two streams of an item of one tile are done, and joined.
+  // Two of each (one a tile); pair: one for each two warps that share rows.
   const uint32_t qfull = bars + 2 * kStages * 8, sfull = qfull + 16, ofull = qfull + 32, turn = qfull + 48,
-                 pfull = qfull + 64, pair = qfull + 80, both = qfull + 144, read = qfull + 152;
+                 pfull = qfull + 64, pair = qfull + 80;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -203,8 +199,6 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       mbar_init(turn + 8 * w, 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(pair + 8 * i, 2);
-    mbar_init(both, 4);
-    mbar_init(read, 8);
     fence_barrier_init();
     abort_s = 0;
   }
@@ -237,11 +231,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     }
     return bool(__all_sync(0xffffffffu, done));
   };
-  // Units of the current item that this CTA takes, and whether it has one tile.
+  // Units of the current item that this CTA takes, and whether it has two tiles.
   const auto part_of = [&](int64_t u) { return int(min(int64_t(cur.units - cur.unit), u1 - u)); };
-  const auto one_tile = [&](const Cursor& it) { return it.s.count * a.group - it.m * kTcItem <= kTcM; };
-  // Units that stream w has of `take`: all of them for its tile, or every other one.
-  const auto own_of = [](int w, bool one, int take) { return one ? (take - w + 1) / 2 : take; };
+  const auto tiles_of = [&](const Cursor& it) { return it.s.count * a.group - it.m * kTcItem > kTcM ? 2 : 1; };
 
   if (warp >= kTcSoftWarps) {
     regs_down<kTcRegsLess>();
@@ -320,40 +312,34 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         mma_commit_elect(empty(stage));
       };
       for (int64_t u = u0; u < u1 && ok;) {
-        const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m);
-        const bool one = one_tile(cur);
-        const int own = own_of(w, one, take);
-        // Two stages (a unit's K and V) that the other stream uses.
-        const auto pass_unit = [&]() {
-          bool done = true;
-          for (int i = 0; i < 2 && done; ++i) {
-            done = wait(full(pos.stage), pos.parity);
-            if (done && lane == 0) mbar_arrive(empty(pos.stage));
+        const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m), nw = tiles_of(cur);
+        if (keys && w >= nw) {
+          // No rows for this tile: its share of releasing the stages.
+          for (int t = 0; t < 2 * take && ok; ++t) {
+            ok = wait(full(pos.stage), pos.parity);
+            if (ok && lane == 0) mbar_arrive(empty(pos.stage));
             pos.next<kStages>();
           }
-          return done;
-        };
-        // With two tiles, this warp's turn: after the other tile's batch before
-        // (of this item or of the last one with two tiles: neither warp may be
-        // two batches ahead, its barrier would pass two phases).
-        const auto my_turn = [&]() {
-          if (one || (w == 0 && !handed)) return true;
-          const bool done = wait(turn + 8 * w, turnpar);
-          turnpar ^= 1;
-          return done;
-        };
-        if (keys && one && w == 1) ok = pass_unit();
-        if (ok && keys && own > 0) {
+        } else if (keys) {
+          // This warp's turn: after the other tile's batch before, if there was one
+          // (of this item or of the last one with two tiles: neither warp may be
+          // two batches ahead, its barrier would pass two phases).
+          const auto my_turn = [&]() {
+            if (nw == 1 || (w == 0 && !handed)) return true;
+            const bool done = wait(turn + 8 * w, turnpar);
+            turnpar ^= 1;
+            return done;
+          };
           ok = wait(qfull + 8 * w, qpar) && wait(full(pos.stage), pos.parity) && my_turn();
           qpar ^= 1;
-          handed |= !one;
+          handed |= nw == 2;
           if (ok) {
             tc_fence_after();
-            scores(pos.stage, !one);
+            scores(pos.stage, nw == 2);
             pos.next<kStages>();
           }
-          for (int i = 0; i < own && ok; ++i) {
-            const int t = one ? 2 * i + w : i, vstage = pos.stage;
+          for (int t = 0; t < take && ok; ++t) {
+            const int vstage = pos.stage;
             ok = wait(full(vstage), pos.parity);
             if (!ok) break;
             const int valid = keys - (cur.unit + t) * kTcKeys;
@@ -361,32 +347,31 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               // Rows past the keys hold whatever lay there: a weight of zero
               // times that must be zero.  (Both tiles' warps may write the same zeros.)
               unsigned char* v = smem + Shape::kOffKV + vstage * Shape::kTileBytes;
-              for (int j = valid * 8 + lane; j < kTcKeys * 8; j += 32)
+              for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
 #pragma unroll
                 for (int h = 0; h < Shape::kHalves; ++h)
-                  *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                  *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
             }
             pos.next<kStages>();
-            const bool more = i + 1 < own;
+            const bool more = t + 1 < take;
             const uint64_t vdesc = desc_mn_sw128(tile_addr(vstage), Shape::kHalfBytes);
-            if (one && t + 1 < take) ok = pass_unit();
-            if (more) ok = ok && wait(full(pos.stage), pos.parity);
+            if (more) ok = wait(full(pos.stage), pos.parity);
             ok = ok && wait(pfull + 8 * w, ppar) && my_turn();
             ppar ^= 1;
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_f16_ts_elect(to, ts + k / 4 * 64 + k % 4 * 8, vdesc + k * (2048 >> 4), kIdO, i > 0 || k > 0);
+              mma_f16_ts_elect(to, ts + k / 4 * 64 + k % 4 * 8, vdesc + k * (2048 >> 4), kIdO, t > 0 || k > 0);
             mma_commit_elect(empty(vstage));
             if (more) {
-              scores(pos.stage, !one);
+              scores(pos.stage, nw == 2);
               pos.next<kStages>();
             } else {
               mma_commit_elect(ofull + 8 * w);
-              hand_on(!one);
+              hand_on(nw == 2);
             }
           }
         }
@@ -403,7 +388,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     constexpr int kCols = D / 2;  // columns of O that this warp rescales and writes
     const uint32_t ts = tmem + lanes + w * 128 + half * 64, to = tmem + lanes + 256 + w * D + half * kCols;
     const uint32_t pair_bar = pair + 8 * (w * 4 + quarter);
-    uint32_t spar = 0, opar[2] = {0, 0}, xpar = 0, dpar = 0;
+    uint32_t spar = 0, opar = 0, xpar = 0;
     // The value of the thread that shares the row (of the exchange whose parity is xpar).
     const auto post = [&](float v) {
       exchange[xpar][w][half][row] = v;
@@ -420,10 +405,8 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
     // Q of an item, if this tile has rows of it that see keys: this warp's 16
     // rows, 16 (8) lanes a row; rows past the last are zero.
-    const auto load_q = [&](const Cursor& it, int take) {
-      const bool one = one_tile(it);
-      if (Tile::keys(a, it.s, it.m) == 0 || own_of(w, one, take) == 0) return;
-      const int row0 = it.m * kTcItem + (one ? 0 : w * kTcM);
+    const auto load_q = [&](const Cursor& it) {
+      if (w >= tiles_of(it) || Tile::keys(a, it.s, it.m) == 0) return;
       constexpr int kLanes = D / 8, kOnce = 32 / kLanes;
       const int piece = lane % kLanes;
       unsigned char* q = smem + w * Shape::kTileBytes + (piece / 8) * Shape::kHalfBytes;
@@ -432,7 +415,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         const int r = (warp & 7) * 16 + r0 + lane / kLanes;
         int qt, qh;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row_of(a, it, row0 + r, qt, qh))
+        if (row_of(a, it, it.m * kTcItem + w * kTcM + r, qt, qh))
           v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
         v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
         *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
@@ -440,32 +423,30 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(qfull + 8 * w);
     };
-    if (u0 < u1) load_q(cur, part_of(u0));
+    if (u0 < u1) load_q(cur);
     for (int64_t u = u0; u < u1 && ok;) {
       const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m);
-      const bool one = one_tile(cur);
-      const int own = own_of(w, one, take);
       Cursor next = cur;
+      bool have_next = false;
       // The next item and its Q: its last reader here, the scores of this
       // item's last unit, is done, so they are under way during the output.
       const auto advance = [&]() {
-        if (u + take < u1) {
+        have_next = u + take < u1;
+        if (have_next) {
           next_item<Tile>(a, next);
-          load_q(next, int(min(int64_t(next.units), u1 - u - take)));
+          load_q(next);
         }
       };
-      if (own > 0) {
-        const int row0 = cur.m * kTcItem + (one ? 0 : w * kTcM);
+      if (w < tiles_of(cur)) {
+        const int row0 = cur.m * kTcItem + w * kTcM;
         int token, head;
         const bool live = row_of(a, cur, row0 + row, token, head);
         // Keys of this half of the CTA's first unit that the row may see.
-        int seen = (live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0) - (cur.unit + (one ? w : 0)) * kTcKeys -
-                   half * 64;
+        int seen = (live ? cur.s.len - cur.s.count + (token - cur.s.first) + 1 : 0) - cur.unit * kTcKeys - half * 64;
         float used = -INFINITY, sum = 0.f;  // the maximum that weights are relative to
-        float f0 = 1.f, f1 = 0.f;           // factors of this stream's O, and of the other's that is added
         if (keys) {
           uint64_t sum2 = 0, base2 = 0;  // two partial sums; minus the maximum in use, twice
-          for (int t = 0; t < own; ++t) {
+          for (int t = 0; t < take; ++t) {
             ok = wait(sfull + 8 * w, spar);
             spar ^= 1;
             if (!ok) break;
@@ -525,7 +506,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
                 sum2 = mul2(sum2, f32x2(f, f));
               }
               if (t > 0) {
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < kCols; c += 16) {
                   uint32_t o[16];
                   tmem_ld16(to + c, o);
@@ -535,35 +516,16 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
                   tmem_st16(to + c, o);
                 }
               }
-              // The weights once more, 16 keys at a time (compact code for a rare path;
-              // a chunk's weights take the place of scores that are read already).
-              part = 0;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t s[16], q[8];
-                tmem_ld16(ts + c * 16, s);
-                tmem_wait_ld16(s);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const int e = c * 16 + 2 * j;
-                  float x, y;
-                  split2(fma2(f32x2(e < seen ? __uint_as_float(s[2 * j]) : -INFINITY,
-                                    e + 1 < seen ? __uint_as_float(s[2 * j + 1]) : -INFINITY), scale2, base2), x, y);
-                  x = ex2(x), y = ex2(y);
-                  part = add2(part, f32x2(x, y));
-                  q[j] = Elem<T>::pack2(x, y);
-                }
-                tmem_st8(ts + c * 8, q);
-                tmem_wait_st();
-              }
-            } else {
-              tmem_st32(ts, p);
+              uint32_t s[2][32];
+              scores(s);
+              part = weights(s);
             }
+            tmem_st32(ts, p);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(pfull + 8 * w);
             sum2 = add2(sum2, part);
-            seen -= one ? 2 * kTcKeys : kTcKeys;
+            seen -= kTcKeys;
           }
           if (!ok) break;
           advance();
@@ -571,52 +533,25 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           split2(sum2, sa, sb);
           sa += sb;
           post(sa);
-          ok = fetch(other);
+          ok = fetch(other) && wait(ofull + 8 * w, opar);
+          opar ^= 1;
           if (!ok) break;
           sum = sa + other;
-          if (one && w == 1) {
-            // The other stream adds this one's O to its own, reading it where it is.
-            if (half == 0) {
-              stat[0][row] = used, stat[1][row] = sum;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(both);
-            }
-            ok = wait(read, dpar);
-          } else {
-            ok = wait(ofull + 8 * w, opar[w]);
-            if (ok && one && take > 1) {
-              ok = wait(ofull + 8, opar[1]) && wait(both, dpar);
-              const float m1 = stat[0][row], l1 = stat[1][row], m = fmaxf(used, m1), zero = m == -INFINITY ? 0.f : m;
-              f0 = ex2(used - zero), f1 = ex2(m1 - zero);
-              used = m, sum = __fmaf_rn(sum, f0, l1 * f1);
-            }
-          }
-          if (!ok) break;
           tc_fence_after();
         } else {
           advance();
         }
-        const bool joined = keys && one && take > 1;
         const bool whole = cur.unit == 0 && take == cur.units;
         const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
         if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
         float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
         T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < kCols; c += 16) {
-          if (one && w == 1) break;  // stream 0 writes
           uint32_t o[16];
           if (keys) {
             tmem_ld16(to + c, o);
             tmem_wait_ld16(o);
-          }
-          if (joined) {
-            uint32_t o1[16];
-            tmem_ld16(to + D + c, o1);
-            tmem_wait_ld16(o1);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              o[j] = __float_as_uint(__fmaf_rn(__uint_as_float(o[j]), f0, __uint_as_float(o1[j]) * f1));
           }
           if (whole) {
             if (live) {
@@ -635,22 +570,13 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             for (int j = 0; j < 16; ++j) part[(half * kCols + c + j) * kTcItem] = __uint_as_float(o[j]);
           }
         }
-        if (!whole && half == 0 && !(one && w == 1)) {
+        if (!whole && half == 0) {
           part[D * kTcItem] = used;
           part[(D + 1) * kTcItem] = sum;
         }
         tc_fence_before();  // the next item's first product overwrites O after this thread's next arrival
-        if (joined) {
-          __syncwarp();
-          if (w == 0 && lane == 0) mbar_arrive(read);
-          dpar ^= 1;
-        }
       } else {
         advance();
-      }
-      if (keys) {
-        opar[0] ^= 1;
-        if (!one || take > 1) opar[1] ^= 1;
       }
       u += take;
       cur = next;
