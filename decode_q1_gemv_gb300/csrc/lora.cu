@@ -4,17 +4,30 @@
 // Few vectors share an adapter, so each adapter's A (rank x n) and B (rows x
 // rank) have to be read about once and take 2 operations a value and vector:
 // bytes bound it, and for one vector the chain of dependent memory reads.
+//
 // Both products run in one launch: a cluster of CTAs takes one bucket (up to
-// kLoraTokens vectors of one adapter), each CTA a slice of n in the first
-// product and a slice of the rows in the second; the rank values between them
-// (at most 128 a vector) pass through distributed shared memory, so there is
-// no workspace and no second launch.  Sums are f32 in a fixed order: the
-// lanes' chains over a slice, the butterfly of a warp, the warps' parts, the
-// cluster's slices.
+// eight vectors of one adapter), each CTA a slice of n in the first product
+// and a slice of the rows in the second; the rank values between them (at
+// most 128 a vector) pass through distributed shared memory, so there is no
+// workspace and no second launch.
+//
+// Weights come through a ring of asynchronous 16-byte copies that is private
+// to each thread (a thread reads only what it copied: no barrier, and the
+// second product's first chunks are under way before the first has ended).
+// The products run on m16n8k8 MMAs with tf32 operands and f32 sums: 16 rank
+// rows (output rows) by the bucket's eight vectors.  Weights of 8 or 11
+// significant bits are exact in tf32; an f32 value x (t) is taken as hi + lo,
+// its first 11 bits and, of the exact rest, the first 11, which leaves out at
+// most 2^-21 of it (f32's own rounding of the sum is of that size).  One form
+// serves one to eight vectors: with products on the FMA pipe the code for each
+// count, unrolled, missed the instruction cache, and eight vectors were bound
+// by instructions (1000 vectors of prompts: 107 us).  An MMA takes its k
+// indices in any order as long as both operands agree, so a lane's 16 bytes,
+// eight neighbouring k, serve four MMAs as they are.
 //
 // Vectors are grouped on the device: in a window of 64 vectors, every
-// kLoraTokens-th vector of an adapter leads a bucket of it and the next ones
-// of that window.  A cluster whose vector leads no bucket has nothing to do.
+// eighth vector of an adapter leads a bucket of it and the next ones of that
+// window.  A cluster whose vector leads no bucket has nothing to do.
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
@@ -36,17 +49,19 @@ struct LoraArgs {
   int nvec, n, rows, rank, adapters;
 };
 
-constexpr int kLoraTokens = 8;    // vectors of a bucket
+constexpr int kLoraTokens = 8;    // vectors of a bucket: an MMA's N
 constexpr int kLoraWindow = 64;   // vectors among which buckets form
-constexpr int kLoraLogThreads = 8, kLoraThreads = 1 << kLoraLogThreads;
+constexpr int kLoraThreads = 256, kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraStages = 4;    // chunks of 16 KB in flight: 64 KB a CTA, two CTAs an SM
+constexpr int kLoraStages = 4;    // stages of four 16-byte pieces a thread: 64 KB a CTA, two CTAs an SM
 constexpr int kLoraRing = kLoraStages * 4 * kLoraThreads * 16;
-constexpr int kLoraX = 8192;      // values of x in shared memory: of all vectors of the bucket
-constexpr int kLoraSmem = kLoraRing + kLoraX * 4;
+// x in shared memory: 8192 values of all vectors, each vector's part padded by
+// four so that the lanes' 16-byte reads of two vectors fall into different banks.
+constexpr int kLoraX = 8192, kLoraXBytes = (kLoraX + 4 * kLoraTokens) * 4;
+constexpr int kLoraSmem = kLoraRing + kLoraXBytes;
+static_assert(kLoraWarps * kLoraMaxRank * kLoraTokens * 4 <= kLoraXBytes, "the warps' sums take x's place");
 
 struct LoraShared {
-  float part[kLoraThreads / 8][4 * kLoraTokens];       // (quad, warp of it): the sums of four rank rows
   float mine[kLoraMaxRank][kLoraTokens];               // this CTA's slice of n
   float t[kLoraMaxRank][kLoraTokens];                  // all slices, scaled
   int token[kLoraTokens];
@@ -56,273 +71,271 @@ struct LoraShared {
 __device__ __forceinline__ void lora_copy(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void lora_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Sums of v over the lanes of aligned groups of `width` lanes, where each
-// halving step gives a lane half of the values it still has: afterwards lane
-// i of a group holds `Keep` consecutive sums.
-template <int N>
-__device__ __forceinline__ void fold(float (&v)[N], int width, int lane) {
-  if constexpr (N > 1) {
-    if (width > 1) {
-      const int half = width / 2;
-      const bool up = lane & half;
-      float r[N / 2];
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const float a0, const float a1, const float a2, const float a3,
+                                         const float b0, const float b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+                 "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+// Eight f32 values as hi + lo, both of 11 significant bits.
+__device__ __forceinline__ void split_tf32(const float (&v)[8], float (&hi)[8], float (&lo)[8]) {
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float send = up ? v[i] : v[i + N / 2], keep = up ? v[i + N / 2] : v[i];
-        r[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, half));
-      }
-      fold<N / 2>(r, half, lane);
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = __uint_as_float(__float_as_uint(v[i]) & 0xffffe000u);
+    lo[i] = __uint_as_float(__float_as_uint(__fsub_rn(v[i], hi[i])) & 0xffffe000u);
+  }
+}
+// c += 16 rows (row g of the lane's quad and g + 8) x 32 k, eight of them in
+// the lane, by the eight vectors (vector g of the lane's quad in v).
+template <class T>
+__device__ __forceinline__ void mma_pieces(float (&c)[4], const uint4& row, const uint4& row8, const float (&hi)[8],
+                                           const float (&lo)[8]) {
+  float a[8], b[8];
+  Elem<T>::unpack(row, a);
+  Elem<T>::unpack(row8, b);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) v[i] = r[i];
-    }
-  } else {
-    for (int half = width / 2; half > 0; half >>= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], half));
+  for (int s = 0; s < 8; s += 2) {
+    mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], lo[s], lo[s + 1]);
+    mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], hi[s], hi[s + 1]);
   }
 }
 
-// What a CTA has to do for a bucket: a slice of n of the first product, then a
-// slice of the rows of the second, both cut into chunks in which every thread
-// has four 16-byte pieces of weights:
-//   first:  four rank rows (quad) at one piece of n (part); parts * 8 values of
-//           n a chunk, parts a power of two;
-//   second: four rows at one piece of the rank; `width` (a power of two) lanes
-//           share a row.
-struct LoraSplit {
-  int rank, r0, r1, slice;   // rank in use; rows; values of n
-  int quads;                 // of four rank rows: a power of two, as are
-  int parts, width;          // parts = 1 << lparts and width = 1 << lwidth
-  int lparts, lwidth;
-  int down, up;              // chunks of each product
-  // The calling thread's place: in the first product its quad and part, in the
-  // second the first row of a chunk and its piece.
-  int quad, part, row, piece;
-  const void* a0;            // its first piece in A (row quad * 4), chunks parts * 8 values apart
-  const void* b0;            // its first piece in B (row r0 + row), chunks 4 * 256 / width rows apart
-  int b_step;                // values of B from one chunk to the next
+// A CTA's part of a bucket.  In the first product warp w takes blocks of 32
+// values of n: w, w + 8, ...; a stage is a block of two tiles of 16 rank rows,
+// or (rank up to 16) two blocks of the one tile.  In the second, chunks of 256
+// output rows, 32 a warp, a stage a chunk's next 32 rank values.
+template <class T>
+struct LoraPart {
+  const LoraArgs& a;
+  const T *A, *B;                // the adapter's, from this CTA's first value and first row on
+  int rank, slice, rows;         // rank in use, values of n, rows of this CTA
+  int tiles, pairs, ranks32;     // of 16 rank rows, of two of those (at least 1), of 32 rank values
+  int warp, quad, piece;         // lane / 4 and lane % 4
+  unsigned char* ring;
+  // What the next copies are of.
+  int f_block, f_pair, f_chunk, f_k, f_slot = 0;
+
+  __device__ __forceinline__ LoraPart(const LoraArgs& args) : a(args) {}
+
+  // The next stage's four pieces, in order; past everything an empty group.
+  __device__ __forceinline__ void fetch() {
+    const uint32_t dst = smem_addr(ring) + f_slot * (4 * kLoraThreads * 16) + threadIdx.x * 16;
+    if (f_block * 32 < slice) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int block = tiles <= 1 ? f_block + (i >> 1) * kLoraWarps : f_block;
+        const int row = (tiles <= 1 ? 0 : (2 * f_pair + (i >> 1)) * 16) + (i & 1) * 8 + quad, j = block * 32 + piece * 8;
+        const bool live = row < rank && j < slice;
+        lora_copy(dst + i * (kLoraThreads * 16), live ? A + int64_t(row) * a.n + j : A, live);
+      }
+      if (++f_pair >= pairs) f_pair = 0, f_block += tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;
+    } else if (f_chunk * 256 < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = f_chunk * 256 + warp * 32 + ((i & 1) * 8 + quad) * 2 + (i >> 1), k = f_k * 32 + piece * 8;
+        const bool live = row < rows && k < rank;
+        lora_copy(dst + i * (kLoraThreads * 16), live ? B + int64_t(row) * a.rank + k : B, live);
+      }
+      if (++f_k >= ranks32) f_k = 0, ++f_chunk;
+    }
+    lora_commit();
+    f_slot = (f_slot + 1) % kLoraStages;
+  }
+  // Waits for the stage in `slot`.
+  __device__ __forceinline__ void take(int slot, uint4 (&w)[4]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(ring + ((slot * 4 + i) * kLoraThreads + threadIdx.x) * 16);
+  }
 };
 
-// The least k with 2^k >= v, v >= 0 (0 for 0 and 1).
-__device__ __forceinline__ int log2_from(int v) { return v <= 1 ? 0 : 32 - __clz(v - 1); }
-
-// Asynchronous copies of chunk c (of both products in turn) into the calling
-// thread's own places of the ring; what lies past an end reads as zero.
-template <class T>
-__device__ __forceinline__ void lora_fetch(const LoraArgs& a, const LoraSplit& s, uint32_t ring, int c) {
-  const uint32_t dst = ring + (c % kLoraStages) * (4 * kLoraThreads * 16) + threadIdx.x * 16;
-  if (c < s.down) {
-    const T* src = static_cast<const T*>(s.a0) + c * s.parts * 8;
-    const bool inside = (c * s.parts + s.part) * 8 < s.slice;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const bool live = inside && s.quad * 4 + r < s.rank;
-      lora_copy(dst + r * (kLoraThreads * 16), live ? src : static_cast<const T*>(a.wa), live);
-      src += a.n;
-    }
-  } else if (c < s.down + s.up) {
-    const int k = c - s.down, left = s.r1 - s.r0 - s.row - k * (4 * kLoraThreads >> s.lwidth);
-    const T* src = static_cast<const T*>(s.b0) + int64_t(k) * s.b_step;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const bool live = r < left && s.piece * 8 < s.rank;
-      lora_copy(dst + r * (kLoraThreads * 16), live ? src : static_cast<const T*>(a.wb), live);
-      src += a.rank;
-    }
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-// The thread's four pieces of chunk c, and the copies of the chunk that takes
-// the place of the one before it.
-template <class T>
-__device__ __forceinline__ void lora_pieces(const LoraArgs& a, const LoraSplit& s, unsigned char* ring, int c, float (&w)[4][8]) {
-  lora_fetch<T>(a, s, smem_addr(ring), c + kLoraStages - 1);
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    Elem<T>::unpack(*reinterpret_cast<const uint4*>(ring + (((c % kLoraStages) * 4 + r) * kLoraThreads + threadIdx.x) * 16), w[r]);
-}
-
-// Copies x from element j0 on (`count` of them, a multiple of 8) of the
-// bucket's vectors into shared memory, 16-byte pieces of even and odd number
-// apart ([vector][2][window / 8]), so that neighbouring lanes read
-// neighbouring pieces.
-template <int M>
-__device__ __forceinline__ void lora_fetch_x(const LoraArgs& a, const LoraShared& sh, uint32_t xs, int j0, int count) {
-  constexpr int kWindow = kLoraX / M;
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const float* x = a.x + sh.token[i] * a.ldx + j0;
+// The window of x from value `from` of the slice on: `count` vectors, each
+// `window` values and four of padding apart.
+__device__ __forceinline__ void lora_fetch_x(const LoraArgs& a, const LoraShared& sh, uint32_t xs, int j0, int window, int size) {
+  for (int v = 0; v < sh.count; ++v) {
+    const float* x = a.x + sh.token[v] * a.ldx + j0;
 #pragma unroll 1
-    for (int p = threadIdx.x; p < count / 4; p += kLoraThreads)
-      lora_copy(xs + (i * (kWindow / 4) + (p & 1) * (kWindow / 8) + p / 2) * 16, x + p * 4, true);
+    for (int p = threadIdx.x; p < size / 4; p += kLoraThreads) lora_copy(xs + (v * (window + 4) + p * 4) * 4, x + p * 4, true);
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  lora_commit();
 }
 
-// First product: mine[k][i] = sum over this CTA's slice of A[k] x_i, k < rank.
-// The first window of x is under way (before the ring's first chunks).
-template <class T, int M>
-__device__ __forceinline__ void lora_down(const LoraArgs& a, LoraShared& sh, const LoraSplit& s, unsigned char* ring, int j0) {
-  constexpr int kWindow = kLoraX / M;  // at least parts * 8: a window is whole chunks
-  constexpr int kLog4M = M == 1 ? 2 : M == 2 ? 3 : M == 4 ? 4 : 5;
-  static_assert(kLoraX / kLoraTokens >= 1024, "a chunk of rank 8 (parts * 8 = 1024) fits the smallest window");
-  const int lane = threadIdx.x & 31;
-  const float4* xs = reinterpret_cast<const float4*>(ring + kLoraRing);
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
-  __syncthreads();
-  float acc[4 * M];
-#pragma unroll
-  for (int i = 0; i < 4 * M; ++i) acc[i] = 0.f;
+// One bucket.  VEC: base and out rows allow 8-byte accesses, rows is even.
+template <class T, bool VEC>
+__device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, LoraPart<T>& part, int j0, int r0, float scale,
+                                            cg::cluster_group& cluster) {
+  const int quad = part.quad, piece = part.piece, count = sh.count;
+  float* xs = reinterpret_cast<float*>(part.ring + kLoraRing);
+  const int window = kLoraX >> (count <= 1 ? 0 : count <= 2 ? 1 : count <= 4 ? 2 : 3);  // values of a vector
+  lora_fetch_x(a, sh, smem_addr(xs), j0, window, min(window, part.slice));
 #pragma unroll 1
-  for (int c = 0; c < s.down; ++c) {
-    const int j = (c * s.parts + s.part) * 8;
-    if (c > 0 && c * s.parts * 8 % kWindow == 0) {  // the next window of x
+  for (int i = 0; i < kLoraStages - 1; ++i) part.fetch();
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
+  __syncthreads();  // the first window of x
+
+  float acc[kLoraMaxRank / 16][4];
+#pragma unroll
+  for (int i = 0; i < kLoraMaxRank / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  int slot = 0;
+  const auto next_slot = [&]() { slot = (slot + 1) % kLoraStages; };
+  const auto x_piece = [&](int block, float (&hi)[8], float (&lo)[8]) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (quad < count && block * 32 + piece * 8 < part.slice) {
+      const float4* src = reinterpret_cast<const float4*>(xs + quad * (window + 4) + (block * 32) % window + piece * 8);
+      const float4 p = src[0], q = src[1];
+      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+    }
+    split_tf32(v, hi, lo);
+  };
+  const int step = part.tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;  // a window is whole steps
+  int in_window = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 * 32 < part.slice; b0 += step) {  // the whole CTA together; warp w's block is b0 + w
+    if (in_window * 32 == window) {  // the next window of x
+      in_window = 0;
       __syncthreads();
-      lora_fetch_x<M>(a, sh, smem_addr(xs), j0 + c * s.parts * 8, min(kWindow, s.slice - c * s.parts * 8));
+      lora_fetch_x(a, sh, smem_addr(xs), j0 + b0 * 32, window, min(window, part.slice - b0 * 32));
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
     }
-    float w[4][8];
-    lora_pieces<T>(a, s, ring, c, w);
-    if (j >= s.slice) continue;
-    const float4* xj = xs + j % kWindow / 8;
+    in_window += step;
+    const int block = b0 + part.warp;
+    if (block * 32 >= part.slice) continue;  // as the copies: nothing is under way for it
+    float hi[8], lo[8];
+    uint4 w[4];
+    if (part.tiles <= 1) {
+      part.fetch();
+      part.take(slot, w);
+      next_slot();
+      x_piece(block, hi, lo);
+      mma_pieces<T>(acc[0], w[0], w[1], hi, lo);
+      x_piece(block + kLoraWarps, hi, lo);
+      mma_pieces<T>(acc[0], w[2], w[3], hi, lo);
+    } else {
+      x_piece(block, hi, lo);
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const float4 lo = xj[i * (kWindow / 4)], hi = xj[i * (kWindow / 4) + kWindow / 8];
-      const float xv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r * M + i] = __fmaf_rn(w[r][e], xv[e], acc[r * M + i]);
+      for (int p = 0; p < kLoraMaxRank / 32; ++p) {
+        if (p >= part.pairs) break;
+        part.fetch();
+        part.take(slot, w);
+        next_slot();
+        mma_pieces<T>(acc[2 * p], w[0], w[1], hi, lo);
+        mma_pieces<T>(acc[2 * p + 1], w[2], w[3], hi, lo);
+      }
     }
   }
-  // Over the parts: the lanes of a quad, then (more than 32 parts) its warps.
-  const int width = s.parts < 32 ? s.parts : 32, lwarps = s.parts < 32 ? 0 : s.lparts - 5;
-  fold<4 * M>(acc, width, lane);
-  // A lane holds 4 M / width sums, or one that width / (4 M) lanes share.
-  const int at = lane & (width - 1), lshare = s.parts < 32 ? s.lparts - kLog4M : 5 - kLog4M;
-  const int keep = lshare > 0 ? 1 : 1 << -lshare;
-  if ((at & ((1 << (lshare > 0 ? lshare : 0)) - 1)) == 0) {
-    float* dst = sh.part[(s.quad << lwarps) + s.part / 32] + (lshare > 0 ? at >> lshare : at << -lshare);
+  // The warps' sums, over the place of x; then in order.
+  __syncthreads();
+  float* sums = xs + part.warp * (kLoraMaxRank * kLoraTokens);
 #pragma unroll
-    for (int i = 0; i < 4 * M; ++i)
-      if (i < keep) dst[i] = acc[i];
+  for (int i = 0; i < kLoraMaxRank / 16; ++i) {
+    if (i >= part.tiles) break;
+    float* dst = sums + (i * 16 + quad) * kLoraTokens + piece * 2;
+    *reinterpret_cast<float2*>(dst) = make_float2(acc[i][0], acc[i][1]);
+    *reinterpret_cast<float2*>(dst + 8 * kLoraTokens) = make_float2(acc[i][2], acc[i][3]);
   }
   __syncthreads();
 #pragma unroll 1
-  for (int i = threadIdx.x; i < s.quads * 4 * M; i += kLoraThreads) {
+  for (int i = threadIdx.x; i < part.rank * kLoraTokens; i += kLoraThreads) {
     float v = 0.f;
-#pragma unroll 1
-    for (int p = 0; p < 1 << lwarps; ++p) v = __fadd_rn(v, sh.part[(i / (4 * M) << lwarps) + p][i % (4 * M)]);
-    sh.mine[i / M][i % M] = v;
+#pragma unroll
+    for (int w = 0; w < kLoraWarps; ++w) v = __fadd_rn(v, xs[w * (kLoraMaxRank * kLoraTokens) + i]);
+    (&sh.mine[0][0])[i] = v;
   }
-}
-
-// Second product: rows [r0, r1) of B t for the bucket's vectors.
-template <class T, int M, bool VEC>
-__device__ __forceinline__ void lora_up(const LoraArgs& a, const LoraShared& sh, const LoraSplit& s, unsigned char* ring) {
-  const int lane = threadIdx.x & 31, piece = s.piece;
-  // A row's lanes share out the vectors to write: `keep` each, from `first` on.
-  constexpr int kLogM = M == 1 ? 0 : M == 2 ? 1 : M == 4 ? 2 : 3;
-  const int lshare = s.lwidth - kLogM, keep = lshare > 0 ? 1 : 1 << -lshare;
-  const int first = lshare > 0 ? piece >> lshare : piece << -lshare;
-  const bool writes = (piece & ((1 << (lshare > 0 ? lshare : 0)) - 1)) == 0;
-  float t[8][M];
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-#pragma unroll
-    for (int i = 0; i < M; ++i) t[e][i] = piece * 8 + e < s.rank ? sh.t[piece * 8 + e][i] : 0.f;
-  // The values that the chunk's results are added to, read one chunk ahead.
-  constexpr int kKeep = M > 1 ? M / 2 : 1;
-  float4 next[kKeep];
-  const int step = 4 * kLoraThreads >> s.lwidth;  // rows of a chunk
-  const auto fetch_base = [&](int row) {
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-      next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!writes || i >= keep || first + i >= sh.count) continue;
-      const float* in = a.base + sh.token[first + i] * a.ldb + row;
-      if constexpr (VEC) {  // rows is a multiple of four
-        if (row < s.r1) next[i] = *reinterpret_cast<const float4*>(in);
-      } else {
-        if (row < s.r1) next[i].x = in[0];
-        if (row + 1 < s.r1) next[i].y = in[1];
-        if (row + 2 < s.r1) next[i].z = in[2];
-        if (row + 3 < s.r1) next[i].w = in[3];
-      }
-    }
-  };
-  int row = s.r0 + s.row;
-  fetch_base(row);
-#pragma unroll 1
-  for (int c = 0; c < s.up; ++c, row += step) {  // whole warps stay together
-    float4 base[kKeep];
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) base[i] = next[i];
-    if (c + 1 < s.up) fetch_base(row + step);
-    float w[4][8], f[4][M];
-    lora_pieces<T>(a, s, ring, s.down + c, w);
-    if (piece * 8 + 8 > s.rank) {  // values past the adapter's rank may be anything
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w[r][e] = piece * 8 + e < s.rank ? w[r][e] : 0.f;
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-#pragma unroll
-      for (int i = 0; i < M; ++i) {
-        f[r][i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[r][i] = __fmaf_rn(w[r][e], t[e][i], f[r][i]);
-      }
-      fold<M>(f[r], s.width, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-      if (!writes || i >= keep || first + i >= sh.count) continue;
-      float* out = a.out + sh.token[first + i] * a.ldo + row;
-      const float4 v = make_float4(__fadd_rn(base[i].x, f[0][i]), __fadd_rn(base[i].y, f[1][i]), __fadd_rn(base[i].z, f[2][i]),
-                                   __fadd_rn(base[i].w, f[3][i]));
-      if constexpr (VEC) {
-        if (row < s.r1) *reinterpret_cast<float4*>(out) = v;
-      } else {
-        if (row < s.r1) out[0] = v.x;
-        if (row + 1 < s.r1) out[1] = v.y;
-        if (row + 2 < s.r1) out[2] = v.z;
-        if (row + 3 < s.r1) out[3] = v.w;
-      }
-    }
-  }
-}
-
-template <class T, int M, bool VEC>
-__device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, const LoraSplit& s, unsigned char* ring,
-                                            int j0, float scale, cg::cluster_group& cluster) {
-  const int C = int(cluster.num_blocks());
-  lora_fetch_x<M>(a, sh, smem_addr(ring + kLoraRing), j0, min(kLoraX / M, s.slice));
-#pragma unroll 1
-  for (int i = 0; i < kLoraStages - 1; ++i) lora_fetch<T>(a, s, smem_addr(ring), i);
-  lora_down<T, M>(a, sh, s, ring, j0);
   cluster.sync();
 #pragma unroll 1
-  for (int i = threadIdx.x; i < s.rank * M; i += kLoraThreads) {
+  for (int i = threadIdx.x; i < part.rank * kLoraTokens; i += kLoraThreads) {
     float v = 0.f;
-    for (int p = 0; p < C; p += 4) {  // four reads at a time; a cluster has 4, 8 or 16 CTAs
-      float part[4];
+    for (int p = 0; p < int(cluster.num_blocks()); p += 4) {  // four reads at a time; a cluster has 8 or 16 CTAs
+      float s[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) part[k] = cluster.map_shared_rank(&sh.mine[0][0], p + k)[i / M * kLoraTokens + i % M];
+      for (int k = 0; k < 4; ++k) s[k] = cluster.map_shared_rank(&sh.mine[0][0], p + k)[i];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v = __fadd_rn(v, part[k]);
+      for (int k = 0; k < 4; ++k) v = __fadd_rn(v, s[k]);
     }
-    sh.t[i / M][i % M] = __fmul_rn(v, scale);
+    (&sh.t[0][0])[i] = __fmul_rn(v, scale);
   }
   cluster.sync();  // every CTA has read `mine`, and t is complete
-  lora_up<T, M, VEC>(a, sh, s, ring);
+
+  // Second product.  A lane's outputs: two neighbouring rows (and the same
+  // eight pairs further on) of vectors 2 piece and 2 piece + 1; what they are
+  // added to is read one chunk ahead.
+  float2 next[2][2];
+  const auto fetch_base = [&](int chunk) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = chunk * 256 + part.warp * 32 + (h * 8 + quad) * 2;
+        next[v][h] = make_float2(0.f, 0.f);
+        if (2 * piece + v >= count || row >= part.rows) continue;
+        const float* in = a.base + sh.token[2 * piece + v] * a.ldb + r0 + row;
+        if constexpr (VEC) {
+          next[v][h] = *reinterpret_cast<const float2*>(in);
+        } else {
+          next[v][h].x = in[0];
+          if (row + 1 < part.rows) next[v][h].y = in[1];
+        }
+      }
+  };
+  fetch_base(0);
+#pragma unroll 1
+  for (int chunk = 0; chunk * 256 < part.rows; ++chunk) {
+    float2 base[2][2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) base[v][h] = next[v][h];
+    fetch_base(chunk + 1);
+    float c[2][4] = {};
+#pragma unroll 1
+    for (int k = 0; k < part.ranks32; ++k) {
+      float v[8], hi[8], lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = k * 32 + piece * 8 + e < part.rank ? sh.t[k * 32 + piece * 8 + e][quad] : 0.f;
+      split_tf32(v, hi, lo);
+      uint4 w[4];
+      part.fetch();
+      part.take(slot, w);
+      next_slot();
+      // Values past the adapter's rank may be anything: zero, like their t.
+      const int inside = part.rank - k * 32 - piece * 8;
+      if (inside < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t* word = reinterpret_cast<uint32_t*>(&w[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            word[e] = inside >= 2 * e + 2 ? word[e] : inside == 2 * e + 1 ? word[e] & 0xffffu : 0u;
+        }
+      }
+      mma_pieces<T>(c[0], w[0], w[1], hi, lo);
+      mma_pieces<T>(c[1], w[2], w[3], hi, lo);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = chunk * 256 + part.warp * 32 + (h * 8 + quad) * 2;
+        if (2 * piece + v >= count || row >= part.rows) continue;
+        float* out = a.out + sh.token[2 * piece + v] * a.ldo + r0 + row;
+        const float2 r = make_float2(__fadd_rn(base[v][h].x, c[0][2 * h + v]), __fadd_rn(base[v][h].y, c[1][2 * h + v]));
+        if constexpr (VEC) {
+          *reinterpret_cast<float2*>(out) = r;
+        } else {
+          out[0] = r.x;
+          if (row + 1 < part.rows) out[1] = r.y;
+        }
+      }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// VEC: base and out rows allow 16-byte accesses, and rows is a multiple of 4.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
   __shared__ LoraShared sh;
@@ -330,7 +343,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   pdl_launch_dependents();
   pdl_wait();
-  const int C = int(cluster.num_blocks()), clusters = int(gridDim.x) / C;
+  const int C = int(cluster.num_blocks()), clusters = int(gridDim.x) / C, c = int(cluster.block_rank());
+#pragma unroll 1
   for (int v = int(blockIdx.x) / C; v < a.nvec; v += clusters) {
     // Warp 0 looks at the window: which of its vectors have v's adapter.
     const int raw = a.index[v];
@@ -349,9 +363,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
       if (threadIdx.x == 0) {
         int count = 0;
         if (before % kLoraTokens == 0) {
+#pragma unroll 1
           for (uint64_t rest = same >> (v - w0) << (v - w0); rest && count < kLoraTokens; rest &= rest - 1)
             sh.token[count++] = w0 + __ffsll(int64_t(rest)) - 1;
-          for (int i = count; i < kLoraTokens; ++i) sh.token[i] = sh.token[0];
         }
         sh.count = count;
         if (raw < -1 || raw >= a.adapters) atomicOr(a.status, kStatusBadIndex);
@@ -361,7 +375,6 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
     const int count = sh.count;
     if (count && adapter < 0) {
       if (a.out != a.base) {
-        const int c = int(cluster.block_rank());
 #pragma unroll 1
         for (int i = 0; i < count; ++i)
 #pragma unroll 1
@@ -369,33 +382,20 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
             a.out[sh.token[i] * a.ldo + r] = a.base[sh.token[i] * a.ldb + r];
       }
     } else if (count) {
-      LoraSplit s;
-      s.rank = a.ranks ? max(0, min(a.ranks[adapter], a.rank)) : a.rank;
-      const int c = int(cluster.block_rank());
-      const int per_n = (a.n / 8 + C - 1) / C * 8, per_r = ((a.rows + 3) / 4 + C - 1) / C * 4;
-      const int j0 = min(a.n, c * per_n);
-      s.slice = min(a.n, j0 + per_n) - j0;
-      s.r0 = min(a.rows, c * per_r), s.r1 = min(a.rows, s.r0 + per_r);
-      const int lquads = max(1, log2_from((s.rank + 3) / 4));
-      s.quads = 1 << lquads, s.lparts = kLoraLogThreads - lquads, s.parts = 1 << s.lparts;
-      s.lwidth = max(1, log2_from((s.rank + 7) / 8)), s.width = 1 << s.lwidth;
-      s.down = s.rank ? (s.slice + s.parts * 8 - 1) >> (s.lparts + 3) : 0;
-      s.up = (((s.r1 - s.r0) << s.lwidth) + 4 * kLoraThreads - 1) / (4 * kLoraThreads);
-      s.quad = threadIdx.x >> s.lparts, s.part = threadIdx.x & (s.parts - 1);
-      s.row = (threadIdx.x >> s.lwidth) * 4, s.piece = threadIdx.x & (s.width - 1);
-      s.a0 = static_cast<const T*>(a.wa) + (int64_t(adapter) * a.rank + s.quad * 4) * a.n + j0 + s.part * 8;
-      s.b0 = static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + s.r0 + s.row) * a.rank + s.piece * 8;
-      s.b_step = (4 * kLoraThreads >> s.lwidth) * a.rank;
-      const float scale = a.scale ? a.scale[adapter] : 1.f;
-      if (count == 1)
-        lora_bucket<T, 1, VEC>(a, sh, s, ring, j0, scale, cluster);
-      else if (count == 2)
-        lora_bucket<T, 2, VEC>(a, sh, s, ring, j0, scale, cluster);
-      else if (count <= 4)
-        lora_bucket<T, 4, VEC>(a, sh, s, ring, j0, scale, cluster);
-      else
-        lora_bucket<T, 8, VEC>(a, sh, s, ring, j0, scale, cluster);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      LoraPart<T> part(a);
+      const int per_n = (a.n / 8 + C - 1) / C * 8, per_r = ((a.rows + 1) / 2 + C - 1) / C * 2;
+      const int j0 = min(a.n, c * per_n), r0 = min(a.rows, c * per_r);
+      part.rank = a.ranks ? max(0, min(a.ranks[adapter], a.rank)) : a.rank;
+      part.A = static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n + j0;
+      part.B = static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + r0) * a.rank;
+      part.rows = min(a.rows, r0 + per_r) - r0;
+      part.tiles = (part.rank + 15) / 16, part.pairs = max(1, (part.tiles + 1) / 2);
+      part.slice = part.rank ? min(a.n, j0 + per_n) - j0 : 0;  // rank 0: no first product
+      part.ranks32 = max(1, (part.rank + 31) / 32);
+      part.warp = threadIdx.x >> 5, part.quad = (threadIdx.x & 31) >> 2, part.piece = threadIdx.x & 3;
+      part.ring = ring;
+      part.f_block = part.warp, part.f_pair = part.f_chunk = part.f_k = 0;
+      lora_bucket<T, VEC>(a, sh, part, j0, r0, a.scale ? a.scale[adapter] : 1.f, cluster);
     }
     __syncthreads();  // sh is free again
   }
@@ -447,7 +447,8 @@ extern "C" int q1_lora_add(const float* x, int64_t ldx, int64_t nvec, int64_t n,
   LoraArgs g = {x, a, b, index, ranks, scale, base, out, nullptr, ldx, ldb, ldo, int(nvec), int(n), int(rows), int(rank),
                 int(adapters)};
   if (int e = ops_status_ptr(&g.status)) return e;
-  const bool vec = aligned16(base) && aligned16(out) && ldb % 4 == 0 && ldo % 4 == 0 && rows % 4 == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(base) % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0 && ldb % 2 == 0 &&
+                   ldo % 2 == 0 && rows % 2 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == Q1_BF16) return vec ? launch_lora<__nv_bfloat16, true>(g, s) : launch_lora<__nv_bfloat16, false>(g, s);
   return vec ? launch_lora<__half, true>(g, s) : launch_lora<__half, false>(g, s);
