@@ -22,6 +22,7 @@
 namespace q1 {
 
 constexpr int kRowsS = 16;   // rows of a tile
+constexpr int kFewRows = 16;  // a key head's rows up to which this kernel takes a sequence
 constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
 constexpr int kWarpsS = 4;
 constexpr int kWholeS = 4;       // units of an item that is not split
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
 // of this file's has.
 // (Sequences of few rows among others with many are this kernel's too, in a launch of
 // their own: a tile of 128 rows costs the same however few are in use.)
-static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kRowsS; }
+static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kFewRows; }
 
 static int attend_ctas() { return 2 * num_sms(); }
 
@@ -366,12 +367,12 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   };
   if (!many_rows(max_new, a.group)) return few();
   const bool both = kv->batch > 1;
-  if (both) a.least_rows = kRowsS + 1;
+  if (both) a.least_rows = kFewRows + 1;
   bool ran = false;
   if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
   if (!ran) a.least_rows = 0;
   if (!ran || both) {
-    if (ran) a.least_rows = 0, a.most_rows = kRowsS;
+    if (ran) a.least_rows = 0, a.most_rows = kFewRows;
     return few();
   }
   return Q1_OK;

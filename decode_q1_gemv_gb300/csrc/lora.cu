@@ -251,7 +251,7 @@ __device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, L
 #pragma unroll 1
   for (int i = threadIdx.x; i < part.rank * kLoraTokens; i += kLoraThreads) {
     float v = 0.f;
-    for (int p = 0; p < int(cluster.num_blocks()); p += 4) {  // four reads at a time; a cluster has 8 or 16 CTAs
+    for (int p = 0; p < int(cluster.num_blocks()); p += 4) {  // four reads at a time; a cluster has 4, 8 or 16 CTAs
       float s[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] = cluster.map_shared_rank(&sh.mine[0][0], p + k)[i];
@@ -414,11 +414,13 @@ static int launch_lora(const LoraArgs& g, cudaStream_t s) {
       return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  // Clusters of 16 while all of them run at once (13 vectors of one adapter,
-  // n 8120: 12.8 us against 15.5 with 8), of 8 beyond (64 vectors, rank 64: 28.7 us
-  // against 47).  Their number is odd: the vectors that lead buckets are every
-  // eighth in a prompt, and a cluster takes every so many-th vector.
-  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : 8;
+  // Clusters of 16 while all of them run at once (one vector of rank 16, 4096 x
+  // 4096: 5.0 us against 6.2 with 8), of 8 up to 128 vectors (64 of rank 64: 27 us
+  // against 39 with 4), of 4 beyond: fewer CTAs wait for each other (1000 vectors of
+  // prompts: 66 us against 82, 163 of rank 48: 29 against 33).  Their number
+  // is odd: the vectors that lead buckets are every eighth in a prompt, and a
+  // cluster takes every so many-th vector.
+  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : g.nvec <= 128 ? 8 : 4;
   const int64_t most = (num_sms() - 1) | 1;
   const dim3 grid(unsigned((g.nvec < most ? g.nvec : most) * cluster));
   return launch_op(k_lora_add<T, VEC>, grid, kLoraThreads, kLoraSmem, cluster, s, who, g);
