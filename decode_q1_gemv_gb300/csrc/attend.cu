@@ -22,7 +22,6 @@
 namespace q1 {
 
 constexpr int kRowsS = 16;   // rows of a tile
-constexpr int kFewRows = 16;  // a key head's rows up to which this kernel takes a sequence
 constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
 constexpr int kWarpsS = 4;
 constexpr int kWholeS = 4;       // units of an item that is not split
@@ -290,11 +289,13 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   }
 }
 
-// Which kernel: the tensor-core one from more rows a key head on than one tile
-// of this file's has.
-// (Sequences of few rows among others with many are this kernel's too, in a launch of
-// their own: a tile of 128 rows costs the same however few are in use.)
-static bool many_rows(int64_t max_new, int64_t group) { return max_new * group > kFewRows; }
+// Which kernel, from the rows a key head at most (new tokens times the group).
+// One sequence: this one up to 32 rows (32 over 4000 keys: 16.4 us against 17.3;
+// 64 over 8000: 26.7 against 23.4).  Several: up to 64 (8 x 64 rows over 3000
+// keys: 21.2 us against 35.6; 16 x 64, mixed lengths: 26.3 against 35.8), since sequences
+// of up to 16 rows among others with more are this kernel's too, in a launch
+// of their own: a tile of 128 rows costs the same however few are in use.
+static bool many_rows(int64_t max_new, int64_t group, bool one) { return max_new * group > (one ? 32 : 64); }
 
 static int attend_ctas() { return 2 * num_sms(); }
 
@@ -325,7 +326,7 @@ extern "C" int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, 
     return fail(Q1_ERR_ARG, "q1_paged_attention_workspace: bad shape max_new=%lld heads=%lld kv_heads=%lld dim=%lld",
                 (long long)max_new, (long long)heads, (long long)kv_heads, (long long)dim);
   const int64_t few = attend_workspace(attend_ctas(), kRowsS, int(dim));
-  if (!many_rows(max_new, heads / kv_heads)) return few;
+  if (!many_rows(max_new, heads / kv_heads, true)) return few;
   const int64_t many = attend_tc_workspace(int(dim));
   return few > many ? few : many;
 }
@@ -365,14 +366,14 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
     if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, workspace, s) : launch_attend<__half, 128>(a, workspace, s);
     return bf ? launch_attend<__nv_bfloat16, 64>(a, workspace, s) : launch_attend<__half, 64>(a, workspace, s);
   };
-  if (!many_rows(max_new, a.group)) return few();
+  if (!many_rows(max_new, a.group, kv->batch == 1)) return few();
   const bool both = kv->batch > 1;
-  if (both) a.least_rows = kFewRows + 1;
+  if (both) a.least_rows = kRowsS + 1;
   bool ran = false;
   if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
   if (!ran) a.least_rows = 0;
   if (!ran || both) {
-    if (ran) a.least_rows = 0, a.most_rows = kFewRows;
+    if (ran) a.least_rows = 0, a.most_rows = kRowsS;
     return few();
   }
   return Q1_OK;
