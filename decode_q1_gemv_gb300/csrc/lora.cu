@@ -17,8 +17,8 @@
 // The products run on m16n8k8 MMAs with tf32 operands and f32 sums: 16 rank
 // rows (output rows) by the bucket's eight vectors.  Weights of 8 or 11
 // significant bits are exact in tf32; an f32 value x (t) is taken as hi + lo,
-// its first 11 bits and, of the exact rest, the first 11, which leaves out at
-// most 2^-21 of it (f32's own rounding of the sum is of that size).  One form
+// x rounded to 11 bits and the exact rest rounded to 11, which is off by 2^-24
+// of it at most, as f32's own roundings are.  One form
 // serves one to eight vectors: with products on the FMA pipe the code for each
 // count, unrolled, missed the instruction cache, and eight vectors were bound
 // by instructions (1000 vectors of prompts: 107 us).  An MMA takes its k
@@ -80,20 +80,25 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const float a0, const fl
                : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
                  "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
-// Eight f32 values as hi + lo, both of 11 significant bits.
+// Eight f32 values as hi + lo, both rounded to 11 significant bits.
+__device__ __forceinline__ float round_tf32(float v) {
+  return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u);
+}
 __device__ __forceinline__ void split_tf32(const float (&v)[8], float (&hi)[8], float (&lo)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    hi[i] = __uint_as_float(__float_as_uint(v[i]) & 0xffffe000u);
-    lo[i] = __uint_as_float(__float_as_uint(__fsub_rn(v[i], hi[i])) & 0xffffe000u);
+    hi[i] = round_tf32(v[i]);
+    lo[i] = round_tf32(__fsub_rn(v[i], hi[i]));
   }
 }
-// c += 16 rows (row g of the lane's quad and g + 8) x 32 k, eight of them in
-// the lane, by the eight vectors (vector g of the lane's quad in v).
+// sum += 16 rows (row g of the lane's quad and g + 8) x 32 k, eight of them in
+// the lane, by the eight vectors (vector g of the lane's quad in v).  The MMAs
+// cut, not round, their sums, so each 32 k start from zero and are added with
+// rounding (14336 values in one accumulator were off by 2e-6).
 template <class T>
-__device__ __forceinline__ void mma_pieces(float (&c)[4], const uint4& row, const uint4& row8, const float (&hi)[8],
+__device__ __forceinline__ void mma_pieces(float (&sum)[4], const uint4& row, const uint4& row8, const float (&hi)[8],
                                            const float (&lo)[8]) {
-  float a[8], b[8];
+  float a[8], b[8], c[4] = {0.f, 0.f, 0.f, 0.f};
   Elem<T>::unpack(row, a);
   Elem<T>::unpack(row8, b);
 #pragma unroll
@@ -101,6 +106,8 @@ __device__ __forceinline__ void mma_pieces(float (&c)[4], const uint4& row, cons
     mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], lo[s], lo[s + 1]);
     mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], hi[s], hi[s + 1]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] = __fadd_rn(sum[i], c[i]);
 }
 
 // A CTA's part of a bucket.  In the first product warp w takes blocks of 32
