@@ -63,7 +63,7 @@ static_assert(kLoraWarps * kLoraMaxRank * kLoraTokens * 4 <= kLoraXBytes, "the w
 
 struct LoraShared {
   float mine[kLoraMaxRank][kLoraTokens];               // this CTA's slice of n
-  float t[kLoraMaxRank][kLoraTokens];                  // all slices, scaled
+  float t[2][kLoraTokens][kLoraMaxRank + 4];           // all slices, scaled, as hi and lo
   int token[kLoraTokens];
   int count;
 };
@@ -122,31 +122,57 @@ struct LoraPart {
   int tiles, pairs, ranks32;     // of 16 rank rows, of two of those (at least 1), of 32 rank values
   int warp, quad, piece;         // lane / 4 and lane % 4
   unsigned char* ring;
-  // What the next copies are of.
-  int f_block, f_pair, f_chunk, f_k, f_slot = 0;
+  // What the next copies are of: the place in the work, and the lane's first
+  // piece there (moved on by addition: products of 64-bit strides for every
+  // piece were a third of all instructions).
+  int f_block, f_pair = 0, f_chunk = 0, f_k = 0, f_slot = 0;
+  const T *f_a, *f_b;
 
   __device__ __forceinline__ LoraPart(const LoraArgs& args) : a(args) {}
+
+  // After the members above `f_block` are set.
+  __device__ __forceinline__ void start() {
+    f_block = warp;
+    f_a = A + int64_t(quad) * a.n + warp * 32 + piece * 8;
+    f_b = B + int64_t(warp * 32 + quad * 2) * a.rank + piece * 8;
+  }
 
   // The next stage's four pieces, in order; past everything an empty group.
   __device__ __forceinline__ void fetch() {
     const uint32_t dst = smem_addr(ring) + f_slot * (4 * kLoraThreads * 16) + threadIdx.x * 16;
     if (f_block * 32 < slice) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int block = tiles <= 1 ? f_block + (i >> 1) * kLoraWarps : f_block;
-        const int row = (tiles <= 1 ? 0 : (2 * f_pair + (i >> 1)) * 16) + (i & 1) * 8 + quad, j = block * 32 + piece * 8;
-        const bool live = row < rank && j < slice;
-        lora_copy(dst + i * (kLoraThreads * 16), live ? A + int64_t(row) * a.n + j : A, live);
+      const int64_t down8 = int64_t(8) * a.n;
+      // Pieces 2 and 3: the next tile of rank rows, or (one tile) the warp's next block.
+      const int64_t second = tiles <= 1 ? 32 * kLoraWarps : 2 * down8;
+      const int j = f_block * 32 + piece * 8, row = f_pair * 32 + quad;
+      const int j2 = tiles <= 1 ? j + 32 * kLoraWarps : j, row2 = tiles <= 1 ? row : row + 16;
+      const bool in0 = j < slice && row < rank, in1 = j < slice && row + 8 < rank;
+      const bool in2 = j2 < slice && row2 < rank, in3 = j2 < slice && row2 + 8 < rank;
+      lora_copy(dst, in0 ? f_a : A, in0);
+      lora_copy(dst + kLoraThreads * 16, in1 ? f_a + down8 : A, in1);
+      lora_copy(dst + 2 * kLoraThreads * 16, in2 ? f_a + second : A, in2);
+      lora_copy(dst + 3 * kLoraThreads * 16, in3 ? f_a + second + down8 : A, in3);
+      f_a += 4 * down8;
+      if (++f_pair >= pairs) {
+        f_pair = 0;
+        f_a -= pairs * 4 * down8;
+        const int blocks = tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;
+        f_block += blocks, f_a += blocks * 32;
       }
-      if (++f_pair >= pairs) f_pair = 0, f_block += tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;
     } else if (f_chunk * 256 < rows) {
+      const int row = f_chunk * 256 + warp * 32 + quad * 2;
+      const bool k_in = f_k * 32 + piece * 8 < rank;
+      const T* p = f_b;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = f_chunk * 256 + warp * 32 + ((i & 1) * 8 + quad) * 2 + (i >> 1), k = f_k * 32 + piece * 8;
-        const bool live = row < rows && k < rank;
-        lora_copy(dst + i * (kLoraThreads * 16), live ? B + int64_t(row) * a.rank + k : B, live);
+      for (int i = 0; i < 4; ++i) {  // rows row, row + 16, row + 1, row + 17
+        const bool live = k_in && row + (i & 1) * 16 + (i >> 1) < rows;
+        lora_copy(dst + i * (kLoraThreads * 16), live ? p + ((i & 1) * 16 + (i >> 1)) * a.rank : B, live);
       }
-      if (++f_k >= ranks32) f_k = 0, ++f_chunk;
+      f_b += 32;
+      if (++f_k >= ranks32) {
+        f_k = 0, ++f_chunk;
+        f_b += 256 * int64_t(a.rank) - ranks32 * 32;
+      }
     }
     lora_commit();
     f_slot = (f_slot + 1) % kLoraStages;
@@ -265,54 +291,65 @@ __device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, L
 #pragma unroll
       for (int k = 0; k < 4; ++k) v = __fadd_rn(v, s[k]);
     }
-    (&sh.t[0][0])[i] = __fmul_rn(v, scale);
+    v = __fmul_rn(v, scale);
+    const float hi = round_tf32(v);
+    sh.t[0][i % kLoraTokens][i / kLoraTokens] = hi;
+    sh.t[1][i % kLoraTokens][i / kLoraTokens] = round_tf32(__fsub_rn(v, hi));
   }
+  // Rank values past the adapter's, up to a multiple of 32, are zero.
+  for (int i = part.rank + (threadIdx.x >> 4); i < part.ranks32 * 32; i += kLoraThreads / 16)
+    sh.t[threadIdx.x >> 3 & 1][threadIdx.x & 7][i] = 0.f;
   cluster.sync();  // every CTA has read `mine`, and t is complete
 
   // Second product.  A lane's outputs: two neighbouring rows (and the same
   // eight pairs further on) of vectors 2 piece and 2 piece + 1; what they are
   // added to is read one chunk ahead.
+  const int row_lane = part.warp * 32 + quad * 2;
+  const float* in[2];
+  float* out[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int64_t token = sh.token[2 * piece + v < count ? 2 * piece + v : 0];
+    in[v] = a.base + token * a.ldb + r0 + row_lane;
+    out[v] = a.out + token * a.ldo + r0 + row_lane;
+  }
   float2 next[2][2];
-  const auto fetch_base = [&](int chunk) {
+  const auto fetch_base = [&](int row0) {
 #pragma unroll
     for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = chunk * 256 + part.warp * 32 + (h * 8 + quad) * 2;
+        const int row = row0 + row_lane + h * 16;
         next[v][h] = make_float2(0.f, 0.f);
         if (2 * piece + v >= count || row >= part.rows) continue;
-        const float* in = a.base + sh.token[2 * piece + v] * a.ldb + r0 + row;
+        const float* src = in[v] + row0 + h * 16;
         if constexpr (VEC) {
-          next[v][h] = *reinterpret_cast<const float2*>(in);
+          next[v][h] = *reinterpret_cast<const float2*>(src);
         } else {
-          next[v][h].x = in[0];
-          if (row + 1 < part.rows) next[v][h].y = in[1];
+          next[v][h].x = src[0];
+          if (row + 1 < part.rows) next[v][h].y = src[1];
         }
       }
   };
   fetch_base(0);
 #pragma unroll 1
-  for (int chunk = 0; chunk * 256 < part.rows; ++chunk) {
+  for (int row0 = 0; row0 < part.rows; row0 += 256) {
     float2 base[2][2];
 #pragma unroll
     for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int h = 0; h < 2; ++h) base[v][h] = next[v][h];
-    fetch_base(chunk + 1);
+    fetch_base(row0 + 256);
     float c[2][4] = {};
 #pragma unroll 1
     for (int k = 0; k < part.ranks32; ++k) {
-      float v[8], hi[8], lo[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = k * 32 + piece * 8 + e < part.rank ? sh.t[k * 32 + piece * 8 + e][quad] : 0.f;
-      split_tf32(v, hi, lo);
       uint4 w[4];
       part.fetch();
       part.take(slot, w);
       next_slot();
       // Values past the adapter's rank may be anything: zero, like their t.
       const int inside = part.rank - k * 32 - piece * 8;
-      if (inside < 8) {
+      if (inside > 0 && inside < 8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t* word = reinterpret_cast<uint32_t*>(&w[i]);
@@ -321,6 +358,14 @@ __device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, L
             word[e] = inside >= 2 * e + 2 ? word[e] : inside == 2 * e + 1 ? word[e] & 0xffffu : 0u;
         }
       }
+      float hi[8], lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 h4 = *reinterpret_cast<const float4*>(&sh.t[0][quad][k * 32 + piece * 8 + e]);
+        const float4 l4 = *reinterpret_cast<const float4*>(&sh.t[1][quad][k * 32 + piece * 8 + e]);
+        hi[e] = h4.x, hi[e + 1] = h4.y, hi[e + 2] = h4.z, hi[e + 3] = h4.w;
+        lo[e] = l4.x, lo[e + 1] = l4.y, lo[e + 2] = l4.z, lo[e + 3] = l4.w;
+      }
       mma_pieces<T>(c[0], w[0], w[1], hi, lo);
       mma_pieces<T>(c[1], w[2], w[3], hi, lo);
     }
@@ -328,15 +373,15 @@ __device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, L
     for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = chunk * 256 + part.warp * 32 + (h * 8 + quad) * 2;
+        const int row = row0 + row_lane + h * 16;
         if (2 * piece + v >= count || row >= part.rows) continue;
-        float* out = a.out + sh.token[2 * piece + v] * a.ldo + r0 + row;
+        float* dst = out[v] + row0 + h * 16;
         const float2 r = make_float2(__fadd_rn(base[v][h].x, c[0][2 * h + v]), __fadd_rn(base[v][h].y, c[1][2 * h + v]));
         if constexpr (VEC) {
-          *reinterpret_cast<float2*>(out) = r;
+          *reinterpret_cast<float2*>(dst) = r;
         } else {
-          out[0] = r.x;
-          if (row + 1 < part.rows) out[1] = r.y;
+          dst[0] = r.x;
+          if (row + 1 < part.rows) dst[1] = r.y;
         }
       }
   }
@@ -401,7 +446,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
       part.ranks32 = max(1, (part.rank + 31) / 32);
       part.warp = threadIdx.x >> 5, part.quad = (threadIdx.x & 31) >> 2, part.piece = threadIdx.x & 3;
       part.ring = ring;
-      part.f_block = part.warp, part.f_pair = part.f_chunk = part.f_k = 0;
+      part.start();
       lora_bucket<T, VEC>(a, sh, part, j0, r0, a.scale ? a.scale[adapter] : 1.f, cluster);
     }
     __syncthreads();  // sh is free again
