@@ -314,6 +314,8 @@ static int launch_attend(AttendArgs& a, void* workspace, cudaStream_t s) {
   a.ctas = attend_ctas();
   place_workspace(a, workspace);
   if (int e = launch_op(k_attend<T, D>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
+  // No item has more units than stay whole: nothing to join.
+  if (a.kv.table_tokens <= kWholeS * kKeysS) return Q1_OK;
   return launch_op(k_attend_join<T, kRowsS, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
 }
 

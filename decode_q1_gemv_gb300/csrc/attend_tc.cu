@@ -652,6 +652,8 @@ static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
   }
   if (int e = launch_op<AttendTcArgs>(k_attend_tc<T, D>, dim3(unsigned(g.a.ctas)), kTcAThreads, TcShape<D>::kSmem, 1, s, who, g))
     return e;
+  // No item has more units than stay whole: nothing to join.
+  if (g.a.kv.table_tokens <= kTcWhole * kTcKeys) return Q1_OK;
   return launch_op(k_attend_join<T, kTcItem, D, true>, dim3(unsigned(g.a.ctas), kTcJoinSlices), kJoinThreads, 0, 1, s, who,
                    g.a);
 }
