@@ -356,6 +356,47 @@ def test_attend_sharp_and_growing_scores(new):
         within(got, want, 4 * dim * 80 * U32 * mag + attend_tol(c, q, want, mag, total, seen))
 
 
+@pytest.mark.parametrize("new", [1, 90])
+def test_attend_scale_zero(new):
+    """All weights equal: the mean of the visible values (masked keys stay masked)."""
+    check_attend(Cache([(new, 300)], 4, 1, 128, 16, torch.bfloat16), 4, torch.bfloat16, 128, scale=0.0)
+
+
+@pytest.mark.parametrize("most", [1, 12])
+def test_attend_many_sequences(most):
+    """More sequences than lanes of a warp, some of them without new tokens."""
+    rng = np.random.default_rng(most)
+    seqs = []
+    for _ in range(300):
+        n = int(rng.integers(0, most + 1))
+        seqs.append((n, int(n + rng.integers(0, 90))))
+    check_attend(Cache(seqs, 8, 2, 64, 16, torch.float16), 8, torch.float16, 64, max_new=most)
+
+
+@pytest.mark.parametrize("max_new", [1, 100])
+def test_attend_nothing_new(max_new):
+    """No sequence has a new token: every row is left as it is."""
+    c = Cache([(0, 40), (0, 0)], 4, 2, 64, 16, torch.float16)
+    q = normal(76, 3, 4, 64, dtype=torch.float16)
+    out = torch.full_like(q, 3.0)
+    binding.paged_attention(q, *c.args(), max_new=max_new, out=out)
+    assert (out == 3).all() and binding.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attend_nan_in_a_row_stays_there(new):
+    """A NaN in one row of q makes that row's output NaN and no other's."""
+    c = Cache([(new, 600), (1, 77)], 4, 2, 128, 16, torch.bfloat16)
+    q = normal(77, c.total, 4, 128, dtype=torch.bfloat16)
+    want = binding.paged_attention(q, *c.args(), max_new=new)
+    q[0, 1, 5] = math.nan
+    got = binding.paged_attention(q, *c.args(), max_new=new)
+    assert torch.isnan(got[0, 1]).all()
+    keep = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    assert torch.equal(got[keep], want[keep])
+
+
 @pytest.mark.parametrize("new,max_new", [(1, 1), (200, 200)])
 def test_attend_repeats_bit_for_bit_and_on_another_stream(new, max_new):
     c = Cache([(new, 3000), (1, 500)], 8, 2, 128, 16, torch.bfloat16)
