@@ -33,6 +33,14 @@
 // has grown by more than 2^8 (weights are then at most 2^8 relative to the
 // maximum in use, which f32 sums and both 16-bit types hold).
 //
+// Measured (32 heads over 8 of 128, bf16): 2048 new tokens over 16001 keys, 0.503
+// Tflop, in 351 us with the join: 1.43 Pflop/s, 0.76 of this card's matrix product
+// rate (1.88); the tensor pipe is active 64 % of the cycles (profiled launch, 343 us).
+// What is left: with D = 128 the two tiles fill tensor memory, so a tile's scores,
+// softmax and product with V follow each other, and two tiles hide each other's only in
+// part.  With D = 64 the softmax bounds it: its arithmetic alone takes 346 cycles a
+// warp and 64 keys (exponentials 256 of them), four warps a scheduler.
+//
 // Every wait is bounded; one that gives up raises the CTA's abort flag and the
 // device status word, and every role winds down.
 #include <cuda.h>

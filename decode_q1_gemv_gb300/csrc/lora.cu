@@ -25,6 +25,12 @@
 // indices in any order as long as both operands agree, so a lane's 16 bytes,
 // eight neighbouring k, serve four MMAs as they are.
 //
+// Measured: 64 vectors, most with an adapter of their own (f16, ranks 16 to 64, 4096
+// to 14336), 63 MB, in 24.3 us: 2.6 TB/s, 0.38 of the copy bandwidth; 1000 vectors of
+// prompts (bf16, rank 32, 14336 to 4096), 94 MB, in 63 us.  Neither DRAM (39 and 15 %) nor issue (38 %)
+// bounds them but each bucket's chain: index, x, first product, exchange through the
+// cluster, second product.  One vector of rank 16, 4096 x 4096: 5.0 us.
+//
 // Vectors are grouped on the device: in a window of 64 vectors, every
 // eighth vector of an adapter leads a bucket of it and the next ones of that
 // window.  A cluster whose vector leads no bucket has nothing to do.

@@ -8,6 +8,11 @@
 // groups, so a q8_0 block of 32 values is 8 (f32) or 4 (16-bit) neighbouring
 // lanes and its maximum costs 3 or 2 shuffles, as in quant.cu.
 //
+// Measured: 8191 rows of 4128 f32 values with residual, 442 MB, in 70.7 us: 6.25 TB/s,
+// 0.92 of the copy bandwidth of the card (6.78 TB/s).  One row of 4096 takes 2.6 us a
+// launch in a chain of them, 64 bf16 rows 2.4 us: the launch and one round of
+// loads, not bytes.
+//
 // The order of every sum depends on n and the type alone (which thread holds
 // which group, the warp's butterfly, then the warps in order), never on the
 // number of rows: a row's outputs are the same bits in any batch.
