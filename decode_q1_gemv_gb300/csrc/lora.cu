@@ -6,34 +6,36 @@
 // bytes bound it, and for one vector the chain of dependent memory reads.
 //
 // Both products run in one launch: a cluster of CTAs takes one bucket (up to
-// eight vectors of one adapter), each CTA a slice of n in the first product
-// and a slice of the rows in the second; the rank values between them (at
-// most 128 a vector) pass through distributed shared memory, so there is no
-// workspace and no second launch.
+// eight or sixteen vectors of one adapter), each CTA a slice of n in the first
+// product and a slice of the rows in the second; the rank values between them
+// (at most 128 a vector) pass through distributed shared memory, so there is
+// no workspace and no second launch.
 //
-// Weights come through a ring of asynchronous 16-byte copies that is private
-// to each thread (a thread reads only what it copied: no barrier, and the
-// second product's first chunks are under way before the first has ended).
-// The products run on m16n8k8 MMAs with tf32 operands and f32 sums: 16 rank
-// rows (output rows) by the bucket's eight vectors.  Weights of 8 or 11
-// significant bits are exact in tf32; an f32 value x (t) is taken as hi + lo,
-// x rounded to 11 bits and the exact rest rounded to 11, which is off by 2^-24
-// of it at most, as f32's own roundings are.  One form
-// serves one to eight vectors: with products on the FMA pipe the code for each
-// count, unrolled, missed the instruction cache, and eight vectors were bound
-// by instructions (1000 vectors of prompts: 107 us).  An MMA takes its k
-// indices in any order as long as both operands agree, so a lane's 16 bytes,
-// eight neighbouring k, serve four MMAs as they are.
+// Weights, x and base come through a ring of asynchronous 16-byte copies that
+// is private to each warp: no barrier in either product, and the second
+// product's first chunks are under way before the first has ended.  (x in
+// windows for the whole CTA, each waited for: 27,000 cycles of the first
+// product of a bucket of prompts, against 15,000 now for as many vectors.)
+//
+// The products run on MMAs with 16-bit weights by parts of the f32 values that
+// are exact in the MMA's type (see LoraMul).  One form serves one to eight
+// vectors: with products on the FMA pipe the code for each count, unrolled,
+// missed the instruction cache, and eight vectors were bound by instructions
+// (1000 vectors of prompts: 107 us).  Instructions bound it still: ldmatrix puts
+// the weights into the MMA's registers in their order (moving them there cost
+// a tenth of all instructions), and a copy outside a matrix is left out, not
+// redirected.
 //
 // Measured: 64 vectors, most with an adapter of their own (f16, ranks 16 to 64, 4096
-// to 14336), 63 MB, in 24.3 us: 2.6 TB/s, 0.38 of the copy bandwidth; 1000 vectors of
-// prompts (bf16, rank 32, 14336 to 4096), 94 MB, in 63 us.  Neither DRAM (39 and 15 %) nor issue (38 %)
-// bounds them but each bucket's chain: index, x, first product, exchange through the
-// cluster, second product.  One vector of rank 16, 4096 x 4096: 5.0 us.
+// to 14336), 63 MB, in 21.8 us: 2.9 TB/s, 0.43 of the copy bandwidth; 1000 vectors of
+// prompts (bf16, rank 32, 14336 to 4096), 94 MB, in 33 us: 2.8 TB/s.  One vector of
+// rank 16, 4096 x 4096: 4.9 us.  Half of the issue slots are used in the
+// products; the rest of a bucket's time is its chain: index, first product,
+// exchange through the cluster, second product.
 //
 // Vectors are grouped on the device: in a window of 64 vectors, every
-// eighth vector of an adapter leads a bucket of it and the next ones of that
-// window.  A cluster whose vector leads no bucket has nothing to do.
+// eighth (sixteenth) vector of an adapter leads a bucket of it and the next
+// ones of that window.
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
@@ -52,436 +54,668 @@ struct LoraArgs {
   float* out;
   unsigned* status;
   int64_t ldx, ldb, ldo;
-  int nvec, n, rows, rank, adapters;
+  int nvec, n, rows, rank, adapters, log_cluster;
 };
 
-constexpr int kLoraTokens = 8;    // vectors of a bucket: an MMA's N
 constexpr int kLoraWindow = 64;   // vectors among which buckets form
 constexpr int kLoraThreads = 256, kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraMaxRank = 128;
-constexpr int kLoraStages = 4;    // stages of four 16-byte pieces a thread: 64 KB a CTA, two CTAs an SM
-constexpr int kLoraRing = kLoraStages * 4 * kLoraThreads * 16;
-// x in shared memory: 8192 values of all vectors, each vector's part padded by
-// four so that the lanes' 16-byte reads of two vectors fall into different banks.
-constexpr int kLoraX = 8192, kLoraXBytes = (kLoraX + 4 * kLoraTokens) * 4;
-constexpr int kLoraSmem = kLoraRing + kLoraXBytes;
-static_assert(kLoraWarps * kLoraMaxRank * kLoraTokens * 4 <= kLoraXBytes, "the warps' sums take x's place");
+constexpr int kLoraRound = kLoraWarps * kLoraWindow;  // vectors whose buckets are counted at a time
 
+// N: groups of eight vectors (an MMA's N) of a bucket.  A stage holds, for each
+// thread, four 16-byte pieces of weights and 2 N of x or of base; 96 KB a CTA,
+// two CTAs an SM.
+template <int N>
+struct LoraTile {
+  static constexpr int kTokens = 8 * N, kMaxRank = N == 1 ? 128 : 64, kTiles = kMaxRank / 16;
+  static constexpr int kPieces = 4 + 2 * N, kStages = N == 1 ? 4 : 3;
+  static constexpr int kStage = kPieces * kLoraThreads * 16, kSmem = kStages * kStage;
+};
+
+template <int N>
 struct LoraShared {
-  float mine[kLoraMaxRank][kLoraTokens];               // this CTA's slice of n
-  float t[2][kLoraTokens][kLoraMaxRank + 4];           // all slices, scaled, as hi and lo
-  int token[kLoraTokens];
+  float mine[LoraTile<N>::kTiles * N * 128];                           // this CTA's slice of n: [tile][group][16 ranks][8]
+  __align__(16) unsigned char t[N == 1 ? 8448 : 9216];                 // all slices, scaled, as parts (LoraMul)
+  uint64_t leads[kLoraWarps];                                          // of a round's windows: the vectors that lead buckets
+  int adapter[kLoraRound];                                             // of a round's vectors
+  const float *x[LoraTile<N>::kTokens], *base[LoraTile<N>::kTokens];   // the vectors' slices of the CTA
+  float* out[LoraTile<N>::kTokens];
+  int slot[kLoraWarps];                                                // the ring's free stage, where a warp leaves its sums
   int count;
 };
 
 __device__ __forceinline__ void lora_copy(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p cp.async.cg.shared.global [%0], [%1], 16;\n}" ::"r"(dst), "l"(src),
+               "r"(int(live)) : "memory");
+}
+// The first `bytes` of 16, zeros after them.
+__device__ __forceinline__ void lora_copy_part(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void lora_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void lora_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint4 lora_read(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const float a0, const float a1, const float a2, const float a3,
-                                         const float b0, const float b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
-                 "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+// Four 8 x 8 matrices of 16-bit values, a row of one at the address of each lane.
+__device__ __forceinline__ void lora_matrix(uint32_t src, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src) : "memory");
 }
-// Eight f32 values as hi + lo, both rounded to 11 significant bits.
-__device__ __forceinline__ float round_tf32(float v) {
-  return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u);
-}
-__device__ __forceinline__ void split_tf32(const float (&v)[8], float (&hi)[8], float (&lo)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = round_tf32(v[i]);
-    lo[i] = round_tf32(__fsub_rn(v[i], hi[i]));
-  }
-}
-// sum += 16 rows (row g of the lane's quad and g + 8) x 32 k, eight of them in
-// the lane, by the eight vectors (vector g of the lane's quad in v).  The MMAs
-// cut, not round, their sums, so each 32 k start from zero and are added with
-// rounding (14336 values in one accumulator were off by 2e-6).
+
+// Two tiles of 16 rows of weights by 32 k: [tile][16 k][operand register].
+// A lane has values 8 c + 2 piece and the next one of each eight k, c = 0 to 3, of rows
+// g (its quad) and g + 8; of x and t it has the same k of vector g.
+using LoraWeights = uint32_t[2][2][4];
+
+// How a lane's eight k of x, or of t, stand as parts that are exact in the
+// MMA's operand type, and their product with two tiles of weights.  The MMAs cut, not round, their sums, so each 32 k
+// start from zero, small parts first, and are added with rounding (14336
+// values in one accumulator were off by 2e-6).  The chains of the tiles and
+// vector groups take turns: one after another, each MMA would wait for the last.
 template <class T>
-__device__ __forceinline__ void mma_pieces(float (&sum)[4], const uint4& row, const uint4& row8, const float (&hi)[8],
-                                           const float (&lo)[8]) {
-  float a[8], b[8], c[4] = {0.f, 0.f, 0.f, 0.f};
-  Elem<T>::unpack(row, a);
-  Elem<T>::unpack(row8, b);
-#pragma unroll
-  for (int s = 0; s < 8; s += 2) {
-    mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], lo[s], lo[s + 1]);
-    mma_tf32(c, a[s], b[s], a[s + 1], b[s + 1], hi[s], hi[s + 1]);
+struct LoraMul;
+// Where t has rank value k: each 32 in the order of the lanes that read them.
+__device__ __forceinline__ int lora_place(int k) { return (k & ~31) | (k & 6) << 2 | (k & 24) >> 2 | (k & 1); }
+
+// bf16: three bf16 parts, 8 bits each, hold all of an f32; weights go into the MMA as they are.
+template <>
+struct LoraMul<__nv_bfloat16> {
+  struct X {
+    uint4 part[3];
+  };
+  static __device__ __forceinline__ uint32_t take(float& a, float& b) {  // a bf16 of each, which leaves the rest
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    a = __fsub_rn(a, __uint_as_float(u << 16));
+    b = __fsub_rn(b, __uint_as_float(u & 0xffff0000u));
+    return u;
   }
+  static __device__ __forceinline__ void split(float (&v)[8], X& x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sum[i] = __fadd_rn(sum[i], c[i]);
-}
-
-// A CTA's part of a bucket.  In the first product warp w takes blocks of 32
-// values of n: w, w + 8, ...; a stage is a block of two tiles of 16 rank rows,
-// or (rank up to 16) two blocks of the one tile.  In the second, chunks of 256
-// output rows, 32 a warp, a stage a chunk's next 32 rank values.
-template <class T>
-struct LoraPart {
-  const LoraArgs& a;
-  const T *A, *B;                // the adapter's, from this CTA's first value and first row on
-  int rank, slice, rows;         // rank in use, values of n, rows of this CTA
-  int tiles, pairs, ranks32;     // of 16 rank rows, of two of those (at least 1), of 32 rank values
-  int warp, quad, piece;         // lane / 4 and lane % 4
-  unsigned char* ring;
-  // What the next copies are of: the place in the work, and the lane's first
-  // piece there (moved on by addition: products of 64-bit strides for every
-  // piece were a third of all instructions).
-  int f_block, f_pair = 0, f_chunk = 0, f_k = 0, f_slot = 0;
-  const T *f_a, *f_b;
-
-  __device__ __forceinline__ LoraPart(const LoraArgs& args) : a(args) {}
-
-  // After the members above `f_block` are set.
-  __device__ __forceinline__ void start() {
-    f_block = warp;
-    f_a = A + int64_t(quad) * a.n + warp * 32 + piece * 8;
-    f_b = B + int64_t(warp * 32 + quad * 2) * a.rank + piece * 8;
-  }
-
-  // The next stage's four pieces, in order; past everything an empty group.
-  __device__ __forceinline__ void fetch() {
-    const uint32_t dst = smem_addr(ring) + f_slot * (4 * kLoraThreads * 16) + threadIdx.x * 16;
-    if (f_block * 32 < slice) {
-      const int64_t down8 = int64_t(8) * a.n;
-      // Pieces 2 and 3: the next tile of rank rows, or (one tile) the warp's next block.
-      const int64_t second = tiles <= 1 ? 32 * kLoraWarps : 2 * down8;
-      const int j = f_block * 32 + piece * 8, row = f_pair * 32 + quad;
-      const int j2 = tiles <= 1 ? j + 32 * kLoraWarps : j, row2 = tiles <= 1 ? row : row + 16;
-      const bool in0 = j < slice && row < rank, in1 = j < slice && row + 8 < rank;
-      const bool in2 = j2 < slice && row2 < rank, in3 = j2 < slice && row2 + 8 < rank;
-      lora_copy(dst, in0 ? f_a : A, in0);
-      lora_copy(dst + kLoraThreads * 16, in1 ? f_a + down8 : A, in1);
-      lora_copy(dst + 2 * kLoraThreads * 16, in2 ? f_a + second : A, in2);
-      lora_copy(dst + 3 * kLoraThreads * 16, in3 ? f_a + second + down8 : A, in3);
-      f_a += 4 * down8;
-      if (++f_pair >= pairs) {
-        f_pair = 0;
-        f_a -= pairs * 4 * down8;
-        const int blocks = tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;
-        f_block += blocks, f_a += blocks * 32;
-      }
-    } else if (f_chunk * 256 < rows) {
-      const int row = f_chunk * 256 + warp * 32 + quad * 2;
-      const bool k_in = f_k * 32 + piece * 8 < rank;
-      const T* p = f_b;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows row, row + 16, row + 1, row + 17
-        const bool live = k_in && row + (i & 1) * 16 + (i >> 1) < rows;
-        lora_copy(dst + i * (kLoraThreads * 16), live ? p + ((i & 1) * 16 + (i >> 1)) * a.rank : B, live);
-      }
-      f_b += 32;
-      if (++f_k >= ranks32) {
-        f_k = 0, ++f_chunk;
-        f_b += 256 * int64_t(a.rank) - ranks32 * 32;
-      }
+    for (int i = 0; i < 3; ++i) {
+      x.part[i].x = take(v[0], v[1]);
+      x.part[i].y = take(v[2], v[3]);
+      x.part[i].z = take(v[4], v[5]);
+      x.part[i].w = take(v[6], v[7]);
     }
-    lora_commit();
-    f_slot = (f_slot + 1) % kLoraStages;
   }
-  // Waits for the stage in `slot`.
-  __device__ __forceinline__ void take(int slot, uint4 (&w)[4]) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
+  // t: [part][vector][kRank + 32 bf16], a lane's eight k together, so that two vectors' 64 bytes fall into different banks.
+  template <int kTokens, int kRank>
+  static __device__ __forceinline__ void store(unsigned char* t, int vec, int row, float v) {
+    float none = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(ring + ((slot * 4 + i) * kLoraThreads + threadIdx.x) * 16);
+    for (int i = 0; i < 3; ++i)
+      *reinterpret_cast<uint16_t*>(t + ((i * kTokens + vec) * (kRank + 32) + lora_place(row)) * 2) = uint16_t(take(v, none));
+  }
+  template <int kTokens, int kRank>
+  static __device__ __forceinline__ void load(uint32_t t, int vec, int k, X& x) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x.part[i] = lora_read(t + ((i * kTokens + vec) * (kRank + 32) + k) * 2);
+  }
+  template <int N>
+  static __device__ __forceinline__ void multiply(float (&c)[2][N][4], const LoraWeights& w, const X (&x)[N]) {
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t b0 = s ? x[g].part[i].z : x[g].part[i].x, b1 = s ? x[g].part[i].w : x[g].part[i].y;
+            if (i == 2 && s == 0)
+              asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                           : "=f"(c[h][g][0]), "=f"(c[h][g][1]), "=f"(c[h][g][2]), "=f"(c[h][g][3])
+                           : "r"(w[h][s][0]), "r"(w[h][s][1]), "r"(w[h][s][2]), "r"(w[h][s][3]), "r"(b0), "r"(b1), "f"(0.f));
+            else
+              asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                           : "+f"(c[h][g][0]), "+f"(c[h][g][1]), "+f"(c[h][g][2]), "+f"(c[h][g][3])
+                           : "r"(w[h][s][0]), "r"(w[h][s][1]), "r"(w[h][s][2]), "r"(w[h][s][3]), "r"(b0), "r"(b1));
+          }
   }
 };
 
-// The window of x from value `from` of the slice on: `count` vectors, each
-// `window` values and four of padding apart.
-__device__ __forceinline__ void lora_fetch_x(const LoraArgs& a, const LoraShared& sh, uint32_t xs, int j0, int window, int size) {
-  for (int v = 0; v < sh.count; ++v) {
-    const float* x = a.x + sh.token[v] * a.ldx + j0;
-#pragma unroll 1
-    for (int p = threadIdx.x; p < size / 4; p += kLoraThreads) lora_copy(xs + (v * (window + 4) + p * 4) * 4, x + p * 4, true);
+// f16: two tf32 parts (x rounded to 11 bits, the exact rest rounded to 11: off by 2^-24 of x at most, as
+// f32's own roundings are; f16 has not x's range), the weights as tf32, which holds them.
+template <>
+struct LoraMul<__half> {
+  struct X {
+    float hi[8], lo[8];
+  };
+  static __device__ __forceinline__ float round_tf32(float v) {
+    return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u);
   }
-  lora_commit();
+  static __device__ __forceinline__ void split(float (&v)[8], X& x) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x.hi[i] = round_tf32(v[i]);
+      x.lo[i] = round_tf32(__fsub_rn(v[i], x.hi[i]));
+    }
+  }
+  // t: [hi, lo][vector][kRank + 4 f32].
+  template <int kTokens, int kRank>
+  static __device__ __forceinline__ void store(unsigned char* t, int vec, int row, float v) {
+    float* at = reinterpret_cast<float*>(t) + vec * (kRank + 4) + lora_place(row);
+    at[0] = round_tf32(v);
+    at[kTokens * (kRank + 4)] = round_tf32(__fsub_rn(v, at[0]));
+  }
+  template <int kTokens, int kRank>
+  static __device__ __forceinline__ void load(uint32_t t, int vec, int k, X& x) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const uint4 h = lora_read(t + (vec * (kRank + 4) + k + e) * 4), l = lora_read(t + ((kTokens + vec) * (kRank + 4) + k + e) * 4);
+      x.hi[e] = __uint_as_float(h.x), x.hi[e + 1] = __uint_as_float(h.y), x.hi[e + 2] = __uint_as_float(h.z), x.hi[e + 3] = __uint_as_float(h.w);
+      x.lo[e] = __uint_as_float(l.x), x.lo[e + 1] = __uint_as_float(l.y), x.lo[e + 2] = __uint_as_float(l.z), x.lo[e + 3] = __uint_as_float(l.w);
+    }
+  }
+  template <int N>
+  static __device__ __forceinline__ void multiply(float (&c)[2][N][4], const LoraWeights& w, const X (&x)[N]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      float a[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Elem<__half>::unpack2(w[h][s / 2][s % 2 * 2], a[h][0], a[h][2]);
+        Elem<__half>::unpack2(w[h][s / 2][s % 2 * 2 + 1], a[h][1], a[h][3]);
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float b0 = part ? x[g].hi[2 * s] : x[g].lo[2 * s], b1 = part ? x[g].hi[2 * s + 1] : x[g].lo[2 * s + 1];
+            if (s == 0 && part == 0)
+              asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                           : "=f"(c[h][g][0]), "=f"(c[h][g][1]), "=f"(c[h][g][2]), "=f"(c[h][g][3])
+                           : "r"(__float_as_uint(a[h][0])), "r"(__float_as_uint(a[h][1])), "r"(__float_as_uint(a[h][2])),
+                             "r"(__float_as_uint(a[h][3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(0.f));
+            else
+              asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                           : "+f"(c[h][g][0]), "+f"(c[h][g][1]), "+f"(c[h][g][2]), "+f"(c[h][g][3])
+                           : "r"(__float_as_uint(a[h][0])), "r"(__float_as_uint(a[h][1])), "r"(__float_as_uint(a[h][2])),
+                             "r"(__float_as_uint(a[h][3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+          }
+    }
+  }
+};
+
+// sum += two tiles of rows by 32 k.
+template <class T, int N>
+__device__ __forceinline__ void lora_mma(float (&sum0)[N][4], float (&sum1)[N][4], const LoraWeights& w,
+                                         const typename LoraMul<T>::X (&x)[N]) {
+  float c[2][N][4];
+  LoraMul<T>::template multiply<N>(c, w, x);
+#pragma unroll
+  for (int g = 0; g < N; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum0[g][i] = __fadd_rn(sum0[g][i], c[0][g][i]);
+      sum1[g][i] = __fadd_rn(sum1[g][i], c[1][g][i]);
+    }
 }
 
-// One bucket.  VEC: base and out rows allow 8-byte accesses, rows is even.
-template <class T, bool VEC>
-__device__ __forceinline__ void lora_bucket(const LoraArgs& a, LoraShared& sh, LoraPart<T>& part, int j0, int r0, float scale,
-                                            cg::cluster_group& cluster) {
-  const int quad = part.quad, piece = part.piece, count = sh.count;
-  float* xs = reinterpret_cast<float*>(part.ring + kLoraRing);
-  const int window = kLoraX >> (count <= 1 ? 0 : count <= 2 ? 1 : count <= 4 ? 2 : 3);  // values of a vector
-  lora_fetch_x(a, sh, smem_addr(xs), j0, window, min(window, part.slice));
-#pragma unroll 1
-  for (int i = 0; i < kLoraStages - 1; ++i) part.fetch();
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLoraStages - 1) : "memory");
-  __syncthreads();  // the first window of x
+// A CTA's part of a bucket.  In the first product warp w takes blocks of 32
+// values of n: w, w + 8, ...; a stage is two tiles of 16 rank rows of a block,
+// the block's first with its x.  In the second, chunks of 256 output rows, 32
+// a warp; a stage is a chunk's next 32 rank values, the chunk's first with
+// what its rows are added to.
+template <class T, int N, bool VEC>
+struct LoraPart {
+  using S = LoraTile<N>;
+  const LoraShared<N>& sh;
+  int rank, a_rank, slice, rows; // rank in use, row stride of B, values of n, rows of this CTA
+  int tiles, pairs, ranks32;     // of 16 rank rows, of two of those (at least 1), of 32 rank values
+  int count, warp, lane, quad, piece;  // vectors of the bucket, lane / 4 and lane % 4
+  uint32_t ring;                 // its address in shared memory
+  // What the next copies are of: the place in the work, and the lane's first
+  // piece there (moved on by addition: products of 64-bit strides for every
+  // piece were a third of all instructions).
+  int f_block, f_pair = 0, f_chunk = 0, f_k = 0, f_slot = 0;  // f_slot: the stage's offset
+  const T *f_a, *f_b;
+  int64_t down8, next_block, next_chunk;  // in A: eight rows on, from past a block's rows to the next block; in B
+  uint32_t to, from;                      // the lane's 16 bytes of a weight copy; its row for lora_matrix
 
-  float acc[kLoraMaxRank / 16][4];
+  // After the members above `f_block` are set.
+  __device__ __forceinline__ LoraPart(const LoraShared<N>& shared) : sh(shared) {}
+  __device__ __forceinline__ void start(const T* A, const T* B, int64_t n) {
+    f_block = warp;
+    f_a = A + quad * n + warp * 32 + piece * 8;
+    f_b = B + int64_t(warp * 32 + quad * 2) * a_rank + piece * 8;
+    down8 = 8 * n, next_block = kLoraWarps * 32 - (pairs - 1) * 4 * down8;
+    next_chunk = 256 * int64_t(a_rank) - (ranks32 - 1) * 32;
+    // A row's four 16-byte pieces are moved by half the row, so that eight rows' are in different banks.
+    to = ring + warp * 512 + quad * 64 + ((piece ^ quad >> 1) & 3) * 16;
+    const int r = lane & 7;
+    from = ring + (lane >> 3 & 1) * (kLoraThreads * 16) + warp * 512 + r * 64 + ((lane >> 4 ^ r >> 1) & 3) * 16;
+  }
+
+  // The next stage's pieces, in order; past everything an empty group.  What
+  // lies outside the matrices is not copied: the ring has old values there.
+  __device__ __forceinline__ void fetch() {
+    constexpr int kPiece = kLoraThreads * 16;
+    const uint32_t stage = ring + f_slot, dst = to + f_slot;
+    if (f_block * 32 < slice) {
+      const int left = slice - f_block * 32, ranks = piece * 8 < left ? rank - f_pair * 32 - quad : 0;
+      const T* p = f_a;
 #pragma unroll
-  for (int i = 0; i < kLoraMaxRank / 16; ++i)
+      for (int i = 0; i < 4; ++i, p += down8) lora_copy(dst + i * kPiece, p, ranks > 8 * i);
+      if (f_pair == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  int slot = 0;
-  const auto next_slot = [&]() { slot = (slot + 1) % kLoraStages; };
-  const auto x_piece = [&](int block, float (&hi)[8], float (&lo)[8]) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (quad < count && block * 32 + piece * 8 < part.slice) {
-      const float4* src = reinterpret_cast<const float4*>(xs + quad * (window + 4) + (block * 32) % window + piece * 8);
-      const float4 p = src[0], q = src[1];
-      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-    }
-    split_tf32(v, hi, lo);
-  };
-  const int step = part.tiles <= 1 ? 2 * kLoraWarps : kLoraWarps;  // a window is whole steps
-  int in_window = 0;
+        for (int i = 0; i < 2 * N; ++i) {
+          const int vec = i * 4 + lane / 8;
+          lora_copy(stage + x_place(vec, lane % 8), sh.x[vec] + f_block * 32 + lane % 8 * 4,
+                    lane % 8 * 4 < left && vec < count);
+        }
+      }
+      const bool turn = f_pair + 1 >= pairs;
+      f_a += turn ? next_block : 4 * down8;
+      f_pair = turn ? 0 : f_pair + 1;
+      f_block += turn ? kLoraWarps : 0;
+    } else if (f_chunk * 256 < rows) {
+      const int first = f_chunk * 256 + warp * 32;
+      const int left = f_k * 32 + piece * 8 < rank ? rows - first - quad * 2 : 0;
+      // Rows row, row + 16, row + 1, row + 17 of row = first + 2 quad.
+      lora_copy(dst, f_b, left > 0);
+      lora_copy(dst + kPiece, f_b + 16 * a_rank, left > 16);
+      lora_copy(dst + 2 * kPiece, f_b + a_rank, left > 1);
+      lora_copy(dst + 3 * kPiece, f_b + 17 * a_rank, left > 17);
+      if (f_k == 0) {
+        const int from = first + lane % 8 * 4;
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) {
+          const int vec = i * 4 + lane / 8;
+          if (vec >= count || from >= rows) continue;
+          const uint32_t at = stage + base_place(vec, lane % 8);
+          const float* src = sh.base[vec] + from;
+          if constexpr (VEC) {
+            lora_copy_part(at, src, min(16, (rows - from) * 4));
+          } else {
 #pragma unroll 1
-  for (int b0 = 0; b0 * 32 < part.slice; b0 += step) {  // the whole CTA together; warp w's block is b0 + w
-    if (in_window * 32 == window) {  // the next window of x
-      in_window = 0;
-      __syncthreads();
-      lora_fetch_x(a, sh, smem_addr(xs), j0 + b0 * 32, window, min(window, part.slice - b0 * 32));
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
+            for (int e = 0; e < min(4, rows - from); ++e) lora_copy4(at + e * 4, src + e);
+          }
+        }
+      }
+      const bool turn = f_k + 1 >= ranks32;
+      f_b += turn ? next_chunk : 32;
+      f_k = turn ? 0 : f_k + 1;
+      f_chunk += turn;
     }
-    in_window += step;
-    const int block = b0 + part.warp;
-    if (block * 32 >= part.slice) continue;  // as the copies: nothing is under way for it
-    float hi[8], lo[8];
-    uint4 w[4];
-    if (part.tiles <= 1) {
+    lora_commit();
+    f_slot = after(f_slot);
+  }
+  static __device__ __forceinline__ int after(int slot) {
+    return slot == (S::kStages - 1) * S::kStage ? 0 : slot + S::kStage;
+  }
+  // Waits for the stage at `slot`.
+  __device__ __forceinline__ void take(int slot, LoraWeights& w) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
+    __syncwarp();  // the warp's copies are for all its lanes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = from + slot + h * (2 * kLoraThreads * 16);
+      lora_matrix(at, w[h][0]);
+      lora_matrix(at ^ 32, w[h][1]);
+    }
+  }
+  // Where a stage has values 4 c to 4 c + 3 of a vector's 32, x or base: 128
+  // bytes a vector, so that a copy takes whole lines, in an order in which the
+  // lanes' reads, of four vectors at a time, fall into different banks.
+  __device__ __forceinline__ uint32_t x_place(int vec, int c) const {
+    return (4 + vec / 4) * (kLoraThreads * 16) + warp * 512 + vec % 4 * 128 + (c ^ (vec & 3) * 2) * 16;
+  }
+  __device__ __forceinline__ uint32_t base_place(int vec, int c) const {
+    return (4 + vec / 4) * (kLoraThreads * 16) + warp * 512 + vec % 4 * 128 + (c ^ (vec & 6)) * 16;
+  }
+  // A warp's sums of a tile of 16 ranks by eight vectors, 512 bytes: in its part of the stage that
+  // is free when its first product ends (stage `slot`), beyond that stage's pieces in t's place.
+  __device__ __forceinline__ float* sums(LoraShared<N>& s, unsigned char* pieces, int slot, int w, int tile) const {
+    if (tile < S::kPieces) return reinterpret_cast<float*>(pieces + slot + tile * (kLoraThreads * 16) + w * 512);
+    return reinterpret_cast<float*>(s.t) + (w * (S::kTiles * N - S::kPieces) + tile - S::kPieces) * 128;
+  }
+};
+static_assert(kLoraWarps * (LoraTile<1>::kTiles - LoraTile<1>::kPieces) * 512 <= sizeof(LoraShared<1>::t), "sums");
+static_assert(LoraTile<2>::kTiles * 2 <= LoraTile<2>::kPieces, "sums");
+static_assert(2 * 8 * (128 + 4) * 4 <= sizeof(LoraShared<1>::t) && 3 * 8 * (128 + 32) * 2 <= sizeof(LoraShared<1>::t), "t");
+static_assert(2 * 16 * (64 + 4) * 4 <= sizeof(LoraShared<2>::t) && 3 * 16 * (64 + 32) * 2 <= sizeof(LoraShared<2>::t), "t");
+
+// One bucket.  VEC: base and out rows start on 16 bytes, rows is even.
+template <class T, int N, bool VEC>
+__device__ __forceinline__ void lora_bucket(LoraShared<N>& sh, unsigned char* pieces, LoraPart<T, N, VEC>& part, float scale,
+                                            cg::cluster_group& cluster) {
+  using S = LoraTile<N>;
+  using M = LoraMul<T>;
+  const int quad = part.quad, piece = part.piece, count = part.count;
+#pragma unroll 1
+  for (int i = 0; i < S::kStages - 1; ++i) part.fetch();
+
+  float acc[S::kTiles][N][4];
+#pragma unroll
+  for (int i = 0; i < S::kTiles; ++i)
+#pragma unroll
+    for (int g = 0; g < N; ++g)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][g][j] = 0.f;
+  int slot = 0;
+#pragma unroll 1
+  for (int block = part.warp; block * 32 < part.slice; block += kLoraWarps) {
+    const int left = part.slice - block * 32;
+    typename M::X x[N];
+#pragma unroll 1
+    for (int p = 0; p < part.pairs; ++p) {
+      LoraWeights w;
       part.fetch();
       part.take(slot, w);
-      next_slot();
-      x_piece(block, hi, lo);
-      mma_pieces<T>(acc[0], w[0], w[1], hi, lo);
-      x_piece(block + kLoraWarps, hi, lo);
-      mma_pieces<T>(acc[0], w[2], w[3], hi, lo);
-    } else {
-      x_piece(block, hi, lo);
+      if (left < 32) {  // both operands are zero past the slice, a multiple of 8
 #pragma unroll
-      for (int p = 0; p < kLoraMaxRank / 32; ++p) {
-        if (p >= part.pairs) break;
-        part.fetch();
-        part.take(slot, w);
-        next_slot();
-        mma_pieces<T>(acc[2 * p], w[0], w[1], hi, lo);
-        mma_pieces<T>(acc[2 * p + 1], w[2], w[3], hi, lo);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t& v = w[i >> 1][c >> 1][(c & 1) * 2 + (i & 1)];
+            v = c * 8 < left ? v : 0u;
+          }
       }
+      if (p == 0) {
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+          float f[8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 u = *reinterpret_cast<const float2*>(pieces + slot + part.x_place(g * 8 + quad, 2 * c + piece / 2) + piece % 2 * 8);
+            f[2 * c] = c * 8 < left ? u.x : 0.f, f[2 * c + 1] = c * 8 < left ? u.y : 0.f;
+          }
+          M::split(f, x[g]);
+        }
+      }
+      slot = part.after(slot);
+      // The tiles' sums are registers, so each pair has its own code; the copies' has one place.
+#pragma unroll
+      for (int q = 0; q < S::kTiles / 2; ++q)
+        if (p == q) lora_mma<T, N>(acc[2 * q], acc[2 * q + 1], w, x);
     }
   }
-  // The warps' sums, over the place of x; then in order.
-  __syncthreads();
-  float* sums = xs + part.warp * (kLoraMaxRank * kLoraTokens);
+  // The warps' sums, then in order.
 #pragma unroll
-  for (int i = 0; i < kLoraMaxRank / 16; ++i) {
+  for (int i = 0; i < S::kTiles; ++i) {
     if (i >= part.tiles) break;
-    float* dst = sums + (i * 16 + quad) * kLoraTokens + piece * 2;
-    *reinterpret_cast<float2*>(dst) = make_float2(acc[i][0], acc[i][1]);
-    *reinterpret_cast<float2*>(dst + 8 * kLoraTokens) = make_float2(acc[i][2], acc[i][3]);
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+      float* dst = part.sums(sh, pieces, part.f_slot, part.warp, i * N + g) + quad * 8 + piece * 2;
+      *reinterpret_cast<float2*>(dst) = make_float2(acc[i][g][0], acc[i][g][1]);
+      *reinterpret_cast<float2*>(dst + 64) = make_float2(acc[i][g][2], acc[i][g][3]);
+    }
   }
+  if (part.lane == 0) sh.slot[part.warp] = part.f_slot;
   __syncthreads();
+  const int sums = part.tiles * N * 128;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < part.rank * kLoraTokens; i += kLoraThreads) {
+  for (int i = threadIdx.x; i < sums; i += kLoraThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLoraWarps; ++w) v = __fadd_rn(v, xs[w * (kLoraMaxRank * kLoraTokens) + i]);
-    (&sh.mine[0][0])[i] = v;
+    for (int w = 0; w < kLoraWarps; ++w) v = __fadd_rn(v, part.sums(sh, pieces, sh.slot[w], w, i >> 7)[i & 127]);
+    sh.mine[i] = v;
   }
   cluster.sync();
 #pragma unroll 1
-  for (int i = threadIdx.x; i < part.rank * kLoraTokens; i += kLoraThreads) {
-    float v = 0.f;
-    for (int p = 0; p < int(cluster.num_blocks()); p += 4) {  // four reads at a time; a cluster has 4, 8 or 16 CTAs
-      float s[4];
+  for (int i = threadIdx.x; i < sums; i += kLoraThreads) {
+    const int row = i / (N * 128) * 16 + (i & 127) / 8, vec = (i >> 7) % N * 8 + (i & 7);
+    float s[16], v = 0.f;  // a cluster has up to 16 CTAs: all reads at once, added in order
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] = cluster.map_shared_rank(&sh.mine[0][0], p + k)[i];
+    for (int k = 0; k < 16; ++k) s[k] = vec < count && k < int(cluster.num_blocks()) ? cluster.map_shared_rank(sh.mine, k)[i] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v = __fadd_rn(v, s[k]);
-    }
-    v = __fmul_rn(v, scale);
-    const float hi = round_tf32(v);
-    sh.t[0][i % kLoraTokens][i / kLoraTokens] = hi;
-    sh.t[1][i % kLoraTokens][i / kLoraTokens] = round_tf32(__fsub_rn(v, hi));
+    for (int k = 0; k < 16; ++k) v = __fadd_rn(v, s[k]);
+    v = row < part.rank ? __fmul_rn(v, scale) : 0.f;  // rows past the rank are old values' products
+    M::template store<S::kTokens, S::kMaxRank>(sh.t, vec, row, v);
   }
-  // Rank values past the adapter's, up to a multiple of 32, are zero.
-  for (int i = part.rank + (threadIdx.x >> 4); i < part.ranks32 * 32; i += kLoraThreads / 16)
-    sh.t[threadIdx.x >> 3 & 1][threadIdx.x & 7][i] = 0.f;
-  cluster.sync();  // every CTA has read `mine`, and t is complete
+  // Rank values past the last tile, up to a multiple of 32, are zero.
+  if (part.tiles * 16 < part.ranks32 * 32) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < (part.ranks32 * 32 - part.tiles * 16) * S::kTokens; i += kLoraThreads)
+      M::template store<S::kTokens, S::kMaxRank>(sh.t, i % S::kTokens, part.tiles * 16 + i / S::kTokens, 0.f);
+  }
+  // Others' `mine` has been read; own t is complete.  That this CTA's has been read is waited for at the end.
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // Second product.  A lane's outputs: two neighbouring rows (and the same
-  // eight pairs further on) of vectors 2 piece and 2 piece + 1; what they are
-  // added to is read one chunk ahead.
+  // sixteen rows further on) of vectors 2 piece and 2 piece + 1.
   const int row_lane = part.warp * 32 + quad * 2;
-  const float* in[2];
-  float* out[2];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    const int64_t token = sh.token[2 * piece + v < count ? 2 * piece + v : 0];
-    in[v] = a.base + token * a.ldb + r0 + row_lane;
-    out[v] = a.out + token * a.ldo + r0 + row_lane;
-  }
-  float2 next[2][2];
-  const auto fetch_base = [&](int row0) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = row0 + row_lane + h * 16;
-        next[v][h] = make_float2(0.f, 0.f);
-        if (2 * piece + v >= count || row >= part.rows) continue;
-        const float* src = in[v] + row0 + h * 16;
-        if constexpr (VEC) {
-          next[v][h] = *reinterpret_cast<const float2*>(src);
-        } else {
-          next[v][h].x = src[0];
-          if (row + 1 < part.rows) next[v][h].y = src[1];
-        }
-      }
-  };
-  fetch_base(0);
+  const uint32_t t = smem_addr(sh.t);
 #pragma unroll 1
   for (int row0 = 0; row0 < part.rows; row0 += 256) {
-    float2 base[2][2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) base[v][h] = next[v][h];
-    fetch_base(row0 + 256);
-    float c[2][4] = {};
+    float c[2][N][4] = {};
+    float2 base[2 * N][2];
 #pragma unroll 1
     for (int k = 0; k < part.ranks32; ++k) {
-      uint4 w[4];
+      LoraWeights w;
       part.fetch();
       part.take(slot, w);
-      next_slot();
+      if (k == 0) {
+#pragma unroll
+        for (int u = 0; u < 2 * N; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            base[u][h] = *reinterpret_cast<const float2*>(pieces + slot + part.base_place((u >> 1) * 8 + piece * 2 + (u & 1), h * 4 + quad / 2) +
+                                                          quad % 2 * 8);
+      }
+      slot = part.after(slot);
       // Values past the adapter's rank may be anything: zero, like their t.
-      const int inside = part.rank - k * 32 - piece * 8;
-      if (inside > 0 && inside < 8) {
+      if (k * 32 + 32 > part.rank) {
+        const int inside = part.rank - k * 32 - piece * 2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t* word = reinterpret_cast<uint32_t*>(&w[i]);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            word[e] = inside >= 2 * e + 2 ? word[e] : inside == 2 * e + 1 ? word[e] & 0xffffu : 0u;
-        }
+          for (int i = 0; i < 4; ++i) {
+            uint32_t& v = w[i >> 1][c >> 1][(c & 1) * 2 + (i & 1)];
+            v = inside >= c * 8 + 2 ? v : inside == c * 8 + 1 ? v & 0xffffu : 0u;
+          }
       }
-      float hi[8], lo[8];
+      typename M::X x[N];
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 h4 = *reinterpret_cast<const float4*>(&sh.t[0][quad][k * 32 + piece * 8 + e]);
-        const float4 l4 = *reinterpret_cast<const float4*>(&sh.t[1][quad][k * 32 + piece * 8 + e]);
-        hi[e] = h4.x, hi[e + 1] = h4.y, hi[e + 2] = h4.z, hi[e + 3] = h4.w;
-        lo[e] = l4.x, lo[e + 1] = l4.y, lo[e + 2] = l4.z, lo[e + 3] = l4.w;
-      }
-      mma_pieces<T>(c[0], w[0], w[1], hi, lo);
-      mma_pieces<T>(c[1], w[2], w[3], hi, lo);
+      for (int g = 0; g < N; ++g) M::template load<S::kTokens, S::kMaxRank>(t, g * 8 + quad, k * 32 + piece * 8, x[g]);
+      lora_mma<T, N>(c[0], c[1], w, x);
     }
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
+    for (int u = 0; u < 2 * N; ++u) {
+      const int vec = (u >> 1) * 8 + piece * 2 + (u & 1);
+      if (vec >= count) continue;
+      float* dst = sh.out[vec] + row0 + row_lane;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = row0 + row_lane + h * 16;
-        if (2 * piece + v >= count || row >= part.rows) continue;
-        float* dst = out[v] + row0 + h * 16;
-        const float2 r = make_float2(__fadd_rn(base[v][h].x, c[0][2 * h + v]), __fadd_rn(base[v][h].y, c[1][2 * h + v]));
+        if (row >= part.rows) continue;
+        const float r = __fadd_rn(base[u][h].x, c[0][u >> 1][2 * h + (u & 1)]);
+        const float r1 = __fadd_rn(base[u][h].y, c[1][u >> 1][2 * h + (u & 1)]);
         if constexpr (VEC) {
-          *reinterpret_cast<float2*>(dst) = r;
+          *reinterpret_cast<float2*>(dst + h * 16) = make_float2(r, r1);
         } else {
-          dst[0] = r.x;
-          if (row + 1 < part.rows) dst[1] = r.y;
+          dst[h * 16] = r;
+          if (row + 1 < part.rows) dst[h * 16 + 1] = r1;
         }
       }
+    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-template <class T, bool VEC>
+template <class T, int N, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
-  __shared__ LoraShared sh;
-  extern __shared__ __align__(16) unsigned char ring[];
+  using S = LoraTile<N>;
+  __shared__ LoraShared<N> sh;
+  extern __shared__ __align__(128) unsigned char ring[];
   cg::cluster_group cluster = cg::this_cluster();
   pdl_launch_dependents();
   pdl_wait();
-  const int C = int(cluster.num_blocks()), clusters = int(gridDim.x) / C, c = int(cluster.block_rank());
+  const int log = a.log_cluster, C = 1 << log, clusters = int(gridDim.x) >> log, c = int(blockIdx.x) & (C - 1);
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+  const auto adapter_of = [&](int u) {  // -1: none, -2: past the end
+    if (u >= a.nvec) return -2;
+    const int i = a.index[u];
+    return i >= 0 && i < a.adapters ? i : -1;
+  };
+  // With a cluster for each vector a cluster looks at its own vector.  Else every
+  // CTA counts the buckets, a window a warp, and cluster i takes buckets i, i +
+  // clusters, ... (looking at every so many-th vector cost 8000 cycles a bucket,
+  // and some clusters found two buckets and others none).
+  const bool few = a.nvec <= clusters;
+  const int per_n = ((a.n / 8 + C - 1) >> log) * 8, per_r = (((a.rows + 3) / 4 + C - 1) >> log) * 4;
+  const int j0 = min(a.n, c * per_n), r0 = min(a.rows, c * per_r);
+  int next = few ? 0 : int(blockIdx.x) >> log, seen = 0;
 #pragma unroll 1
-  for (int v = int(blockIdx.x) / C; v < a.nvec; v += clusters) {
-    // Warp 0 looks at the window: which of its vectors have v's adapter.
-    const int raw = a.index[v];
-    const int adapter = raw >= 0 && raw < a.adapters ? raw : -1;
-    const int w0 = v / kLoraWindow * kLoraWindow;
-    if (threadIdx.x < 32) {
-      uint64_t same = 0;
+  for (int from = 0; from < a.nvec; from += kLoraRound) {
+    if (!few) {
+      const int u = from + warp * kLoraWindow + lane;
+      const int lo = adapter_of(u), hi = adapter_of(u + 32);
+      int before = 0;  // vectors of hi's adapter among the window's first 32
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) before += __shfl_sync(0xffffffffu, lo, i) == hi;
+      const uint32_t below = (1u << lane) - 1u;
+      const int lo_nth = __popc(__match_any_sync(0xffffffffu, lo) & below);
+      const int hi_nth = before + __popc(__match_any_sync(0xffffffffu, hi) & below);
+      const uint32_t lo_leads = __ballot_sync(0xffffffffu, lo != -2 && lo_nth % S::kTokens == 0);
+      const uint32_t hi_leads = __ballot_sync(0xffffffffu, hi != -2 && hi_nth % S::kTokens == 0);
+      __syncthreads();  // the last round's are not needed any more
+      if (lane == 0) sh.leads[warp] = uint64_t(hi_leads) << 32 | lo_leads;
+      sh.adapter[warp * kLoraWindow + lane] = lo, sh.adapter[warp * kLoraWindow + 32 + lane] = hi;
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int w = 0; w < (few ? 1 : kLoraWarps) && from + w * kLoraWindow < a.nvec; ++w) {
+      const int own = int(blockIdx.x) >> log;
+      const int w0 = few ? own / kLoraWindow * kLoraWindow : from + w * kLoraWindow;
+      uint64_t leads = !few ? sh.leads[w] : own < a.nvec ? uint64_t(1) << (own - w0) : 0;
+      const int end = seen + __popcll(leads);
+#pragma unroll 1
+      for (; next < end; next += clusters) {
+#pragma unroll 1
+        for (; seen < next; ++seen) leads &= leads - 1;
+        const int v = w0 + __ffsll(int64_t(leads)) - 1;
+        int adapter, near[kLoraWindow / 32];
+        if (few) {  // one round of loads
+          adapter = a.index[v];
 #pragma unroll
-      for (int h = 0; h < kLoraWindow / 32; ++h) {
-        const int u = w0 + h * 32 + int(threadIdx.x);
-        int au = u < a.nvec ? a.index[u] : -2;
-        if (u < a.nvec && (au < 0 || au >= a.adapters)) au = -1;
-        same |= uint64_t(__ballot_sync(0xffffffffu, au == adapter)) << (32 * h);
-      }
-      const int before = __popcll(same & ((uint64_t(1) << (v - w0)) - 1));
-      if (threadIdx.x == 0) {
-        int count = 0;
-        if (before % kLoraTokens == 0) {
-#pragma unroll 1
-          for (uint64_t rest = same >> (v - w0) << (v - w0); rest && count < kLoraTokens; rest &= rest - 1)
-            sh.token[count++] = w0 + __ffsll(int64_t(rest)) - 1;
+          for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = a.index[min(w0 + h * 32 + lane, a.nvec - 1)];
+          adapter = adapter >= 0 && adapter < a.adapters ? adapter : -1;
+#pragma unroll
+          for (int h = 0; h < kLoraWindow / 32; ++h)
+            near[h] = w0 + h * 32 + lane >= a.nvec ? -2 : near[h] >= 0 && near[h] < a.adapters ? near[h] : -1;
+        } else {
+          adapter = sh.adapter[v - from];
+#pragma unroll
+          for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = sh.adapter[w0 - from + h * 32 + lane];
         }
-        sh.count = count;
-        if (raw < -1 || raw >= a.adapters) atomicOr(a.status, kStatusBadIndex);
-      }
-    }
-    __syncthreads();
-    const int count = sh.count;
-    if (count && adapter < 0) {
-      if (a.out != a.base) {
+        const int ranks = adapter >= 0 && a.ranks ? a.ranks[adapter] : a.rank;
+        const float scale = adapter >= 0 && a.scale ? a.scale[adapter] : 1.f;
+        // Warp 0 looks at the window: which of its vectors have v's adapter.
+        if (warp == 0) {
+          uint64_t same = 0;
+#pragma unroll
+          for (int h = 0; h < kLoraWindow / 32; ++h) same |= uint64_t(__ballot_sync(0xffffffffu, near[h] == adapter)) << (32 * h);
+          const int before = __popcll(same & ((uint64_t(1) << (v - w0)) - 1));
+          const uint64_t rest = same >> (v - w0) << (v - w0);
+          // The first kTokens of the rest, each by the lane of its place.
+          const bool lead = before % S::kTokens == 0;
+#pragma unroll
+          for (int h = 0; h < kLoraWindow / 32; ++h) {
+            const int at = h * 32 + lane, nth = __popcll(rest & ((uint64_t(1) << at) - 1));
+            if (lead && (rest >> at & 1) && nth < S::kTokens) {
+              const int64_t token = w0 + at;
+              sh.x[nth] = a.x + token * a.ldx + j0;
+              sh.base[nth] = a.base + token * a.ldb + r0;
+              sh.out[nth] = a.out + token * a.ldo + r0;
+              if (adapter < 0 && a.index[token] != -1) atomicOr(a.status, kStatusBadIndex);
+            }
+          }
+          if (lane == 0) sh.count = lead ? min(S::kTokens, __popcll(rest)) : 0;
+        }
+        __syncthreads();
+        const int count = sh.count, rows = min(a.rows, r0 + per_r) - r0;
+        if (count && adapter < 0) {
+          if (a.out != a.base) {
 #pragma unroll 1
-        for (int i = 0; i < count; ++i)
+            for (int i = 0; i < count; ++i)
 #pragma unroll 1
-          for (int r = c * kLoraThreads + threadIdx.x; r < a.rows; r += C * kLoraThreads)
-            a.out[sh.token[i] * a.ldo + r] = a.base[sh.token[i] * a.ldb + r];
+              for (int r = threadIdx.x; r < rows; r += kLoraThreads) sh.out[i][r] = sh.base[i][r];
+          }
+        } else if (count) {
+          LoraPart<T, N, VEC> part(sh);
+          part.rank = max(0, min(ranks, a.rank)), part.a_rank = a.rank, part.count = count;
+          part.rows = rows;
+          part.tiles = (part.rank + 15) / 16, part.pairs = max(1, (part.tiles + 1) / 2);
+          part.slice = part.rank ? min(a.n, j0 + per_n) - j0 : 0;  // rank 0: no first product
+          part.ranks32 = max(1, (part.rank + 31) / 32);
+          part.warp = warp, part.lane = lane, part.quad = lane >> 2, part.piece = lane & 3;
+          part.ring = smem_addr(ring);
+          part.start(static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n + j0,
+                     static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + r0) * a.rank, a.n);
+          lora_bucket<T, N, VEC>(sh, ring, part, scale, cluster);
+        }
+        __syncthreads();  // sh is free again
       }
-    } else if (count) {
-      LoraPart<T> part(a);
-      const int per_n = (a.n / 8 + C - 1) / C * 8, per_r = ((a.rows + 1) / 2 + C - 1) / C * 2;
-      const int j0 = min(a.n, c * per_n), r0 = min(a.rows, c * per_r);
-      part.rank = a.ranks ? max(0, min(a.ranks[adapter], a.rank)) : a.rank;
-      part.A = static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n + j0;
-      part.B = static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + r0) * a.rank;
-      part.rows = min(a.rows, r0 + per_r) - r0;
-      part.tiles = (part.rank + 15) / 16, part.pairs = max(1, (part.tiles + 1) / 2);
-      part.slice = part.rank ? min(a.n, j0 + per_n) - j0 : 0;  // rank 0: no first product
-      part.ranks32 = max(1, (part.rank + 31) / 32);
-      part.warp = threadIdx.x >> 5, part.quad = (threadIdx.x & 31) >> 2, part.piece = threadIdx.x & 3;
-      part.ring = ring;
-      part.start();
-      lora_bucket<T, VEC>(a, sh, part, j0, r0, a.scale ? a.scale[adapter] : 1.f, cluster);
+      seen = end;
     }
-    __syncthreads();  // sh is free again
+    if (few) break;
   }
 }
 
-template <class T, bool VEC>
-static int launch_lora(const LoraArgs& g, cudaStream_t s) {
+template <class T, int N, bool VEC>
+static int launch_lora(LoraArgs g, int cluster, cudaStream_t s) {
+  using S = LoraTile<N>;
   const char* who = "q1_lora_add launch";
+  const auto kernel = k_lora_add<T, N, VEC>;
   static bool set[64] = {};
   int dev = 0;
   if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (int e = cuda_status(cudaFuncSetAttribute(k_lora_add<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLoraSmem), who))
-      return e;
-    if (int e = cuda_status(cudaFuncSetAttribute(k_lora_add<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
-      return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem), who)) return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who)) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  // Clusters of 16 while all of them run at once (one vector of rank 16, 4096 x
-  // 4096: 5.0 us against 6.2 with 8), of 8 up to 128 vectors (64 of rank 64: 27 us
-  // against 39 with 4), of 4 beyond: fewer CTAs wait for each other (1000 vectors of
-  // prompts: 66 us against 82, 163 of rank 48: 29 against 33).  Their number
-  // is odd: the vectors that lead buckets are every eighth in a prompt, and a
-  // cluster takes every so many-th vector.
-  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : g.nvec <= 128 ? 8 : 4;
-  const int64_t most = (num_sms() - 1) | 1;
-  const dim3 grid(unsigned((g.nvec < most ? g.nvec : most) * cluster));
-  return launch_op(k_lora_add<T, VEC>, grid, kLoraThreads, kLoraSmem, cluster, s, who, g);
+  g.log_cluster = cluster == 16 ? 4 : cluster == 8 ? 3 : 2;
+  // A cluster for each vector where they all run at once, else as many as do.
+  static int most[64][5] = {};
+  int once = dev >= 0 && dev < 64 ? most[dev][g.log_cluster] : 0;
+  if (!once) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(cluster), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(cluster)), cfg.blockDim = dim3(kLoraThreads), cfg.dynamicSmemBytes = S::kSmem;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    if (int e = cuda_status(cudaOccupancyMaxActiveClusters(&once, kernel, &cfg), who)) return e;
+    once = max(once, 1);
+    if (dev >= 0 && dev < 64) most[dev][g.log_cluster] = once;
+  }
+  const dim3 grid(unsigned((g.nvec < once ? g.nvec : once) * cluster));
+  return launch_op(kernel, grid, kLoraThreads, S::kSmem, cluster, s, who, g);
+}
+
+template <class T, bool VEC>
+static int launch_lora(const LoraArgs& g, cudaStream_t s) {
+  // Buckets of sixteen vectors where the prompts are long enough to fill them: 1000
+  // vectors of 6 adapters 33 us against 40.5 with eight, 652 of 17 63 against 72, 379 of
+  // 5 16.2 against 17.6; half filled they cost more (285 of 62: 44 against 33).
+  const bool two = g.nvec > 128 && g.nvec >= 8 * int64_t(g.adapters) && g.rank <= LoraTile<2>::kMaxRank;
+  // The buckets that the vectors can make at most (adapters at random), for the size of the clusters:
+  // 16 CTAs while a cluster for each vector runs at once (one vector of rank 16, 4096
+  // x 4096: 4.8 us against 5.6 with 8), 8 while there are few buckets (64 vectors of 48 adapters: 22 us
+  // against 31 with 4, 88 of 21 16.5 against 17), 4 beyond, where fewer CTAs wait for
+  // each other (338 of 48: 51 us against 79 with 8, 87 of 43 12 against 14.8).
+  int64_t buckets = 0;
+  for (int w = 0; w < g.nvec; w += kLoraWindow) {
+    const int in = min(kLoraWindow, g.nvec - w);
+    buckets += max((in + (two ? 15 : 7)) / (two ? 16 : 8), min(in, g.adapters));
+  }
+  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : buckets <= 48 ? 8 : 4;
+  if (two) return launch_lora<T, 2, VEC>(g, cluster, s);
+  return launch_lora<T, 1, VEC>(g, cluster, s);
 }
 
 }  // namespace q1
@@ -494,7 +728,7 @@ extern "C" int q1_lora_add(const float* x, int64_t ldx, int64_t nvec, int64_t n,
                            int64_t ldo, void* stream) {
   const char* who = "q1_lora_add";
   if (nvec < 1 || nvec > 65535 || n < 8 || n > (int64_t(1) << 24) || n % 8 || rows < 1 || rows > (int64_t(1) << 26) ||
-      adapters < 1 || adapters > (1 << 20) || rank < 8 || rank > kLoraMaxRank || rank % 8)
+      adapters < 1 || adapters > (1 << 20) || rank < 8 || rank > LoraTile<1>::kMaxRank || rank % 8)
     return fail(Q1_ERR_ARG, "%s: bad shape nvec=%lld n=%lld rows=%lld adapters=%lld rank=%lld (n and rank multiples of 8, "
                 "rank in 8..128)", who, (long long)nvec, (long long)n, (long long)rows, (long long)adapters, (long long)rank);
   if (dtype != Q1_BF16 && dtype != Q1_F16) return fail(Q1_ERR_ARG, "%s: bad weight type %d", who, dtype);
@@ -505,10 +739,9 @@ extern "C" int q1_lora_add(const float* x, int64_t ldx, int64_t nvec, int64_t n,
   if (ldx < n || ldb < rows || ldo < rows) return fail(Q1_ERR_ARG, "%s: a row stride is less than its row", who);
   if (base == out && ldb != ldo) return fail(Q1_ERR_ARG, "%s: in place, base and out need the same stride", who);
   LoraArgs g = {x, a, b, index, ranks, scale, base, out, nullptr, ldx, ldb, ldo, int(nvec), int(n), int(rows), int(rank),
-                int(adapters)};
+                int(adapters), 0};
   if (int e = ops_status_ptr(&g.status)) return e;
-  const bool vec = reinterpret_cast<uintptr_t>(base) % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0 && ldb % 2 == 0 &&
-                   ldo % 2 == 0 && rows % 2 == 0;
+  const bool vec = aligned16(base) && aligned16(out) && ldb % 4 == 0 && ldo % 4 == 0 && rows % 2 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == Q1_BF16) return vec ? launch_lora<__nv_bfloat16, true>(g, s) : launch_lora<__nv_bfloat16, false>(g, s);
   return vec ? launch_lora<__half, true>(g, s) : launch_lora<__half, false>(g, s);

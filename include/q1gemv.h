@@ -398,7 +398,7 @@ int q8_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ld
  * adapter i = index[v],
  *   out_v = base_v + scale[i] * (b_i (a_i x_v)),
  * and out_v = base_v where index[v] is -1.
- *   x : f32 [nvec][n], rows ldx apart, finite.  base, out : f32 [nvec][rows], rows ldb
+ *   x : f32 [nvec][n], rows ldx apart, of magnitude below 2^127.  base, out : f32 [nvec][rows], rows ldb
  *     and ldo apart; base may be out (in place).  1 <= nvec <= 65535.
  *   a : [adapters][rank][n], b : [adapters][rows][rank] of `dtype` (Q1_BF16 or
  *     Q1_F16); n and rank multiples of 8, rank in 8..128.

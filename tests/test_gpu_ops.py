@@ -193,6 +193,53 @@ def test_lora_strided_rows_and_bad_index():
     assert binding.device_status() == 2 and binding.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nvec, adapters, run, n, rows, rank", [
+    (129, 16, 1, 520, 301, 24),      # buckets of sixteen, rows that start off 16 bytes
+    (129, 17, 1, 520, 304, 24),      # buckets of eight
+    (1100, 2, 37, 264, 132, 64),     # more than one round of windows
+    (700, 90, 1, 136, 66, 8),        # more buckets than run at once
+    (300, 5, 50, 2056, 516, 72),     # a rank beyond the buckets of sixteen
+    (600, 1, 600, 40, 8, 16),        # slices without values and without rows
+    (140, 3, 140, 1032, 1030, 56),
+])
+def test_lora_many_vectors(nvec, adapters, run, n, rows, rank, dtype):
+    rng = np.random.default_rng(nvec + rank)
+    which = np.repeat(rng.integers(-1, adapters, -(-nvec // run)), run)[:nvec].astype(np.int32)
+    bad = rng.choice(nvec, 3, replace=False)
+    which[bad] = [adapters, -2, 1 << 30]
+    index = torch.from_numpy(which).cuda()
+    ranks = torch.from_numpy(rng.integers(0, rank + 1, adapters).astype(np.int32)).cuda()
+    ranks[0] = rank
+    x, base = normal(33, nvec, n), normal(34, nvec, rows)
+    a, b = normal(35, adapters, rank, n, std=0.05, dtype=dtype), normal(36, adapters, rows, rank, dtype=dtype)
+    for i in range(adapters):
+        a[i, ranks[i]:] = math.nan
+        b[i, :, ranks[i]:] = math.inf
+    scale = normal(37, adapters)
+    got = binding.lora_add(x, a, b, index, scale, ranks=ranks, base=base)
+    assert binding.device_status() == 2 and binding.device_status() == 0
+    want, mag = lora_reference(x, a, b, index, scale, ranks, base)
+    within(got, want, lora_tol(n, mag))
+    none = ((index < 0) | (index >= adapters)).nonzero()[:, 0]
+    assert torch.equal(got[none], base[none])
+    assert torch.equal(got, binding.lora_add(x, a, b, index, scale, ranks=ranks, base=base))
+    binding.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rank", [88, 96, 104, 120, 128])
+def test_lora_high_ranks(rank, dtype):
+    """x of very different sizes, up to 2^100, with ranks beyond a stage's room for sums."""
+    x, base = normal(38, 9, 1416), normal(39, 9, 520)
+    x *= torch.tensor([2.0 ** e for e in (0, 100, -60, 20, -20, 10, 1, 2, 3)], device="cuda")[:, None]
+    a, b = normal(40, 2, rank, 1416, std=0.05, dtype=dtype), normal(41, 2, 520, rank, dtype=dtype)
+    index = torch.tensor([0, 1, 1, 0, 1, 1, 1, 1, 1], dtype=torch.int32, device="cuda")
+    got = binding.lora_add(x, a, b, index, base=base)
+    want, mag = lora_reference(x, a, b, index, None, None, base)
+    within(got, want, lora_tol(1416, mag))
+
+
 # ----------------------------------------------------------------- paged --
 class Cache:
     """A paged cache with random content, random pages and poison wherever no token lies."""
