@@ -26,9 +26,13 @@
 #include <cmath>
 #include <type_traits>
 
+#include <cooperative_groups.h>
+
 #include "attend.cuh"
 
 namespace q1 {
+
+namespace cg = cooperative_groups;
 
 constexpr int kRowsS = 16;   // rows of a tile
 constexpr int kKeysS = 64;   // keys of a unit: 16 for each warp
@@ -80,7 +84,10 @@ constexpr int attend_smem() {
   return kWarpsS * kStagesS * 2 * 16 * D * 2;
 }
 
-template <class T, int D>
+// kCluster: not shares of the axis but a cluster of a.ctas CTAs for each sequence
+// and key head, each with its share of the units, which joins its parts through
+// distributed shared memory: no cursor to find, no second launch.
+template <class T, int D, bool kCluster>
 __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   using Tile = Tiling<kRowsS, kKeysS>;
   constexpr int kRowBytes = D * 2, kChunkBytes = 16 * kRowBytes, kPieces = kRowBytes / 16;  // 16-byte pieces of a row
@@ -88,18 +95,36 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ LocateScratch scratch;
   __shared__ float ml[kWarpsS][16][2];
+  __shared__ float2 own[kRowsS];  // kCluster: the CTA's maxima and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
-  const int64_t total = locate<Tile, kWholeS>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
-  if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
+  int64_t total = 0;
+  if constexpr (kCluster) {
+    const int item = int(blockIdx.x) / ctas;
+    bool bad;
+    cur.b = item / a.kv.kv_heads, cur.h = item - cur.b * a.kv.kv_heads;
+    cur.s = seq_span(a.kv, cur.b, &bad);
+    if (bad && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
+    u0 = 0, u1 = Tile::tiles(a, cur.s);  // tiles, here
+  } else {
+    total = locate<Tile, kWholeS>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+    if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
+  }
   const uint32_t ring = smem_addr(smem) + warp * (kStagesS * 2 * kChunkBytes);
   const int page_mask = (1 << a.kv.page_shift) - 1;
   for (int64_t u = u0; u < u1;) {
-    const int take = int(min(int64_t(cur.units - cur.unit), u1 - u));  // units of this item here
+    int take = 0;  // units of this item here
+    if constexpr (kCluster) {
+      const int c = int(blockIdx.x) % ctas;
+      cur.m = int(u), cur.units = Tile::units(a, cur.s, cur.m);
+      cur.unit = int(share(cur.units, c, ctas)), take = int(share(cur.units, c + 1, ctas)) - cur.unit;
+    } else {
+      take = int(min(int64_t(cur.units - cur.unit), u1 - u));
+    }
     const int keys = Tile::keys(a, cur.s, cur.m);
     const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
     const T* kbase = static_cast<const T*>(a.kv.k) + cur.h * a.kv.head_stride;
@@ -268,7 +293,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     }
     __syncthreads();
     const bool whole = cur.unit == 0 && take == cur.units;
-    if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
+    if (!kCluster && threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
     float* part = partial<kRowsS, D>(a, blockIdx.x, cur.unit == 0);
     for (int i = threadIdx.x; i < 16 * (D / 4); i += kWarpsS * 32) {
       const int r = i / (D / 4), col = i % (D / 4) * 4;
@@ -285,7 +310,10 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
 #pragma unroll
       for (int w = 0; w < kWarpsS; ++w)
         if (ml[w][r][1] != 0.f) l += ml[w][r][1] * ex2(ml[w][r][0] - m);
-      if (whole) {
+      if (kCluster) {  // in place: no other thread reads these
+        *reinterpret_cast<float4*>(joined + r * kLd + col) = v;
+        if (col == 0) own[r] = make_float2(m, l);
+      } else if (whole) {
         const float inv = l > 0.f ? __fdiv_rn(1.0f, l) : 0.f;
         const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
@@ -294,9 +322,44 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         if (col == 0) part[kRowsS * D + r] = m, part[kRowsS * (D + 1) + r] = l;
       }
     }
-    __syncthreads();  // the ring and ml are free again
-    u += take;
-    if (u < u1) next_item<Tile>(a, cur);
+    if constexpr (kCluster) {
+      // Thread p of every ctas threads reads CTA p's part of four columns of a row.
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      const int rows = min(kRowsS, cur.s.count * a.group - cur.m * kRowsS), values = rows * (D / 4);
+      const int p = int(threadIdx.x) % ctas, per = kWarpsS * 32 / ctas;
+      for (int e0 = int(blockIdx.x) % ctas * per; e0 < values; e0 += kWarpsS * 32) {
+        const int e = e0 + int(threadIdx.x) / ctas, r = e / (D / 4), col = e % (D / 4) * 4;
+        float2 his = make_float2(-INFINITY, 0.f);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < values) {
+          his = *cluster.map_shared_rank(own + r, p);
+          v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(joined + r * kLd + col, p));
+        }
+        float m = his.x;
+        for (int off = 1; off < ctas; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float f = his.y != 0.f ? ex2(his.x - (m == -INFINITY ? 0.f : m)) : 0.f;  // a sum that is NaN counts
+        float l = his.y * f;
+        v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+        for (int off = 1; off < ctas; off <<= 1) {
+          l += __shfl_xor_sync(0xffffffffu, l, off);
+          v.x += __shfl_xor_sync(0xffffffffu, v.x, off), v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+          v.z += __shfl_xor_sync(0xffffffffu, v.z, off), v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
+        }
+        int token, head;
+        if (p == 0 && e < values && row_of(a, cur, cur.m * kRowsS + r, token, head)) {
+          const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+          const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
+        }
+      }
+      cluster.sync();  // the parts have been read
+      ++u;
+    } else {
+      __syncthreads();  // the ring and ml are free again
+      u += take;
+      if (u < u1) next_item<Tile>(a, cur);
+    }
   }
 }
 
@@ -310,21 +373,63 @@ static bool many_rows(int64_t max_new, int64_t group, bool one) { return max_new
 
 static int attend_ctas() { return 2 * num_sms(); }
 
+// The CTAs of a cluster for each sequence and key head, which saves the join's
+// launch; 0: shares of the axis and a join.  Clusters want all of them to run
+// at once, rows of one tile and a short table: CTAs a cluster until each has two
+// units at most (32 heads over 8 of 128, one token over 200 keys: 4.9 us with
+// 4, 6.4 with 16, 7.1 by shares; over 500: 5.6, 6.4, 7.6), then as many as fit up
+// to seven units each (4000 keys: 9.0 us with 16 against 9.8; 8191: 12.2 against 11.9;
+// 4 sequences of 2000: 8.6 us with 8 against 12.0, of 8191: 19.9 against 18.8).
 template <class T, int D>
-static int launch_attend(AttendArgs& a, void* workspace, cudaStream_t s) {
+static int attend_cluster(const AttendArgs& a, int64_t max_new, int dev, const char* who, int& ctas) {
+  ctas = 0;
+  const int units = (a.kv.table_tokens + kKeysS - 1) / kKeysS;
+  if (max_new * a.group > kRowsS || units <= kWholeS || units > 7 * 16) return Q1_OK;
+  static int most[64][3] = {};  // clusters of 4, 8, 16 CTAs that run at once
+  for (int i = 0; i < 3; ++i) {
+    int once = dev >= 0 && dev < 64 ? most[dev][i] : 0;
+    if (!once) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = unsigned(4 << i), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(unsigned(4 << i)), cfg.blockDim = dim3(kWarpsS * 32), cfg.dynamicSmemBytes = attend_smem<D>();
+      cfg.attrs = &attr, cfg.numAttrs = 1;
+      if (int e = cuda_status(cudaOccupancyMaxActiveClusters(&once, k_attend<T, D, true>, &cfg), who)) return e;
+      if (dev >= 0 && dev < 64) most[dev][i] = once;
+    }
+    if (int64_t(a.kv.batch) * a.kv.kv_heads > once) break;
+    ctas = 4 << i;
+    if (units <= 2 * ctas) break;
+  }
+  if (units > 7 * ctas) ctas = 0;
+  return Q1_OK;
+}
+
+template <class T, int D>
+static int launch_attend(AttendArgs& a, int64_t max_new, void* workspace, cudaStream_t s) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
   if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (int e = cuda_status(cudaFuncSetAttribute(k_attend<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem<D>()),
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem<D>()),
                             who))
+      return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem<D>()),
+                            who))
+      return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend<T, D, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
       return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
+  if (int e = attend_cluster<T, D>(a, max_new, dev, who, a.ctas)) return e;
+  if (const int ctas = a.ctas)
+    return launch_op(k_attend<T, D, true>, dim3(unsigned(a.kv.batch * a.kv.kv_heads * ctas)), kWarpsS * 32, attend_smem<D>(), ctas, s,
+                     who, a);
   a.ctas = attend_ctas();
   place_workspace(a, workspace);
-  if (int e = launch_op(k_attend<T, D>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
+  if (int e = launch_op(k_attend<T, D, false>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
   // No item has more units than stay whole: nothing to join.
   if (a.kv.table_tokens <= kWholeS * kKeysS) return Q1_OK;
   return launch_op(k_attend_join<T, kRowsS, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
@@ -376,8 +481,8 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   const bool bf = kv->dtype == Q1_BF16;
   a.least_rows = 0, a.most_rows = INT_MAX;
   const auto few = [&] {
-    if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, workspace, s) : launch_attend<__half, 128>(a, workspace, s);
-    return bf ? launch_attend<__nv_bfloat16, 64>(a, workspace, s) : launch_attend<__half, 64>(a, workspace, s);
+    if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, max_new, workspace, s) : launch_attend<__half, 128>(a, max_new, workspace, s);
+    return bf ? launch_attend<__nv_bfloat16, 64>(a, max_new, workspace, s) : launch_attend<__half, 64>(a, max_new, workspace, s);
   };
   if (!many_rows(max_new, a.group, kv->batch == 1)) return few();
   const bool both = kv->batch > 1;

@@ -328,6 +328,26 @@ def test_attend_one_token(length, heads, kv_heads, dim, dtype):
     check_attend(Cache([(1, length)], heads, kv_heads, dim, 16, dtype), heads, dtype, dim)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 8), (16, 1), (32, 8), (36, 12)])
+@pytest.mark.parametrize("width", [4, 8, 17, 40, 110, 200])
+def test_attend_whatever_the_table_holds(width, heads, kv_heads, dim):
+    """The length of the table chooses how the work is split, the lengths do not: short and full
+    sequences in short and long tables, fewer units than a cluster has CTAs, nothing new, several rows."""
+    full = min(width * 64, 7000)
+    for seqs in ([(1, 1)], [(1, full)], [(1, 200), (0, 77), (1, full - 63)], [(0, 9)], [(3, 2), (2, 130)]):
+        c = Cache(seqs, heads, kv_heads, dim, 64, torch.bfloat16, width=width)
+        for max_new in {max(1, max(c.new)), 1}:
+            if c.total:
+                check_attend(c, heads, torch.bfloat16, dim, max_new=max_new)
+            else:
+                q = normal(77, 1, heads, dim, dtype=torch.bfloat16)  # a row of no sequence
+                out = torch.full_like(q, 3.0)
+                binding.paged_attention(q, *c.args(), max_new=max_new, out=out)
+                assert (out == 3).all()
+    assert binding.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("page", [8, 16, 64, 128, 256])
