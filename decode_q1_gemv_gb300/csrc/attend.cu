@@ -15,13 +15,14 @@
 // is taken in f32 before that.
 //
 // Rows past 16 are further tiles (their keys come from L2) up to where the
-// tensor-core kernel is faster, see many_rows.  96 KB of ring a CTA (D = 128) and
+// tensor-core kernel is faster, see attend_cluster and many_rows.  96 KB of ring a CTA (D = 128) and
 // two CTAs an SM hold 29 MB of reads in flight.
 //
 // Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64
 // sequences, 2.04 GB of keys and values, 309 us: 6.6 TB/s, 0.97 of the copy
 // bandwidth; one token over 8191 keys, 34 MB, 11.8 us with its join (5.0 at that
 // bandwidth: finding the share, the pages and the join's launch are the rest).
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -84,8 +85,8 @@ constexpr int attend_smem() {
   return kWarpsS * kStagesS * 2 * 16 * D * 2;
 }
 
-// kCluster: not shares of the axis but a cluster of a.ctas CTAs for each sequence
-// and key head, each with its share of the units, which joins its parts through
+// kCluster: not shares of the axis but a cluster of a.ctas CTAs for each sequence,
+// key head and tile (of a.tiles a key head; more are taken in turn), each with its share of the units, which joins its parts through
 // distributed shared memory: no cursor to find, no second launch.
 template <class T, int D, bool kCluster>
 __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
@@ -104,12 +105,12 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   int ctas = a.ctas;
   int64_t total = 0;
   if constexpr (kCluster) {
-    const int item = int(blockIdx.x) / ctas;
+    const int item = int(blockIdx.x) / ctas, head = item / a.tiles;
     bool bad;
-    cur.b = item / a.kv.kv_heads, cur.h = item - cur.b * a.kv.kv_heads;
+    cur.b = head / a.kv.kv_heads, cur.h = head - cur.b * a.kv.kv_heads;
     cur.s = seq_span(a.kv, cur.b, &bad);
     if (bad && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
-    u0 = 0, u1 = Tile::tiles(a, cur.s);  // tiles, here
+    u0 = item - head * a.tiles, u1 = Tile::tiles(a, cur.s);  // tiles, here
   } else {
     total = locate<Tile, kWholeS>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
     if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         }
       }
       cluster.sync();  // the parts have been read
-      ++u;
+      u += a.tiles;
     } else {
       __syncthreads();  // the ring and ml are free again
       u += take;
@@ -363,7 +364,8 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   }
 }
 
-// Which kernel, from the rows a key head at most (new tokens times the group).
+// Where clusters do not take the call (attend_cluster): which kernel, from the
+// rows a key head at most (new tokens times the group).
 // One sequence: this one up to 32 rows (32 over 4000 keys: 16.4 us against 17.3;
 // 64 over 8000: 26.7 against 23.4).  Several: up to 64 (8 x 64 rows over 3000
 // keys: 21.2 us against 35.6; 16 x 64, mixed lengths: 26.3 against 35.8), since sequences
@@ -373,18 +375,22 @@ static bool many_rows(int64_t max_new, int64_t group, bool one) { return max_new
 
 static int attend_ctas() { return 2 * num_sms(); }
 
-// The CTAs of a cluster for each sequence and key head, which saves the join's
-// launch; 0: shares of the axis and a join.  Clusters want all of them to run
-// at once, rows of one tile and a short table: CTAs a cluster until each has two
-// units at most (32 heads over 8 of 128, one token over 200 keys: 4.9 us with
-// 4, 6.4 with 16, 7.1 by shares; over 500: 5.6, 6.4, 7.6), then as many as fit up
-// to seven units each (4000 keys: 9.0 us with 16 against 9.8; 8191: 12.2 against 11.9;
-// 4 sequences of 2000: 8.6 us with 8 against 12.0, of 8191: 19.9 against 18.8).
+// The CTAs of a cluster for each sequence, key head and tile, which joins its
+// own parts; 0: shares of the axis and a join, or the tensor-core kernel.
+// Clusters want all of them to run at once and a short table: CTAs a cluster
+// until each has two units at most (32 heads over 8 of 128, one token over 200 keys: 4.9
+// us with 4, 6.4 with 16, 7.1 by shares; over 500: 5.6, 6.4, 7.6), then as many as
+// fit up to seven units each (4000 keys: 9.0 us with 16 against 9.8; 8191: 12.2
+// against 11.9; 4 sequences of 2000: 8.6 us with 8 against 12.0, of 8191: 19.9
+// against 18.8).  Further rows are further tiles as long as they fit (32 heads over 8,
+// 16 tokens over 1000 keys: 9.9 us, 20.0 with the tensor-core kernel; 128 tokens of 8 heads: 11.0, 20.8).
+// A table of one or two units wants no join by shares either (3 sequences: 4.9 us).
 template <class T, int D>
-static int attend_cluster(const AttendArgs& a, int64_t max_new, int dev, const char* who, int& ctas) {
+static int attend_cluster(AttendArgs& a, int64_t max_new, int dev, const char* who, int& ctas) {
   ctas = 0;
   const int units = (a.kv.table_tokens + kKeysS - 1) / kKeysS;
-  if (max_new * a.group > kRowsS || units <= kWholeS || units > 7 * 16) return Q1_OK;
+  a.tiles = int(std::min<int64_t>((max_new * a.group + kRowsS - 1) / kRowsS, 1024));
+  if (units > 7 * 16 || (units <= kWholeS && !many_rows(max_new, a.group, a.kv.batch == 1))) return Q1_OK;
   static int most[64][3] = {};  // clusters of 4, 8, 16 CTAs that run at once
   for (int i = 0; i < 3; ++i) {
     int once = dev >= 0 && dev < 64 ? most[dev][i] : 0;
@@ -398,7 +404,7 @@ static int attend_cluster(const AttendArgs& a, int64_t max_new, int dev, const c
       if (int e = cuda_status(cudaOccupancyMaxActiveClusters(&once, k_attend<T, D, true>, &cfg), who)) return e;
       if (dev >= 0 && dev < 64) most[dev][i] = once;
     }
-    if (int64_t(a.kv.batch) * a.kv.kv_heads > once) break;
+    if (int64_t(a.kv.batch) * a.kv.kv_heads * a.tiles > once) break;
     ctas = 4 << i;
     if (units <= 2 * ctas) break;
   }
@@ -407,7 +413,7 @@ static int attend_cluster(const AttendArgs& a, int64_t max_new, int dev, const c
 }
 
 template <class T, int D>
-static int launch_attend(AttendArgs& a, int64_t max_new, void* workspace, cudaStream_t s) {
+static int launch_attend(AttendArgs& a, int64_t max_new, bool only_clusters, void* workspace, cudaStream_t s, bool& ran) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
@@ -423,9 +429,14 @@ static int launch_attend(AttendArgs& a, int64_t max_new, void* workspace, cudaSt
       return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  if (int e = attend_cluster<T, D>(a, max_new, dev, who, a.ctas)) return e;
-  if (const int ctas = a.ctas)
-    return launch_op(k_attend<T, D, true>, dim3(unsigned(a.kv.batch * a.kv.kv_heads * ctas)), kWarpsS * 32, attend_smem<D>(), ctas, s,
+  int ctas = 0;
+  if (only_clusters)
+    if (int e = attend_cluster<T, D>(a, max_new, dev, who, ctas)) return e;
+  ran = ctas || !only_clusters;
+  if (!ran) return Q1_OK;
+  a.ctas = ctas;
+  if (ctas)
+    return launch_op(k_attend<T, D, true>, dim3(unsigned(a.kv.batch * a.kv.kv_heads * a.tiles * ctas)), kWarpsS * 32, attend_smem<D>(), ctas, s,
                      who, a);
   a.ctas = attend_ctas();
   place_workspace(a, workspace);
@@ -480,19 +491,24 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = kv->dtype == Q1_BF16;
   a.least_rows = 0, a.most_rows = INT_MAX;
-  const auto few = [&] {
-    if (kv->dim == 128) return bf ? launch_attend<__nv_bfloat16, 128>(a, max_new, workspace, s) : launch_attend<__half, 128>(a, max_new, workspace, s);
-    return bf ? launch_attend<__nv_bfloat16, 64>(a, max_new, workspace, s) : launch_attend<__half, 64>(a, max_new, workspace, s);
+  bool ran = false;
+  const auto few = [&](bool only_clusters) {
+    if (kv->dim == 128)
+      return bf ? launch_attend<__nv_bfloat16, 128>(a, max_new, only_clusters, workspace, s, ran)
+                : launch_attend<__half, 128>(a, max_new, only_clusters, workspace, s, ran);
+    return bf ? launch_attend<__nv_bfloat16, 64>(a, max_new, only_clusters, workspace, s, ran)
+              : launch_attend<__half, 64>(a, max_new, only_clusters, workspace, s, ran);
   };
-  if (!many_rows(max_new, a.group, kv->batch == 1)) return few();
+  if (int e = few(true)) return e;
+  if (ran) return Q1_OK;
+  if (!many_rows(max_new, a.group, kv->batch == 1)) return few(false);
   const bool both = kv->batch > 1;
   if (both) a.least_rows = kRowsS + 1;
-  bool ran = false;
   if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
   if (!ran) a.least_rows = 0;
   if (!ran || both) {
     if (ran) a.least_rows = 0, a.most_rows = kRowsS;
-    return few();
+    return few(false);
   }
   return Q1_OK;
 }

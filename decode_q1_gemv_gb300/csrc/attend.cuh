@@ -17,7 +17,8 @@ struct AttendArgs {
   int heads, group;        // query heads, and of one key head
   uint32_t group_inverse;  // 2^32 / group + 1 (group > 1), see by_group
   float scale_log2;        // scale * log2(e)
-  int ctas;                // CTAs the units are split over
+  int ctas;                // CTAs the units are split over, or of a cluster
+  int tiles;               // with clusters: of a key head, at once
   int least_rows, most_rows;  // of a sequence that this launch takes (its new tokens times the group)
 };
 

@@ -244,11 +244,13 @@ def test_lora_high_ranks(rank, dtype):
 class Cache:
     """A paged cache with random content, random pages and poison wherever no token lies."""
 
+    least_tokens = 0  # that a row of the table covers
+
     def __init__(self, seqs, heads, kv_heads, dim, page, dtype, layout="token", width=None, seed=40, spare=2):
         self.new, self.len = [s[0] for s in seqs], [s[1] for s in seqs]
         rng = np.random.default_rng(seed)
         need = [-(-n // page) for n in self.len]
-        self.width = width or max(1, max(need))
+        self.width = max(width or max(1, max(need)), -(-self.least_tokens // page))
         pages = sum(need) + spare
         order = rng.permutation(pages).astype(np.int32)
         table = rng.choice(np.array([-5, pages, 1 << 30], dtype=np.int32), (len(seqs), self.width))
@@ -526,6 +528,33 @@ def test_attend_bad_pages_are_not_followed(max_new):
     c.table[1, 3] = 1 << 28
     got = binding.paged_attention(q, *c.args(), max_new=max_new)
     assert binding.device_status() == 2 and torch.equal(got[0], want[0]) and torch.isfinite(got).all()
+
+
+LONG_TABLE = [(test_attend_chunk, (new, length, *heads, dtype))
+              for new, length in [(15, 200), (64, 64), (65, 700), (127, 129), (128, 128), (129, 1025), (257, 300)]
+              for heads in [(4, 1, 128), (2, 2, 64), (5, 1, 128), (8, 1, 64), (3, 1, 64)] for dtype in TYPES]
+LONG_TABLE += [(test_attend_one_token, (length, *heads, dim, torch.bfloat16)) for length in [1, 16, 65, 129, 1000]
+               for heads in [(8, 2), (7, 1)] for dim in [64, 128]]
+LONG_TABLE += [(test_attend_rows_that_see_nothing, (*seq, dim))
+               for seq in [(1, 0), (4, 2), (40, 10), (300, 1), (130, 129)] for dim in [64, 128]]
+LONG_TABLE += [(test_attend_ragged_batch, (64, dim, torch.float16)) for dim in [64, 128]]
+LONG_TABLE += [(test_attend_max_new_is_only_a_hint, (n,)) for n in [1, 40, 4096]]
+LONG_TABLE += [(test_attend_layouts_and_strides, (n,)) for n in [1, 100]]
+LONG_TABLE += [(test_attend_sharp_and_growing_scores, (n,)) for n in [1, 64]]
+LONG_TABLE += [(test_attend_scale_zero, (n,)) for n in [1, 90]]
+LONG_TABLE += [(test_attend_nothing_new, (n,)) for n in [1, 100]]
+LONG_TABLE += [(test_attend_nan_in_a_row_stays_there, (n,)) for n in [1, 40]]
+LONG_TABLE += [(test_attend_repeats_bit_for_bit_and_on_another_stream, n) for n in [(1, 1), (200, 200)]]
+LONG_TABLE += [(test_attend_in_a_graph_with_changing_lengths, ())]
+LONG_TABLE += [(test_attend_bad_pages_are_not_followed, (n,)) for n in [1, 64]]
+
+
+@pytest.mark.parametrize("case", range(len(LONG_TABLE)))
+def test_attend_in_a_long_table(case, monkeypatch):
+    """A table for more tokens than clusters take: the same calls by shares of the keys or on the tensor cores."""
+    monkeypatch.setattr(Cache, "least_tokens", 7300)
+    test, args = LONG_TABLE[case]
+    test(*args)
 
 
 # ------------------------------------------------------------------- rope --
