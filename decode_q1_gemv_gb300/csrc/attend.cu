@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   __shared__ float2 own[kRowsS];  // kCluster: the CTA's maxima and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  pdl_wait();
+  if (!a.beside) pdl_wait();
   Cursor cur = {};
   int64_t u0, u1;
   int ctas = a.ctas;
@@ -362,6 +362,23 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
       if (u < u1) next_item<Tile>(a, cur);
     }
   }
+  if (a.beside) pdl_wait();  // what follows waits for this launch, and with it for the one before
+}
+
+// The joins of a call that ran both kernels, in one launch.
+struct JoinBoth {
+  AttendArgs many, few;
+};
+template <class T, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join_both(const __grid_constant__ JoinBoth a) {
+  __shared__ float sh[kJoinThreads][6];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x, first = a.many.ctas * kTcJoinSlices;
+  if (b < first)
+    join_item<T, kTcRows, D, true>(a.many, b / kTcJoinSlices, b % kTcJoinSlices, kTcJoinSlices, sh);
+  else
+    join_item<T, kRowsS, D, false>(a.few, (b - first) / kJoinSlices, (b - first) % kJoinSlices, kJoinSlices, sh);
 }
 
 // Where clusters do not take the call (attend_cluster): which kernel, from the
@@ -413,7 +430,8 @@ static int attend_cluster(AttendArgs& a, int64_t max_new, int dev, const char* w
 }
 
 template <class T, int D>
-static int launch_attend(AttendArgs& a, int64_t max_new, bool only_clusters, void* workspace, cudaStream_t s, bool& ran) {
+static int launch_attend(AttendArgs& a, int64_t max_new, bool only_clusters, void* workspace, cudaStream_t s, bool& ran,
+                         const AttendArgs* many) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
@@ -443,6 +461,9 @@ static int launch_attend(AttendArgs& a, int64_t max_new, bool only_clusters, voi
   if (int e = launch_op(k_attend<T, D, false>, dim3(unsigned(a.ctas)), kWarpsS * 32, attend_smem<D>(), 1, s, who, a)) return e;
   // No item has more units than stay whole: nothing to join.
   if (a.kv.table_tokens <= kWholeS * kKeysS) return Q1_OK;
+  if (many && many->ctas)
+    return launch_op<JoinBoth>(k_attend_join_both<T, D>, dim3(unsigned(many->ctas * kTcJoinSlices + a.ctas * kJoinSlices)), kJoinThreads, 0, 1, s,
+                               who, {*many, a});
   return launch_op(k_attend_join<T, kRowsS, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
 }
 
@@ -456,8 +477,7 @@ extern "C" int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, 
                 (long long)max_new, (long long)heads, (long long)kv_heads, (long long)dim);
   const int64_t few = attend_workspace(attend_ctas(), kRowsS, int(dim));
   if (!many_rows(max_new, heads / kv_heads, true)) return few;
-  const int64_t many = attend_tc_workspace(int(dim));
-  return few > many ? few : many;
+  return few + attend_tc_workspace(int(dim));  // a call may run both kernels
 }
 
 extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
@@ -492,23 +512,27 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   const bool bf = kv->dtype == Q1_BF16;
   a.least_rows = 0, a.most_rows = INT_MAX;
   bool ran = false;
-  const auto few = [&](bool only_clusters) {
+  const auto few = [&](bool only_clusters, const AttendArgs* many = nullptr) {
     if (kv->dim == 128)
-      return bf ? launch_attend<__nv_bfloat16, 128>(a, max_new, only_clusters, workspace, s, ran)
-                : launch_attend<__half, 128>(a, max_new, only_clusters, workspace, s, ran);
-    return bf ? launch_attend<__nv_bfloat16, 64>(a, max_new, only_clusters, workspace, s, ran)
-              : launch_attend<__half, 64>(a, max_new, only_clusters, workspace, s, ran);
+      return bf ? launch_attend<__nv_bfloat16, 128>(a, max_new, only_clusters, workspace, s, ran, many)
+                : launch_attend<__half, 128>(a, max_new, only_clusters, workspace, s, ran, many);
+    return bf ? launch_attend<__nv_bfloat16, 64>(a, max_new, only_clusters, workspace, s, ran, many)
+              : launch_attend<__half, 64>(a, max_new, only_clusters, workspace, s, ran, many);
   };
   if (int e = few(true)) return e;
   if (ran) return Q1_OK;
   if (!many_rows(max_new, a.group, kv->batch == 1)) return few(false);
+  // Several sequences: those of one tile at most go to the kernel for few rows.  It
+  // starts where the tensor-core kernel's CTAs end, and one launch joins
+  // both's items (a mixed batch: 66 us, 78 one after the other).
   const bool both = kv->batch > 1;
   if (both) a.least_rows = kRowsS + 1;
-  if (int e = launch_attend_tc(a, workspace, bf, int(kv->dim), s, ran)) return e;
-  if (!ran) a.least_rows = 0;
-  if (!ran || both) {
-    if (ran) a.least_rows = 0, a.most_rows = kRowsS;
-    return few(false);
-  }
-  return Q1_OK;
+  AttendArgs many = {};
+  void* second = static_cast<char*>(workspace) + attend_workspace(attend_ctas(), kRowsS, int(kv->dim));
+  if (int e = launch_attend_tc(a, second, bf, int(kv->dim), s, ran, both ? &many : nullptr)) return e;
+  a.least_rows = 0;
+  if (!ran) return few(false);
+  if (!both) return Q1_OK;
+  a.most_rows = kRowsS, a.beside = true;
+  return few(false, &many);
 }

@@ -20,6 +20,7 @@ struct AttendArgs {
   int ctas;                // CTAs the units are split over, or of a cluster
   int tiles;               // with clusters: of a key head, at once
   int least_rows, most_rows;  // of a sequence that this launch takes (its new tokens times the group)
+  bool beside;             // the launch before is the same call's, of other sequences
 };
 
 // n / group, 0 <= n < 2^31: n * (2^32 / group + 1) / 2^32 is the quotient or
@@ -204,9 +205,9 @@ constexpr int kJoinGroups = 8;   // threads that share a value's parts, at most
 constexpr int kJoinHeld = 4;     // parts whose weights a thread holds
 
 // The join of up to kJoinHeld column-by-column partials: a thread takes a row,
-// the y CTAs share out the columns in fours.
+// the slices share out the columns in fours.
 template <class T, int TM, int D>
-__device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& it) {
+__device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& it, int cta, int slice, int slices) {
   static_assert(TM == kJoinThreads, "a row a thread");
   const int r = threadIdx.x;
   if (r >= it.count * a.group - it.tile * TM) return;
@@ -214,7 +215,7 @@ __device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& i
   float pm[kJoinHeld], pl[kJoinHeld];
 #pragma unroll
   for (int p = 0; p < kJoinHeld; ++p) {
-    part[p] = partial<TM, D>(a, blockIdx.x + (p < it.parts ? p : 0), p == 0 || p >= it.parts) + r;
+    part[p] = partial<TM, D>(a, cta + (p < it.parts ? p : 0), p == 0 || p >= it.parts) + r;
     pm[p] = p < it.parts ? part[p][TM * D] : -INFINITY;
     pl[p] = p < it.parts ? part[p][TM * (D + 1)] : 0.f;
   }
@@ -228,7 +229,7 @@ __device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& i
   const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
   const int row = it.tile * TM + r, t = by_group(a, row), head = it.head * a.group + row - t * a.group;
   T* out = static_cast<T*>(a.out) + (it.first + t) * a.o_token + head * a.o_head;
-  for (int col = blockIdx.y * 4; col < D; col += gridDim.y * 4) {
+  for (int col = slice * 4; col < D; col += slices * 4) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < kJoinHeld; ++p)
@@ -241,22 +242,19 @@ __device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& i
   }
 }
 
-// Joins the items that were split: blockIdx.x is the CTA where the item
-// begins, the y CTAs share its values.  A thread takes four columns of a row;
+// Joins an item that was split: `cta` is where the item begins, the slices
+// share its values.  A thread takes four columns of a row;
 // up to eight of them share out the parts, so that a long row of parts (one
 // token over a long cache) costs few dependent reads.  Parts are added in a fixed order.
 template <class T, int TM, int D, bool Turned>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
-  __shared__ float sh[kJoinThreads][6];
-  pdl_launch_dependents();
-  pdl_wait();
-  const JoinItem it = a.joins[blockIdx.x];
+__device__ __forceinline__ void join_item(const AttendArgs& a, int cta, int slice, int slices, float (&sh)[kJoinThreads][6]) {
+  const JoinItem it = a.joins[cta];
   if (it.parts == 0) return;
   if constexpr (Turned) {
     // Few parts of many rows (a chunk of 2048 tokens: 351 us this way, 360 the other;
     // 20 tokens over 30000 keys, 19 parts: 51 and 46).
     if (it.parts <= kJoinHeld) {
-      join_rows<T, TM, D>(a, it);
+      join_rows<T, TM, D>(a, it, cta, slice, slices);
       return;
     }
   }
@@ -264,7 +262,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
   while (groups < kJoinGroups && groups * 2 <= it.parts) groups *= 2;
   const int width = kJoinThreads / groups, g = threadIdx.x / width;
   const int rows = min(TM, it.count * a.group - it.tile * TM), values = rows * (D / 4);
-  for (int base = blockIdx.y * width; base < values; base += gridDim.y * width) {
+  for (int base = slice * width; base < values; base += slices * width) {
     const int e = base + threadIdx.x % width;
     const int r = Turned ? e % rows : e / (D / 4), col = (Turned ? e / rows : e % (D / 4)) * 4;
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) po[i][k] = 0.f;
           if (p < it.parts) {
-            const float* src = partial<TM, D>(a, blockIdx.x + p, p == 0);
+            const float* src = partial<TM, D>(a, cta + p, p == 0);
             pm[i] = src[TM * D + r], pl[i] = src[TM * (D + 1) + r];
             if constexpr (Turned) {
 #pragma unroll
@@ -325,7 +323,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
   }
 }
 
-// Bytes of a call's workspace: the join items, then two partials a CTA.
+template <class T, int TM, int D, bool Turned>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
+  __shared__ float sh[kJoinThreads][6];
+  pdl_launch_dependents();
+  pdl_wait();
+  join_item<T, TM, D, Turned>(a, blockIdx.x, blockIdx.y, gridDim.y, sh);
+}
+
+// Bytes of a launch's workspace: the join items, then two partials a CTA.
 inline int64_t attend_workspace(int ctas, int tm, int dim) {
   return int64_t(ctas) * sizeof(JoinItem) + int64_t(2) * ctas * tm * (dim + 2) * 4;
 }
@@ -335,7 +341,9 @@ inline void place_workspace(AttendArgs& a, void* workspace) {
 }
 
 // attend_tc.cu: the kernel for many rows, its workspace in bytes.
+// Split items are joined by it, or (`joined` given and its CTAs not 0) by the caller, with those arguments.
+constexpr int kTcRows = 256, kTcJoinSlices = 16;  // rows of an item; CTAs that join it
 int64_t attend_tc_workspace(int dim);
-int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran);
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined);
 
 }  // namespace q1

@@ -57,6 +57,7 @@ namespace q1 {
 
 constexpr int kTcM = 128;            // rows of a tile
 constexpr int kTcItem = 2 * kTcM;    // rows of an item
+static_assert(kTcItem == kTcRows, "");
 constexpr int kTcKeys = 128;         // keys of a unit
 constexpr int kTcSoftWarps = 16;     // softmax warps: two a 32-row quarter of a tile
 constexpr int kTcAThreads = (kTcSoftWarps + 4) * 32;
@@ -75,7 +76,6 @@ __device__ __forceinline__ void regs_up() {
 // Units of an item that is not split (a mixed batch: 80.6 us with 8, 85.2 with 4,
 // 80.4 with 12; 16 sequences of up to 72 tokens: 49.0, 49.0, 55.4).
 constexpr int kTcWhole = 8;
-constexpr int kTcJoinSlices = 16;    // CTAs that join an item
 constexpr float kTcGrow = 8.f;       // log2 units a maximum may be behind
 
 struct AttendTcArgs {
@@ -217,8 +217,10 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  pdl_launch_dependents();
+  // In this order: the next launch may go on without waiting for this one (`beside`), and
+  // then relies on what was before it.
   pdl_wait();
+  pdl_launch_dependents();
 
   Cursor cur = {};
   int64_t u0, u1;
@@ -649,7 +651,7 @@ static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base
 int64_t attend_tc_workspace(int dim) { return attend_workspace(num_sms(), kTcItem, dim); }
 
 template <class T, int D>
-static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
+static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s, AttendArgs* joined) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
@@ -664,12 +666,16 @@ static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s) {
     return e;
   // No item has more units than stay whole: nothing to join.
   if (g.a.kv.table_tokens <= kTcWhole * kTcKeys) return Q1_OK;
+  if (joined) {
+    *joined = g.a;
+    return Q1_OK;
+  }
   return launch_op(k_attend_join<T, kTcItem, D, true>, dim3(unsigned(g.a.ctas), kTcJoinSlices), kJoinThreads, 0, 1, s, who,
                    g.a);
 }
 
 // False in `ran` where no tensor map can describe the cache's strides.
-int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran) {
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined) {
   AttendTcArgs g = {};
   g.a = a;
   g.a.ctas = num_sms();
@@ -684,8 +690,8 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, c
         encode_map(&g.v, bf16, a.kv, a.kv.v, dim, g.box_keys, axis) == CUDA_SUCCESS;
   if (!ran) return Q1_OK;
   g.axis_head = axis[0], g.axis_slot = axis[1], g.axis_page = axis[2];
-  if (dim == 128) return bf16 ? launch_tc_kernel<__nv_bfloat16, 128>(g, s) : launch_tc_kernel<__half, 128>(g, s);
-  return bf16 ? launch_tc_kernel<__nv_bfloat16, 64>(g, s) : launch_tc_kernel<__half, 64>(g, s);
+  if (dim == 128) return bf16 ? launch_tc_kernel<__nv_bfloat16, 128>(g, s, joined) : launch_tc_kernel<__half, 128>(g, s, joined);
+  return bf16 ? launch_tc_kernel<__nv_bfloat16, 64>(g, s, joined) : launch_tc_kernel<__half, 64>(g, s, joined);
 }
 
 }  // namespace q1
