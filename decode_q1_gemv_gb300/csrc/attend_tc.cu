@@ -35,7 +35,7 @@
 //
 // Measured (32 heads over 8 of 128, bf16): 2048 new tokens over 16001 keys, 0.503
 // Tflop, in 351 us with the join: 1.43 Pflop/s, 0.76 of this card's matrix product
-// rate (1.88); the tensor pipe is active 64 % of the cycles (profiled launch, 343 us).
+// rate (1.88); the tensor pipe is active 64 % of the cycles (profiled launch, 342 us).
 // What is left: with D = 128 the two tiles fill tensor memory, so a tile's scores,
 // softmax and product with V follow each other, and two tiles hide each other's only in
 // part.  With D = 64 the softmax bounds it: its arithmetic alone takes 346 cycles a
@@ -73,8 +73,8 @@ template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// Units of an item that is not split (a mixed batch: 80.6 us with 8, 85.2 with 4,
-// 80.4 with 12; 16 sequences of up to 72 tokens: 49.0, 49.0, 55.4).
+// Units of an item that is not split (a mixed batch: 66.4 us with 8, 71.4 with 4,
+// 66.7 with 12; 16 sequences of up to 72 tokens: 36.8, 36.9, 43.5).
 constexpr int kTcWhole = 8;
 constexpr float kTcGrow = 8.f;       // log2 units a maximum may be behind
 
