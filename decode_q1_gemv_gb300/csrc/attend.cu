@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join_both(const __grid_
 // keys: 21.2 us against 35.6; 16 x 64, mixed lengths: 26.3 against 35.8), since sequences
 // of up to 16 rows among others with more are this kernel's too, in a launch
 // of their own: a tile of 128 rows costs the same however few are in use.
-static bool many_rows(int64_t max_new, int64_t group, bool one) { return max_new * group > (one ? 32 : 64); }
+static bool many_rows(int64_t max_new, int64_t group, bool one) { return max_new > (one ? 32 : 64) / group; }
 
 static int attend_ctas() { return 2 * num_sms(); }
 
@@ -509,6 +509,7 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   a.q = q, a.out = out, a.q_token = q_token_stride, a.q_head = q_head_stride;
   a.o_token = out_token_stride, a.o_head = out_head_stride;
   if (int e = ops_status_ptr(&a.status)) return e;
+  max_new = std::min<int64_t>(max_new, a.kv.total_new);
   a.heads = int(heads), a.group = int(heads / kv->kv_heads);
   a.group_inverse = uint32_t((uint64_t(1) << 32) / uint64_t(a.group) + 1);
   a.scale_log2 = scale * 1.4426950408889634f;

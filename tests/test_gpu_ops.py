@@ -386,6 +386,41 @@ def test_attend_rows_that_see_nothing(new, length, dim):
     assert empty.shape[0] == new - length and (empty == 0).all()
 
 
+@pytest.mark.parametrize("width", [None, 500])
+@pytest.mark.parametrize("max_new", [1 << 40, (1 << 63) - 1])
+def test_attend_max_new_beyond_any_sequence(max_new, width):
+    c = Cache([(1, 100), (40, 333), (7, 50)], 8, 2, 64, 16, torch.float16, width=width)
+    check_attend(c, 8, torch.float16, 64, max_new=max_new)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_mixed_calls_one_after_another(dim):
+    """Calls of short and long sequences back to back on one workspace, in a graph: each starts before the
+    one before it has ended, and none may see the other's parts or outputs."""
+    heads, calls = 16, 12
+    cs = [Cache([(200, 1500), (1, 900), (3, 2500), (130, 131), (16, 40)], heads, 4, dim, 32, torch.bfloat16, seed=90 + i,
+                width=250) for i in range(3)]
+    qs = [normal(95 + i, cs[0].total, heads, dim, dtype=torch.bfloat16) for i in range(3)]
+    ws = torch.empty(binding.paged_attention_workspace(200, heads, 4, dim), dtype=torch.uint8, device="cuda")
+    want = [binding.paged_attention(q, *c.args(), max_new=200) for q, c in zip(qs, cs)]
+    for q, c, w in zip(qs, cs, want):
+        ref = attend_reference(c, q, dim ** -0.5)
+        within(w, ref[0], attend_tol(c, q, *ref))
+    outs = [torch.empty_like(qs[0]) for _ in range(calls)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in range(calls):
+            binding.paged_attention(qs[i % 3], *cs[i % 3].args(), max_new=200, out=outs[i], workspace=ws)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(7.0)
+        g.replay()
+        for i, o in enumerate(outs):
+            assert torch.equal(o, want[i % 3])
+    assert binding.device_status() == 0
+
+
 @pytest.mark.parametrize("max_new", [1, 40, 4096])
 def test_attend_max_new_is_only_a_hint(max_new):
     c = Cache([(1, 100), (40, 333), (7, 50)], 8, 2, 128, 16, torch.bfloat16)
