@@ -9,8 +9,8 @@
 // threads for the sequence, then two dependent loads.
 //
 // Measured: 5751 tokens of seven prompts (32 + 8 + 8 heads of 64, 107 MB) in
-// 18.5 us: 5.8 TB/s, 0.86 of the copy bandwidth.  64 single tokens (heads of 128):
-// 2.6 us a launch; while there are fewer tokens than SMs, several CTAs share a token's units.
+// 16.4 us: 6.5 TB/s, 0.96 of the copy bandwidth.  64 single tokens (heads of 128):
+// 2.5 us a launch; while there are fewer tokens than SMs, several CTAs share a token's units.
 #include "paged.cuh"
 
 namespace q1 {
@@ -23,10 +23,13 @@ struct RopeArgs {
   void* q_out;
   unsigned* status;
   int heads, dim, rot, positions, interleaved;
-  int units_head, units;  // units of 8 values: of a head, of a token's q, k and v
+  int shift, units;  // units of 8 values: log2 of a head's, of a token's q, k and v
 };
 
-constexpr int kRopeThreads = 256;
+// 5751 tokens of 384 units: 16.4 us with 128 threads, 17.6 with 64, 16.5 with 96,
+// 16.9 with 192, 17.8 with 256; loading a thread's first values before the
+// token's place is known took 50 registers and 20.9.
+constexpr int kRopeThreads = 128;
 
 // One CTA takes a token (or a part of its units, blockIdx.y); a unit is 8
 // values of one head: with half-split rotation 4 of the first and the same 4
@@ -54,11 +57,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_append(RopeArgs a) {
   if (owned && !good && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadIndex);
   const int64_t slot = int64_t(page) * kv.page_stride + int64_t(pos & ((1 << kv.page_shift) - 1)) * kv.slot_stride;
 
-  const int qunits = a.heads * a.units_head, kunits = kv.kv_heads * a.units_head;
+  const int qunits = a.heads << a.shift, kunits = kv.kv_heads << a.shift;
   for (int u = blockIdx.y * kRopeThreads + threadIdx.x; u < a.units; u += gridDim.y * kRopeThreads) {
     const int part = u < qunits ? 0 : u < qunits + kunits ? 1 : 2;
     const int v = part == 0 ? u : part == 1 ? u - qunits : u - qunits - kunits;
-    const int head = v / a.units_head, unit = v - head * a.units_head;
+    const int head = v >> a.shift, unit = v & ((1 << a.shift) - 1);
     const float* src = part == 0 ? a.q + token * a.ldq : part == 1 ? a.k + token * a.ldk : a.v + token * a.ldv;
     src += head * a.dim;
     T* dst;
@@ -156,8 +159,8 @@ extern "C" int q1_rope_append(const float* q, int64_t ldq, const float* k, int64
   if (int e = ops_status_ptr(&a.status)) return e;
   a.heads = int(heads), a.dim = int(kv->dim), a.rot = int(rot), a.positions = int(positions);
   a.interleaved = interleaved != 0;
-  a.units_head = a.dim / 8;
-  a.units = (a.heads + 2 * a.kv.kv_heads) * a.units_head;
+  a.shift = a.dim == 64 ? 3 : 4;
+  a.units = (a.heads + 2 * a.kv.kv_heads) << a.shift;
   const int per = (a.units + kRopeThreads - 1) / kRopeThreads;
   const dim3 grid(unsigned(a.kv.total_new), unsigned(a.kv.total_new < num_sms() ? per : 1));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
