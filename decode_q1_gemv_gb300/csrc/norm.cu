@@ -8,8 +8,8 @@
 // groups, so a q8_0 block of 32 values is 8 (f32) or 4 (16-bit) neighbouring
 // lanes and its maximum costs 3 or 2 shuffles, as in quant.cu.
 //
-// Measured: 8191 rows of 4128 f32 values with residual, 442 MB, in 70.7 us: 6.25 TB/s,
-// 0.92 of the copy bandwidth of the card (6.78 TB/s).  One row of 4096 takes 2.6 us a
+// Measured: 8191 rows of 4128 f32 values with residual, 442 MB, in 67.8 us: 6.5 TB/s,
+// 0.96 of the copy bandwidth of the card (6.78 TB/s).  One row of 4096 takes 2.6 us a
 // launch in a chain of them, 64 bf16 rows 2.4 us: the launch and one round of
 // loads, not bytes.
 //
@@ -199,22 +199,32 @@ __global__ void __launch_bounds__(1024) k_add_rms_norm_long(NormArgs a) {
   }
 }
 
-// Threads a row, from n and the type alone: one group of 16 bytes each up to
-// 256, then 256 with up to six groups in registers, then more threads.
+// Threads a row, from n and the type alone (not from the rows: their bits
+// must not depend on the batch): two groups of 16 bytes a thread up to 256
+// groups, three where that leaves fewer threads idle (8191 rows of 2048 bf16:
+// 21.5 us against 26.2 with one, of 1024 f32 17.6 against 19.9, of 768 bf16 9.6
+// against 11.0), then 256 threads of up to six groups, each count a form of its
+// own (8191 x 4128 f32: 67.8 us with five, 71.9 in the form for six; 8000 x 5120
+// bf16: 51.3 with three, 66.5 in the form for four), then 384 (4096 x 14336
+// bf16: 74 us, 93 with 512; one row 4.5 and 4.8), then 1024 (14336 f32: 64 rows
+// 5.1 us, 7.3 with 512; 2000 rows 71.5 and 67).
 template <class T>
 static int launch_norm(const NormArgs& a, int64_t nvec, bool vec, cudaStream_t s) {
   constexpr int G = Elem<T>::kGroup;
   const char* who = "q8_add_rms_norm launch";
   const int groups = (a.n + G - 1) / G;
-  int threads = groups <= 256 ? (groups + 31) / 32 * 32 : 256;
-  while (threads < 1024 && groups > 6 * threads) threads *= 2;
+  const auto each = [&](int k) { return (groups + 32 * k - 1) / (32 * k) * 32; };  // threads of k groups
+  int threads = groups > 6 * 384 ? 1024 : groups > 6 * 256 ? 384 : 256;
+  if (groups <= 256) threads = 3 * each(3) < 2 * each(2) ? each(3) : each(2);
   const int k = (groups + threads - 1) / threads;
   const dim3 grid{unsigned(nvec)};
   if (!vec) return launch_op(k_add_rms_norm_long<T, false>, grid, threads, 0, 1, s, who, a);
-  if (k <= 1) return launch_op(k_add_rms_norm<T, 1>, grid, threads, 0, 1, s, who, a);
-  if (k <= 2) return launch_op(k_add_rms_norm<T, 2>, grid, threads, 0, 1, s, who, a);
-  if (k <= 4) return launch_op(k_add_rms_norm<T, 4>, grid, threads, 0, 1, s, who, a);
-  if (k <= 6) return launch_op(k_add_rms_norm<T, 6>, grid, threads, 0, 1, s, who, a);
+  if (k == 1) return launch_op(k_add_rms_norm<T, 1>, grid, threads, 0, 1, s, who, a);
+  if (k == 2) return launch_op(k_add_rms_norm<T, 2>, grid, threads, 0, 1, s, who, a);
+  if (k == 3) return launch_op(k_add_rms_norm<T, 3>, grid, threads, 0, 1, s, who, a);
+  if (k == 4) return launch_op(k_add_rms_norm<T, 4>, grid, threads, 0, 1, s, who, a);
+  if (k == 5) return launch_op(k_add_rms_norm<T, 5>, grid, threads, 0, 1, s, who, a);
+  if (k == 6) return launch_op(k_add_rms_norm<T, 6>, grid, threads, 0, 1, s, who, a);
   return launch_op(k_add_rms_norm_long<T, true>, grid, threads, 0, 1, s, who, a);
 }
 
