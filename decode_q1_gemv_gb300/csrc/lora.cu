@@ -180,29 +180,27 @@ struct LoraMul<__nv_bfloat16> {
   }
 };
 
-// f16: two tf32 parts (x rounded to 11 bits, the exact rest rounded to 11: off by 2^-24 of x at most, as
-// f32's own roundings are; f16 has not x's range), the weights as tf32, which holds them.
+// f16: two tf32 parts (x rounded to 11 bits, the exact rest cut to 11: of its 12 bits at most the last may go,
+// 2^-23 of x, twice f32's own rounding; f16 has not x's range), the weights as tf32, which holds them.
+// A NaN stays one: hi may lose it (0x7fffffff + 0x1000 is -0), the rest is arithmetic, and cut.
 template <>
 struct LoraMul<__half> {
   struct X {
     float hi[8], lo[8];
   };
-  static __device__ __forceinline__ float round_tf32(float v) {
-    return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u);
+  static __device__ __forceinline__ void take(float v, float& hi, float& lo) {
+    hi = __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u);
+    lo = __uint_as_float(__float_as_uint(__fsub_rn(v, hi)) & 0xffffe000u);
   }
   static __device__ __forceinline__ void split(float (&v)[8], X& x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x.hi[i] = round_tf32(v[i]);
-      x.lo[i] = round_tf32(__fsub_rn(v[i], x.hi[i]));
-    }
+    for (int i = 0; i < 8; ++i) take(v[i], x.hi[i], x.lo[i]);
   }
   // t: [hi, lo][vector][kRank + 4 f32].
   template <int kTokens, int kRank>
   static __device__ __forceinline__ void store(unsigned char* t, int vec, int row, float v) {
     float* at = reinterpret_cast<float*>(t) + vec * (kRank + 4) + lora_place(row);
-    at[0] = round_tf32(v);
-    at[kTokens * (kRank + 4)] = round_tf32(__fsub_rn(v, at[0]));
+    take(v, at[0], at[kTokens * (kRank + 4)]);
   }
   template <int kTokens, int kRank>
   static __device__ __forceinline__ void load(uint32_t t, int vec, int k, X& x) {

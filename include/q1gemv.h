@@ -405,6 +405,8 @@ int q8_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ld
  *   index : int32 [nvec].  ranks : int32 [adapters] or NULL: the ranks in use
  *     (0..rank) of each adapter; what lies past them is not used and may hold
  *     anything.  scale : f32 [adapters] or NULL (1).
+ * A value of x, or of a weight within the rank, that is no number makes what
+ * it goes into no number (an infinite one NaN or infinite), and nothing else.
  * x, a and b must be 16-byte aligned, ldx a multiple of 4.  An index outside
  * -1..adapters-1 counts as -1 and sets the status bit. */
 int q1_lora_add(const float *x, int64_t ldx, int64_t nvec, int64_t n, int64_t rows, const void *a, const void *b,

@@ -1,0 +1,92 @@
+"""The operators between the products where inputs are not ordinary: values that
+are no numbers, streams of the caller's, rows and axes of one entry, long sums,
+caches past 32-bit offsets in every form of the attention.  Plain forms and
+tolerances are those of test_gpu_ops.py where nothing else is said."""
+import math
+
+import pytest
+import torch
+
+from decode_q1_gemv_gb300 import binding
+from tests.test_gpu_ops import normal
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.bfloat16, torch.float16]
+# The NaN that the GPU's arithmetic gives, the host's, and the largest patterns of both signs.
+NANS = [0x7FFFFFFF, 0x7FC00000, 0x7F800001, -1, -0x400000]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    binding.load()
+    binding.device_status()
+
+
+def only_these(got, clean, bad, nan=True):
+    """NaN (or an infinity) where `bad` is, elsewhere the bits of the call with numbers."""
+    assert torch.isnan(got[bad]).all() if nan else not torch.isfinite(got[bad]).any()
+    assert torch.equal(got[~bad], clean[~bad])
+
+
+# ------------------------------------------------------------------- lora --
+def lora_inputs(dtype, nvec, rank=24, n=264, rows=70, adapters=3):
+    x, base = normal(1, nvec, n), normal(2, nvec, rows)
+    a, b = normal(3, adapters, rank, n, std=0.05, dtype=dtype), normal(4, adapters, rows, rank, dtype=dtype)
+    index = torch.arange(nvec, dtype=torch.int32, device="cuda") * 3 % (adapters + 1) - 1
+    return x, a, b, index, base
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("nvec", [4, 40, 200])  # a cluster a vector, buckets of eight, of sixteen
+@pytest.mark.parametrize("bits", NANS)
+def test_lora_nan_in_x(bits, nvec, dtype):
+    x, a, b, index, base = lora_inputs(dtype, nvec)
+    clean = binding.lora_add(x, a, b, index, base=base)
+    hit = (index == 1).nonzero()[-1, 0]
+    x.view(torch.int32)[hit, 77] = bits
+    got = binding.lora_add(x, a, b, index, base=base)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[hit] = True
+    only_these(got, clean, bad)
+    x.view(torch.int32)[(index < 0).nonzero()[0, 0], 3] = bits  # a vector without an adapter: base
+    assert torch.equal(binding.lora_add(x, a, b, index, base=base)[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("nvec", [4, 40, 200])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_lora_no_numbers_in_weights(value, nvec, dtype):
+    """Within the rank: in A the adapter's vectors, in B one output of them.  (An infinite weight of B
+    may give NaN: the parts of a rank value may be zero or of both signs.)"""
+    x, a, b, index, base = lora_inputs(dtype, nvec)
+    ranks = torch.tensor([24, 17, 8], dtype=torch.int32, device="cuda")
+    clean = binding.lora_add(x, a, b, index, ranks=ranks, base=base)
+    mine = index == 1
+    a1, b1 = a.clone(), b.clone()
+    a1[1, 16, 263] = value
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    bad[mine] = True
+    only_these(binding.lora_add(x, a1, b, index, ranks=ranks, base=base), clean, bad)
+    b1[1, 33, 16] = value
+    bad[:] = False
+    bad[mine, 33] = True
+    only_these(binding.lora_add(x, a, b1, index, ranks=ranks, base=base), clean, bad, math.isnan(value))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_lora_infinity_in_x_and_scale(value, dtype):
+    x, a, b, index, base = lora_inputs(dtype, 40)
+    clean = binding.lora_add(x, a, b, index, base=base)
+    scale = torch.tensor([1.0, 1.0, value], device="cuda")
+    got = binding.lora_add(x, a, b, index, scale, base=base)
+    assert not torch.isfinite(got[index == 2]).any()
+    assert torch.equal(got[index != 2], clean[index != 2])
+    x[0, 0] = value
+    index[0] = 0
+    clean = binding.lora_add(normal(1, 40, 264), a, b, index, base=base)
+    got = binding.lora_add(x, a, b, index, base=base)
+    assert not torch.isfinite(got[0]).any() and torch.equal(got[1:], clean[1:])
