@@ -14,7 +14,8 @@ Tensors:
   d       torch.int16/uint16 [nvec, n/32] (fp16 bit patterns; torch.float16 accepted)
   out     torch.float32 [nvec, rows] (or [rows])
 The operators between the products (add_rms_norm, lora_add, rope_append,
-paged_attention) name their tensors in their own docstrings.
+paged_attention) name their tensors in their own docstrings.  With `stream`
+they run on it and allocate from it what they return; without, on the current one.
 """
 from __future__ import annotations
 
@@ -500,13 +501,17 @@ class NormOut(NamedTuple):
     d: torch.Tensor | None
 
 
-def _stream_of(t, stream) -> int:
-    """The given stream, or the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return 0  # the call refuses t
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _on_stream(call, stream, t, *args):
+    """call(*args, stream) on the given stream, or the current one of t's device.
+    What the call allocates (outputs that are not given, the workspace) comes from
+    the stream that it runs on, so it cannot be memory that work pending on another
+    stream still uses; a caller that reads it elsewhere orders the streams, and
+    records an output on a stream that uses it longer than the caller holds it."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(t.get_device()) if isinstance(t, torch.Tensor) and t.is_cuda else 0
+        return call(*args, raw)  # (0: the call refuses t)
+    with torch.cuda.stream(stream):
+        return call(*args, stream.cuda_stream)
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
@@ -520,8 +525,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
     or x; allocated when not given)."""
     if out not in ("q8", "y", "both"):
         raise ValueError("out must be 'q8', 'y' or 'both'")
-    return NormOut(*(_marshal or _native()).add_rms_norm(x, weight, eps, residual, residual_out, out != "y", out != "q8", y, q, d,
-                                                         _stream_of(x, stream)))
+    return NormOut(*_on_stream((_marshal or _native()).add_rms_norm, stream, x, x, weight, eps, residual, residual_out, out != "y",
+                               out != "q8", y, q, d))
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor, scale: torch.Tensor | None = None,
@@ -532,7 +537,7 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Ten
     rows, rank] bf16 or f16, index int32 [nvec], scale f32 and ranks int32
     [adapters].  base f32 [nvec, rows] is the product the adapters stand
     beside; without one, out is (it is added to in place)."""
-    return (_marshal or _native()).lora_add(x, a, b, index, scale, ranks, base, out, _stream_of(x, stream))
+    return _on_stream((_marshal or _native()).lora_add, stream, x, x, a, b, index, scale, ranks, base, out)
 
 
 def paged_kv(cache_k: torch.Tensor, cache_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
@@ -556,8 +561,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torc
     table int32 [batch, width] of page numbers, kv_len int32 [batch] the cached
     tokens of each sequence, the new ones among them, new_start int32 [batch +
     1] where each sequence's new tokens begin in q, k and v."""
-    return (_marshal or _native()).rope_append(q, k, v, cos_sin, cache_k, cache_v, table, kv_len, new_start, q_out,
-                                               bool(interleaved), _stream_of(q, stream))
+    return _on_stream((_marshal or _native()).rope_append, stream, q, q, k, v, cos_sin, cache_k, cache_v, table, kv_len,
+                      new_start, q_out, bool(interleaved))
 
 
 def paged_attention_workspace(max_new: int, heads: int, kv_heads: int, dim: int) -> int:
@@ -577,12 +582,8 @@ def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tenso
     max_new is the most new tokens of any sequence; scale defaults to
     dim ** -0.5.  A given workspace (uint8) must hold
     paged_attention_workspace(...) bytes."""
-    if stream is not None and workspace is None and isinstance(q, torch.Tensor) and q.dim() == 3:
-        workspace = torch.empty(paged_attention_workspace(max_new, q.shape[1], cache_k.shape[2], q.shape[2]), dtype=torch.uint8,
-                                device=q.device)
-        workspace.record_stream(stream)  # it goes back to the allocator on return, while `stream` may still use it
-    return (_marshal or _native()).paged_attention(q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace,
-                                                   _stream_of(q, stream))
+    return _on_stream((_marshal or _native()).paged_attention, stream, q, q, cache_k, cache_v, table, kv_len, new_start, max_new,
+                      scale, out, workspace)
 
 
 class Q1Linear:

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from decode_q1_gemv_gb300 import binding
-from tests.test_gpu_ops import normal
+from tests.test_gpu_ops import Cache, normal, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,54 @@ def test_lora_infinity_in_x_and_scale(value, dtype):
     clean = binding.lora_add(normal(1, 40, 264), a, b, index, base=base)
     got = binding.lora_add(x, a, b, index, base=base)
     assert not torch.isfinite(got[0]).any() and torch.equal(got[1:], clean[1:])
+
+
+# ---------------------------------------------------------------- streams --
+def stream_calls():
+    """Each operator, and the first tensor that it allocates."""
+    x, w, r = normal(10, 512, 4096), 1 + normal(11, 4096, std=0.1), normal(12, 512, 4096)
+    a, b = normal(13, 2, 16, 4096, std=0.02, dtype=torch.bfloat16), normal(14, 2, 4096, 16, dtype=torch.bfloat16)
+    index = torch.arange(512, dtype=torch.int32, device="cuda") % 3 - 1
+    c = Cache([(700, 900), (1, 8000), (5, 300)], 32, 8, 128, 64, torch.bfloat16)
+    q, kv = normal(15, c.total, 32 * 128), normal(16, c.total, 8 * 128)
+    heads = normal(17, c.total, 32, 128, dtype=torch.bfloat16)
+    cs = rope_table(8000, 128)
+    ws = binding.paged_attention_workspace(700, 32, 8, 128)
+    return dict(
+        norm=(lambda **k: binding.add_rms_norm(x, w, residual=r, out="both", **k), 512 * 4096 * 4),
+        lora=(lambda **k: [binding.lora_add(x, a, b, index, base=r, **k)], 512 * 4096 * 4),
+        rope=(lambda **k: [binding.rope_append(q, kv, kv, cs, *c.args(), **k)], c.total * 32 * 128 * 2),
+        attention=(lambda **k: [binding.paged_attention(heads, *c.args(), max_new=700, **k)], c.total * 32 * 128 * 2),
+        workspace=(lambda **k: [binding.paged_attention(heads, *c.args(), max_new=700, **k)], ws))
+
+
+@pytest.mark.parametrize("name", ["norm", "lora", "rope", "attention", "workspace"])
+def test_another_stream_leaves_pending_work_alone(name):
+    """A call on another stream allocates its outputs: not from memory that was given back while work
+    pending on the current stream still reads it."""
+    call, size = stream_calls()[name]
+    want = call()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    block = torch.full((size // 4,), 7, dtype=torch.int32, device="cuda")
+    keep = torch.empty_like(block)
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(100_000_000)
+    keep.copy_(block)
+    del block
+    got = call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert (keep == 7).all()
+
+
+def test_the_current_stream_is_the_default():
+    call, _ = stream_calls()["lora"]
+    want = call()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = call()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0])
