@@ -510,6 +510,8 @@ def _on_stream(call, stream, t, *args):
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(t.get_device()) if isinstance(t, torch.Tensor) and t.is_cuda else 0
         return call(*args, raw)  # (0: the call refuses t)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+        raise ValueError(f"stream is of {stream.device}, the tensors of {t.device}")
     with torch.cuda.stream(stream):
         return call(*args, stream.cuda_stream)
 

@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -128,11 +129,28 @@ void check(int64_t rc, const char* what) {
   throw Refused{};
 }
 
-// Runs a call's body; whatever it throws becomes a Python exception.
+// The device of a call: that of its first tensor, and every other one's too
+// (addresses of another device would be followed on this one).  Tensors that are
+// on no CUDA device are left to `pointer`.
+c10::Device one_device(PyObject* const* a, Py_ssize_t count) {
+  const at::Tensor* first = nullptr;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    if (!THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (!t.is_cuda()) continue;
+    if (!first) first = &t;
+    if (t.device() != first->device())
+      refuse(PyExc_ValueError, "tensors on different devices: %s and %s", first->device().str().c_str(), t.device().str().c_str());
+  }
+  return first ? first->device() : c10::Device(c10::kCPU);
+}
+
+// Runs a call's body with its tensors' device current; whatever it throws becomes a Python exception.
 template <class F>
-PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& body) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted, F&& body) {
   if (given != wanted) return PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", given, wanted);
   try {
+    const c10::DeviceGuard device(one_device(a, given));
     return body();
   } catch (const Refused&) {
   } catch (const std::exception& e) {
@@ -145,7 +163,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& body) {
 
 // x, weight, eps, residual, residual_out, want_q8, want_y, y, q, d, stream
 PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 11, [&]() -> PyObject* {
+  return guarded(a, count, 11, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "x");
     if (x.dim() != 2) refuse(PyExc_ValueError, "x must be [nvec, n]");
     const int64_t nvec = x.size(0), n = x.size(1);
@@ -184,7 +202,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
 
 // x, a, b, index, scale, ranks, base, out, stream
 PyObject* lora_add(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 9, [&]() -> PyObject* {
+  return guarded(a, count, 9, [&]() -> PyObject* {
     const at::Tensor &x = tensor(a[0], "x"), &wa = tensor(a[1], "a"), &wb = tensor(a[2], "b");
     if (x.dim() != 2 || wa.dim() != 3 || wb.dim() != 3)
       refuse(PyExc_ValueError, "x must be [nvec, n], a [adapters, rank, n], b [adapters, rows, rank]");
@@ -235,7 +253,7 @@ q1_paged_kv paged_kv(PyObject* const* a, int64_t total_new) {
 
 // q, k, v, cos_sin, cache_k, cache_v, table, kv_len, new_start, q_out, interleaved, stream
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 12, [&]() -> PyObject* {
+  return guarded(a, count, 12, [&]() -> PyObject* {
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &cs = tensor(a[3], "cos_sin");
     if (q.dim() != 2 || cs.dim() != 2) refuse(PyExc_ValueError, "q must be [tokens, heads * dim] and cos_sin [positions, rot]");
     const int64_t total = q.size(0);
@@ -260,7 +278,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
 
 // q, cache_k, cache_v, table, kv_len, new_start, max_new, scale (or None), out, workspace, stream
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 11, [&]() -> PyObject* {
+  return guarded(a, count, 11, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
     if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [tokens, heads, dim]");
     const int64_t total = q.size(0), heads = q.size(1), dim = q.size(2);
@@ -289,7 +307,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
 
 // cache_k, cache_v, table, kv_len, new_start, total_new -> the bytes of the q1_paged_kv
 PyObject* make_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 6, [&]() -> PyObject* {
+  return guarded(a, count, 6, [&]() -> PyObject* {
     const q1_paged_kv kv = paged_kv(a, integer(a[5]));
     return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&kv), sizeof kv);
   });
