@@ -13,7 +13,6 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <algorithm>
 #include <array>
 #include <cmath>
 #include <string>
@@ -90,11 +89,9 @@ void* pointer(PyObject* o, const char* name, unsigned types, at::IntArrayRef sha
   return o == Py_None ? nullptr : pointer(tensor(o, name), name, types, shape, whole);
 }
 
-// Stride of an axis; an axis of one entry may have any (`least` is given).
-int64_t stride(const at::Tensor& t, int axis, int64_t least) {
-  const int64_t s = t.stride(axis);
-  return t.size(axis) > 1 ? s : std::max(s, least);
-}
+// Stride of an axis; `least` for an axis of one entry, whose stride means nothing
+// (one row of a buffer may have any, also one that no kernel takes).
+int64_t stride(const at::Tensor& t, int axis, int64_t least) { return t.size(axis) > 1 ? t.stride(axis) : least; }
 int64_t row_stride(PyObject* o, int64_t least) {
   return o == Py_None ? 0 : stride(THPVariable_Unpack(o), 0, least);
 }
@@ -237,7 +234,8 @@ q1_paged_kv paged_kv(PyObject* const* a, int64_t total_new) {
   q1_paged_kv p = {};
   p.k = pointer(k, "cache_k", kBf16 | kF16, k.sizes());
   p.v = pointer(v, "cache_v", type_bit(k.scalar_type()), k.sizes());
-  if (k.strides() != v.strides()) refuse(PyExc_ValueError, "cache_k and cache_v must have the same strides");
+  for (int i = 0; i < 3; ++i)
+    if (stride(k, i, 0) != stride(v, i, 0)) refuse(PyExc_ValueError, "cache_k and cache_v must have the same strides");
   p.pages = k.size(0), p.page_size = k.size(1), p.kv_heads = k.size(2), p.dim = k.size(3);
   p.page_stride = stride(k, 0, p.dim), p.slot_stride = stride(k, 1, p.dim), p.head_stride = stride(k, 2, p.dim);
   p.batch = table.size(0), p.table_width = table.size(1);

@@ -141,3 +141,39 @@ def test_the_current_stream_is_the_default():
         got = call()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0])
+
+
+# ------------------------------------------------------ axes of one entry --
+def one_row(x):
+    """x [1, ...] with a stride of its first axis that no kernel would take, 16-byte aligned."""
+    return x.as_strided(x.shape, (x[0].numel() + 3,) + x.stride()[1:])
+
+
+def test_one_row_may_have_any_stride():
+    x, w, base = normal(20, 1, 4096), 1 + normal(21, 4096, std=0.1), normal(22, 1, 300)
+    want = binding.add_rms_norm(x, w, residual=x, out="both")
+    got = binding.add_rms_norm(one_row(x), w, residual=one_row(x), out="both", y=one_row(torch.empty_like(x)))
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    a, b = normal(23, 2, 16, 4096, std=0.02, dtype=torch.bfloat16), normal(24, 2, 300, 16, dtype=torch.bfloat16)
+    index = torch.ones(1, dtype=torch.int32, device="cuda")
+    want = binding.lora_add(x, a, b, index, base=base)
+    assert torch.equal(binding.lora_add(one_row(x), a, b, index, base=one_row(base), out=one_row(torch.empty_like(base))), want)
+    inplace = one_row(base.clone())
+    assert torch.equal(binding.lora_add(x, a, b, index, out=inplace), want)
+
+
+@pytest.mark.parametrize("kv_heads,page", [(1, 16), (2, 512)])
+def test_axes_of_one_entry_may_have_any_stride(kv_heads, page):
+    """One token, one head of keys, one page, one sequence: their strides are not looked at."""
+    c = Cache([(1, 300)], 4, kv_heads, 64, page, torch.bfloat16, spare=0)
+    q, kv = normal(25, 1, 256), normal(26, 1, kv_heads * 64)
+    cs = rope_table(300, 64)
+    turned = binding.rope_append(q, kv, kv, cs, *c.args())
+    want = binding.paged_attention(turned, *c.args(), max_new=1)
+    odd = lambda t, off: t.as_strided(t.shape, [s if n > 1 else s + off for n, s in zip(t.shape, t.stride())])  # noqa: E731
+    args = [odd(c.k, 3), odd(c.v, 5), odd(c.table, -1), c.kv_len, c.new_start]
+    got = binding.rope_append(one_row(q), one_row(kv), one_row(kv), cs, *args)
+    assert torch.equal(got, turned)
+    assert torch.equal(binding.paged_attention(odd(turned, 1), *args, max_new=1, out=odd(torch.empty_like(turned), 7)), want)
+    pkv = binding.paged_kv(*args, 1)
+    assert pkv.table_stride == c.table.shape[1] and pkv.head_stride == 64
