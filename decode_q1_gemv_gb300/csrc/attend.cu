@@ -499,7 +499,7 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
     return fail(Q1_ERR_ARG, "%s: buffers must be 16-byte aligned, strides multiples of 8", who);
   if (q_head_stride < kv->dim || q_token_stride < kv->dim || out_head_stride < kv->dim || out_token_stride < kv->dim)
     return fail(Q1_ERR_ARG, "%s: a stride is less than dim", who);
-  if (!std::isfinite(scale)) return fail(Q1_ERR_ARG, "%s: scale must be finite", who);
+  if (!std::isfinite(scale * 1.4426950408889634f)) return fail(Q1_ERR_ARG, "%s: scale must be finite", who);
   if (max_new < 1) return fail(Q1_ERR_ARG, "%s: max_new must be positive", who);
   const int64_t need = q1_paged_attention_workspace(max_new, heads, kv->kv_heads, kv->dim);
   if (need < 0) return int(need);

@@ -462,6 +462,7 @@ int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_
  *   q, out : [total_new][heads][dim] of the cache's type, strides in elements
  *     (multiples of 8).  A row that sees no key (p < 0) is zero; rows of no
  *     sequence are left as they are.
+ *   scale : finite, and so is scale * log2(e).
  *   max_new : the most new tokens any sequence has (with the batch and the
  *     length of the table it picks the kernel: a larger or smaller number costs
  *     time, not correctness).
