@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         *reinterpret_cast<float4*>(joined + r * kLd + col) = v;
         if (col == 0) own[r] = make_float2(m, l);
       } else if (whole) {
-        const float inv = l > 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+        const float inv = inverse(l, keys_seen(cur.s, token - cur.s.first));
         const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
       } else {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         }
         int token, head;
         if (p == 0 && e < values && row_of(a, cur, cur.m * kRowsS + r, token, head)) {
-          const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+          const float inv = inverse(l, keys_seen(cur.s, token - cur.s.first));
           const uint2 w = make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
           *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + token * a.o_token + head * a.o_head + col) = w;
         }

@@ -170,13 +170,23 @@ __device__ __forceinline__ bool row_of(const AttendArgs& a, const Cursor& cur, i
   return t < cur.s.count;
 }
 
+// Keys that new token t (of the sequence's) sees.
+__device__ __forceinline__ int keys_seen(const SeqSpan& s, int t) { return max(0, s.len - s.count + t + 1); }
+
+// What a row's sums are multiplied with, l the sum of its weights: a row that
+// sees no key is zero; one whose visible scores are all -inf is 0 / 0.
+__device__ __forceinline__ float inverse(float l, int seen) {
+  return l != 0.f ? __fdiv_rn(1.0f, l) : seen ? __int_as_float(0x7fc00000) : 0.f;
+}
+
 // An item that begins in a CTA and ends in a later one: what the join has to
 // know of it, left by that CTA (parts = 0: none begins there).
 struct JoinItem {
   int parts;              // CTAs with a part, from this one on
   int first, count;       // the sequence's new tokens
   int head, tile;         // key head and tile
-  int pad[3];
+  int len;                // the sequence's keys
+  int pad[2];
 };
 
 // Left by one thread of every CTA: first with no item, then for the one item
@@ -187,7 +197,7 @@ __device__ __forceinline__ void leave_join(const AttendArgs& a, const Cursor& cu
   const bool small = total < (int64_t(1) << 31) / ctas;
   const int k = small ? int((uint32_t(end) * uint32_t(ctas) + uint32_t(total) - 1) / uint32_t(total))
                       : int((end * ctas + total - 1) / total);
-  a.joins[blockIdx.x] = {k - int(blockIdx.x), cur.s.first, cur.s.count, cur.h, cur.m, {0, 0, 0}};
+  a.joins[blockIdx.x] = {k - int(blockIdx.x), cur.s.first, cur.s.count, cur.h, cur.m, cur.s.len, {0, 0}};
 }
 
 // A partial result of TM rows: dim sums of p v relative to the row's maximum,
@@ -226,8 +236,9 @@ __device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& i
     w[p] = pl[p] != 0.f ? ex2(pm[p] - (m == -INFINITY ? 0.f : m)) : 0.f;
     l = __fmaf_rn(pl[p], w[p], l);
   }
-  const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
   const int row = it.tile * TM + r, t = by_group(a, row), head = it.head * a.group + row - t * a.group;
+  const int seen = keys_seen({it.first, it.count, it.len}, t);
+  const float inv = inverse(l, seen);
   T* out = static_cast<T*>(a.out) + (it.first + t) * a.o_token + head * a.o_head;
   for (int col = slice * 4; col < D; col += slices * 4) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -237,7 +248,7 @@ __device__ __forceinline__ void join_rows(const AttendArgs& a, const JoinItem& i
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(part[p][(col + k) * TM], w[p], o[k]);
     uint2 v = make_uint2(0u, 0u);  // a row that sees nothing
-    if (l != 0.f) v = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
+    if (seen) v = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
     *reinterpret_cast<uint2*>(out + col) = v;
   }
 }
@@ -315,7 +326,7 @@ __device__ __forceinline__ void join_item(const AttendArgs& a, int cta, int slic
     }
     const int row = it.tile * TM + r, t = by_group(a, row);
     if (g == 0 && e < values) {
-      const float inv = l != 0.f ? __fdiv_rn(1.0f, l) : 0.f;
+      const float inv = inverse(l, keys_seen({it.first, it.count, it.len}, t));
       const uint2 w = make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
       const int head = it.head * a.group + row - t * a.group;
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.first + t) * a.o_token + head * a.o_head + col) = w;

@@ -3,7 +3,7 @@
 //
 // The same formula as attend.cu, 4 D operations a (row, key) pair: from some
 // tens of rows on these bound it, so both products run on tcgen05 MMAs of 128
-// rows x 128 keys and the softmax between them on eight warps.
+// rows x 128 keys and the softmax between them on sixteen warps.
 //
 // An item is 256 rows (two tiles of 128) of one key head; a row is a new token
 // and one of the group's heads, so grouped heads share each key and value
@@ -557,7 +557,8 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           advance();
         }
         const bool whole = cur.unit == 0 && take == cur.units;
-        const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+        const int sees = live ? keys_seen(cur.s, token - cur.s.first) : 0;
+        const float inv = inverse(sum, sees);
         if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
         float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
         T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
@@ -574,8 +575,8 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               for (int j = 0; j < 16; j += 8) {
                 uint32_t pk[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)  // a row that saw nothing is zero, whatever O holds
-                  pk[e] = sum != 0.f ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv)
+                for (int e = 0; e < 4; ++e)  // a row that sees nothing is zero, whatever O holds
+                  pk[e] = sees ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv)
                                      : 0u;
                 *reinterpret_cast<uint4*>(out + c + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }

@@ -469,7 +469,8 @@ int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_
  *   workspace : device, 16-byte aligned, q1_paged_attention_workspace bytes;
  *     needs no initial value; calls that may overlap need one each.
  * Keys and values of cached tokens must be finite; slots past a sequence's
- * length may hold anything.  The weights w_j are rounded to the cache's type
+ * length may hold anything.  A row whose visible scores are all -inf (an infinite
+ * q) is NaN.  The weights w_j are rounded to the cache's type
  * for their product with v (their sum is not).  A page out of range reads as
  * zeros and sets the status bit, as does a kv_len outside the table (it is
  * clamped). */

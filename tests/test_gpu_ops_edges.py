@@ -177,3 +177,31 @@ def test_axes_of_one_entry_may_have_any_stride(kv_heads, page):
     assert torch.equal(binding.paged_attention(odd(turned, 1), *args, max_new=1, out=odd(torch.empty_like(turned), 7)), want)
     pkv = binding.paged_kv(*args, 1)
     assert pkv.table_stride == c.table.shape[1] and pkv.head_stride == 64
+
+
+# -------------------------------------------- attention: what is no number --
+# (new, length) of the sequences and the table's least tokens: which form takes the call.
+FORMS = dict(cluster=([(20, 300), (1, 40)], 0), shares=([(6, 3000), (2, 2)], 7300), one=([(7, 5000)], 7300),
+             tensor=([(300, 1500), (1, 700), (70, 90)], 7300), split=([(100, 9000)], 7300))
+
+
+@pytest.mark.parametrize("form", [*FORMS, "first"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_all_scores_minus_infinity(dim, form, monkeypatch):
+    """A row whose visible scores are all -inf has no weights to divide by: NaN, not the zeros of a row
+    that sees no key."""
+    seqs, least = ([(3, 2)], 0) if form == "first" else FORMS[form]
+    monkeypatch.setattr(Cache, "least_tokens", least)
+    c = Cache(seqs, 8, 2, dim, 32, torch.bfloat16)
+    for i, n in enumerate(c.len):
+        pos = torch.arange(n, device="cuda")
+        c.k[c.table[i, pos // 32].long(), pos % 32, :, 0] = 1
+    q = normal(32, c.total, 8, dim, dtype=torch.bfloat16)
+    clean = binding.paged_attention(q, *c.args(), max_new=max(c.new))
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    for token in {seqs[0][0] - 1, 1}:
+        q[token, 2, 0] = -math.inf
+        bad[token, 2] = True
+    only_these(binding.paged_attention(q, *c.args(), max_new=max(c.new)), clean, bad)
+    if form == "first":
+        assert (clean[0] == 0).all()
