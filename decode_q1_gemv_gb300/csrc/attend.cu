@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
     } else {
       take = int(min(int64_t(cur.units - cur.unit), u1 - u));
     }
-    const int keys = Tile::keys(a, cur.s, cur.m);
+    const int keys = Tile::keys(a, cur.s, cur.m), of_all = Tile::keys_of_all(a, cur.s, cur.m);
     const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
     const T* kbase = static_cast<const T*>(a.kv.k) + cur.h * a.kv.head_stride;
     const T* vbase = static_cast<const T*>(a.kv.v) + cur.h * a.kv.head_stride;
@@ -253,6 +253,29 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
         }
       const uint32_t p[4] = {Elem<T>::pack2(s[0][0], s[0][1]), Elem<T>::pack2(s[0][2], s[0][3]),
                              Elem<T>::pack2(s[1][0], s[1][1]), Elem<T>::pack2(s[1][2], s[1][3])};
+      if (min(j0 + i * kKeysS + 16, keys) > of_all) {  // some rows may not see all of these keys
+        unsigned char* values = smem + (vt - smem_addr(smem));
+        NoNumbers<T> none;
+#pragma unroll
+        for (int e = 0; e < 16 * kPieces; e += 32) none.look(reinterpret_cast<const uint4*>(values)[e + lane]);
+        if (__any_sync(0xffffffffu, none.found())) {
+#pragma unroll 1
+          for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int n = 0; n < 2 * kSteps; ++n) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(values + r * kRowBytes + ((n ^ (r & 7)) << 4) + (lane & 3) * 4);
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                if (j0 + i * kKeysS + r < limit[half]) add_no_numbers<T>(v, o[n][half * 2], o[n][half * 2 + 1]);
+            }
+          __syncwarp();
+          for (int e = lane; e < 16 * kPieces; e += 32) {
+            uint4& v = reinterpret_cast<uint4*>(values)[e];
+            v = numbers<T>(v);
+          }
+        }
+        __syncwarp();
+      }
       const int r = lane & 15;
 #pragma unroll
       for (int n = 0; n < kSteps; ++n) {

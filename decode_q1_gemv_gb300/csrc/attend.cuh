@@ -2,6 +2,8 @@
 // the split of the work into items and units, and the join of split items.
 #pragma once
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace q1 {
@@ -53,6 +55,10 @@ struct Tiling {
   __device__ static int keys(const AttendArgs& a, const SeqSpan& s, int m) {
     const int last = min(s.count - 1, by_group(a, m * TM + TM - 1));
     return max(0, s.len - s.count + last + 1);
+  }
+  // Keys that the first row of tile m of s sees: all its rows do.
+  __device__ static int keys_of_all(const AttendArgs& a, const SeqSpan& s, int m) {
+    return max(0, s.len - s.count + by_group(a, m * TM) + 1);
   }
   __device__ static int units(const AttendArgs& a, const SeqSpan& s, int m) { return max(1, (keys(a, s, m) + TK - 1) / TK); }
   __device__ static int64_t seq_units(const AttendArgs& a, const SeqSpan& s) {  // of one key head
@@ -177,6 +183,49 @@ __device__ __forceinline__ int keys_seen(const SeqSpan& s, int t) { return max(0
 // sees no key is zero; one whose visible scores are all -inf is 0 / 0.
 __device__ __forceinline__ float inverse(float l, int seen) {
   return l != 0.f ? __fdiv_rn(1.0f, l) : seen ? __int_as_float(0x7fc00000) : 0.f;
+}
+
+// Values of the cache that are no numbers.  A weight of zero does not keep them
+// from a row that may not see them (0 * inf is NaN), so they are taken out of
+// the products of keys that only some rows of a tile see, and added to the rows
+// that do see them (as they are: the weight of a visible key is positive).
+template <class T>
+__device__ __forceinline__ bool no_number(uint32_t bits) {  // of a value's 16 bits
+  constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  return (bits & e) == e;
+}
+template <class T>
+__device__ __forceinline__ uint32_t numbers(uint32_t w) {  // of two values; zero for the others
+  return (no_number<T>(w) ? 0u : w & 0xffffu) | (no_number<T>(w >> 16) ? 0u : w & 0xffff0000u);
+}
+template <class T>
+__device__ __forceinline__ uint4 numbers(const uint4& v) {
+  return make_uint4(numbers<T>(v.x), numbers<T>(v.y), numbers<T>(v.z), numbers<T>(v.w));
+}
+// Whether one of many values is none: the sums of their products with zero are then NaN.
+template <class T>
+struct NoNumbers {
+  using Two = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+  uint32_t sum[2] = {0u, 0u};
+  static __device__ __forceinline__ uint32_t add(uint32_t w, uint32_t sum) {
+    const uint32_t zero = 0u;
+    const Two r = __hfma2(reinterpret_cast<const Two&>(w), reinterpret_cast<const Two&>(zero), reinterpret_cast<const Two&>(sum));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+  __device__ __forceinline__ void look(const uint4& v) {
+    sum[0] = add(v.y, add(v.x, sum[0]));
+    sum[1] = add(v.w, add(v.z, sum[1]));
+  }
+  __device__ __forceinline__ bool found() const {
+    return no_number<T>(sum[0]) || no_number<T>(sum[0] >> 16) || no_number<T>(sum[1]) || no_number<T>(sum[1] >> 16);
+  }
+};
+template <class T>
+__device__ __forceinline__ void add_no_numbers(uint32_t w, float& lo, float& hi) {
+  float x, y;
+  Elem<T>::unpack2(w, x, y);
+  if (no_number<T>(w)) lo += x;
+  if (no_number<T>(w >> 16)) hi += y;
 }
 
 // An item that begins in a CTA and ends in a later one: what the join has to

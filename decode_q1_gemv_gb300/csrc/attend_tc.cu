@@ -33,6 +33,11 @@
 // has grown by more than 2^8 (weights are then at most 2^8 relative to the
 // maximum in use, which f32 sums and both 16-bit types hold).
 //
+// Where V of a unit is looked at (only where not all rows see all of its keys): by
+// the issuing warps, which wait for P then.  2 % of a mixed batch; by the softmax
+// warps 12 %, by a warp of its own 5 % (and 3 % of a long chunk: the kernel's
+// registers come out worse).
+//
 // Measured (32 heads over 8 of 128, bf16): 2048 new tokens over 16001 keys, 0.503
 // Tflop, in 351 us with the join: 1.43 Pflop/s, 0.76 of this card's matrix product
 // rate (1.88); the tensor pipe is active 64 % of the cycles (profiled launch, 342 us).
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   __shared__ LocateScratch scratch;
   __shared__ float exchange[2][2][2][kTcM];  // [unit parity][tile][half][row]
   __shared__ uint32_t tmem_base_s;
-  __shared__ volatile uint32_t abort_s;
+  __shared__ volatile uint32_t abort_s, taken_out_s;  // taken_out_s: V had values that are no numbers
   unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   const uint32_t s0 = smem_addr(smem);
   const uint32_t bars = s0 + Shape::kOffBars;
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
     }
     for (int i = 0; i < 8; ++i) mbar_init(pair + 8 * i, 2);
     fence_barrier_init();
-    abort_s = 0;
+    abort_s = taken_out_s = 0;
   }
   if (warp == kTcSoftWarps) tmem_alloc(smem_addr(&tmem_base_s), 512);
   tc_fence_before();
@@ -328,6 +333,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       };
       for (int64_t u = u0; u < u1 && ok;) {
         const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m), nw = tiles_of(cur);
+        const int of_all = Tile::keys_of_all(a, cur.s, cur.m);
         if (keys && w >= nw) {
           // No rows for this tile: its share of releasing the stages.
           for (int t = 0; t < 2 * take && ok; ++t) {
@@ -357,15 +363,31 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             const int vstage = pos.stage;
             ok = wait(full(vstage), pos.parity);
             if (!ok) break;
-            const int valid = keys - (cur.unit + t) * kTcKeys;
-            if (valid < kTcKeys) {
-              // Rows past the keys hold whatever lay there: a weight of zero
-              // times that must be zero.  (Both tiles' warps may write the same zeros.)
-              unsigned char* v = smem + Shape::kOffKV + vstage * Shape::kTileBytes;
+            // V is made ready while the softmax is under way.  (Both tiles' warps look at all of it
+            // and may write the same zeros.)
+            const int unit0 = (cur.unit + t) * kTcKeys, valid = keys - unit0;
+            if (valid < kTcKeys || of_all < unit0 + kTcKeys) {
+              uint4* v = reinterpret_cast<uint4*>(smem + Shape::kOffKV + vstage * Shape::kTileBytes);
+              constexpr int kHalf = Shape::kHalfBytes / 16;
+              // Values that are no numbers, of keys that not all rows of the item see, are taken
+              // out; the output adds them to the rows that see them.
+              const int lo = max(0, of_all - unit0) * 8 + lane, hi = min(valid, kTcKeys) * 8;
+              NoNumbers<T> none;
+#pragma unroll 4
+              for (int i = lo; i < hi; i += 32)
+#pragma unroll
+                for (int h = 0; h < Shape::kHalves; ++h) none.look(v[h * kHalf + i]);
+              if (__any_sync(0xffffffffu, none.found())) {
+                taken_out_s = 1;
+                __threadfence_block();  // whoever finds them gone finds this
+#pragma unroll 1
+                for (int i = lo; i < hi; i += 32)
+                  for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = numbers<T>(v[h * kHalf + i]);
+              }
+              // Rows past the keys hold whatever lay there: a weight of zero times that must be zero.
               for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
 #pragma unroll
-                for (int h = 0; h < Shape::kHalves; ++h)
-                  *reinterpret_cast<uint4*>(v + h * Shape::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = make_uint4(0u, 0u, 0u, 0u);
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
             }
@@ -584,6 +606,25 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) part[(half * kCols + c + j) * kTcItem] = __uint_as_float(o[j]);
+          }
+        }
+        if (taken_out_s) {  // (rolled, on what has been written: the loops above have no registers for it)
+          const int j1 = min(sees, (cur.unit + take) * kTcKeys);
+#pragma unroll 1
+          for (int j = max(Tile::keys_of_all(a, cur.s, cur.m), cur.unit * kTcKeys); j < j1; ++j) {
+            const int page = a.kv.table[cur.b * a.kv.table_stride + (j >> a.kv.page_shift)];
+            if (page < 0 || page >= a.kv.pages) continue;
+            const T* v = static_cast<const T*>(a.kv.v) + page * a.kv.page_stride +
+                         (j & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride + cur.h * a.kv.head_stride + half * kCols;
+#pragma unroll 1
+            for (int c = 0; c < kCols; ++c) {
+              const float x = Elem<T>::to(v[c]);
+              if (fabsf(x) <= FLT_MAX) continue;
+              if (whole)
+                out[c] = Elem<T>::from(Elem<T>::to(out[c]) + x);
+              else
+                part[(half * kCols + c) * kTcItem] += x;
+            }
           }
         }
         if (!whole && half == 0) {

@@ -468,12 +468,12 @@ int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_
  *     time, not correctness).
  *   workspace : device, 16-byte aligned, q1_paged_attention_workspace bytes;
  *     needs no initial value; calls that may overlap need one each.
- * Keys and values of cached tokens must be finite; slots past a sequence's
- * length may hold anything.  A row whose visible scores are all -inf (an infinite
- * q) is NaN.  The weights w_j are rounded to the cache's type
- * for their product with v (their sum is not).  A page out of range reads as
- * zeros and sets the status bit, as does a kv_len outside the table (it is
- * clamped). */
+ * Slots past a sequence's length may hold anything.  A value of q, k or v that
+ * is no number (NaN, infinite) reaches the rows that see it by the formula, and
+ * no others: not those of earlier tokens of the call.  (A row whose visible scores
+ * are all -inf is NaN.)  The weights w_j are rounded to the cache's type for their
+ * product with v (their sum is not).  A page out of range reads as zeros and sets
+ * the status bit, as does a kv_len outside the table (it is clamped). */
 int q1_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
                        const q1_paged_kv *kv, int64_t max_new, void *out, int64_t out_token_stride,
                        int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);

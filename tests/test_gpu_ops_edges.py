@@ -185,6 +185,51 @@ FORMS = dict(cluster=([(20, 300), (1, 40)], 0), shares=([(6, 3000), (2, 2)], 730
              tensor=([(300, 1500), (1, 700), (70, 90)], 7300), split=([(100, 9000)], 7300))
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_attend_values_that_earlier_tokens_do_not_see(form, dim, dtype, value, monkeypatch):
+    """A value of a new token that is no number: its column of the rows from that token on, no other bit."""
+    seqs, least = FORMS[form]
+    monkeypatch.setattr(Cache, "least_tokens", least)
+    c = Cache(seqs, 8, 2, dim, 32, dtype)
+    q = normal(30, c.total, 8, dim, dtype=dtype)
+    clean = binding.paged_attention(q, *c.args(), max_new=max(c.new))
+    new, n = seqs[0]
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    for token, head, col in ((new - 1, 0, 3), (new // 2, 1, dim - 1), (1, 1, 17)):
+        pos = n - new + token
+        c.v[c.table[0, pos // 32], pos % 32, head, col] = value
+        bad[token:new, head * 4:head * 4 + 4, col] = True
+        got = binding.paged_attention(q, *c.args(), max_new=max(c.new))
+        only_these(got, clean, bad, math.isnan(value))
+        if math.isinf(value):
+            assert (got[bad] == value).all()
+    old = n - new - 1  # and one that all rows see
+    c.v[c.table[0, old // 32], old % 32, 0, 5] = value
+    bad[:new, :4, 5] = True
+    only_these(binding.paged_attention(q, *c.args(), max_new=max(c.new)), clean, bad, math.isnan(value))
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_attend_keys_that_earlier_tokens_do_not_see(form, dim, monkeypatch):
+    seqs, least = FORMS[form]
+    monkeypatch.setattr(Cache, "least_tokens", least)
+    c = Cache(seqs, 8, 2, dim, 32, torch.bfloat16)
+    q = normal(31, c.total, 8, dim, dtype=torch.bfloat16)
+    clean = binding.paged_attention(q, *c.args(), max_new=max(c.new))
+    new, n = seqs[0]
+    token = new // 3
+    pos = n - new + token
+    c.k[c.table[0, pos // 32], pos % 32, 1, 9] = math.nan
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    bad[token:new, 4:] = True
+    only_these(binding.paged_attention(q, *c.args(), max_new=max(c.new)), clean, bad)
+
+
 @pytest.mark.parametrize("form", [*FORMS, "first"])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_attend_all_scores_minus_infinity(dim, form, monkeypatch):
