@@ -11,8 +11,11 @@
 // asynchronous copies, scores and p v by m16n8k16 MMAs (16-bit operands, f32
 // sums), maximum, sum and output in registers, no barrier between warps until
 // an item ends.  p is rounded to the cache's type for its product with v (off
-// by 2^-8 or 2^-11 of a term at most, as the output's own rounding is); the sum of p
-// is taken in f32 before that.
+// by 2^-8 or 2^-11 of a term at most, as the output's own rounding is, or, f16
+// below 2^-14, by 2^-25 of the largest weight's); the sum of p is taken in f32
+// before that.  The MMAs cut their sums, not round them: over 16384 keys, a
+// thousand MMAs on one accumulator, by 2^-13 at most; equal values of one sign
+// come out as they went in, in both types.
 //
 // Rows past 16 are further tiles (their keys come from L2) up to where the
 // tensor-core kernel is faster, see attend_cluster and many_rows.  96 KB of ring a CTA (D = 128) and

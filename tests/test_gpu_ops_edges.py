@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from decode_q1_gemv_gb300 import binding
-from tests.test_gpu_ops import Cache, normal, rope_table
+from tests.test_gpu_ops import Cache, U, normal, rope_table, within
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +250,24 @@ def test_attend_all_scores_minus_infinity(dim, form, monkeypatch):
     only_these(binding.paged_attention(q, *c.args(), max_new=max(c.new)), clean, bad)
     if form == "first":
         assert (clean[0] == 0).all()
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.3, 2.0])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch,new", [(1, 2048), (64, 1)])  # the tensor cores, whole items; the streaming kernel
+def test_attend_long_sums_of_one_sign(batch, new, dim, dtype, spread):
+    """Positive values, the same for all of 16384 keys, are their own mean: what the MMAs cut from a sum does
+    not average out here.  Each of 1024 cuts at most an ulp (2^-23) of the sum, 2^-13 together; a weight is off
+    by U for its product with v, and the result by U."""
+    length, page = 16384, 64
+    k = normal(40, batch * length // page, page, 8, dim, dtype=dtype)
+    column = (0.5 + torch.rand(dim, generator=torch.Generator().manual_seed(41))).to(dtype).cuda()
+    v = column.expand_as(k).contiguous()
+    table = torch.arange(batch * length // page, dtype=torch.int32, device="cuda").view(batch, -1)
+    kv_len = torch.full((batch,), length, dtype=torch.int32, device="cuda")
+    starts = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * new
+    q = normal(42, batch * new, 32, dim, std=spread, dtype=dtype)
+    got = binding.paged_attention(q, k, v, table, kv_len, starts, max_new=new)
+    want = column.to(torch.float64).expand(got.shape)
+    within(got, want, (2 * U[dtype] + 2.0 ** -13) * want)
