@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from decode_q1_gemv_gb300 import binding
-from tests.test_gpu_ops import Cache, U, normal, rope_table, within
+from tests.test_gpu_ops import Cache, U, check_attend, normal, rope_table, within
 
 pytestmark = pytest.mark.gpu
 
@@ -271,3 +271,33 @@ def test_attend_long_sums_of_one_sign(batch, new, dim, dtype, spread):
     got = binding.paged_attention(q, k, v, table, kv_len, starts, max_new=new)
     want = column.to(torch.float64).expand(got.shape)
     within(got, want, (2 * U[dtype] + 2.0 ** -13) * want)
+
+
+# ------------------------------------------------- caches past 32 bits --
+@pytest.mark.parametrize("least", [0, 7300])
+def test_far_pages_in_every_form(least, monkeypatch):
+    """Pages at the end of a cache of more than 2^32 elements: rotary append by bits, then attention by clusters
+    (the short table), and by shares of the keys and on the tensor cores (the long one: few rows, many)."""
+    monkeypatch.setattr(Cache, "least_tokens", least)
+    page, kv_heads, dim, heads = 256, 8, 128, 16
+    pages = (1 << 32) // (page * kv_heads * dim) + 8
+    big = [torch.empty(pages, page, kv_heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for seqs in ([(1, 600), (20, 500)], [(40, 900), (3, 300)]):
+        c = Cache(seqs, heads, kv_heads, dim, page, torch.bfloat16, spare=0)
+        used = c.k.shape[0]
+        far = torch.where((c.table >= 0) & (c.table < used), c.table + (pages - used), c.table)
+        for b, near in zip(big, (c.k, c.v)):
+            b[pages - used:] = near
+        q, kv = normal(50, c.total, heads * dim), normal(51, c.total, kv_heads * dim)
+        cs = rope_table(900, dim)
+        turned = binding.rope_append(q, kv, kv, cs, *c.args())
+        assert torch.equal(binding.rope_append(q, kv, kv, cs, *big, far, c.kv_len, c.new_start), turned)
+        for b, near in zip(big, (c.k, c.v)):
+            assert torch.equal(b[pages - used:].view(torch.int16), near.view(torch.int16))
+        for i, n in enumerate(c.len):
+            pos = torch.arange(n, device="cuda")
+            at = c.table[i, pos // page].long(), pos % page
+            c.dense[i] = c.k[at], c.v[at]
+        c.k, c.v, c.table = *big, far
+        for max_new in {1, max(c.new)}:
+            check_attend(c, heads, torch.bfloat16, dim, max_new=max_new)
