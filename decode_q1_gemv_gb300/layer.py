@@ -23,6 +23,7 @@ import torch
 from . import binding, synth
 
 MAX_VECTORS = 64  # of one batched product
+MAX_ADAPTED = 65535  # of one lora_add
 
 
 class PagedCache:
@@ -98,7 +99,9 @@ class DecoderLayer:
     def _adapt(self, name, x, out, index):
         if name in self.adapters and index is not None:
             a, b, scale = self.adapters[name]
-            binding.lora_add(x, a, b, index, scale, out=out)
+            for t in range(0, x.shape[0], MAX_ADAPTED):
+                e = t + MAX_ADAPTED
+                binding.lora_add(x[t:e], a, b, index[t:e], scale, out=out[t:e])
         return out
 
     def __call__(self, x: torch.Tensor, residual: torch.Tensor | None, cache: PagedCache,

@@ -6,6 +6,7 @@ import torch
 
 from decode_q1_gemv_gb300 import binding, layer
 from tests.test_gpu_layer import make
+from tests.test_gpu_ops import lora_reference, lora_tol, within
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,17 @@ def test_prompt_at_once_and_token_by_token_agree(whole_tokens, step_tokens):
         off = (one - out[:, t]).norm() / out[:, t].norm()
         assert off < 0.05, (t, off.item())
     assert binding.device_status() == 0
+
+
+def test_more_tokens_than_one_adapter_call_takes():
+    m = make(adapters=2)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    tokens = 65535 + 40
+    x = torch.randn(tokens, 256, generator=g, device="cuda")
+    index = (torch.arange(tokens, device="cuda") % 3 - 1).to(torch.int32)
+    out = m._adapt("v", x, torch.zeros(tokens, 256, device="cuda"), index)
+    a, b, scale = m.adapters["v"]
+    for part in (slice(0, 100), slice(65500, 65535), slice(65535, tokens)):
+        want, mag = lora_reference(x[part], a, b, index[part], scale, None, torch.zeros_like(out[part]))
+        within(out[part], want, lora_tol(256, mag))
