@@ -47,6 +47,8 @@ class PagedCache:
         """Room for new[i] more tokens of sequence i: the next call's new tokens."""
         if len(new) != len(self.lengths):
             raise ValueError("one count of new tokens a sequence")
+        if min(new) < 0:
+            raise ValueError("a count of new tokens is below zero")
         need = [-(-(n + m) // self.page_size) - len(p) for n, m, p in zip(self.lengths, new, self.pages)]
         if any(n + m > self.table.shape[1] * self.page_size for n, m in zip(self.lengths, new)):
             raise ValueError("a sequence outgrows its table")
