@@ -67,6 +67,17 @@ class PagedCache:
         self.new_start.copy_(torch.tensor(starts, dtype=torch.int32))
         self.max_new = max(new)
 
+    def release(self, sequence: int) -> None:
+        """Sequence `sequence` is empty and its pages are free: the next extend may
+        hand them out (work on the current stream that reads them comes before).
+        Its row of the table keeps old entries, which no call reads."""
+        self.free += self.pages[sequence]
+        self.pages[sequence] = []
+        self.lengths[sequence] = 0
+        self.kv_len.copy_(torch.tensor(self.lengths, dtype=torch.int32))
+        self.new_start.zero_()  # nothing is new until the next extend
+        self.max_new = 0
+
     def args(self):
         return self.k, self.v, self.table, self.kv_len, self.new_start
 
