@@ -85,9 +85,9 @@ __device__ __forceinline__ void finish_group(const NormArgs& a, int64_t row, int
   for (int i = 0; i < G; ++i) y[i] = __fmul_rn(__fmul_rn(h[i], rs), w[i]);
   if (a.y) store_group<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, g, a.n, y);
   if (a.q) {
-    float amax = 0.f;
+    float amax = fabsf(y[0]);  // (not 0: the scale of values that are all NaN is NaN, as in quant.cu)
 #pragma unroll
-    for (int i = 0; i < G; ++i) amax = fmaxf(amax, fabsf(y[i]));
+    for (int i = 1; i < G; ++i) amax = fmaxf(amax, fabsf(y[i]));
 #pragma unroll
     for (int off = kSub / G / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     if (g * G >= a.n) return;

@@ -387,6 +387,8 @@ int q1_0_verify(int flags, char *report, size_t report_len);
  *     and y may be NULL.  residual_out may be x or residual itself, and y may be x.
  *   weight : f32 [n].  q : int8 [nvec][n], d : fp16 bits [nvec][n/32], both or
  *     neither (NULL); with them n is a multiple of 32, else any n >= 1.
+ * The sum of h^2 must be finite in f32 (|h| below 1e19 / sqrt(n) is enough).  A row
+ * with a NaN is NaN in residual_out (there), in y and in the scales d (everywhere).
  * Alignment: q and d 16 bytes, the others their type's size (16-byte aligned
  * rows are faster).  1 <= nvec <= 2^24, n <= 2^24.  A row's outputs do not
  * depend on the number of rows, bit for bit. */

@@ -92,6 +92,26 @@ def test_lora_infinity_in_x_and_scale(value, dtype):
     assert not torch.isfinite(got[0]).any() and torch.equal(got[1:], clean[1:])
 
 
+# ------------------------------------------------------------------- norm --
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [96, 4096, 24608])
+def test_norm_of_a_row_with_nan(n, dtype):
+    """NaN in residual_out there, in y and the q8_0 scales of the row, as the quantize call gives them of y;
+    the other rows as they were."""
+    x, r, w = normal(60, 3, n, dtype=dtype), normal(61, 3, n, dtype=dtype), 1 + normal(62, n, std=0.1)
+    clean = binding.add_rms_norm(x, w, residual=r, out="both")
+    x[1, n // 3] = math.nan
+    got = binding.add_rms_norm(x, w, residual=r, out="both")
+    bad = torch.zeros(3, n, dtype=torch.bool, device="cuda")
+    bad[1, n // 3] = True
+    only_these(got.residual, clean.residual, bad)
+    bad[1] = True
+    only_these(got.y, clean.y, bad)
+    q, d = binding.quantize(got.y[1].float())
+    assert torch.isnan(got.d[1].view(torch.float16)).all() and torch.equal(q, got.q[1]) and torch.equal(d, got.d[1])
+    assert torch.equal(got.q[~bad], clean.q[~bad]) and torch.equal(got.d[::2], clean.d[::2])
+
+
 # ---------------------------------------------------------------- streams --
 def stream_calls():
     """Each operator, and the first tensor that it allocates."""
