@@ -85,7 +85,8 @@ class PagedCache:
 class DecoderLayer:
     """blocks: Q1_0 blocks (uint8 [rows, n/128, 18]) of q, k, v, o, gate, up and
     down; norms: two f32 [hidden] weights; cos_sin: f32 [positions, rot];
-    adapters: {product: (a, b, scale)} of low-rank adapters, or None."""
+    adapters: {product: (a, b, scale)} or {product: (a, b, scale, ranks)} of
+    low-rank adapters, or None; ranks int32 [adapters] are the ranks in use."""
 
     PRODUCTS = ("q", "k", "v", "o", "gate", "up", "down")
 
@@ -111,10 +112,10 @@ class DecoderLayer:
 
     def _adapt(self, name, x, out, index):
         if name in self.adapters and index is not None:
-            a, b, scale = self.adapters[name]
+            a, b, scale, *ranks = self.adapters[name]
             for t in range(0, x.shape[0], MAX_ADAPTED):
                 e = t + MAX_ADAPTED
-                binding.lora_add(x[t:e], a, b, index[t:e], scale, out=out[t:e])
+                binding.lora_add(x[t:e], a, b, index[t:e], scale, *ranks, out=out[t:e])
         return out
 
     def __call__(self, x: torch.Tensor, residual: torch.Tensor | None, cache: PagedCache,
@@ -191,7 +192,7 @@ def main() -> None:
         out, residual = layer(x, None, cache, of.repeat_interleave(new))
         end.record()
         torch.cuda.synchronize()
-        assert torch.isfinite(out).all() and binding.device_status() == 0
+        assert torch.isfinite(out).all() and torch.isfinite(residual).all() and binding.device_status() == 0
         return start.elapsed_time(end)
 
     print(f"prompt: {args.sequences} x {args.prompt} tokens, {run(args.prompt):.3f} ms (first call)")

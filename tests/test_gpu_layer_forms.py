@@ -1,6 +1,8 @@
 """The decoder layer over tables of every length: what a prompt at once gives and what
 its tokens give one by one, with the attention by clusters (a short table), on the
 tensor cores and by shares of the keys (a table too long for clusters)."""
+import math
+
 import pytest
 import torch
 
@@ -54,3 +56,22 @@ def test_more_tokens_than_one_adapter_call_takes():
     for part in (slice(0, 100), slice(65500, 65535), slice(65535, tokens)):
         want, mag = lora_reference(x[part], a, b, index[part], scale, None, torch.zeros_like(out[part]))
         within(out[part], want, lora_tol(256, mag))
+
+
+def test_adapters_of_different_ranks():
+    """(a, b, scale, ranks): what lies past a rank is not used."""
+    m, plain = make(adapters=2), make(adapters=2)
+    x = torch.randn(9, 256, device="cuda")
+    index = torch.arange(9, dtype=torch.int32, device="cuda") % 3 - 1
+    ranks = torch.tensor([3, 8], dtype=torch.int32, device="cuda")
+    for name, (a, b, scale) in m.adapters.items():
+        plain.adapters[name] = (a.clone(), b.clone(), scale)
+        plain.adapters[name][0][0, 3:] = 0
+        a[0, 3:] = math.nan
+        m.adapters[name] = (a, b, scale, ranks)
+    outs = []
+    for layer_ in (m, plain):
+        c = layer.PagedCache(1, 2, 16, 2, 128, 32)
+        c.extend([9])
+        outs.append(layer_(x, None, c, index))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
