@@ -501,19 +501,22 @@ class NormOut(NamedTuple):
     d: torch.Tensor | None
 
 
+def _current_stream_of(t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return 0  # the call refuses t
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _on_stream(call, stream, t, *args):
-    """call(*args, stream) on the given stream, or the current one of t's device.
-    What the call allocates (outputs that are not given, the workspace) comes from
-    the stream that it runs on, so it cannot be memory that work pending on another
-    stream still uses; a caller that reads it elsewhere orders the streams, and
-    records an output on a stream that uses it longer than the caller holds it."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(t.get_device()) if isinstance(t, torch.Tensor) and t.is_cuda else 0
-        return call(*args, raw)  # (0: the call refuses t)
+    """call(t, *args, stream) on a given stream.  What the call allocates (outputs that
+    are not given, the workspace) comes from the stream that it runs on, so it cannot
+    be memory that work pending on another stream still uses; a caller that reads it
+    elsewhere orders the streams, and records an output on a stream that uses it
+    longer than the caller holds it."""
     if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
         raise ValueError(f"stream is of {stream.device}, the tensors of {t.device}")
     with torch.cuda.stream(stream):
-        return call(*args, stream.cuda_stream)
+        return call(t, *args, stream.cuda_stream)
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
@@ -527,8 +530,10 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
     or x; allocated when not given)."""
     if out not in ("q8", "y", "both"):
         raise ValueError("out must be 'q8', 'y' or 'both'")
-    return NormOut(*_on_stream((_marshal or _native()).add_rms_norm, stream, x, x, weight, eps, residual, residual_out, out != "y",
-                               out != "q8", y, q, d))
+    call = (_marshal or _native()).add_rms_norm
+    if stream is not None:
+        return NormOut(*_on_stream(call, stream, x, weight, eps, residual, residual_out, out != "y", out != "q8", y, q, d))
+    return NormOut(*call(x, weight, eps, residual, residual_out, out != "y", out != "q8", y, q, d, _current_stream_of(x)))
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor, scale: torch.Tensor | None = None,
@@ -539,7 +544,10 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Ten
     rows, rank] bf16 or f16, index int32 [nvec], scale f32 and ranks int32
     [adapters].  base f32 [nvec, rows] is the product the adapters stand
     beside; without one, out is (it is added to in place)."""
-    return _on_stream((_marshal or _native()).lora_add, stream, x, x, a, b, index, scale, ranks, base, out)
+    call = (_marshal or _native()).lora_add
+    if stream is not None:
+        return _on_stream(call, stream, x, a, b, index, scale, ranks, base, out)
+    return call(x, a, b, index, scale, ranks, base, out, _current_stream_of(x))
 
 
 def paged_kv(cache_k: torch.Tensor, cache_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
@@ -563,8 +571,10 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torc
     table int32 [batch, width] of page numbers, kv_len int32 [batch] the cached
     tokens of each sequence, the new ones among them, new_start int32 [batch +
     1] where each sequence's new tokens begin in q, k and v."""
-    return _on_stream((_marshal or _native()).rope_append, stream, q, q, k, v, cos_sin, cache_k, cache_v, table, kv_len,
-                      new_start, q_out, bool(interleaved))
+    call = (_marshal or _native()).rope_append
+    if stream is not None:
+        return _on_stream(call, stream, q, k, v, cos_sin, cache_k, cache_v, table, kv_len, new_start, q_out, bool(interleaved))
+    return call(q, k, v, cos_sin, cache_k, cache_v, table, kv_len, new_start, q_out, bool(interleaved), _current_stream_of(q))
 
 
 def paged_attention_workspace(max_new: int, heads: int, kv_heads: int, dim: int) -> int:
@@ -584,8 +594,10 @@ def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tenso
     max_new is the most new tokens of any sequence; scale defaults to
     dim ** -0.5.  A given workspace (uint8) must hold
     paged_attention_workspace(...) bytes."""
-    return _on_stream((_marshal or _native()).paged_attention, stream, q, q, cache_k, cache_v, table, kv_len, new_start, max_new,
-                      scale, out, workspace)
+    call = (_marshal or _native()).paged_attention
+    if stream is not None:
+        return _on_stream(call, stream, q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace)
+    return call(q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace, _current_stream_of(q))
 
 
 class Q1Linear:

@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -132,7 +133,7 @@ void check(int64_t rc, const char* what) {
 c10::Device one_device(PyObject* const* a, Py_ssize_t count) {
   const at::Tensor* first = nullptr;
   for (Py_ssize_t i = 0; i < count; ++i) {
-    if (!THPVariable_Check(a[i])) continue;
+    if (a[i] == Py_None || PyLong_Check(a[i]) || !THPVariable_Check(a[i])) continue;  // (the check of others is slow)
     const at::Tensor& t = THPVariable_Unpack(a[i]);
     if (!t.is_cuda()) continue;
     if (!first) first = &t;
@@ -147,7 +148,12 @@ template <class F>
 PyObject* guarded(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted, F&& body) {
   if (given != wanted) return PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", given, wanted);
   try {
-    const c10::DeviceGuard device(one_device(a, given));
+    const c10::Device device = one_device(a, given);
+    c10::OptionalDeviceGuard current;
+    if (device.is_cuda()) {  // (asked once: with one device the guard's calls are for nothing, 0.2 us)
+      static const bool several = c10::impl::VirtualGuardImpl(c10::kCUDA).deviceCount() > 1;
+      if (several) current.reset_device(device);
+    }
     return body();
   } catch (const Refused&) {
   } catch (const std::exception& e) {
