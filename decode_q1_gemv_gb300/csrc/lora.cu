@@ -5,9 +5,9 @@
 // rank) have to be read about once and take 2 operations a value and vector:
 // bytes bound it, and for one vector the chain of dependent memory reads.
 //
-// Both products run in one launch: a cluster of CTAs takes one bucket (up to
-// eight or sixteen vectors of one adapter), each CTA a slice of n in the first
-// product and a slice of the rows in the second; the rank values between them
+// Both products run in one launch: a cluster of CTAs, or half of one, takes one
+// bucket (up to eight or sixteen vectors of one adapter), each CTA a slice of n in the
+// first product and a slice of the rows in the second; the rank values between them
 // (at most 128 a vector) pass through distributed shared memory, so there is
 // no workspace and no second launch.
 //
@@ -35,7 +35,9 @@
 //
 // Vectors are grouped on the device: in a window of 64 vectors, every
 // eighth (sixteenth) vector of an adapter leads a bucket of it and the next
-// ones of that window.
+// ones of that window.  The device also counts the buckets, and gives each a
+// cluster while all run at once, else half a cluster: what a call takes depends
+// on the adapters that its vectors name, not on how many there are.
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
@@ -68,20 +70,28 @@ template <int N>
 struct LoraTile {
   static constexpr int kTokens = 8 * N, kMaxRank = N == 1 ? 128 : 64, kTiles = kMaxRank / 16;
   static constexpr int kPieces = 4 + 2 * N, kStages = N == 1 ? 4 : 3;
-  static constexpr int kStage = kPieces * kLoraThreads * 16, kSmem = kStages * kStage;
+  static constexpr int kStage = kPieces * kLoraThreads * 16, kRing = kStages * kStage;
 };
 
-template <int N>
 struct LoraShared {
-  float mine[LoraTile<N>::kTiles * N * 128];                           // this CTA's slice of n: [tile][group][16 ranks][8]
-  __align__(16) unsigned char t[N == 1 ? 8448 : 9216];                 // all slices, scaled, as parts (LoraMul)
-  uint64_t leads[kLoraWarps];                                          // of a round's windows: the vectors that lead buckets
-  int adapter[kLoraRound];                                             // of a round's vectors
-  const float *x[LoraTile<N>::kTokens], *base[LoraTile<N>::kTokens];   // the vectors' slices of the CTA
-  float* out[LoraTile<N>::kTokens];
-  int slot[kLoraWarps];                                                // the ring's free stage, where a warp leaves its sums
-  int count;
+  float mine[1024];                         // this CTA's slice of n: [tile][group][16 ranks][8]
+  __align__(16) unsigned char t[9216];      // all slices, scaled, as parts (LoraMul)
+  uint64_t leads[kLoraWarps];               // of a round's windows: the vectors that lead buckets
+  int adapter[kLoraRound];                  // of a round's vectors
+  const float *x[16], *base[16];            // the vectors' slices of the CTA
+  float* out[16];
+  int slot[kLoraWarps];                     // the ring's free stage, where a warp leaves its sums
+  int count;                                // vectors of the bucket
+  int log, step;                            // CTAs that share one (log2), the next one's distance
+  bool halves;                              // of the cluster have buckets of their own, and meet at these:
+  uint64_t ready, read;                     // everyone's `mine` is there; mine has been read by everyone
+  uint32_t parity;                          // of the bucket's phase of both
+  int total;                                // of this round and those before
 };
+
+// Dynamic shared memory: this, then the ring.
+extern __shared__ __align__(128) unsigned char lora_smem[];
+constexpr int kLoraRingAt = (sizeof(LoraShared) + 127) / 128 * 128;
 
 __device__ __forceinline__ void lora_copy(uint32_t dst, const void* src, bool live) {
   asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p cp.async.cg.shared.global [%0], [%1], 16;\n}" ::"r"(dst), "l"(src),
@@ -266,7 +276,7 @@ __device__ __forceinline__ void lora_mma(float (&sum0)[N][4], float (&sum1)[N][4
 template <class T, int N, bool VEC>
 struct LoraPart {
   using S = LoraTile<N>;
-  const LoraShared<N>& sh;
+  const LoraShared& sh;
   int rank, a_rank, slice, rows; // rank in use, row stride of B, values of n, rows of this CTA
   int tiles, pairs, ranks32;     // of 16 rank rows, of two of those (at least 1), of 32 rank values
   int count, warp, lane, quad, piece;  // vectors of the bucket, lane / 4 and lane % 4
@@ -280,7 +290,7 @@ struct LoraPart {
   uint32_t to, from;                      // the lane's 16 bytes of a weight copy; its row for lora_matrix
 
   // After the members above `f_block` are set.
-  __device__ __forceinline__ LoraPart(const LoraShared<N>& shared) : sh(shared) {}
+  __device__ __forceinline__ LoraPart(const LoraShared& shared) : sh(shared) {}
   __device__ __forceinline__ void start(const T* A, const T* B, int64_t n) {
     f_block = warp;
     f_a = A + quad * n + warp * 32 + piece * 8;
@@ -372,20 +382,41 @@ struct LoraPart {
   }
   // A warp's sums of a tile of 16 ranks by eight vectors, 512 bytes: in its part of the stage that
   // is free when its first product ends (stage `slot`), beyond that stage's pieces in t's place.
-  __device__ __forceinline__ float* sums(LoraShared<N>& s, unsigned char* pieces, int slot, int w, int tile) const {
+  __device__ __forceinline__ float* sums(LoraShared& s, unsigned char* pieces, int slot, int w, int tile) const {
     if (tile < S::kPieces) return reinterpret_cast<float*>(pieces + slot + tile * (kLoraThreads * 16) + w * 512);
     return reinterpret_cast<float*>(s.t) + (w * (S::kTiles * N - S::kPieces) + tile - S::kPieces) * 128;
   }
 };
-static_assert(kLoraWarps * (LoraTile<1>::kTiles - LoraTile<1>::kPieces) * 512 <= sizeof(LoraShared<1>::t), "sums");
+static_assert(kLoraWarps * (LoraTile<1>::kTiles - LoraTile<1>::kPieces) * 512 <= sizeof(LoraShared::t), "sums");
 static_assert(LoraTile<2>::kTiles * 2 <= LoraTile<2>::kPieces, "sums");
-static_assert(2 * 8 * (128 + 4) * 4 <= sizeof(LoraShared<1>::t) && 3 * 8 * (128 + 32) * 2 <= sizeof(LoraShared<1>::t), "t");
-static_assert(2 * 16 * (64 + 4) * 4 <= sizeof(LoraShared<2>::t) && 3 * 16 * (64 + 32) * 2 <= sizeof(LoraShared<2>::t), "t");
+static_assert(2 * 8 * (128 + 4) * 4 <= sizeof(LoraShared::t) && 3 * 8 * (128 + 32) * 2 <= sizeof(LoraShared::t), "t");
+static_assert(2 * 16 * (64 + 4) * 4 <= sizeof(LoraShared::t) && 3 * 16 * (64 + 32) * 2 <= sizeof(LoraShared::t), "t");
+
+// A barrier of the CTAs first .. first + count - 1 of the cluster: every CTA has one, each arrives
+// at everyone's and waits at its own.  The CTA's threads are at one before they arrive.
+__device__ __forceinline__ void half_arrive(uint64_t& bar, int first, int count) {
+  if (int(threadIdx.x) < count)
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nmbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(
+                     smem_addr(&bar)), "r"(first + int(threadIdx.x)) : "memory");
+}
+// (Bounded; a wait that gives up is reported, and the launch's results are not to be used.)
+__device__ __forceinline__ void half_wait(uint64_t& bar, uint32_t parity, unsigned* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(smem_addr(&bar)), "r"(parity) : "memory");
+    if (done) return;
+    if (i == 0) t0 = globaltimer();
+    if ((i & 63) == 63 && globaltimer() - t0 > 1000000000ull) break;
+  }
+  atomicOr(status, kStatusWaitTimeout);
+}
 
 // One bucket.  VEC: base and out rows start on 16 bytes, rows is even.
 template <class T, int N, bool VEC>
-__device__ __forceinline__ void lora_bucket(LoraShared<N>& sh, unsigned char* pieces, LoraPart<T, N, VEC>& part, float scale,
-                                            cg::cluster_group& cluster) {
+__device__ __forceinline__ void lora_bucket(LoraShared& sh, unsigned char* pieces, LoraPart<T, N, VEC>& part, float scale,
+                                            unsigned* status) {
   using S = LoraTile<N>;
   using M = LoraMul<T>;
   const int quad = part.quad, piece = part.piece, count = part.count;
@@ -458,13 +489,21 @@ __device__ __forceinline__ void lora_bucket(LoraShared<N>& sh, unsigned char* pi
     for (int w = 0; w < kLoraWarps; ++w) v = __fadd_rn(v, part.sums(sh, pieces, sh.slot[w], w, i >> 7)[i & 127]);
     sh.mine[i] = v;
   }
-  cluster.sync();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = 1 << sh.log, first = int(cluster.block_rank()) & -ctas;
+  if (sh.halves) {
+    __syncthreads();
+    half_arrive(sh.ready, first, ctas);
+    half_wait(sh.ready, sh.parity, status);
+  } else {
+    cluster.sync();
+  }
 #pragma unroll 1
   for (int i = threadIdx.x; i < sums; i += kLoraThreads) {
     const int row = i / (N * 128) * 16 + (i & 127) / 8, vec = (i >> 7) % N * 8 + (i & 7);
-    float s[16], v = 0.f;  // a cluster has up to 16 CTAs: all reads at once, added in order
+    float s[16], v = 0.f;  // up to 16 CTAs share a bucket: all reads at once, added in order
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s[k] = vec < count && k < int(cluster.num_blocks()) ? cluster.map_shared_rank(sh.mine, k)[i] : 0.f;
+    for (int k = 0; k < 16; ++k) s[k] = vec < count && k < ctas ? cluster.map_shared_rank(sh.mine, first + k)[i] : 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) v = __fadd_rn(v, s[k]);
     v = row < part.rank ? __fmul_rn(v, scale) : 0.f;  // rows past the rank are old values' products
@@ -478,7 +517,10 @@ __device__ __forceinline__ void lora_bucket(LoraShared<N>& sh, unsigned char* pi
   }
   // Others' `mine` has been read; own t is complete.  That this CTA's has been read is waited for at the end.
   __syncthreads();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (sh.halves)
+    half_arrive(sh.read, first, ctas);
+  else
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // Second product.  A lane's outputs: two neighbouring rows (and the same
   // sixteen rows further on) of vectors 2 piece and 2 piece + 1.
@@ -540,18 +582,36 @@ __device__ __forceinline__ void lora_bucket(LoraShared<N>& sh, unsigned char* pi
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (sh.halves)
+    half_wait(sh.read, sh.parity, status);
+  else
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// A bucket of sh.count vectors.
+template <class T, int N, bool VEC>
+__device__ __forceinline__ void lora_part(const T* A, const T* B, int n, int a_rank, int rank, int slice, int rows, float scale,
+                                          unsigned* status) {
+  LoraShared& sh = *reinterpret_cast<LoraShared*>(lora_smem);
+  unsigned char* ring = lora_smem + kLoraRingAt;
+  const int lane = threadIdx.x & 31;
+  LoraPart<T, N, VEC> part(sh);
+  part.rank = rank, part.a_rank = a_rank, part.count = sh.count;
+  part.rows = rows, part.slice = slice;
+  part.tiles = (rank + 15) / 16, part.pairs = max(1, (part.tiles + 1) / 2);
+  part.ranks32 = max(1, (rank + 31) / 32);
+  part.warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), part.lane = lane, part.quad = lane >> 2, part.piece = lane & 3;
+  part.ring = smem_addr(ring);
+  part.start(A, B, n);
+  lora_bucket<T, N, VEC>(sh, ring, part, scale, status);
+}
 template <class T, int N, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
   using S = LoraTile<N>;
-  __shared__ LoraShared<N> sh;
-  extern __shared__ __align__(128) unsigned char ring[];
-  cg::cluster_group cluster = cg::this_cluster();
+  LoraShared& sh = *reinterpret_cast<LoraShared*>(lora_smem);
   pdl_launch_dependents();
   pdl_wait();
-  const int log = a.log_cluster, C = 1 << log, clusters = int(gridDim.x) >> log, c = int(blockIdx.x) & (C - 1);
+  const int clusters = int(gridDim.x) >> a.log_cluster, own = int(blockIdx.x) >> a.log_cluster;
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const auto adapter_of = [&](int u) {  // -1: none, -2: past the end
     if (u >= a.nvec) return -2;
@@ -559,13 +619,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
     return i >= 0 && i < a.adapters ? i : -1;
   };
   // With a cluster for each vector a cluster looks at its own vector.  Else every
-  // CTA counts the buckets, a window a warp, and cluster i takes buckets i, i +
-  // clusters, ... (looking at every so many-th vector cost 8000 cycles a bucket,
+  // CTA counts the buckets, a window a warp, and (half) cluster i of m takes buckets i, i +
+  // m, ... (looking at every so many-th vector cost 8000 cycles a bucket,
   // and some clusters found two buckets and others none).
   const bool few = a.nvec <= clusters;
-  const int per_n = ((a.n / 8 + C - 1) >> log) * 8, per_r = (((a.rows + 3) / 4 + C - 1) >> log) * 4;
-  const int j0 = min(a.n, c * per_n), r0 = min(a.rows, c * per_r);
-  int next = few ? 0 : int(blockIdx.x) >> log, seen = 0;
+  int next = 0, seen = 0;  // this CTA's next bucket, buckets of the rounds before
+  if (few && threadIdx.x == 0) sh.log = a.log_cluster, sh.step = sh.total = 1, sh.halves = false;
 #pragma unroll 1
   for (int from = 0; from < a.nvec; from += kLoraRound) {
     if (!few) {
@@ -583,116 +642,150 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_add(LoraArgs a) {
       if (lane == 0) sh.leads[warp] = uint64_t(hi_leads) << 32 | lo_leads;
       sh.adapter[warp * kLoraWindow + lane] = lo, sh.adapter[warp * kLoraWindow + 32 + lane] = hi;
       __syncthreads();
-    }
-#pragma unroll 1
-    for (int w = 0; w < (few ? 1 : kLoraWarps) && from + w * kLoraWindow < a.nvec; ++w) {
-      const int own = int(blockIdx.x) >> log;
-      const int w0 = few ? own / kLoraWindow * kLoraWindow : from + w * kLoraWindow;
-      uint64_t leads = !few ? sh.leads[w] : own < a.nvec ? uint64_t(1) << (own - w0) : 0;
-      const int end = seen + __popcll(leads);
-#pragma unroll 1
-      for (; next < end; next += clusters) {
-#pragma unroll 1
-        for (; seen < next; ++seen) leads &= leads - 1;
-        const int v = w0 + __ffsll(int64_t(leads)) - 1;
-        int adapter, near[kLoraWindow / 32];
-        if (few) {  // one round of loads
-          adapter = a.index[v];
-#pragma unroll
-          for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = a.index[min(w0 + h * 32 + lane, a.nvec - 1)];
-          adapter = adapter >= 0 && adapter < a.adapters ? adapter : -1;
-#pragma unroll
-          for (int h = 0; h < kLoraWindow / 32; ++h)
-            near[h] = w0 + h * 32 + lane >= a.nvec ? -2 : near[h] >= 0 && near[h] < a.adapters ? near[h] : -1;
-        } else {
-          adapter = sh.adapter[v - from];
-#pragma unroll
-          for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = sh.adapter[w0 - from + h * 32 + lane];
-        }
-        const int ranks = adapter >= 0 && a.ranks ? a.ranks[adapter] : a.rank;
-        const float scale = adapter >= 0 && a.scale ? a.scale[adapter] : 1.f;
-        // Warp 0 looks at the window: which of its vectors have v's adapter.
-        if (warp == 0) {
-          uint64_t same = 0;
-#pragma unroll
-          for (int h = 0; h < kLoraWindow / 32; ++h) same |= uint64_t(__ballot_sync(0xffffffffu, near[h] == adapter)) << (32 * h);
-          const int before = __popcll(same & ((uint64_t(1) << (v - w0)) - 1));
-          const uint64_t rest = same >> (v - w0) << (v - w0);
-          // The first kTokens of the rest, each by the lane of its place.
-          const bool lead = before % S::kTokens == 0;
-#pragma unroll
-          for (int h = 0; h < kLoraWindow / 32; ++h) {
-            const int at = h * 32 + lane, nth = __popcll(rest & ((uint64_t(1) << at) - 1));
-            if (lead && (rest >> at & 1) && nth < S::kTokens) {
-              const int64_t token = w0 + at;
-              sh.x[nth] = a.x + token * a.ldx + j0;
-              sh.base[nth] = a.base + token * a.ldb + r0;
-              sh.out[nth] = a.out + token * a.ldo + r0;
-              if (adapter < 0 && a.index[token] != -1) atomicOr(a.status, kStatusBadIndex);
-            }
+      if (threadIdx.x == 0) {
+        int total = 0;
+        for (int w = 0; w < kLoraWarps; ++w) total += __popcll(sh.leads[w]);
+        sh.total = seen + total;
+        if (from == 0) {
+          // The first round's buckets tell how many there are: a cluster each where they run
+          // at once (36 of eight CTAs do), else half a cluster each.  f16, rank 64, 4096 to
+          // 14336: 64 vectors of 32 adapters 20.3 us with whole clusters, 32 with halves; of 64
+          // adapters 38.8 and 33.1; 128 vectors of 64 (100 buckets) 64.8 and 59, 256 of 256 204 and 121.
+          const int64_t buckets = a.nvec > kLoraRound ? int64_t(total) * a.nvec / kLoraRound : total;
+          const int half = buckets > clusters ? 1 : 0;
+          sh.log = a.log_cluster - half, sh.step = clusters << half, sh.halves = half;
+          if (half) {
+            mbar_init(smem_addr(&sh.ready), 1 << sh.log), mbar_init(smem_addr(&sh.read), 1 << sh.log);
+            fence_barrier_init();
+            sh.parity = 1;
           }
-          if (lane == 0) sh.count = lead ? min(S::kTokens, __popcll(rest)) : 0;
         }
-        __syncthreads();
-        const int count = sh.count, rows = min(a.rows, r0 + per_r) - r0;
-        if (count && adapter < 0) {
-          if (a.out != a.base) {
-#pragma unroll 1
-            for (int i = 0; i < count; ++i)
-#pragma unroll 1
-              for (int r = threadIdx.x; r < rows; r += kLoraThreads) sh.out[i][r] = sh.base[i][r];
-          }
-        } else if (count) {
-          LoraPart<T, N, VEC> part(sh);
-          part.rank = max(0, min(ranks, a.rank)), part.a_rank = a.rank, part.count = count;
-          part.rows = rows;
-          part.tiles = (part.rank + 15) / 16, part.pairs = max(1, (part.tiles + 1) / 2);
-          part.slice = part.rank ? min(a.n, j0 + per_n) - j0 : 0;  // rank 0: no first product
-          part.ranks32 = max(1, (part.rank + 31) / 32);
-          part.warp = warp, part.lane = lane, part.quad = lane >> 2, part.piece = lane & 3;
-          part.ring = smem_addr(ring);
-          part.start(static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n + j0,
-                     static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + r0) * a.rank, a.n);
-          lora_bucket<T, N, VEC>(sh, ring, part, scale, cluster);
-        }
-        __syncthreads();  // sh is free again
       }
-      seen = end;
+      __syncthreads();
+      if (from == 0) {
+        const int half = a.log_cluster - sh.log;
+        next = own << half | (int(blockIdx.x) & ((1 << a.log_cluster) - 1)) >> sh.log;
+        if (half) cg::this_cluster().sync();  // everyone's barriers are there
+      }
     }
-    if (few) break;
+#pragma unroll 1
+    for (; next < sh.total; next += sh.step) {
+      int v = own;
+      if (!few) {
+        int w = 0, nth = next - seen;
+        uint64_t leads;
+        for (;; ++w) {
+          leads = sh.leads[w];
+          const int n = __popcll(leads);
+          if (nth < n) break;
+          nth -= n;
+        }
+#pragma unroll 1
+        for (; nth > 0; --nth) leads &= leads - 1;
+        v = from + w * kLoraWindow + __ffsll(int64_t(leads)) - 1;
+      }
+      const int w0 = v / kLoraWindow * kLoraWindow;
+      int adapter, near[kLoraWindow / 32];
+      if (few) {  // one round of loads
+        adapter = a.index[v];
+#pragma unroll
+        for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = a.index[min(w0 + h * 32 + lane, a.nvec - 1)];
+        adapter = adapter >= 0 && adapter < a.adapters ? adapter : -1;
+#pragma unroll
+        for (int h = 0; h < kLoraWindow / 32; ++h)
+          near[h] = w0 + h * 32 + lane >= a.nvec ? -2 : near[h] >= 0 && near[h] < a.adapters ? near[h] : -1;
+      } else {
+        adapter = sh.adapter[v - from];
+#pragma unroll
+        for (int h = 0; h < kLoraWindow / 32; ++h) near[h] = sh.adapter[w0 - from + h * 32 + lane];
+      }
+      const int log = few ? a.log_cluster : sh.log, c = int(blockIdx.x) & ((1 << log) - 1);
+      const int per_n = ((a.n / 8 + (1 << log) - 1) >> log) * 8, per_r = (((a.rows + 3) / 4 + (1 << log) - 1) >> log) * 4;
+      const int j0 = min(a.n, c * per_n), r0 = min(a.rows, c * per_r);
+      const int ranks = adapter >= 0 && a.ranks ? a.ranks[adapter] : a.rank;
+      const float scale = adapter >= 0 && a.scale ? a.scale[adapter] : 1.f;
+      // Warp 0 looks at the window: which of its vectors have v's adapter.
+      if (warp == 0) {
+        uint64_t same = 0;
+#pragma unroll
+        for (int h = 0; h < kLoraWindow / 32; ++h) same |= uint64_t(__ballot_sync(0xffffffffu, near[h] == adapter)) << (32 * h);
+        const int before = __popcll(same & ((uint64_t(1) << (v - w0)) - 1));
+        const uint64_t rest = same >> (v - w0) << (v - w0);
+        // The first kTokens of the rest, each by the lane of its place.
+        const bool lead = before % S::kTokens == 0;
+#pragma unroll
+        for (int h = 0; h < kLoraWindow / 32; ++h) {
+          const int at = h * 32 + lane, nth = __popcll(rest & ((uint64_t(1) << at) - 1));
+          if (lead && (rest >> at & 1) && nth < S::kTokens) {
+            const int64_t token = w0 + at;
+            sh.x[nth] = a.x + token * a.ldx + j0;
+            sh.base[nth] = a.base + token * a.ldb + r0;
+            sh.out[nth] = a.out + token * a.ldo + r0;
+            if (adapter < 0 && a.index[token] != -1) atomicOr(a.status, kStatusBadIndex);
+          }
+        }
+        if (lane == 0) sh.count = lead ? min(S::kTokens, __popcll(rest)) : 0;
+        if (lane == 0 && adapter >= 0) sh.parity ^= 1;
+      }
+      __syncthreads();
+      const int count = sh.count, rows = min(a.rows, r0 + per_r) - r0;
+      if (count && adapter < 0) {
+        if (a.out != a.base) {
+#pragma unroll 1
+          for (int i = 0; i < count; ++i)
+#pragma unroll 1
+            for (int r = threadIdx.x; r < rows; r += kLoraThreads) sh.out[i][r] = sh.base[i][r];
+        }
+      } else if (count) {
+        const int rank = max(0, min(ranks, a.rank));
+        const T* A = static_cast<const T*>(a.wa) + int64_t(adapter) * a.rank * a.n + j0;
+        const T* B = static_cast<const T*>(a.wb) + (int64_t(adapter) * a.rows + r0) * a.rank;
+        const int slice = rank ? min(a.n, j0 + per_n) - j0 : 0;  // rank 0: no first product
+        lora_part<T, N, VEC>(A, B, a.n, a.rank, rank, slice, rows, scale, a.status);
+      }
+      __syncthreads();  // sh is free again
+    }
+    if (few) return;
+    seen = sh.total;
   }
+  if (sh.halves) cg::this_cluster().sync();  // no one arrives at a CTA that has left
 }
 
+// Launches in clusters of 1 << log CTAs: how many of them run at once, and (`g`) the call, with a
+// cluster for each vector where they do, else as many as do.
 template <class T, int N, bool VEC>
-static int launch_lora(LoraArgs g, int cluster, cudaStream_t s) {
+static int launch_lora(int log, int& once, const LoraArgs* call, cudaStream_t s) {
   using S = LoraTile<N>;
+  constexpr int kSmem = kLoraRingAt + S::kRing;
   const char* who = "q1_lora_add launch";
   const auto kernel = k_lora_add<T, N, VEC>;
   static bool set[64] = {};
+  static int most[64][5] = {};
   int dev = 0;
   if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (int e = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem), who)) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (!known || !set[dev]) {
+    if (int e = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem), who)) return e;
     if (int e = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who)) return e;
-    if (dev >= 0 && dev < 64) set[dev] = true;
+    if (known) set[dev] = true;
   }
-  g.log_cluster = cluster == 16 ? 4 : cluster == 8 ? 3 : 2;
-  // A cluster for each vector where they all run at once, else as many as do.
-  static int most[64][5] = {};
-  int once = dev >= 0 && dev < 64 ? most[dev][g.log_cluster] : 0;
+  once = known ? most[dev][log] : 0;
   if (!once) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = unsigned(cluster), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(cluster)), cfg.blockDim = dim3(kLoraThreads), cfg.dynamicSmemBytes = S::kSmem;
+    attr.val.clusterDim.x = 1u << log, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1u << log), cfg.blockDim = dim3(kLoraThreads), cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = &attr, cfg.numAttrs = 1;
     if (int e = cuda_status(cudaOccupancyMaxActiveClusters(&once, kernel, &cfg), who)) return e;
     once = max(once, 1);
-    if (dev >= 0 && dev < 64) most[dev][g.log_cluster] = once;
+    if (known) most[dev][log] = once;
   }
-  const dim3 grid(unsigned((g.nvec < once ? g.nvec : once) * cluster));
-  return launch_op(kernel, grid, kLoraThreads, S::kSmem, cluster, s, who, g);
+  if (!call) return Q1_OK;
+  LoraArgs g = *call;
+  g.log_cluster = log;
+  const dim3 grid(unsigned((g.nvec < once ? g.nvec : once) << log));
+  return launch_op(kernel, grid, kLoraThreads, kSmem, 1 << log, s, who, g);
 }
 
 template <class T, bool VEC>
@@ -700,20 +793,15 @@ static int launch_lora(const LoraArgs& g, cudaStream_t s) {
   // Buckets of sixteen vectors where the prompts are long enough to fill them: 1000
   // vectors of 6 adapters 33 us against 40.5 with eight, 652 of 17 63 against 72, 379 of
   // 5 16.2 against 17.6; half filled they cost more (285 of 62: 44 against 33).
-  const bool two = g.nvec > 128 && g.nvec >= 8 * int64_t(g.adapters) && g.rank <= LoraTile<2>::kMaxRank;
-  // The buckets that the vectors can make at most (adapters at random), for the size of the clusters:
-  // 16 CTAs while a cluster for each vector runs at once (one vector of rank 16, 4096
-  // x 4096: 4.8 us against 5.6 with 8), 8 while there are few buckets (64 vectors of 48 adapters: 22 us
-  // against 31 with 4, 88 of 21 16.5 against 17), 4 beyond, where fewer CTAs wait for
-  // each other (338 of 48: 51 us against 79 with 8, 87 of 43 12 against 14.8).
-  int64_t buckets = 0;
-  for (int w = 0; w < g.nvec; w += kLoraWindow) {
-    const int in = min(kLoraWindow, g.nvec - w);
-    buckets += max((in + (two ? 15 : 7)) / (two ? 16 : 8), min(in, g.adapters));
-  }
-  const int cluster = g.nvec * 16 <= 2 * num_sms() ? 16 : buckets <= 48 ? 8 : 4;
-  if (two) return launch_lora<T, 2, VEC>(g, cluster, s);
-  return launch_lora<T, 1, VEC>(g, cluster, s);
+  int once;
+  // (The only use of the number of adapters there are: it bounds those in use.)
+  if (g.nvec > 128 && g.nvec >= 8 * int64_t(g.adapters) && g.rank <= LoraTile<2>::kMaxRank)
+    return launch_lora<T, 2, VEC>(3, once, &g, s);
+  // Clusters of sixteen CTAs while halves of those that run at once are enough for every vector:
+  // one vector of rank 16, 4096 x 4096, 4.8 us against 5.6 with eight; 20 of rank 64, 4096 to
+  // 14336, of one adapter 10.9 against 14.3, of 20 19.0 against 18.9.
+  if (int e = launch_lora<T, 1, VEC>(4, once, nullptr, s)) return e;
+  return launch_lora<T, 1, VEC>(g.nvec <= 2 * once ? 4 : 3, once, &g, s);
 }
 
 }  // namespace q1

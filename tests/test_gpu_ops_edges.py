@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from decode_q1_gemv_gb300 import binding
-from tests.test_gpu_ops import Cache, U, check_attend, normal, rope_table, within
+from tests.test_gpu_ops import Cache, U, check_attend, lora_reference, lora_tol, normal, rope_table, within
 
 pytestmark = pytest.mark.gpu
 
@@ -90,6 +90,29 @@ def test_lora_infinity_in_x_and_scale(value, dtype):
     clean = binding.lora_add(normal(1, 40, 264), a, b, index, base=base)
     got = binding.lora_add(x, a, b, index, base=base)
     assert not torch.isfinite(got[0]).any() and torch.equal(got[1:], clean[1:])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("adapters", [200, 9])  # in the pool, whatever is used: buckets of eight, of sixteen too
+@pytest.mark.parametrize("nvec,used", [(15, 3), (17, 17), (35, 35), (37, 5), (37, 37), (72, 36), (72, 72), (73, 73), (130, 2),
+                                       (130, 130), (300, 3), (511, 100), (513, 7), (1025, 150)])
+def test_lora_buckets_around_what_runs_at_once(nvec, used, adapters, dtype):
+    """The device counts the buckets: clusters whole, in halves, several rounds of either, and vectors without an
+    adapter among them, alone in a half or all of them."""
+    used = min(used, adapters)
+    g = torch.Generator().manual_seed(nvec)
+    of = (torch.randperm(nvec, generator=g) % used).to(torch.int32) + adapters - used
+    of[torch.randperm(nvec, generator=g)[:nvec // 7]] = -1
+    x, base = normal(5, nvec, 136), normal(6, nvec, 50)
+    a, b = normal(7, adapters, 16, 136, std=0.1, dtype=dtype), normal(8, adapters, 50, 16, dtype=dtype)
+    ranks = (torch.arange(adapters, dtype=torch.int32) * 7 % 17).cuda()
+    for index in (of.cuda(), torch.full((nvec,), -1, dtype=torch.int32, device="cuda")):
+        got = binding.lora_add(x, a, b, index, ranks=ranks, base=base)
+        want, mag = lora_reference(x, a, b, index, None, ranks, base)
+        within(got, want, lora_tol(136, mag))
+        assert torch.equal(got[index < 0], base[index < 0])
+        assert torch.equal(got, binding.lora_add(x, a, b, index, ranks=ranks, base=base))
+    assert binding.device_status() == 0
 
 
 # ------------------------------------------------------------------- norm --
