@@ -519,6 +519,9 @@ extern "C" int q1_paged_attention(const void* q, int64_t q_token_stride, int64_t
   if (heads < 1 || heads > 4096 || heads % kv->kv_heads)
     return fail(Q1_ERR_ARG, "%s: heads=%lld is no multiple of kv_heads=%lld up to 4096", who, (long long)heads,
                 (long long)kv->kv_heads);
+  if (int64_t(a.kv.total_new) * (heads / kv->kv_heads) >= (int64_t(1) << 31))
+    return fail(Q1_ERR_ARG, "%s: %lld new tokens of %lld heads a key head are 2^31 rows or more", who, (long long)kv->total_new,
+                (long long)(heads / kv->kv_heads));
   if (!q || !out || !workspace) return fail(Q1_ERR_ARG, "%s: null pointer", who);
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || q_token_stride % 8 || q_head_stride % 8 ||
       out_token_stride % 8 || out_head_stride % 8)

@@ -822,6 +822,8 @@ extern "C" int q1_lora_add(const float* x, int64_t ldx, int64_t nvec, int64_t n,
   if (!aligned16(x) || !aligned16(a) || !aligned16(b) || ldx % 4 || reinterpret_cast<uintptr_t>(base) % 4 ||
       reinterpret_cast<uintptr_t>(out) % 4)
     return fail(Q1_ERR_ARG, "%s: x, a and b must be 16-byte aligned, rows of x multiples of 4", who);
+  if (!aligned4(index) || !aligned4(ranks) || !aligned4(scale))
+    return fail(Q1_ERR_ARG, "%s: index, ranks and scale must be 4-byte aligned", who);
   if (ldx < n || ldb < rows || ldo < rows) return fail(Q1_ERR_ARG, "%s: a row stride is less than its row", who);
   if (base == out && ldb != ldo) return fail(Q1_ERR_ARG, "%s: in place, base and out need the same stride", who);
   LoraArgs g = {x, a, b, index, ranks, scale, base, out, nullptr, ldx, ldb, ldo, int(nvec), int(n), int(rows), int(rank),

@@ -74,6 +74,7 @@ struct Elem<__half> {
 };
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+inline bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 // A launch with programmatic dependent launch (the kernel starts while its
 // predecessor on the stream drains; every thread of it calls pdl_wait before

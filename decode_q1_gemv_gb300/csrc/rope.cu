@@ -116,6 +116,8 @@ int check_paged(const char* who, const q1_paged_kv* kv, Paged& p) {
   if (kv->dim != 64 && kv->dim != 128) return fail(Q1_ERR_ARG, "%s: dim=%lld is not 64 or 128", who, (long long)kv->dim);
   if (!kv->k || !kv->v || !kv->table || !kv->kv_len || !kv->new_start) return fail(Q1_ERR_ARG, "%s: null pointer", who);
   if (!aligned16(kv->k) || !aligned16(kv->v)) return fail(Q1_ERR_ARG, "%s: the cache must be 16-byte aligned", who);
+  if (!aligned4(kv->table) || !aligned4(kv->kv_len) || !aligned4(kv->new_start))
+    return fail(Q1_ERR_ARG, "%s: table, kv_len and new_start must be 4-byte aligned", who);
   if (kv->page_stride % 8 || kv->slot_stride % 8 || kv->head_stride % 8 || kv->page_stride < kv->dim ||
       kv->slot_stride < kv->dim || kv->head_stride < kv->dim || kv->page_stride >= (int64_t(1) << 38) ||
       kv->slot_stride >= (int64_t(1) << 38) || kv->head_stride >= (int64_t(1) << 38))

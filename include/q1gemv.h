@@ -409,7 +409,8 @@ int q8_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ld
  *     anything.  scale : f32 [adapters] or NULL (1).
  * A value of x, or of a weight within the rank, that is no number makes what
  * it goes into no number (an infinite one NaN or infinite), and nothing else.
- * x, a and b must be 16-byte aligned, ldx a multiple of 4.  An index outside
+ * x, a and b must be 16-byte aligned, ldx a multiple of 4, the other arrays 4-byte
+ * aligned.  An index outside
  * -1..adapters-1 counts as -1 and sets the status bit. */
 int q1_lora_add(const float *x, int64_t ldx, int64_t nvec, int64_t n, int64_t rows, const void *a, const void *b,
                 int dtype, int64_t adapters, int64_t rank, const int32_t *index, const int32_t *ranks,
@@ -464,6 +465,7 @@ int64_t q1_paged_attention_workspace(int64_t max_new, int64_t heads, int64_t kv_
  *   q, out : [total_new][heads][dim] of the cache's type, strides in elements
  *     (multiples of 8).  A row that sees no key (p < 0) is zero; rows of no
  *     sequence are left as they are.
+ *   total_new * heads / kv_heads below 2^31.
  *   scale : finite, and so is scale * log2(e).
  *   max_new : the most new tokens any sequence has (with the batch and the
  *     length of the table it picks the kernel: a larger or smaller number costs
