@@ -22,7 +22,11 @@ struct AttendArgs {
   int ctas;                // CTAs the units are split over, or of a cluster
   int tiles;               // with clusters: of a key head, at once
   int least_rows, most_rows;  // of a sequence that this launch takes (its new tokens times the group)
-  bool beside;             // the launch before is the same call's, of other sequences
+  // The launch before is the same call's, of other sequences: no wait for it at the start.
+  // All of this library's kernels wait for the one before them before they end, and k_attend_tc
+  // before it lets the next start, so this holds also where another thread launches one of them
+  // in between: it starts behind k_attend_tc's wait, and what follows waits for all of them.
+  bool beside;
 };
 
 // n / group, 0 <= n < 2^31: n * (2^32 / group + 1) / 2^32 is the quotient or

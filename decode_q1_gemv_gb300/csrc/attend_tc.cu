@@ -373,10 +373,18 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               // out; the output adds them to the rows that see them.
               const int lo = max(0, of_all - unit0) * 8 + lane, hi = min(valid, kTcKeys) * 8;
               NoNumbers<T> none;
-#pragma unroll 4
-              for (int i = lo; i < hi; i += 32)
+#pragma unroll 1
+              for (int i = lo - lane; i < hi; i += 128) {  // (loads side by side: 22.8 us for two prompts of 400, 23.5 without)
+                uint4 x[4][Shape::kHalves];
 #pragma unroll
-                for (int h = 0; h < Shape::kHalves; ++h) none.look(v[h * kHalf + i]);
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                  for (int h = 0; h < Shape::kHalves; ++h) x[e][h] = v[h * kHalf + min(i + e * 32 + lane, hi - 1)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                  for (int h = 0; h < Shape::kHalves; ++h) none.look(x[e][h]);
+              }
               if (__any_sync(0xffffffffu, none.found())) {
                 taken_out_s = 1;
                 __threadfence_block();  // whoever finds them gone finds this
