@@ -36,8 +36,8 @@
 // Vectors are grouped on the device: in a window of 64 vectors, every
 // eighth (sixteenth) vector of an adapter leads a bucket of it and the next
 // ones of that window.  The device also counts the buckets, and gives each a
-// cluster while all run at once, else half a cluster: what a call takes depends
-// on the adapters that its vectors name, not on how many there are.
+// cluster while all run at once, else half a cluster: what a call of up to 288 vectors
+// takes depends on the adapters that its vectors name, not on how many there are.
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
@@ -790,18 +790,23 @@ static int launch_lora(int log, int& once, const LoraArgs* call, cudaStream_t s)
 
 template <class T, bool VEC>
 static int launch_lora(const LoraArgs& g, cudaStream_t s) {
-  // Buckets of sixteen vectors where the prompts are long enough to fill them: 1000
-  // vectors of 6 adapters 33 us against 40.5 with eight, 652 of 17 63 against 72, 379 of
-  // 5 16.2 against 17.6; half filled they cost more (285 of 62: 44 against 33).
-  int once;
-  // (The only use of the number of adapters there are: it bounds those in use.)
-  if (g.nvec > 128 && g.nvec >= 8 * int64_t(g.adapters) && g.rank <= LoraTile<2>::kMaxRank)
-    return launch_lora<T, 2, VEC>(3, once, &g, s);
   // Clusters of sixteen CTAs while halves of those that run at once are enough for every vector:
   // one vector of rank 16, 4096 x 4096, 4.8 us against 5.6 with eight; 20 of rank 64, 4096 to
   // 14336, of one adapter 10.9 against 14.3, of 20 19.0 against 18.9.
+  int once;
   if (int e = launch_lora<T, 1, VEC>(4, once, nullptr, s)) return e;
-  return launch_lora<T, 1, VEC>(g.nvec <= 2 * once ? 4 : 3, once, &g, s);
+  if (g.nvec <= 2 * once) return launch_lora<T, 1, VEC>(4, once, &g, s);
+  if (int e = launch_lora<T, 1, VEC>(3, once, nullptr, s)) return e;
+  // Buckets of sixteen vectors pay where those of eight are more than run at once even if all are
+  // full, and if they fill: 1000 vectors of one adapter 52 us against 62 in eights, 384 29 against 32, but
+  // 192 27.5 against 19.5; in runs of 16 tokens 78 against 63 (1000 of 62), of 12 in any order 70 against
+  // 53 (300 of 18).  Runs of 32 break even.  How many adapters there are bounds those in use, and
+  // is all that the host knows; of prompts of few adapters out of many it makes eights (in
+  // one kernel that has both, which the device could choose from, either takes a third longer,
+  // and a launch of each, one of which leaves, 2 to 6 us).
+  if (g.nvec > 8 * once && g.nvec >= 32 * int64_t(g.adapters) && g.rank <= LoraTile<2>::kMaxRank)
+    return launch_lora<T, 2, VEC>(3, once, &g, s);
+  return launch_lora<T, 1, VEC>(3, once, &g, s);
 }
 
 }  // namespace q1
