@@ -22,7 +22,7 @@
 // two CTAs an SM hold 29 MB of reads in flight.
 //
 // Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64
-// sequences, 2.04 GB of keys and values, 309 us: 6.6 TB/s, 0.97 of the copy
+// sequences, 2.04 GB of keys and values, 312 us: 6.5 TB/s, 0.98 of the copy
 // bandwidth; one token over 8191 keys, 34 MB, 11.8 us with its join (5.0 at that
 // bandwidth: finding the share, the pages and the join's launch are the rest).
 #include <algorithm>

@@ -39,8 +39,8 @@
 // registers come out worse).
 //
 // Measured (32 heads over 8 of 128, bf16): 2048 new tokens over 16001 keys, 0.503
-// Tflop, in 351 us with the join: 1.43 Pflop/s, 0.76 of this card's matrix product
-// rate (1.88); the tensor pipe is active 64 % of the cycles (profiled launch, 342 us).
+// Tflop, in 351 us with the join: 1.43 Pflop/s, 0.73 of this card's matrix product
+// rate (1.95); the tensor pipe is active 63 % of the cycles (profiled launch, 345 us).
 // What is left: with D = 128 the two tiles fill tensor memory, so a tile's scores,
 // softmax and product with V follow each other, and two tiles hide each other's only in
 // part.  With D = 64 the softmax bounds it: its arithmetic alone takes 346 cycles a

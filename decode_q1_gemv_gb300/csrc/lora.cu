@@ -27,9 +27,9 @@
 // redirected.
 //
 // Measured: 64 vectors, most with an adapter of their own (f16, ranks 16 to 64, 4096
-// to 14336), 63 MB, in 20.7 us: 3.0 TB/s, 0.45 of the copy bandwidth; 1000 vectors of
-// prompts (bf16, rank 32, 14336 to 4096), 94 MB, in 33 us: 2.8 TB/s.  One vector of
-// rank 16, 4096 x 4096: 4.6 us.  Half of the issue slots are used in the
+// to 14336), 63 MB, in 20.4 us: 3.1 TB/s, 0.46 of the copy bandwidth; 1000 vectors of
+// prompts (bf16, rank 32, 14336 to 4096), 94 MB, in 32 us: 3.0 TB/s.  One vector of
+// rank 16, 4096 x 4096: 4.7 us.  Half of the issue slots are used in the
 // products; the rest of a bucket's time is its chain: index, first product,
 // exchange through the cluster, second product.
 //

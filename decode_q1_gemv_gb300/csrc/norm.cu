@@ -8,8 +8,8 @@
 // groups, so a q8_0 block of 32 values is 8 (f32) or 4 (16-bit) neighbouring
 // lanes and its maximum costs 3 or 2 shuffles, as in quant.cu.
 //
-// Measured: 8191 rows of 4128 f32 values with residual, 442 MB, in 67.8 us: 6.5 TB/s,
-// 0.96 of the copy bandwidth of the card (6.78 TB/s).  One row of 4096 takes 2.6 us a
+// Measured: 8191 rows of 4128 f32 values with residual, 442 MB, in 66.7 us: 6.6 TB/s,
+// 0.99 of the copy bandwidth of the card (6.69 TB/s).  One row of 4096 takes 2.6 us a
 // launch in a chain of them, 64 bf16 rows 2.4 us: the launch and one round of
 // loads, not bytes.
 //

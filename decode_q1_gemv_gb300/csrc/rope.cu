@@ -9,7 +9,7 @@
 // threads for the sequence, then two dependent loads.
 //
 // Measured: 5751 tokens of seven prompts (32 + 8 + 8 heads of 64, 107 MB) in
-// 16.4 us: 6.5 TB/s, 0.96 of the copy bandwidth.  64 single tokens (heads of 128):
+// 16.4 us (15.3 in a chain of launches, where a part stays in L2): the copy bandwidth.  64 single tokens (heads of 128):
 // 2.5 us a launch; while there are fewer tokens than SMs, several CTAs share a token's units.
 #include "paged.cuh"
 
