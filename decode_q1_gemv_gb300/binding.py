@@ -14,7 +14,7 @@ Tensors:
   d       torch.int16/uint16 [nvec, n/32] (fp16 bit patterns; torch.float16 accepted)
   out     torch.float32 [nvec, rows] (or [rows])
 The operators between the products (add_rms_norm, lora_add, rope_append,
-paged_attention) name their tensors in their own docstrings.  With `stream`
+paged_attention and their forms for a q8_0 cache, gated_act) and sample name their tensors in their own docstrings.  With `stream`
 they run on it and allocate from it what they return; without, on the current one.
 """
 from __future__ import annotations
@@ -41,7 +41,8 @@ EXPORTS = ("q1_last_error", "q1_0_packed_bytes", "q1_0_pack", "q1_0_unpack", "q8
            "q1_device_status", "q2_0_packed_bytes", "q2_0_pack", "q2_0_unpack", "q2_0_gemv", "q2_0_gemv_multi",
            "q2_0_gemv_multi_plan", "q1_gemm_small_kernel", "q1_0_gemm_small_noalloc",
            "q1_0_gemv_multi_prefetch", "q2_0_gemv_multi_prefetch", "q8_add_rms_norm", "q1_lora_add",
-           "q1_rope_append", "q1_paged_attention_workspace", "q1_paged_attention")
+           "q1_rope_append", "q1_paged_attention_workspace", "q1_paged_attention", "q1_rope_append_q8",
+           "q1_cache_read_q8", "q1_paged_attention_q8_workspace", "q1_paged_attention_q8", "q8_gated_act", "q1_sample")
 
 MAX_PRODUCTS = 256
 
@@ -76,6 +77,24 @@ class PagedKV(ctypes.Structure):
                 ("new_start", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
                 ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64), ("batch", ctypes.c_int64),
                 ("total_new", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class PagedQ8(ctypes.Structure):
+    """Mirror of q1_paged_q8 (include/q1gemv.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_slot_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p), ("new_start", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("batch", ctypes.c_int64), ("total_new", ctypes.c_int64)]
+
+
+class Sampling(ctypes.Structure):
+    """Mirror of q1_sampling (include/q1gemv.h)."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
 
 
 class Q1Error(RuntimeError):
@@ -155,6 +174,18 @@ def load():
         lib.q1_paged_attention_workspace.restype = I64
         lib.q1_paged_attention.argtypes = [P, I64, I64, I64, F, ctypes.POINTER(PagedKV), I64, P, I64, I64, P, I64, P]
         lib.q1_paged_attention.restype = I
+        lib.q1_rope_append_q8.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, I, I64, P, I, ctypes.POINTER(PagedQ8), P]
+        lib.q1_rope_append_q8.restype = I
+        lib.q1_cache_read_q8.argtypes = [ctypes.POINTER(PagedQ8), I, P, P, P]
+        lib.q1_cache_read_q8.restype = I
+        lib.q1_paged_attention_q8_workspace.argtypes = [I64, I64, I64, I64, I64, I64]
+        lib.q1_paged_attention_q8_workspace.restype = I64
+        lib.q1_paged_attention_q8.argtypes = [P, I64, I64, I64, F, I, ctypes.POINTER(PagedQ8), I64, P, I64, I64, P, I64, P]
+        lib.q1_paged_attention_q8.restype = I
+        lib.q8_gated_act.argtypes = [P, I64, P, I64, I64, I64, I, I, P, I64, P, P, P]
+        lib.q8_gated_act.restype = I
+        lib.q1_sample.argtypes = [P, I64, I64, I64, I, P, ctypes.POINTER(Sampling), P, P]
+        lib.q1_sample.restype = I
         lib.q1_0_verify.argtypes = [I, ctypes.c_char_p, ctypes.c_size_t]
         lib.q1_0_verify.restype = I
         spec = importlib.util.spec_from_file_location("decode_q1_gemv_gb300._marshal", _build.MARSHAL)
@@ -598,6 +629,129 @@ def paged_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tenso
     if stream is not None:
         return _on_stream(call, stream, q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace)
     return call(q, cache_k, cache_v, table, kv_len, new_start, max_new, scale, out, workspace, _current_stream_of(q))
+
+
+# ------------------------------------------- the cache in q8_0 --
+_TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _type_code(dtype) -> int:
+    if dtype not in _TYPE_CODES:
+        raise TypeError(f"dtype {dtype} is none of {list(_TYPE_CODES)}")
+    return _TYPE_CODES[dtype]
+
+
+def paged_q8(cache_k: torch.Tensor, cache_v: torch.Tensor, scale_k: torch.Tensor, scale_v: torch.Tensor,
+             table: torch.Tensor, kv_len: torch.Tensor, new_start: torch.Tensor, total_new: int) -> PagedQ8:
+    """The q1_paged_q8 that the calls below make of these tensors, for callers of the C ABI."""
+    return PagedQ8.from_buffer_copy((_marshal or _native()).paged_q8(cache_k, cache_v, scale_k, scale_v, table, kv_len,
+                                                                     new_start, total_new))
+
+
+def rope_append_q8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, cache_k: torch.Tensor,
+                   cache_v: torch.Tensor, scale_k: torch.Tensor, scale_v: torch.Tensor, table: torch.Tensor,
+                   kv_len: torch.Tensor, new_start: torch.Tensor, q_out: torch.Tensor | None = None,
+                   interleaved: bool = False, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """q1_rope_append_q8: rope_append into a q8_0 cache; q comes back in q_out's
+    type, or `dtype` (bf16 or f16).
+
+    The cache: cache_k and cache_v int8 [pages, page_size, kv_heads, dim] hold
+    quants, scale_k and scale_v (fp16, or its bits as int16) [pages, page_size,
+    kv_heads, dim / 32] the scale of each 32 of them (the first three axes in any order of
+    storage; a head's slots side by side are read fastest); table, kv_len and
+    new_start as in rope_append."""
+    call = (_marshal or _native()).rope_append_q8
+    if stream is not None:
+        return _on_stream(call, stream, q, k, v, cos_sin, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, q_out,
+                          bool(interleaved), _type_code(dtype))
+    return call(q, k, v, cos_sin, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, q_out, bool(interleaved),
+                _type_code(dtype), _current_stream_of(q))
+
+
+def cache_read_q8(cache_k: torch.Tensor, cache_v: torch.Tensor, scale_k: torch.Tensor, scale_v: torch.Tensor,
+                  table: torch.Tensor, kv_len: torch.Tensor, new_start: torch.Tensor, tokens: int,
+                  dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """q1_cache_read_q8: keys and values [tokens, kv_heads, dim] (f32, bf16 or f16)
+    of the last new_start[b + 1] - new_start[b] tokens of each sequence (the
+    new ones of a call; all, where new_start counts whole lengths), packed as new_start says."""
+    call = (_marshal or _native()).cache_read_q8
+    if stream is not None:
+        return _on_stream(call, stream, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, tokens, _type_code(dtype),
+                          k_out, v_out)
+    return call(cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, tokens, _type_code(dtype), k_out, v_out,
+                _current_stream_of(cache_k))
+
+
+def paged_attention_q8_workspace(max_new: int, heads: int, kv_heads: int, dim: int, table_tokens: int,
+                                 sequences: int = 1) -> int:
+    """Bytes of paged_attention_q8's workspace on the current device; where max_new
+    asks for the tensor-core kernel, with 16-bit copies of `sequences`
+    sequences of up to table_tokens (the table's width times the page size)."""
+    v = load().q1_paged_attention_q8_workspace(int(max_new), int(heads), int(kv_heads), int(dim), int(table_tokens), int(sequences))
+    if v < 0:
+        raise Q1Error(int(v), last_error())
+    return int(v)
+
+
+def paged_attention_q8(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tensor, scale_k: torch.Tensor,
+                       scale_v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, new_start: torch.Tensor,
+                       max_new: int, scale: float | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q1_paged_attention_q8: paged_attention over a q8_0 cache (as in
+    rope_append_q8), q [tokens, heads, dim] bf16 or f16.  A given workspace
+    (uint8) must hold paged_attention_q8_workspace(...) bytes of one
+    sequence; the call's own has room for the copies of a gigabyte of sequences."""
+    call = (_marshal or _native()).paged_attention_q8
+    if stream is not None:
+        return _on_stream(call, stream, q, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, max_new, scale, out,
+                          workspace)
+    return call(q, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, max_new, scale, out, workspace,
+                _current_stream_of(q))
+
+
+# ------------------------- the gated activation, and the next token --
+class GateOut(NamedTuple):
+    """What gated_act returns; None where an output was not asked for."""
+    y: torch.Tensor | None
+    q: torch.Tensor | None
+    d: torch.Tensor | None
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def gated_act(gate: torch.Tensor, up: torch.Tensor, activation: str = "silu", out: str = "q8", y: torch.Tensor | None = None,
+              q: torch.Tensor | None = None, d: torch.Tensor | None = None, stream=None) -> GateOut:
+    """q8_gated_act of gate and up [nvec, n] (f32, bf16 or f16; rows may be strided):
+    y = activation(gate) * up ("silu", or "gelu" by its tanh form).  out "q8" gives the q8_0
+    form of y (q int8 [nvec, n], d int16 fp16 bits [nvec, n/32]), "y" y itself in the
+    inputs' type (which may be gate or up), "both" both."""
+    if out not in ("q8", "y", "both"):
+        raise ValueError("out must be 'q8', 'y' or 'both'")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    call = (_marshal or _native()).gated_act
+    code = ACTIVATIONS[activation]
+    if stream is not None:
+        return GateOut(*_on_stream(call, stream, gate, up, code, out != "q8", out != "y", y, q, d))
+    return GateOut(*call(gate, up, code, out != "q8", out != "y", y, q, d, _current_stream_of(gate)))
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q1_sample: the next token (int32 [rows]) of each row of logits [rows, vocab]
+    (f32, bf16 or f16; rows may be strided), drawn with the random numbers uniform
+    (f32 [rows], in [0, 1)).  temperature, top_p and min_p are numbers or f32
+    [rows], top_k a number or int32 [rows].  Of the tokens by falling
+    logits (equal ones by rising index) the first top_k stay (0: all), of
+    these the fewest first ones with top_p of their probability, of these those of at
+    least min_p times the largest; temperature 0 takes the largest.  A row
+    without a distribution (a NaN, +inf, all -inf) gives -1."""
+    call = (_marshal or _native()).sample
+    if stream is not None:
+        return _on_stream(call, stream, logits, uniform, temperature, top_k, top_p, min_p, out)
+    return call(logits, uniform, temperature, top_k, top_p, min_p, out, _current_stream_of(logits))
 
 
 class Q1Linear:

@@ -44,25 +44,8 @@ constexpr int kWarpsS = 4;
 // Units of an item that is not split (30 tokens over up to 909 keys: 7.2 us with
 // 2, 8.0 with 4, 9.8 with 8; two short prompts 22.8, 23.6, 22.0).
 constexpr int kWholeS = 2;
-constexpr int kJoinSlices = 4;   // CTAs that join an item
 constexpr int kStagesS = 3;  // 2 x 96 KB of reads in flight an SM at D = 128
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 template <class T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
@@ -395,22 +378,6 @@ __global__ void __launch_bounds__(kWarpsS * 32) k_attend(AttendArgs a) {
   if (a.beside) pdl_wait();  // what follows waits for this launch, and with it for the one before
 }
 
-// The joins of a call that ran both kernels, in one launch.
-struct JoinBoth {
-  AttendArgs many, few;
-};
-template <class T, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join_both(const __grid_constant__ JoinBoth a) {
-  __shared__ float sh[kJoinThreads][6];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int b = blockIdx.x, first = a.many.ctas * kTcJoinSlices;
-  if (b < first)
-    join_item<T, kTcRows, D, true>(a.many, b / kTcJoinSlices, b % kTcJoinSlices, kTcJoinSlices, sh);
-  else
-    join_item<T, kRowsS, D, false>(a.few, (b - first) / kJoinSlices, (b - first) % kJoinSlices, kJoinSlices, sh);
-}
-
 // Where clusters do not take the call (attend_cluster): which kernel, from the
 // rows a key head at most (new tokens times the group).
 // One sequence: this one up to 32 rows (32 over 4000 keys: 16.4 us against 17.3;
@@ -492,7 +459,7 @@ static int launch_attend(AttendArgs& a, int64_t max_new, bool only_clusters, voi
   // No item has more units than stay whole: nothing to join.
   if (a.kv.table_tokens <= kWholeS * kKeysS) return Q1_OK;
   if (many && many->ctas)
-    return launch_op<JoinBoth>(k_attend_join_both<T, D>, dim3(unsigned(many->ctas * kTcJoinSlices + a.ctas * kJoinSlices)), kJoinThreads, 0, 1, s,
+    return launch_op<JoinBoth>(k_attend_join_both<T, kRowsS, D>, dim3(unsigned(many->ctas * kTcJoinSlices + a.ctas * kJoinSlices)), kJoinThreads, 0, 1, s,
                                who, {*many, a});
   return launch_op(k_attend_join<T, kRowsS, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
 }

@@ -43,6 +43,23 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 at -inf
   return y;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
 // The work.  Rows of (sequence b, key head h) are its new tokens times the
 // group's heads, token-major; a tile is TM of them, an item a tile with all
 // keys it may see, cut into units of TK keys (one unit at least).  Items lie on one axis,
@@ -263,6 +280,7 @@ __device__ __forceinline__ float* partial(const AttendArgs& a, int cta, int slot
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinSlices = 4;   // CTAs that join an item of few rows
 constexpr int kJoinGroups = 8;   // threads that share a value's parts, at most
 
 constexpr int kJoinHeld = 4;     // parts whose weights a thread holds
@@ -409,5 +427,21 @@ inline void place_workspace(AttendArgs& a, void* workspace) {
 constexpr int kTcRows = 256, kTcJoinSlices = 16;  // rows of an item; CTAs that join it
 int64_t attend_tc_workspace(int dim);
 int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined);
+
+// The joins of a call that ran both kernels, in one launch; `few` has tiles of TM rows.
+struct JoinBoth {
+  AttendArgs many, few;
+};
+template <class T, int TM, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join_both(const __grid_constant__ JoinBoth a) {
+  __shared__ float sh[kJoinThreads][6];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x, first = a.many.ctas * kTcJoinSlices;
+  if (b < first)
+    join_item<T, kTcRows, D, true>(a.many, b / kTcJoinSlices, b % kTcJoinSlices, kTcJoinSlices, sh);
+  else
+    join_item<T, TM, D, false>(a.few, (b - first) / kJoinSlices, (b - first) % kJoinSlices, kJoinSlices, sh);
+}
 
 }  // namespace q1

@@ -133,7 +133,7 @@ void check(int64_t rc, const char* what) {
 c10::Device one_device(PyObject* const* a, Py_ssize_t count) {
   const at::Tensor* first = nullptr;
   for (Py_ssize_t i = 0; i < count; ++i) {
-    if (a[i] == Py_None || PyLong_Check(a[i]) || !THPVariable_Check(a[i])) continue;  // (the check of others is slow)
+    if (a[i] == Py_None || PyLong_Check(a[i]) || PyFloat_Check(a[i]) || !THPVariable_Check(a[i])) continue;  // (the check of others is slow)
     const at::Tensor& t = THPVariable_Unpack(a[i]);
     if (!t.is_cuda()) continue;
     if (!first) first = &t;
@@ -309,10 +309,204 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
   });
 }
 
+// cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start
+q1_paged_q8 paged_q8(PyObject* const* a, int64_t total_new) {
+  const at::Tensor &k = tensor(a[0], "cache_k"), &v = tensor(a[1], "cache_v"), &ks = tensor(a[2], "scale_k"),
+                   &vs = tensor(a[3], "scale_v"), &table = tensor(a[4], "table");
+  if (k.dim() != 4) refuse(PyExc_ValueError, "cache_k must be [pages, page_size, kv_heads, dim]");
+  if (table.dim() != 2) refuse(PyExc_ValueError, "table must be [batch, width]");
+  q1_paged_q8 p = {};
+  p.pages = k.size(0), p.page_size = k.size(1), p.kv_heads = k.size(2), p.dim = k.size(3);
+  if (p.dim % 32) refuse(PyExc_ValueError, "the cache's dim %lld is no multiple of 32", (long long)p.dim);
+  const Sizes<4> scales = {p.pages, p.page_size, p.kv_heads, p.dim / 32};
+  p.k = static_cast<int8_t*>(pointer(k, "cache_k", kI8, k.sizes()));
+  p.v = static_cast<int8_t*>(pointer(v, "cache_v", kI8, k.sizes()));
+  p.k_scale = static_cast<uint16_t*>(pointer(ks, "scale_k", kScale, scales));
+  p.v_scale = static_cast<uint16_t*>(pointer(vs, "scale_v", kScale, scales));
+  for (int i = 0; i < 3; ++i) {
+    if (stride(k, i, 0) != stride(v, i, 0)) refuse(PyExc_ValueError, "cache_k and cache_v must have the same strides");
+    if (stride(ks, i, 0) != stride(vs, i, 0)) refuse(PyExc_ValueError, "scale_k and scale_v must have the same strides");
+  }
+  p.page_stride = stride(k, 0, p.dim), p.slot_stride = stride(k, 1, p.dim), p.head_stride = stride(k, 2, p.dim);
+  p.scale_page_stride = stride(ks, 0, p.dim / 32), p.scale_slot_stride = stride(ks, 1, p.dim / 32);
+  p.scale_head_stride = stride(ks, 2, p.dim / 32);
+  p.batch = table.size(0), p.table_width = table.size(1);
+  p.table = static_cast<const int32_t*>(pointer(table, "table", kI32, table.sizes()));
+  p.table_stride = stride(table, 0, p.table_width);
+  const Sizes<1> batch = {p.batch}, bounds = {p.batch + 1};
+  p.kv_len = static_cast<const int32_t*>(pointer(tensor(a[5], "kv_len"), "kv_len", kI32, batch, true));
+  p.new_start = static_cast<const int32_t*>(pointer(tensor(a[6], "new_start"), "new_start", kI32, bounds, true));
+  p.total_new = total_new;
+  return p;
+}
+
+// The type of a code, for calls that do not take it from a tensor.
+at::ScalarType type_of_code(PyObject* o, unsigned types) {
+  const int64_t code = integer(o);
+  const at::ScalarType t = code == Q1_F32 ? at::kFloat : code == Q1_BF16 ? at::kBFloat16 : code == Q1_F16 ? at::kHalf : at::kByte;
+  if (!is_type(t, types)) refuse(PyExc_TypeError, "dtype must be one of %s", names_of(types).c_str());
+  return t;
+}
+
+// q, k, v, cos_sin, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, q_out, interleaved, type code, stream
+PyObject* rope_append_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 15, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &cs = tensor(a[3], "cos_sin");
+    if (q.dim() != 2 || cs.dim() != 2) refuse(PyExc_ValueError, "q must be [tokens, heads * dim] and cos_sin [positions, rot]");
+    const int64_t total = q.size(0);
+    const q1_paged_q8 kv = paged_q8(a + 4, total);
+    if (q.size(1) % kv.dim) refuse(PyExc_ValueError, "q must be [tokens, heads * dim] and cos_sin [positions, rot]");
+    const int64_t heads = q.size(1) / kv.dim, width = kv.kv_heads * kv.dim;
+    const Sizes<2> kv_shape = {total, width};
+    const Sizes<3> out_shape = {total, heads, kv.dim};
+    const at::ScalarType type = a[11] == Py_None ? type_of_code(a[13], kBf16 | kF16) : tensor(a[11], "q_out").scalar_type();
+    void* pq = pointer(q, "q", kF32, q.sizes());
+    at::Tensor out = given_or_new(a[11], "q_out", out_shape, q, type);
+    check(q1_rope_append_q8(static_cast<const float*>(pq), stride(q, 0, heads * kv.dim),
+                            static_cast<const float*>(pointer(k, "k", kF32, kv_shape)), stride(k, 0, width),
+                            static_cast<const float*>(pointer(v, "v", kF32, kv_shape)), stride(v, 0, width),
+                            static_cast<const float*>(pointer(cs, "cos_sin", kF32, cs.sizes(), true)), cs.size(0), cs.size(1),
+                            a[12] == Py_True, heads, pointer(out, "q_out", kBf16 | kF16, out_shape, true), type_code(type), &kv,
+                            reinterpret_cast<void*>(integer(a[14]))),
+          "q1_rope_append_q8");
+    return THPVariable_Wrap(out);
+  });
+}
+
+// cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, tokens, type code, k_out, v_out, stream
+PyObject* cache_read_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 12, [&]() -> PyObject* {
+    const int64_t total = integer(a[7]);
+    const q1_paged_q8 kv = paged_q8(a, total);
+    if (total < 1) refuse(PyExc_ValueError, "tokens must be positive");
+    const unsigned types = kF32 | kBf16 | kF16;
+    const Sizes<3> shape = {total, kv.kv_heads, kv.dim};
+    const at::ScalarType type = a[9] != Py_None    ? tensor(a[9], "k_out").scalar_type()
+                                : a[10] != Py_None ? tensor(a[10], "v_out").scalar_type()
+                                                   : type_of_code(a[8], types);
+    const at::Tensor& like = THPVariable_Unpack(a[0]);
+    at::Tensor k = given_or_new(a[9], "k_out", shape, like, type), v = given_or_new(a[10], "v_out", shape, like, type);
+    void* pk = pointer(k, "k_out", types, shape, true);
+    check(q1_cache_read_q8(&kv, type_code(type), pk, pointer(v, "v_out", type_bit(type), shape, true),
+                           reinterpret_cast<void*>(integer(a[11]))),
+          "q1_cache_read_q8");
+    return Py_BuildValue("(NN)", THPVariable_Wrap(k), THPVariable_Wrap(v));
+  });
+}
+
+// Sequences whose 16-bit copies the attention's own workspace holds at once: a
+// gigabyte of them, and one at least.
+int64_t copied_at_once(int64_t max_new, int64_t heads, const q1_paged_q8& kv) {
+  const int64_t tokens = kv.table_width * kv.page_size;
+  const int64_t one = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, tokens, 1);
+  const int64_t two = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, tokens, 2);
+  if (one < 0 || two <= one) return 1;
+  const int64_t fit = (int64_t(1) << 30) / (two - one);
+  return fit < 1 ? 1 : fit < kv.batch ? fit : kv.batch;
+}
+
+// q, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, max_new, scale (or None), out, workspace, stream
+PyObject* paged_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 13, [&]() -> PyObject* {
+    const at::Tensor& q = tensor(a[0], "q");
+    if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [tokens, heads, dim]");
+    const int64_t total = q.size(0), heads = q.size(1), dim = q.size(2);
+    const q1_paged_q8 kv = paged_q8(a + 1, total);
+    if (kv.dim != dim) refuse(PyExc_ValueError, "q has dim %lld, the cache %lld", (long long)dim, (long long)kv.dim);
+    void* pq = pointer(q, "q", kBf16 | kF16, q.sizes());
+    const unsigned type = type_bit(q.scalar_type());
+    const int64_t max_new = integer(a[8]);
+    const double scale = a[9] == Py_None ? 1.0 / std::sqrt(double(dim)) : number(a[9]);
+    at::Tensor out = given_or_new(a[10], "out", q.sizes(), q, q.scalar_type());
+    at::Tensor ws;
+    if (a[11] != Py_None) {
+      ws = tensor(a[11], "workspace");
+    } else {
+      const int64_t bytes = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, dim, kv.table_width * kv.page_size,
+                                                            copied_at_once(max_new, heads, kv));
+      check(bytes < 0 ? bytes : Q1_OK, "q1_paged_attention_q8");
+      ws = at::empty({bytes}, q.options().dtype(at::kByte));
+    }
+    check(q1_paged_attention_q8(pq, stride(q, 0, heads * dim), stride(q, 1, dim), heads, static_cast<float>(scale),
+                                type_code(q.scalar_type()), &kv, max_new, pointer(out, "out", type, q.sizes()),
+                                stride(out, 0, heads * dim), stride(out, 1, dim), pointer(ws, "workspace", kU8, ws.sizes(), true),
+                                ws.numel(), reinterpret_cast<void*>(integer(a[12]))),
+          "q1_paged_attention_q8");
+    return THPVariable_Wrap(out);
+  });
+}
+
+// gate, up, activation code, want_y, want_q8, y, q, d, stream
+PyObject* gated_act(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 9, [&]() -> PyObject* {
+    const at::Tensor &gate = tensor(a[0], "gate"), &up = tensor(a[1], "up");
+    if (gate.dim() != 2) refuse(PyExc_ValueError, "gate must be [nvec, n]");
+    const int64_t nvec = gate.size(0), n = gate.size(1);
+    const unsigned type = type_bit(gate.scalar_type());
+    if (!type) refuse(PyExc_TypeError, "gate has dtype %s, expected one of float32, bfloat16, float16", at::toString(gate.scalar_type()));
+    const bool want_y = a[3] == Py_True, want_q8 = a[4] == Py_True;
+    if (want_q8 && n % 32) refuse(PyExc_ValueError, "the q8_0 form needs n to be a multiple of 32");
+    const Sizes<2> shape = {nvec, n}, scales = {nvec, n / 32};
+    void* pg = pointer(gate, "gate", type, shape);
+    void* pu = pointer(up, "up", type, shape);
+    at::Tensor y, q, d;
+    if (want_y) y = given_or_new(a[5], "y", shape, gate, gate.scalar_type());
+    if (want_q8) q = given_or_new(a[6], "q", shape, gate, at::kChar), d = given_or_new(a[7], "d", scales, gate, at::kShort);
+    check(q8_gated_act(pg, stride(gate, 0, n), pu, stride(up, 0, n), nvec, n, type_code(gate.scalar_type()),
+                       static_cast<int>(integer(a[2])), want_y ? pointer(y, "y", type, shape) : nullptr, want_y ? stride(y, 0, n) : 0,
+                       want_q8 ? static_cast<int8_t*>(pointer(q, "q", kI8, shape, true)) : nullptr,
+                       want_q8 ? static_cast<uint16_t*>(pointer(d, "d", kScale, scales, true)) : nullptr,
+                       reinterpret_cast<void*>(integer(a[8]))),
+          "q8_gated_act");
+    return Py_BuildValue("(NNN)", want_y ? THPVariable_Wrap(y) : Py_NewRef(Py_None), want_q8 ? THPVariable_Wrap(q) : Py_NewRef(Py_None),
+                         want_q8 ? THPVariable_Wrap(d) : Py_NewRef(Py_None));
+  });
+}
+
+// logits, uniform, temperature, top_k, top_p, min_p (tensors or numbers), out, stream
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 8, [&]() -> PyObject* {
+    const at::Tensor& logits = tensor(a[0], "logits");
+    if (logits.dim() != 2) refuse(PyExc_ValueError, "logits must be [rows, vocab]");
+    const Sizes<1> rows = {logits.size(0)};
+    void* pl = pointer(logits, "logits", kF32 | kBf16 | kF16, logits.sizes());
+    q1_sampling s = {};
+    const auto real = [&](PyObject* o, const char* name, const float** each, float* all) {
+      if (!PyFloat_Check(o) && !PyLong_Check(o) && THPVariable_Check(o))
+        *each = static_cast<const float*>(pointer(o, name, kF32, rows, true));
+      else
+        *all = static_cast<float>(number(o));
+    };
+    real(a[2], "temperature", &s.temperature, &s.temperature_all);
+    real(a[4], "top_p", &s.top_p, &s.top_p_all);
+    real(a[5], "min_p", &s.min_p, &s.min_p_all);
+    if (!PyLong_Check(a[3]) && THPVariable_Check(a[3])) {
+      s.top_k = static_cast<const int32_t*>(pointer(a[3], "top_k", kI32, rows, true));
+    } else {
+      const int64_t k = integer(a[3]);  // beyond any vocabulary: as good as all
+      s.top_k_all = k < 0 ? 0 : k > (int64_t(1) << 30) ? 1 << 30 : static_cast<int32_t>(k);
+    }
+    at::Tensor out = given_or_new(a[6], "out", rows, logits, at::kInt);
+    check(q1_sample(pl, stride(logits, 0, logits.size(1)), rows[0], logits.size(1), type_code(logits.scalar_type()),
+                    static_cast<const float*>(pointer(tensor(a[1], "uniform"), "uniform", kF32, rows, true)), &s,
+                    static_cast<int32_t*>(pointer(out, "out", kI32, rows, true)), reinterpret_cast<void*>(integer(a[7]))),
+          "q1_sample");
+    return THPVariable_Wrap(out);
+  });
+}
+
 // cache_k, cache_v, table, kv_len, new_start, total_new -> the bytes of the q1_paged_kv
 PyObject* make_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t count) {
   return guarded(a, count, 6, [&]() -> PyObject* {
     const q1_paged_kv kv = paged_kv(a, integer(a[5]));
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&kv), sizeof kv);
+  });
+}
+
+// cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, total_new -> the bytes of the q1_paged_q8
+PyObject* make_paged_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(a, count, 8, [&]() -> PyObject* {
+    const q1_paged_q8 kv = paged_q8(a, integer(a[7]));
     return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&kv), sizeof kv);
   });
 }
@@ -329,6 +523,12 @@ PyMethodDef kMethods[] = {
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_append)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_attention)), METH_FASTCALL, nullptr},
     {"paged_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(make_paged_kv)), METH_FASTCALL, nullptr},
+    {"rope_append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_append_q8)), METH_FASTCALL, nullptr},
+    {"cache_read_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cache_read_q8)), METH_FASTCALL, nullptr},
+    {"paged_attention_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_attention_q8)), METH_FASTCALL, nullptr},
+    {"gated_act", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gated_act)), METH_FASTCALL, nullptr},
+    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(sample)), METH_FASTCALL, nullptr},
+    {"paged_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(make_paged_q8)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

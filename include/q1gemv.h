@@ -482,6 +482,121 @@ int q1_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_str
                        const q1_paged_kv *kv, int64_t max_new, void *out, int64_t out_token_stride,
                        int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged cache in q8_0: one byte a value and an f16 scale for 32 of them,
+ * 0.53 of a 16-bit cache's bytes.  The conventions of the operators above.
+ * ------------------------------------------------------------------------- */
+
+/* As q1_paged_kv, with keys and values as q8_0 blocks of 32 along dim. */
+typedef struct q1_paged_q8 {
+  int8_t *k, *v;              /* device [pages][page_size][kv_heads][dim], in any order of the
+                                 first three axes, the same for both                        */
+  uint16_t *k_scale, *v_scale; /* device fp16 bits [pages][page_size][kv_heads][dim/32], in any
+                                 order of the first three axes, the same for both; a head's
+                                 slots side by side (as in [pages][kv_heads][page_size]
+                                 [dim/32]) make the attention's reads whole sectors         */
+  int64_t page_stride, slot_stride, head_stride; /* of k and v, in values: multiples of 16, at least dim */
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride; /* in scales: multiples of dim/32 */
+  const int32_t *table;       /* these as in q1_paged_kv */
+  int64_t table_width, table_stride;
+  const int32_t *kv_len;
+  const int32_t *new_start;
+  int64_t pages, page_size;
+  int64_t kv_heads, dim;      /* dim 64 or 128 */
+  int64_t batch, total_new;
+} q1_paged_q8;
+
+/* q1_rope_append into a q8_0 cache: k (turned, in f32) and v are quantized as
+ * q8_quantize_act does each 32 values of a head.  q_out is of `dtype` (Q1_BF16
+ * or Q1_F16).  A block with a value that is no number (NaN, infinite) gets the
+ * scale NaN; |k| and |v| up to 65504 * 127 keep the scale finite. */
+int q1_rope_append_q8(const float *q, int64_t ldq, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                      const float *cos_sin, int64_t positions, int64_t rot, int interleaved, int64_t heads,
+                      void *q_out, int dtype, const q1_paged_q8 *kv, void *stream);
+
+/* Reads keys and values back: rows new_start[b] .. new_start[b+1]-1 of k_out and
+ * v_out, [total_new][kv_heads][dim] of `dtype` (Q1_F32, Q1_BF16, Q1_F16), are
+ * the last tokens of sequence b (all of them where new_start counts whole
+ * lengths), each value quant * scale rounded once.  Rows of no sequence, and
+ * of tokens whose page is out of range (which sets the status bit), are zero.
+ * Either output may be NULL.  16-byte aligned. */
+int q1_cache_read_q8(const q1_paged_q8 *kv, int dtype, void *k_out, void *v_out, void *stream);
+
+/* Bytes of q1_paged_attention_q8's workspace, on the current device, for
+ * sequences of up to max_new new tokens.  Where max_new asks for the
+ * tensor-core kernel that includes 16-bit copies of the keys and values of
+ * `sequences` sequences of up to table_tokens (the table's width times the page
+ * size); else both are not looked at.  Negative Q1_ERR_ARG for a bad shape. */
+int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t heads, int64_t kv_heads, int64_t dim,
+                                        int64_t table_tokens, int64_t sequences);
+
+/* q1_paged_attention over a q8_0 cache; q and out are of `dtype` (Q1_BF16 or
+ * Q1_F16).  Up to some tens of rows a key head (new tokens times the group) the
+ * quants are multiplied as they are, which is exact, and scales are applied to
+ * sums (keys) and weights (values, whose product with the scale is rounded to
+ * bf16, with f16 q to the sum of two bf16).  More rows take the tensor-core kernel over a 16-bit copy
+ * of the sequence, each value quant * scale rounded once to q's type (with
+ * f16 it must stay below 65504), made by the call in the workspace, for as many
+ * sequences at a time as it holds: at least q1_paged_attention_q8_workspace(...,
+ * 1) bytes are needed, and more make fewer launches of several such sequences.
+ * All else as q1_paged_attention; a value is no number where its scale is none. */
+int q1_paged_attention_q8(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
+                          int dtype, const q1_paged_q8 *kv, int64_t max_new, void *out, int64_t out_token_stride,
+                          int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated activation between the up and the down product, and the choice of
+ * the next token from the output product's logits.
+ * ------------------------------------------------------------------------- */
+
+#define Q1_ACT_SILU 0 /* x / (1 + e^-x)                                                          */
+#define Q1_ACT_GELU 1 /* x (1 + tanh u) / 2 = x / (1 + e^-2u), u = sqrt(2/pi) (x + 0.044715 x^3) */
+
+/* y = act(gate) * up in f32, and its q8_0 form exactly as q8_quantize_act gives
+ * it (of y before any rounding).
+ *   gate, up, y : [nvec][n] of `dtype` (Q1_F32, Q1_BF16, Q1_F16), rows ldg, ldu,
+ *     ldy elements apart; y may be NULL, or gate or up itself.
+ *   q : int8 [nvec][n], d : fp16 bits [nvec][n/32], both or neither (NULL); with
+ *     them n is a multiple of 32, else any n >= 1.
+ * A block with a value that is no number (NaN, infinite) has the scale NaN.
+ * Alignment: q and d 16 bytes, the others their type's size (16-byte aligned
+ * rows are faster).  1 <= nvec <= 2^24, n <= 2^24. */
+int q8_gated_act(const void *gate, int64_t ldg, const void *up, int64_t ldu, int64_t nvec, int64_t n, int dtype,
+                 int activation, void *y, int64_t ldy, int8_t *q, uint16_t *d, void *stream);
+
+/* The settings of q1_sample: for each, an array of one value a row, or (NULL)
+ * one value for all of them. */
+typedef struct q1_sampling {
+  const float *temperature; /* device f32 [rows], or NULL */
+  const int32_t *top_k;     /* device int32 [rows], or NULL */
+  const float *top_p;       /* device f32 [rows], or NULL */
+  const float *min_p;       /* device f32 [rows], or NULL */
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all, min_p_all;
+} q1_sampling;
+
+/* The next token of each row, drawn with a given random number:
+ *   w_i = exp((x_i - max x) / temperature);
+ *   of the tokens in the order of falling logits (equal ones by rising index)
+ *   the first top_k stay (0 and below: all), of these the fewest first ones whose w
+ *   sum to at least top_p of theirs (1 and above: all; one token always stays), and
+ *   of these the ones with w_i >= min_p (0 and below: all; the largest always stay);
+ *   out = the first token, in the order of the vocabulary, at which the sum of the w that
+ *   stayed exceeds uniform times all of it.
+ * temperature 0 and below: the first token with the largest logit.
+ *   logits : [rows][vocab] of `dtype` (Q1_F32, Q1_BF16, Q1_F16), rows ld apart,
+ *     aligned to the type's size (16-byte aligned rows are faster).
+ *   uniform : f32 [rows], in [0, 1) (held within it).
+ *   out : int32 [rows].
+ * The weights are fixed-point numbers of 44 bits behind the point, off by 2^-30 of
+ * themselves or the last bit; their sums are whole numbers, so a row's token does not
+ * depend on the order of anything, nor on the other rows.  -inf masks a token.  A row with a NaN or
+ * +inf, one whose logits are all -inf, and one with a setting that is NaN give -1.
+ * 1 <= rows <= 65535, 1 <= vocab <= 2^19. */
+int q1_sample(const void *logits, int64_t ld, int64_t rows, int64_t vocab, int dtype, const float *uniform,
+              const q1_sampling *settings, int32_t *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
