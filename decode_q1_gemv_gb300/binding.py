@@ -178,7 +178,7 @@ def load():
         lib.q1_rope_append_q8.restype = I
         lib.q1_cache_read_q8.argtypes = [ctypes.POINTER(PagedQ8), I, P, P, P]
         lib.q1_cache_read_q8.restype = I
-        lib.q1_paged_attention_q8_workspace.argtypes = [I64, I64, I64, I64, I64, I64]
+        lib.q1_paged_attention_q8_workspace.argtypes = [I64, I64, I64, I64, I, I64, I64]
         lib.q1_paged_attention_q8_workspace.restype = I64
         lib.q1_paged_attention_q8.argtypes = [P, I64, I64, I64, F, I, ctypes.POINTER(PagedQ8), I64, P, I64, I64, P, I64, P]
         lib.q1_paged_attention_q8.restype = I
@@ -684,11 +684,12 @@ def cache_read_q8(cache_k: torch.Tensor, cache_v: torch.Tensor, scale_k: torch.T
 
 
 def paged_attention_q8_workspace(max_new: int, heads: int, kv_heads: int, dim: int, table_tokens: int,
-                                 sequences: int = 1) -> int:
-    """Bytes of paged_attention_q8's workspace on the current device; where max_new
-    asks for the tensor-core kernel, with 16-bit copies of `sequences`
+                                 sequences: int = 1, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of paged_attention_q8's workspace for q of type `dtype`, on the current device;
+    where max_new asks for the tensor-core kernel, with copies of `sequences`
     sequences of up to table_tokens (the table's width times the page size)."""
-    v = load().q1_paged_attention_q8_workspace(int(max_new), int(heads), int(kv_heads), int(dim), int(table_tokens), int(sequences))
+    v = load().q1_paged_attention_q8_workspace(int(max_new), int(heads), int(kv_heads), int(dim), _type_code(dtype),
+                                                    int(table_tokens), int(sequences))
     if v < 0:
         raise Q1Error(int(v), last_error())
     return int(v)

@@ -426,7 +426,10 @@ inline void place_workspace(AttendArgs& a, void* workspace) {
 // Split items are joined by it, or (`joined` given and its CTAs not 0) by the caller, with those arguments.
 constexpr int kTcRows = 256, kTcJoinSlices = 16;  // rows of an item; CTAs that join it
 int64_t attend_tc_workspace(int dim);
-int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined);
+// With `factors` keys and values are a copy from a q8_0 cache (cache8.cu): f16, divided by them, and in
+// two parts where q is f16 (a.kv.pages: of one part).
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined,
+                     const float* factors = nullptr);
 
 // The joins of a call that ran both kernels, in one launch; `few` has tiles of TM rows.
 struct JoinBoth {

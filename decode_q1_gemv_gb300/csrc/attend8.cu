@@ -559,16 +559,21 @@ static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, v
   return launch_op(k_attend_join<T, Shape::kRows, D, false>, dim3(unsigned(a.ctas), kJoinSlices), kJoinThreads, 0, 1, s, who, a);
 }
 
-// A 16-bit copy of one sequence: pages of 128 tokens, keys and values, and their table's entries.
+// The f16 copy of one sequence: pages of 128 tokens, keys and values in one or two parts, its
+// table's entries, its factors and their making.
 static int64_t copy_pages(int64_t table_tokens) { return (table_tokens + 127) / 128; }
-static int64_t copy_bytes(int64_t pages, int64_t kv_heads, int64_t dim) { return pages * (2 * kv_heads * 128 * dim * 2 + 16); }
+static int copy_parts(int dtype) { return dtype == Q1_BF16 ? 1 : 2; }
+static int64_t copy_bytes(int64_t pages, int64_t kv_heads, int64_t dim, int parts) {
+  return pages * (2 * parts * kv_heads * 128 * dim * 2 + 16) + kv_heads * 2 * (4 + 4 * kTopSlices) + 16;
+}
 
 }  // namespace q1
 
 using namespace q1;
 
 extern "C" int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t heads, int64_t kv_heads, int64_t dim,
-                                                   int64_t table_tokens, int64_t sequences) {
+                                                   int dtype, int64_t table_tokens, int64_t sequences) {
+  if (dtype != Q1_BF16 && dtype != Q1_F16) return fail(Q1_ERR_ARG, "q1_paged_attention_q8_workspace: bad type %d", dtype);
   if (max_new < 1 || heads < 1 || kv_heads < 1 || heads > 4096 || heads % kv_heads || (dim != 64 && dim != 128) || table_tokens < 1 ||
       table_tokens > (int64_t(1) << 42) || sequences < 1 || sequences > (1 << 20))
     return fail(Q1_ERR_ARG, "q1_paged_attention_q8_workspace: bad shape max_new=%lld heads=%lld kv_heads=%lld dim=%lld table_tokens=%lld "
@@ -576,7 +581,7 @@ extern "C" int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t head
                 (long long)table_tokens, (long long)sequences);
   const int64_t few = few_workspace8(int(dim));
   if (!many_rows8(max_new, heads / kv_heads, true)) return few;
-  const int64_t pages = copy_pages(std::min<int64_t>(table_tokens, int64_t(1) << 30)), one = copy_bytes(pages, kv_heads, dim);
+  const int64_t pages = copy_pages(std::min<int64_t>(table_tokens, int64_t(1) << 30)), one = copy_bytes(pages, kv_heads, dim, copy_parts(dtype));
   if (one > (int64_t(1) << 62) / sequences)
     return fail(Q1_ERR_ARG, "q1_paged_attention_q8_workspace: bad shape, %lld sequences of %lld tokens are too much", (long long)sequences,
                 (long long)table_tokens);
@@ -605,7 +610,7 @@ extern "C" int q1_paged_attention_q8(const void* q, int64_t q_token_stride, int6
   if (!std::isfinite(scale * 1.4426950408889634f)) return fail(Q1_ERR_ARG, "%s: scale must be finite", who);
   if (max_new < 1) return fail(Q1_ERR_ARG, "%s: max_new must be positive", who);
   const int64_t table_tokens = kv->table_width * kv->page_size;
-  const int64_t need = q1_paged_attention_q8_workspace(max_new, heads, kv->kv_heads, kv->dim, table_tokens, 1);
+  const int64_t need = q1_paged_attention_q8_workspace(max_new, heads, kv->kv_heads, kv->dim, dtype, table_tokens, 1);
   if (need < 0) return int(need);
   if (workspace_bytes < need)
     return fail(Q1_ERR_ARG, "%s: the workspace holds %lld bytes, %lld are needed", who, (long long)workspace_bytes,
@@ -644,12 +649,12 @@ extern "C" int q1_paged_attention_q8(const void* q, int64_t q_token_stride, int6
 
   // As many sequences at a time as the workspace has room for; those of one tile at most among
   // several go to the kernel for few rows, beside the last launch of the other.
-  const int64_t pages = copy_pages(a.kv.table_tokens), one = copy_bytes(pages, kv->kv_heads, kv->dim);
+  const int64_t pages = copy_pages(a.kv.table_tokens), one = copy_bytes(pages, kv->kv_heads, kv->dim, copy_parts(dtype));
   char* tc_space = static_cast<char*>(workspace) + few_workspace8(int(kv->dim));
   char* copies = tc_space + attend_tc_workspace(int(kv->dim));
   const int64_t fit = (workspace_bytes - (copies - static_cast<char*>(workspace))) / one;
   const int at_once = int(std::min<int64_t>({fit, kv->batch, 65535, (int64_t(1) << 30) / pages}));
-  const int64_t half_bytes = int64_t(at_once) * pages * kv->kv_heads * 128 * kv->dim * 2;
+  const int64_t tensor = int64_t(at_once) * pages * kv->kv_heads * 128 * kv->dim * copy_parts(dtype);  // values
   const bool both = kv->batch > 1;
   constexpr int kFewRows = 16;
   AttendArgs many = {};
@@ -658,9 +663,13 @@ extern "C" int q1_paged_attention_q8(const void* q, int64_t q_token_stride, int6
     CopyQ8 c = {};
     c.p = p;
     c.p.kv.table += b0 * p.kv.table_stride, c.p.kv.kv_len += b0, c.p.kv.new_start += b0, c.p.kv.batch = count;
-    c.k = copies, c.v = copies + half_bytes, c.table = reinterpret_cast<int32_t*>(copies + 2 * half_bytes);
-    c.status = a.status, c.pages = int(pages), c.dim = int(kv->dim), c.group = a.group, c.least_rows = both ? kFewRows + 1 : 1;
-    if (int e = launch_copy_q8(c, bf, s)) return e;
+    c.k = reinterpret_cast<__half*>(copies), c.v = c.k + tensor;
+    c.table = reinterpret_cast<int32_t*>(c.v + tensor);
+    c.tops = reinterpret_cast<uint32_t*>(c.table + at_once * pages);
+    c.factors = reinterpret_cast<float*>(c.tops + int64_t(at_once) * kv->kv_heads * 2 * kTopSlices);
+    c.status = a.status, c.pages = int(pages), c.parts = copy_parts(dtype);
+    c.dim = int(kv->dim), c.group = a.group, c.least_rows = both ? kFewRows + 1 : 1;
+    if (int e = launch_copy_q8(c, s)) return e;
     AttendArgs t = a;
     t.kv = c.p.kv;
     t.kv.k = c.k, t.kv.v = c.v;
@@ -668,7 +677,7 @@ extern "C" int q1_paged_attention_q8(const void* q, int64_t q_token_stride, int6
     t.kv.table = c.table, t.kv.table_stride = pages, t.kv.pages = int(pages * count), t.kv.page_shift = 7;
     if (both) t.least_rows = kFewRows + 1;
     const bool last = b0 + count == a.kv.batch;
-    if (int e = launch_attend_tc(t, tc_space, bf, int(kv->dim), s, ran, both && last ? &many : nullptr)) return e;
+    if (int e = launch_attend_tc(t, tc_space, bf, int(kv->dim), s, ran, both && last ? &many : nullptr, c.factors)) return e;
     if (!ran) return fail(Q1_ERR_CUDA, "%s: no tensor map for the workspace", who);
   }
   if (!both) return Q1_OK;

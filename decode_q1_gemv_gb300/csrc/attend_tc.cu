@@ -46,6 +46,13 @@
 // part.  With D = 64 the softmax bounds it: its arithmetic alone takes 346 cycles a
 // warp and 64 keys (exponentials 256 of them), four warps a scheduler.
 //
+// Keys and values that were copied from a q8_0 cache (cache8.cu) are f16 for q of
+// either type, since bf16 would add 2^-9 of every key's value to the weights' own rounding:
+// divided by a power of two a sequence and key head (kNormed), which the scale of
+// the scores and the output take back, as rows of bf16 q are by one each (kept in
+// shared memory from when they are loaded).  With f16 q they come in two parts, value
+// and remainder, twice the products.
+//
 // Every wait is bounded; one that gives up raises the CTA's abort flag and the
 // device status word, and every role winds down.
 #include <cuda.h>
@@ -89,6 +96,7 @@ struct AttendTcArgs {
   uint32_t q_sign;    // 0x80008000 where the scale is negative: -q and |scale| instead
   int box_keys;
   int axis_head, axis_slot, axis_page;  // positions (1..3) of the axes in the maps
+  const float* factors;  // kNormed: what keys and values of [sequence][key head] were divided by
 };
 
 template <int D>
@@ -183,15 +191,19 @@ struct RingPos {
   }
 };
 
-template <class T, int D>
+// T: the products' type; U: that of q and the output; kParts: of each key and
+// value, the second one's pages behind the first one's.
+template <class T, int D, class U = T, int kParts = 1>
 __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_constant__ AttendTcArgs g) {
   using Tile = Tiling<kTcItem, kTcKeys>;
   using Shape = TcShape<D>;
   constexpr int kStages = Shape::kStages;
+  constexpr bool kTurned = !std::is_same<T, U>::value, kNormed = kTurned || kParts > 1;  // kTurned: q is made another type
   const AttendArgs& a = g.a;
   extern __shared__ unsigned char raw_smem[];
   __shared__ LocateScratch scratch;
   __shared__ float exchange[2][2][2][kTcM];  // [unit parity][tile][half][row]
+  __shared__ float q_factor[kTurned ? 2 : 1][2][kTurned ? kTcM : 1];  // [item parity][tile][row]
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile uint32_t abort_s, taken_out_s;  // taken_out_s: V had values that are no numbers
   unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -274,14 +286,14 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
           const int next = t + 1 < take ? page_at(unit + 1) : 0;
           if (lane < boxes && (page < 0 || page >= a.kv.pages)) {
             atomicOr(a.status, kStatusBadIndex);
-            page = a.kv.pages;  // past the map's end: the box reads as zeros
+            page = kParts * a.kv.pages;  // past the map's end: the box reads as zeros
           }
-          int c[3];
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page;
+          for (int kv = 0; kv < 2 * kParts; ++kv) {
+            int c[3];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
+            for (int i = 0; i < 3; ++i)
+              c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page + kv % kParts * a.kv.pages;
             if (!wait(empty(pos.stage), pos.parity ^ 1)) {
               ok = false;
               break;
@@ -292,7 +304,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               const uint32_t dst = s0 + Shape::kOffKV + pos.stage * Shape::kTileBytes + lane * g.box_keys * 128;
 #pragma unroll
               for (int h = 0; h < Shape::kHalves; ++h)
-                tma_box(dst + h * Shape::kHalfBytes, kv ? &g.v : &g.k, full(pos.stage), h * 64, c[0], c[1], c[2]);
+                tma_box(dst + h * Shape::kHalfBytes, kv / kParts ? &g.v : &g.k, full(pos.stage), h * 64, c[0], c[1], c[2]);
             }
             __syncwarp();
             pos.next<kStages>();
@@ -319,24 +331,39 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         if (kTurns && hand && lane == 0) mbar_arrive(turn + 8 * (w ^ 1));
         __syncwarp();
       };
-      const auto scores = [&](int stage, bool hand) {  // S_w = Q_w K^T
-        const uint64_t kdesc = desc_k_sw128(tile_addr(stage));
+      const auto scores = [&](bool hand) {  // S_w = Q_w K^T, of the parts from pos on
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          constexpr int kHalf = Shape::kHalfBytes;
-          const int off = ((k / 4) * kHalf + (k % 4) * 32) >> 4;
-          mma_f16_ss_elect(ts, qdesc + off, kdesc + off, kIdS, k > 0);
+        for (int part = 0; part < kParts; ++part) {
+          const int stage = pos.stage;
+          const uint64_t kdesc = desc_k_sw128(tile_addr(stage));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            constexpr int kHalf = Shape::kHalfBytes;
+            const int off = ((k / 4) * kHalf + (k % 4) * 32) >> 4;
+            mma_f16_ss_elect(ts, qdesc + off, kdesc + off, kIdS, k > 0 || part > 0);
+          }
+          if (part == kParts - 1) mma_commit_elect(sfull + 8 * w);
+          mma_commit_elect(empty(stage));
+          pos.next<kStages>();
         }
-        mma_commit_elect(sfull + 8 * w);
-        mma_commit_elect(empty(stage));
         hand_on(hand);
+      };
+      const auto parts_full = [&]() {  // from pos on
+        RingPos at = pos;
+        bool done = wait(full(at.stage), at.parity);
+#pragma unroll
+        for (int part = 1; part < kParts; ++part) {
+          at.next<kStages>();
+          done = done && wait(full(at.stage), at.parity);
+        }
+        return done;
       };
       for (int64_t u = u0; u < u1 && ok;) {
         const int take = part_of(u), keys = Tile::keys(a, cur.s, cur.m), nw = tiles_of(cur);
         const int of_all = Tile::keys_of_all(a, cur.s, cur.m);
         if (keys && w >= nw) {
           // No rows for this tile: its share of releasing the stages.
-          for (int t = 0; t < 2 * take && ok; ++t) {
+          for (int t = 0; t < 2 * kParts * take && ok; ++t) {
             ok = wait(full(pos.stage), pos.parity);
             if (ok && lane == 0) mbar_arrive(empty(pos.stage));
             pos.next<kStages>();
@@ -351,69 +378,75 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             turnpar ^= 1;
             return done;
           };
-          ok = wait(qfull + 8 * w, qpar) && wait(full(pos.stage), pos.parity) && my_turn();
+          ok = wait(qfull + 8 * w, qpar) && parts_full() && my_turn();
           qpar ^= 1;
           handed |= nw == 2;
           if (ok) {
             tc_fence_after();
-            scores(pos.stage, nw == 2);
-            pos.next<kStages>();
+            scores(nw == 2);
           }
           for (int t = 0; t < take && ok; ++t) {
-            const int vstage = pos.stage;
-            ok = wait(full(vstage), pos.parity);
-            if (!ok) break;
-            // V is made ready while the softmax is under way.  (Both tiles' warps look at all of it
-            // and may write the same zeros.)
-            const int unit0 = (cur.unit + t) * kTcKeys, valid = keys - unit0;
-            if (valid < kTcKeys || of_all < unit0 + kTcKeys) {
-              uint4* v = reinterpret_cast<uint4*>(smem + Shape::kOffKV + vstage * Shape::kTileBytes);
-              constexpr int kHalf = Shape::kHalfBytes / 16;
-              // Values that are no numbers, of keys that not all rows of the item see, are taken
-              // out; the output adds them to the rows that see them.
-              const int lo = max(0, of_all - unit0) * 8 + lane, hi = min(valid, kTcKeys) * 8;
-              NoNumbers<T> none;
+            int vstages[kParts];
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+              const int vstage = vstages[part] = pos.stage;
+              ok = wait(full(vstage), pos.parity);
+              if (!ok) break;
+              // V is made ready while the softmax is under way.  (Both tiles' warps look at all of it
+              // and may write the same zeros.)
+              const int unit0 = (cur.unit + t) * kTcKeys, valid = keys - unit0;
+              if (valid < kTcKeys || of_all < unit0 + kTcKeys) {
+                uint4* v = reinterpret_cast<uint4*>(smem + Shape::kOffKV + vstage * Shape::kTileBytes);
+                constexpr int kHalf = Shape::kHalfBytes / 16;
+                // Values that are no numbers, of keys that not all rows of the item see, are taken
+                // out; the output adds them to the rows that see them.
+                const int lo = max(0, of_all - unit0) * 8 + lane, hi = min(valid, kTcKeys) * 8;
+                NoNumbers<T> none;
 #pragma unroll 1
-              for (int i = lo - lane; i < hi; i += 128) {  // (loads side by side: 22.8 us for two prompts of 400, 23.5 without)
-                uint4 x[4][Shape::kHalves];
+                for (int i = lo - lane; i < hi; i += 128) {  // (loads side by side: 22.8 us for two prompts of 400, 23.5 without)
+                  uint4 x[4][Shape::kHalves];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                  for (int e = 0; e < 4; ++e)
 #pragma unroll
-                  for (int h = 0; h < Shape::kHalves; ++h) x[e][h] = v[h * kHalf + min(i + e * 32 + lane, hi - 1)];
+                    for (int h = 0; h < Shape::kHalves; ++h) x[e][h] = v[h * kHalf + min(i + e * 32 + lane, hi - 1)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                  for (int e = 0; e < 4; ++e)
 #pragma unroll
-                  for (int h = 0; h < Shape::kHalves; ++h) none.look(x[e][h]);
-              }
-              if (__any_sync(0xffffffffu, none.found())) {
-                taken_out_s = 1;
-                __threadfence_block();  // whoever finds them gone finds this
+                    for (int h = 0; h < Shape::kHalves; ++h) none.look(x[e][h]);
+                }
+                if (__any_sync(0xffffffffu, none.found())) {
+                  taken_out_s = 1;
+                  __threadfence_block();  // whoever finds them gone finds this
 #pragma unroll 1
-                for (int i = lo; i < hi; i += 32)
-                  for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = numbers<T>(v[h * kHalf + i]);
-              }
-              // Rows past the keys hold whatever lay there: a weight of zero times that must be zero.
-              for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
+                  for (int i = lo; i < hi; i += 32)
+                    for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = numbers<T>(v[h * kHalf + i]);
+                }
+                // Rows past the keys hold whatever lay there: a weight of zero times that must be zero.
+                for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
 #pragma unroll
-                for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = make_uint4(0u, 0u, 0u, 0u);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
+                  for (int h = 0; h < Shape::kHalves; ++h) v[h * kHalf + i] = make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+              }
+              pos.next<kStages>();
             }
-            pos.next<kStages>();
+            if (!ok) break;
             const bool more = t + 1 < take;
-            const uint64_t vdesc = desc_mn_sw128(tile_addr(vstage), Shape::kHalfBytes);
-            if (more) ok = wait(full(pos.stage), pos.parity);
+            if (more) ok = parts_full();
             ok = ok && my_turn() && wait(pfull + 8 * w, ppar);
             ppar ^= 1;
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ts_elect(to, ts + k / 4 * 64 + k % 4 * 8, vdesc + k * (2048 >> 4), kIdO, t > 0 || k > 0);
-            mma_commit_elect(empty(vstage));
+            for (int part = 0; part < kParts; ++part) {
+              const uint64_t vdesc = desc_mn_sw128(tile_addr(vstages[part]), Shape::kHalfBytes);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_f16_ts_elect(to, ts + k / 4 * 64 + k % 4 * 8, vdesc + k * (2048 >> 4), kIdO, t > 0 || k > 0 || part > 0);
+              mma_commit_elect(empty(vstages[part]));
+            }
             if (more) {
-              scores(pos.stage, nw == 2);
-              pos.next<kStages>();
+              scores(nw == 2);
             } else {
               mma_commit_elect(ofull + 8 * w);
               hand_on(nw == 2);
@@ -447,7 +480,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       return done;
     };
     bool ok = true;
-    const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+    float scale = a.scale_log2, v_factor = 1.f;
+    uint64_t scale2 = f32x2(scale, scale);
+    int q_load = 0, q_use = 0;  // parities of the items whose Q is loaded, and of the one at work
     // Q of an item, if this tile has rows of it that see keys: this warp's 16
     // rows, 16 (8) lanes a row; rows past the last are zero.
     const auto load_q = [&](const Cursor& it) {
@@ -461,12 +496,28 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         int qt, qh;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (row_of(a, it, it.m * kTcItem + w * kTcM + r, qt, qh))
-          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
+          v = *reinterpret_cast<const uint4*>(static_cast<const U*>(a.q) + qt * a.q_token + qh * a.q_head + piece * 8);
         v.x ^= g.q_sign, v.y ^= g.q_sign, v.z ^= g.q_sign, v.w ^= g.q_sign;
+        if constexpr (kTurned) {
+          // Divided by a power of two near the row's largest value, which f16's 11 bits
+          // hold exactly down to 2^-14 of it.
+          const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          uint32_t top = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const uint32_t e = min(max(top >> 7, 1u), 253u);  // the exponent's bits
+          float x[8];
+          Elem<U>::unpack(v, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= __uint_as_float((254u - e) << 23);
+          v = Elem<T>::pack(x);
+          if (piece == 0) q_factor[q_load][w][r] = __uint_as_float(e << 23);
+        }
         *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(qfull + 8 * w);
+      q_load ^= 1;
     };
     if (u0 < u1) load_q(cur);
     for (int64_t u = u0; u < u1 && ok;) {
@@ -496,6 +547,16 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             spar ^= 1;
             if (!ok) break;
             tc_fence_after();
+            if constexpr (kNormed) {
+              if (t == 0) {  // (the row's factor was written before its Q, which these scores come from)
+                const float* f = g.factors + 2 * (cur.b * a.kv.kv_heads + cur.h);
+                scale = a.scale_log2 * f[0], v_factor = f[1];
+                if constexpr (kTurned) scale *= q_factor[q_use][w][row];
+                q_use ^= 1;
+                scale = fminf(fmaxf(scale, FLT_MIN), FLT_MAX);
+                scale2 = f32x2(scale, scale);
+              }
+            }
             uint32_t p[32];
             const auto scores = [&](uint32_t (&s)[2][32]) {
               tmem_ld32(ts, s[0]);
@@ -540,7 +601,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             }
             ok = fetch(other);
             if (!ok) break;
-            const float top = fmaxf(mine, other) * a.scale_log2;
+            const float top = fmaxf(mine, other) * scale;
             const bool grown = top > used + kTcGrow || (used == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, grown)) {
               float f = 1.f;
@@ -588,10 +649,10 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         }
         const bool whole = cur.unit == 0 && take == cur.units;
         const int sees = live ? keys_seen(cur.s, token - cur.s.first) : 0;
-        const float inv = inverse(sum, sees);
+        const float inv = kNormed ? inverse(sum, sees) * v_factor : inverse(sum, sees);
         if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
         float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
-        T* out = static_cast<T*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
+        U* out = static_cast<U*>(a.out) + (live ? token * a.o_token + head * a.o_head : 0) + half * kCols;
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           uint32_t o[16];
@@ -606,14 +667,15 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
                 uint32_t pk[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)  // a row that sees nothing is zero, whatever O holds
-                  pk[e] = sees ? Elem<T>::pack2(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv)
+                  pk[e] = sees ? Elem<U>::pack2(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv)
                                      : 0u;
                 *reinterpret_cast<uint4*>(out + c + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) part[(half * kCols + c + j) * kTcItem] = __uint_as_float(o[j]);
+            for (int j = 0; j < 16; ++j)
+              part[(half * kCols + c + j) * kTcItem] = kNormed ? __uint_as_float(o[j]) * v_factor : __uint_as_float(o[j]);
           }
         }
         if (taken_out_s) {  // (rolled, on what has been written: the loops above have no registers for it)
@@ -629,7 +691,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
               const float x = Elem<T>::to(v[c]);
               if (fabsf(x) <= FLT_MAX) continue;
               if (whole)
-                out[c] = Elem<T>::from(Elem<T>::to(out[c]) + x);
+                out[c] = Elem<U>::from(Elem<U>::to(out[c]) + x);
               else
                 part[(half * kCols + c) * kTcItem] += x;
             }
@@ -660,7 +722,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
   if (warp == kTcSoftWarps) tmem_free(tmem, 512);
 }
 
-static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base, int dim, int box_keys, int (&axis)[3]) {
+static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, int parts, void* base, int dim, int box_keys, int (&axis)[3]) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -677,7 +739,7 @@ static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base
   }
   // The axes head, slot, page in the order of their strides.
   const int64_t stride[3] = {p.head_stride, p.slot_stride, p.page_stride};
-  const uint64_t size[3] = {uint64_t(p.kv_heads), uint64_t(1) << p.page_shift, uint64_t(p.pages)};
+  const uint64_t size[3] = {uint64_t(p.kv_heads), uint64_t(1) << p.page_shift, uint64_t(p.pages) * uint64_t(parts)};
   int order[3] = {0, 1, 2};
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2 - i; ++j)
@@ -700,19 +762,19 @@ static CUresult encode_map(CUtensorMap* m, bool bf16, const Paged& p, void* base
 
 int64_t attend_tc_workspace(int dim) { return attend_workspace(num_sms(), kTcItem, dim); }
 
-template <class T, int D>
+template <class T, int D, class U, int kParts>
 static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s, AttendArgs* joined) {
   const char* who = "q1_paged_attention launch";
   static bool set[64] = {};
   int dev = 0;
   if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_tc<T, D, U, kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  TcShape<D>::kSmem), who))
       return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  if (int e = launch_op<AttendTcArgs>(k_attend_tc<T, D>, dim3(unsigned(g.a.ctas)), kTcAThreads, TcShape<D>::kSmem, 1, s, who, g))
+  if (int e = launch_op<AttendTcArgs>(k_attend_tc<T, D, U, kParts>, dim3(unsigned(g.a.ctas)), kTcAThreads, TcShape<D>::kSmem, 1, s, who, g))
     return e;
   // No item has more units than stay whole: nothing to join.
   if (g.a.kv.table_tokens <= kTcWhole * kTcKeys) return Q1_OK;
@@ -720,15 +782,17 @@ static int launch_tc_kernel(AttendTcArgs& g, cudaStream_t s, AttendArgs* joined)
     *joined = g.a;
     return Q1_OK;
   }
-  return launch_op(k_attend_join<T, kTcItem, D, true>, dim3(unsigned(g.a.ctas), kTcJoinSlices), kJoinThreads, 0, 1, s, who,
+  return launch_op(k_attend_join<U, kTcItem, D, true>, dim3(unsigned(g.a.ctas), kTcJoinSlices), kJoinThreads, 0, 1, s, who,
                    g.a);
 }
 
 // False in `ran` where no tensor map can describe the cache's strides.
-int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined) {
+int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, cudaStream_t s, bool& ran, AttendArgs* joined,
+                     const float* factors) {
   AttendTcArgs g = {};
   g.a = a;
   g.a.ctas = num_sms();
+  g.factors = factors;
   place_workspace(g.a, workspace);
   // The largest score comes from the largest q.k, and a masked one stays -inf
   // when scaled, where the scale is positive.
@@ -736,12 +800,18 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, bool bf16, int dim, c
   g.a.scale_log2 = std::max(std::fabs(a.scale_log2), FLT_MIN);
   g.box_keys = a.kv.page_shift < 7 ? 1 << a.kv.page_shift : kTcKeys;
   int axis[3] = {};
-  ran = encode_map(&g.k, bf16, a.kv, a.kv.k, dim, g.box_keys, axis) == CUDA_SUCCESS &&
-        encode_map(&g.v, bf16, a.kv, a.kv.v, dim, g.box_keys, axis) == CUDA_SUCCESS;
+  const bool as_bf16 = bf16 && !factors;  // the copies are f16
+  const int parts = factors && !bf16 ? 2 : 1;
+  ran = encode_map(&g.k, as_bf16, a.kv, parts, a.kv.k, dim, g.box_keys, axis) == CUDA_SUCCESS &&
+        encode_map(&g.v, as_bf16, a.kv, parts, a.kv.v, dim, g.box_keys, axis) == CUDA_SUCCESS;
   if (!ran) return Q1_OK;
   g.axis_head = axis[0], g.axis_slot = axis[1], g.axis_page = axis[2];
-  if (dim == 128) return bf16 ? launch_tc_kernel<__nv_bfloat16, 128>(g, s, joined) : launch_tc_kernel<__half, 128>(g, s, joined);
-  return bf16 ? launch_tc_kernel<__nv_bfloat16, 64>(g, s, joined) : launch_tc_kernel<__half, 64>(g, s, joined);
+  const auto with = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (factors) return bf16 ? launch_tc_kernel<__half, D, __nv_bfloat16, 1>(g, s, joined) : launch_tc_kernel<__half, D, __half, 2>(g, s, joined);
+    return bf16 ? launch_tc_kernel<__nv_bfloat16, D, __nv_bfloat16, 1>(g, s, joined) : launch_tc_kernel<__half, D, __half, 1>(g, s, joined);
+  };
+  return dim == 128 ? with(std::integral_constant<int, 128>()) : with(std::integral_constant<int, 64>());
 }
 
 }  // namespace q1

@@ -166,47 +166,118 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache_read_q8(const __grid_co
   }
 }
 
-// 16 tokens of a head at a time: the CTAs of a sequence (blockIdx.y) take its
-// groups in turn, so that short sequences of a wide table cost little.
-constexpr int kCopyTokens = 16;
-template <class T>
-__global__ void __launch_bounds__(256) k_copy_q8(const __grid_constant__ CopyQ8 a) {
+// The largest finite scales of keys and values of a sequence's head, a sixteenth
+// of the tokens a CTA.
+constexpr int kTopThreads = 256;
+__global__ void __launch_bounds__(kTopThreads) k_scale_tops(const __grid_constant__ CopyQ8 a) {
+  __shared__ uint32_t top_s[kTopThreads / 32][2];
   pdl_launch_dependents();
   pdl_wait();
   const Paged& kv = a.p.kv;
-  const int b = blockIdx.y;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < a.pages; i += gridDim.x * 256) a.table[int64_t(b) * a.pages + i] = b * a.pages + i;
+  const int slice = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
   const SeqSpan s = seq_span(kv, b);  // (the attention reports what it changes)
   if (int64_t(s.count) * a.group < a.least_rows) return;
-  const int units = a.dim / 16, per = kCopyTokens * units, page_mask = (1 << kv.page_shift) - 1;
-  const int64_t all = int64_t((s.len + kCopyTokens - 1) / kCopyTokens) * kv.kv_heads;
   const int32_t* table = kv.table + b * kv.table_stride;
-  // The threads of a unit of work: 64 (dim 64) or 128 for a token group and head; keys and values in turn.
-  const int together = 256 / per;
-  for (int64_t w = int64_t(blockIdx.x) * together + threadIdx.x / per; w < all; w += int64_t(gridDim.x) * together) {
-    const int group = int(w / kv.kv_heads), head = int(w - int64_t(group) * kv.kv_heads);
-    const int r = threadIdx.x % per, j = group * kCopyTokens + r / units, e = r % units * 16;
-    if (j >= s.len) continue;
+  const int j0 = int(int64_t(s.len) * slice / kTopSlices), j1 = int(int64_t(s.len) * (slice + 1) / kTopSlices);
+  uint32_t top[2] = {0u, 0u};
+#pragma unroll 4
+  for (int j = j0 + threadIdx.x; j < j1; j += kTopThreads) {
+    const int page = table[j >> kv.page_shift];
+    if (page < 0 || page >= kv.pages) continue;
+    const int64_t at = scale_offset(a.p, page, j & ((1 << kv.page_shift) - 1)) + head * a.p.s_head;
+#pragma unroll
+    for (int second = 0; second < 2; ++second) {
+      const uint32_t* d = reinterpret_cast<const uint32_t*>((second ? a.p.vs : a.p.ks) + at);
+      for (int i = 0; i < a.dim / 64; ++i) {
+        const uint32_t w = d[i], lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+        if (lo < 0x7c00u) top[second] = max(top[second], lo);
+        if (hi < 0x7c00u) top[second] = max(top[second], hi);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+    if ((threadIdx.x & 31) == 0) top_s[threadIdx.x >> 5][i] = top[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    uint32_t m = 0;
+    for (int w = 0; w < kTopThreads / 32; ++w) m = max(m, top_s[w][threadIdx.x]);
+    a.tops[((int64_t(b) * kv.kv_heads + head) * 2 + threadIdx.x) * kTopSlices + slice] = m;
+  }
+}
+
+// A CTA takes 16 tokens for every dim threads; those of a sequence's head (blockIdx.x) take
+// its tokens in turn, so that short sequences of a wide table cost little.
+constexpr int kCopyThreads = 256;
+template <int kParts>
+__global__ void __launch_bounds__(kCopyThreads) k_copy_q8(const __grid_constant__ CopyQ8 a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const Paged& kv = a.p.kv;
+  const int head = blockIdx.y, b = blockIdx.z;
+  if (head == 0)
+    for (int i = blockIdx.x * kCopyThreads + threadIdx.x; i < a.pages; i += gridDim.x * kCopyThreads)
+      a.table[int64_t(b) * a.pages + i] = b * a.pages + i;
+  const SeqSpan s = seq_span(kv, b);
+  if (int64_t(s.count) * a.group < a.least_rows) return;
+  // Values are at most 127 scales: below 2^15 once divided by the largest scale's power of two and 2^-7.
+  const uint32_t* tops = a.tops + (int64_t(b) * kv.kv_heads + head) * 2 * kTopSlices;
+  float factor[2], inverse[2];
+  {
+    uint32_t top = tops[threadIdx.x & 31];
+    static_assert(2 * kTopSlices == 32, "a lane a slice");
+#pragma unroll
+    for (int off = kTopSlices / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t t = __shfl_sync(0xffffffffu, top, i * kTopSlices);
+      const uint32_t e = t ? (__float_as_uint(__half2float(__ushort_as_half(uint16_t(t)))) >> 23) - 7u : 127u;
+      factor[i] = __uint_as_float(e << 23), inverse[i] = __uint_as_float((254u - e) << 23);
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.factors[(int64_t(b) * kv.kv_heads + head) * 2 + threadIdx.x] = threadIdx.x ? factor[1] : factor[0];
+  const int units = a.dim / 16, page_mask = (1 << kv.page_shift) - 1, step = kCopyThreads / units;  // tokens at a time
+  const int e = int(threadIdx.x) % units * 16;
+  const int32_t* table = kv.table + b * kv.table_stride;
+  const int64_t part = int64_t(kv.batch) * a.pages * kv.kv_heads * 128 * a.dim;
+  for (int j = blockIdx.x * step + int(threadIdx.x) / units; j < s.len; j += gridDim.x * step) {
     const int page = table[j >> kv.page_shift];
     const bool good = page >= 0 && page < kv.pages;
     if (!good) atomicOr(a.status, kStatusBadIndex);
     const int64_t from = value_offset(a.p, page, j & page_mask) + head * kv.head_stride + e;
     const int64_t scale = scale_offset(a.p, page, j & page_mask) + head * a.p.s_head + e / kSub;
     const int64_t to = (((int64_t(b) * a.pages + j / 128) * kv.kv_heads + head) * 128 + j % 128) * a.dim + e;
-    float x[16] = {}, y[16] = {};
-    if (good) read16(static_cast<const int8_t*>(kv.k) + from, a.p.ks + scale, x), read16(static_cast<const int8_t*>(kv.v) + from, a.p.vs + scale, y);
-    write16(static_cast<T*>(a.k) + to, x);
-    write16(static_cast<T*>(a.v) + to, y);
+    float x[2][16] = {};
+    if (good) {
+      read16(static_cast<const int8_t*>(kv.k) + from, a.p.ks + scale, x[0]);
+      read16(static_cast<const int8_t*>(kv.v) + from, a.p.vs + scale, x[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      __half* out = (i ? a.v : a.k) + to;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) x[i][n] = __fmul_rn(x[i][n], inverse[i]);
+      write16(out, x[i]);
+      if constexpr (kParts == 2) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) x[i][n] = __fsub_rn(x[i][n], __half2float(__float2half_rn(x[i][n])));
+        write16(out + part, x[i]);
+      }
+    }
   }
 }
 
-int launch_copy_q8(const CopyQ8& c, bool bf16, cudaStream_t s) {
+int launch_copy_q8(const CopyQ8& c, cudaStream_t s) {
   const char* who = "q1_paged_attention_q8 launch";
-  const int64_t groups = int64_t((c.p.kv.table_tokens + kCopyTokens - 1) / kCopyTokens) * c.p.kv.kv_heads * (kCopyTokens * c.dim / 16) / 256 + 1;
-  const int64_t fill = (int64_t(8) * num_sms() + c.p.kv.batch - 1) / c.p.kv.batch;  // eight CTAs an SM
-  const dim3 grid(unsigned(groups < fill ? groups : fill), unsigned(c.p.kv.batch));
-  if (bf16) return launch_op<CopyQ8>(k_copy_q8<__nv_bfloat16>, grid, 256, 0, 1, s, who, c);
-  return launch_op<CopyQ8>(k_copy_q8<__half>, grid, 256, 0, 1, s, who, c);
+  const Paged& kv = c.p.kv;
+  if (int e = launch_op<CopyQ8>(k_scale_tops, dim3(kTopSlices, unsigned(kv.kv_heads), unsigned(kv.batch)), kTopThreads, 0, 1, s, who, c)) return e;
+  const int64_t step = kCopyThreads / (c.dim / 16), most = (kv.table_tokens + step - 1) / step;
+  const int64_t fill = (int64_t(8) * num_sms() + kv.batch * kv.kv_heads - 1) / (int64_t(kv.batch) * kv.kv_heads);  // eight CTAs an SM
+  const dim3 grid(unsigned(most < fill ? most : fill), unsigned(kv.kv_heads), unsigned(kv.batch));
+  if (c.parts == 2) return launch_op<CopyQ8>(k_copy_q8<2>, grid, kCopyThreads, 0, 1, s, who, c);
+  return launch_op<CopyQ8>(k_copy_q8<1>, grid, kCopyThreads, 0, 1, s, who, c);
 }
 
 int check_paged_q8(const char* who, const q1_paged_q8* kv, Paged8& p) {

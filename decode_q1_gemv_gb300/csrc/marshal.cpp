@@ -394,12 +394,12 @@ PyObject* cache_read_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
   });
 }
 
-// Sequences whose 16-bit copies the attention's own workspace holds at once: a
+// Sequences whose copies the attention's own workspace holds at once: a
 // gigabyte of them, and one at least.
-int64_t copied_at_once(int64_t max_new, int64_t heads, const q1_paged_q8& kv) {
+int64_t copied_at_once(int64_t max_new, int64_t heads, const q1_paged_q8& kv, int dtype) {
   const int64_t tokens = kv.table_width * kv.page_size;
-  const int64_t one = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, tokens, 1);
-  const int64_t two = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, tokens, 2);
+  const int64_t one = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, dtype, tokens, 1);
+  const int64_t two = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, kv.dim, dtype, tokens, 2);
   if (one < 0 || two <= one) return 1;
   const int64_t fit = (int64_t(1) << 30) / (two - one);
   return fit < 1 ? 1 : fit < kv.batch ? fit : kv.batch;
@@ -415,6 +415,7 @@ PyObject* paged_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (kv.dim != dim) refuse(PyExc_ValueError, "q has dim %lld, the cache %lld", (long long)dim, (long long)kv.dim);
     void* pq = pointer(q, "q", kBf16 | kF16, q.sizes());
     const unsigned type = type_bit(q.scalar_type());
+    const int dtype = type_code(q.scalar_type());
     const int64_t max_new = integer(a[8]);
     const double scale = a[9] == Py_None ? 1.0 / std::sqrt(double(dim)) : number(a[9]);
     at::Tensor out = given_or_new(a[10], "out", q.sizes(), q, q.scalar_type());
@@ -422,13 +423,13 @@ PyObject* paged_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (a[11] != Py_None) {
       ws = tensor(a[11], "workspace");
     } else {
-      const int64_t bytes = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, dim, kv.table_width * kv.page_size,
-                                                            copied_at_once(max_new, heads, kv));
+      const int64_t bytes = q1_paged_attention_q8_workspace(max_new, heads, kv.kv_heads, dim, dtype, kv.table_width * kv.page_size,
+                                                            copied_at_once(max_new, heads, kv, dtype));
       check(bytes < 0 ? bytes : Q1_OK, "q1_paged_attention_q8");
       ws = at::empty({bytes}, q.options().dtype(at::kByte));
     }
     check(q1_paged_attention_q8(pq, stride(q, 0, heads * dim), stride(q, 1, dim), heads, static_cast<float>(scale),
-                                type_code(q.scalar_type()), &kv, max_new, pointer(out, "out", type, q.sizes()),
+                                dtype, &kv, max_new, pointer(out, "out", type, q.sizes()),
                                 stride(out, 0, heads * dim), stride(out, 1, dim), pointer(ws, "workspace", kU8, ws.sizes(), true),
                                 ws.numel(), reinterpret_cast<void*>(integer(a[12]))),
           "q1_paged_attention_q8");

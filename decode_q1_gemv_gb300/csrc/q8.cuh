@@ -46,17 +46,22 @@ struct Paged8 {
 // Checks the descriptor and fills in the kernels' form of it.
 int check_paged_q8(const char* who, const q1_paged_q8* kv, Paged8& p);
 
-// cache8.cu: the keys and values of sequences [0, batch) of p with more than
-// `least_rows` / group new tokens, of type `bf16` or f16, to k and v of pages of 128 tokens,
-// [sequence * pages + page][kv_heads][128][dim], and the table of those pages (`table`,
-// `pages` a sequence).
+// cache8.cu: f16 copies of the keys and values of the sequences of p with at least
+// `least_rows` / group new tokens, for the tensor-core kernel: pages of 128 tokens,
+// [part][sequence * pages + page][kv_heads][128][dim], `pages` of them a sequence, and their
+// `table`.  Values of a sequence and head are divided by a power of two that brings the
+// largest possible one near f16's, [sequence][kv_heads][keys, values] in `factors`; a second part
+// holds what rounding to f16 took.
+constexpr int kTopSlices = 16;
 struct CopyQ8 {
   Paged8 p;
-  void *k, *v;
+  __half *k, *v;
   int32_t* table;
+  float* factors;
+  uint32_t* tops;  // [sequence][kv_heads][keys, values][slices]: the largest scales
   unsigned* status;
-  int pages, dim, group, least_rows;
+  int pages, parts, dim, group, least_rows;
 };
-int launch_copy_q8(const CopyQ8& c, bool bf16, cudaStream_t s);
+int launch_copy_q8(const CopyQ8& c, cudaStream_t s);
 
 }  // namespace q1

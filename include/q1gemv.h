@@ -524,21 +524,22 @@ int q1_cache_read_q8(const q1_paged_q8 *kv, int dtype, void *k_out, void *v_out,
 
 /* Bytes of q1_paged_attention_q8's workspace, on the current device, for
  * sequences of up to max_new new tokens.  Where max_new asks for the
- * tensor-core kernel that includes 16-bit copies of the keys and values of
- * `sequences` sequences of up to table_tokens (the table's width times the page
- * size); else both are not looked at.  Negative Q1_ERR_ARG for a bad shape. */
+ * tensor-core kernel that includes f16 copies of the keys and values (for f16 q
+ * in two parts) of `sequences` sequences of up to table_tokens (the table's width
+ * times the page size); else both are not looked at.  Negative Q1_ERR_ARG for a bad shape. */
 int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t heads, int64_t kv_heads, int64_t dim,
-                                        int64_t table_tokens, int64_t sequences);
+                                        int dtype, int64_t table_tokens, int64_t sequences);
 
 /* q1_paged_attention over a q8_0 cache; q and out are of `dtype` (Q1_BF16 or
  * Q1_F16).  Up to some tens of rows a key head (new tokens times the group) the
  * quants are multiplied as they are, which is exact, and scales are applied to
  * sums (keys) and weights (values, whose product with the scale is rounded to
- * bf16, with f16 q to the sum of two bf16).  More rows take the tensor-core kernel over a 16-bit copy
- * of the sequence, each value quant * scale rounded once to q's type (with
- * f16 it must stay below 65504), made by the call in the workspace, for as many
- * sequences at a time as it holds: at least q1_paged_attention_q8_workspace(...,
- * 1) bytes are needed, and more make fewer launches of several such sequences.
+ * bf16, with f16 q to the sum of two bf16).  More rows take the tensor-core kernel
+ * over a copy of the sequence that the call makes in the workspace: each value quant *
+ * scale, divided by a power of two for its sequence and head (so its size does not
+ * matter), rounded to f16, and with f16 q the remainder as a second f16.  As many sequences
+ * are copied at a time as the workspace holds: at least q1_paged_attention_q8_workspace(...,
+ * 1) bytes are needed, and more make fewer launches for several such sequences.
  * All else as q1_paged_attention; a value is no number where its scale is none. */
 int q1_paged_attention_q8(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
                           int dtype, const q1_paged_q8 *kv, int64_t max_new, void *out, int64_t out_token_stride,
