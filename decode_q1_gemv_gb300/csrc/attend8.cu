@@ -95,8 +95,9 @@ __device__ __forceinline__ uint32_t quants_bf16(uint32_t w) {
   const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(low), reinterpret_cast<const __nv_bfloat162&>(sign));
   return reinterpret_cast<const uint32_t&>(r);
 }
-// Scales of one key, `kBlocks` of them, from shared memory.
-template <int kBlocks>
+// Scales of one key, `kBlocks` of them, from shared memory.  For keys (kSum) an infinite one
+// is NaN, as the sum of the block's values is: the scale only meets the sum of the quants.
+template <int kBlocks, bool kSum>
 __device__ __forceinline__ void scales_of(const unsigned char* at, float (&d)[kBlocks]) {
   uint32_t w[kBlocks / 2];
   if constexpr (kBlocks == 4) {
@@ -106,7 +107,14 @@ __device__ __forceinline__ void scales_of(const unsigned char* at, float (&d)[kB
     w[0] = *reinterpret_cast<const uint32_t*>(at);
   }
 #pragma unroll
-  for (int i = 0; i < kBlocks / 2; ++i) Elem<__half>::unpack2(w[i], d[2 * i], d[2 * i + 1]);
+  for (int i = 0; i < kBlocks / 2; ++i) {
+    if constexpr (kSum) {  // d * 0 + d
+      const uint32_t zero = 0u;
+      const __half2 r = __hfma2(reinterpret_cast<const __half2&>(w[i]), reinterpret_cast<const __half2&>(zero), reinterpret_cast<const __half2&>(w[i]));
+      w[i] = reinterpret_cast<const uint32_t&>(r);
+    }
+    Elem<__half>::unpack2(w[i], d[2 * i], d[2 * i + 1]);
+  }
 }
 
 // kCluster: not shares of the axis but a cluster of a.ctas CTAs for each
@@ -273,8 +281,8 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
       const int r = (lane & 7) + (lane & 8), second = lane >> 4;
       {
         float d0[kBlocks], d8[kBlocks];
-        scales_of<kBlocks>(stage + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes, d0);
-        scales_of<kBlocks>(stage + 2 * Shape::kChunkBytes + (g + 8) * Shape::kScaleBytes, d8);
+        scales_of<kBlocks, true>(stage + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes, d0);
+        scales_of<kBlocks, true>(stage + 2 * Shape::kChunkBytes + (g + 8) * Shape::kScaleBytes, d8);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           uint32_t w[4];
@@ -334,8 +342,8 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
           sum[t][e & 1] += s[t][e];
         }
       float d0[kBlocks], d8[kBlocks];
-      scales_of<kBlocks>(stage + 2 * Shape::kChunkBytes + (16 + g) * Shape::kScaleBytes, d0);
-      scales_of<kBlocks>(stage + 2 * Shape::kChunkBytes + (24 + g) * Shape::kScaleBytes, d8);
+      scales_of<kBlocks, false>(stage + 2 * Shape::kChunkBytes + (16 + g) * Shape::kScaleBytes, d0);
+      scales_of<kBlocks, false>(stage + 2 * Shape::kChunkBytes + (24 + g) * Shape::kScaleBytes, d8);
       // A scale that is no number must not reach, as 0 * inf, the rows that may not see its key.
       bool careful = false;
       if (partial_view) {

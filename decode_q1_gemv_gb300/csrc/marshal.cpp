@@ -488,7 +488,7 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t count) {
       s.top_k_all = k < 0 ? 0 : k > (int64_t(1) << 30) ? 1 << 30 : static_cast<int32_t>(k);
     }
     at::Tensor out = given_or_new(a[6], "out", rows, logits, at::kInt);
-    check(q1_sample(pl, stride(logits, 0, logits.size(1)), rows[0], logits.size(1), type_code(logits.scalar_type()),
+    check(q1_sample(pl, logits.size(0) > 1 ? logits.stride(0) : logits.size(1), rows[0], logits.size(1), type_code(logits.scalar_type()),
                     static_cast<const float*>(pointer(tensor(a[1], "uniform"), "uniform", kF32, rows, true)), &s,
                     static_cast<int32_t*>(pointer(out, "out", kI32, rows, true)), reinterpret_cast<void*>(integer(a[7]))),
           "q1_sample");

@@ -632,7 +632,7 @@ extern "C" int q1_sample(const void* logits, int64_t ld, int64_t rows, int64_t v
     return fail(Q1_ERR_ARG, "%s: bad shape rows=%lld vocab=%lld", who, (long long)rows, (long long)vocab);
   if (dtype != Q1_F32 && dtype != Q1_BF16 && dtype != Q1_F16) return fail(Q1_ERR_ARG, "%s: bad type %d", who, dtype);
   if (!logits || !uniform || !settings || !out) return fail(Q1_ERR_ARG, "%s: null pointer", who);
-  if (ld < vocab) return fail(Q1_ERR_ARG, "%s: a row stride is less than vocab", who);
+  if (ld < vocab && ld != 0) return fail(Q1_ERR_ARG, "%s: a row stride is less than vocab", who);
   if (reinterpret_cast<uintptr_t>(logits) % (dtype == Q1_F32 ? 4 : 2) || !aligned4(uniform) || !aligned4(out) ||
       !aligned4(settings->temperature) || !aligned4(settings->top_k) || !aligned4(settings->top_p) || !aligned4(settings->min_p))
     return fail(Q1_ERR_ARG, "%s: a misaligned pointer", who);

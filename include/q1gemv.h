@@ -586,8 +586,8 @@ typedef struct q1_sampling {
  *   out = the first token, in the order of the vocabulary, at which the sum of the w that
  *   stayed exceeds uniform times all of it.
  * temperature 0 and below: the first token with the largest logit.
- *   logits : [rows][vocab] of `dtype` (Q1_F32, Q1_BF16, Q1_F16), rows ld apart,
- *     aligned to the type's size (16-byte aligned rows are faster).
+ *   logits : [rows][vocab] of `dtype` (Q1_F32, Q1_BF16, Q1_F16), rows ld apart
+ *     (0: one row for all), aligned to the type's size.
  *   uniform : f32 [rows], in [0, 1) (held within it).
  *   out : int32 [rows].
  * The weights are fixed-point numbers of 44 bits behind the point, off by 2^-30 of
