@@ -10,19 +10,23 @@
 // weights are fixed-point numbers (44 bits behind the point, 2^-30 of themselves) and
 // sums are 64-bit integers: exact, in any order, the same in every launch.  Sums of
 // f32 weights in f32 would give another token in some percent of rows.
-//   x - max in two floats, times c in two floats: the exponent's whole part n,
-//   a 256th part k (a table of 2^(k/256)) and a rest below 2^-9, whose 2^r - 1 is a
-//   polynomial of degree three (what follows is below 2^-43).
+//   x - max in two floats, times c in two floats: the exponent's whole part n, a
+//   512th part k (a table of 2^(k/512)) and a rest r below 2^-10, whose 2^r - 1 is
+//   r (ln 2 + r ln^2(2) / 2) (what follows is below 2^-34).
 //
 // A row belongs to a cluster of up to 16 CTAs (as many as all rows leave room
 // for), each with a slice of the vocabulary, each warp with a part of it:
 //   1  the maximum, and whether all values are numbers;
-//   2  (top-k, top-p) a histogram over the exponent, 1024 bins, of counts and sums, joined
-//      through distributed shared memory: the bin where the threshold lies;
-//   3a few tokens down to that bin (512 at most; the usual case): they go to one CTA,
-//      which sorts them, cuts, and draws;
-//   3b many: the threshold within the bin by histograms of its tokens' bits, ten at a time;
-//   4  (3b, and without top-k and top-p) sums by warp, whose one holds the token, and the
+//   2  (small top-k) a value that top-k tokens at least reach: of the threads' own
+//      maxima the one with k / CTAs - 1 others above it in each CTA, the least of these;
+//      what reaches it is listed: 4a;
+//   3  (top-p, large top-k, or a list that is too long) a histogram over the exponent, 1024
+//      bins, of counts and sums, joined through distributed shared memory: the
+//      bin where the threshold lies.  The tokens down to that bin are listed if they are few: 4a;
+//      else those of the bin alone are, for the threshold; else (many equal ones) it is found by
+//      histograms of their bits, ten at a time: 4b;
+//   4a one CTA sorts the list, cuts, and draws;
+//   4b (and without top-k and top-p) sums by warp, whose one holds the token, and the
 //      token in it.
 // Bytes bound the largest calls, a few barriers of the cluster the smallest ones.
 #include <algorithm>
@@ -39,24 +43,21 @@ namespace cg = cooperative_groups;
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kListed = 512;         // tokens that one CTA sorts
-constexpr int kSteps = 256;          // parts of an exponent
+constexpr int kListed = 1024;        // tokens that one CTA sorts
+constexpr int kFewTopK = 256;        // top-k by the threads' maxima
+constexpr int kSteps = 512;          // parts of an exponent
 constexpr int kOne = 44;             // bits behind the point
-constexpr float kLeast = -45.5f;     // exponents below are weights of zero
+constexpr float kLeast = -44.f;      // exponents from here down are weights of zero
 
 struct Powers {
-  uint32_t bits[kSteps + 1];  // 2^(k/256) 2^31, k = -128..128
+  uint32_t bits[kSteps];  // 2^(k/512) 2^31
 };
 constexpr Powers make_powers() {
   Powers t = {};
-  // 2^(1/256) to 2^-53: its powers are off by some 2^-46
-  const double root = 1.0027112750502024854;
+  // 2^(1/512) to 2^-53: its powers are off by some 2^-44
+  const double root = 1.0013547198921082058;
   double up = 1.0;
-  for (int k = 0; k <= kSteps / 2; ++k) {
-    t.bits[kSteps / 2 + k] = uint32_t(up * 2147483648.0 + 0.5);
-    t.bits[kSteps / 2 - k] = uint32_t(2147483648.0 / up + 0.5);
-    up *= root;
-  }
+  for (int k = 0; k < kSteps; ++k) t.bits[k] = uint32_t(up * 2147483648.0 + 0.5), up *= root;
   return t;
 }
 __device__ const Powers g_powers = make_powers();
@@ -86,17 +87,18 @@ __device__ __forceinline__ uint64_t weight_of(const Weigh& w, float x) {
   const float back = __fsub_rn(d, x);
   const float lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(w.max, back));  // x - max - d
   const float rest = __fmaf_rn(lost, w.ch, __fmaf_rn(d, w.cl, __fmaf_rn(d, w.ch, -y)));
-  // y = n + k / 256 + r: rounded by adding 1.5 2^23 (|y| 256 < 2^22)
-  const float n = __fsub_rn(__fadd_rn(y, kMagic), kMagic), f = __fsub_rn(y, n);
-  const float scaled = __fadd_rn(__fmul_rn(f, float(kSteps)), kMagic);
-  const int k = int(__float_as_uint(scaled) - kMagicBits);
-  const float r = __fadd_rn(__fmaf_rn(__fsub_rn(scaled, kMagic), -1.0f / kSteps, f), rest);
-  const float p = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.05550411f, 0.24022651f), 0.69314718f));  // 2^r - 1
-  const uint32_t t = w.powers[k + kSteps / 2];
-  // |t p| < 2^22: rounded by the same addition
-  const uint32_t bits = t + (__float_as_uint(__fmaf_rn(__uint2float_rn(t), p, kMagic)) - kMagicBits);
-  return (uint64_t(bits) << (kOne - 31)) >> int(-n);
+  // y = n + k / 512 + r: rounded by adding 1.5 2^23 (|y| 512 < 2^22)
+  const float z = __fmaf_rn(y, float(kSteps), kMagic);
+  const int whole = int(__float_as_uint(z) - kMagicBits);
+  const float r = __fadd_rn(__fmaf_rn(__fsub_rn(z, kMagic), -1.0f / kSteps, y), rest);
+  const float p = __fmul_rn(r, __fmaf_rn(r, 0.24022651f, 0.69314718f));  // 2^r - 1
+  const uint32_t t = w.powers[whole & (kSteps - 1)];
+  // t p < 2^22, rounded by the same addition; t as a float (truncated) by its bits
+  const float tf = __uint_as_float((t >> 8) + (157u << 23));
+  const uint32_t bits = t + (__float_as_uint(__fmaf_rn(tf, p, kMagic)) - kMagicBits);
+  return (uint64_t(bits) << 32) >> (32 + 31 - kOne - (whole >> 9));
 }
+static_assert(kSteps == 512, "the shift above");
 
 __device__ __forceinline__ uint32_t order_of(float x) {  // rises with x; -0 as 0
   const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));
@@ -135,19 +137,24 @@ struct Found {
 };
 
 struct SampleShared {
-  uint32_t powers[kSteps + 1];
+  uint32_t powers[kSteps];
   uint32_t count[kBins], low[kBins], high[kBins];        // of this CTA
   uint32_t all_count[kBins];                             // of the row
-  uint64_t all_mass[kBins];
-  uint64_t list[kListed], sorted[kListed];
+  union {
+    uint64_t all_mass[kBins];
+    uint64_t sorted[kListed];  // (once the bins have been searched)
+  };
+  uint64_t list[kListed];
   uint64_t warp_mass[kSampleWarps];
   uint32_t warp_count[kSampleWarps];
   Found found;
-  float row_max, own_max;
+  float own_max;
+  uint32_t own_reached;
   int own_bad, listed, token;
   uint64_t own_mass;
   uint32_t own_ties;
-  uint64_t row_mass;
+  uint32_t cut;            // of the leader: what a list's threshold is
+  uint64_t cut_ties;
 };
 
 template <class T>
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = int(blockIdx.x) / a.ctas, rank = int(blockIdx.x) - row * a.ctas;
-  for (int i = threadIdx.x; i <= kSteps; i += kSampleThreads) sh.powers[i] = g_powers.bits[i];
+  for (int i = threadIdx.x; i < kSteps; i += kSampleThreads) sh.powers[i] = g_powers.bits[i];
   pdl_launch_dependents();
   pdl_wait();
   const float temperature = a.set.temperature ? a.set.temperature[row] : a.set.temperature_all;
@@ -315,18 +322,30 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
             to = x.first + int(int64_t(mine) * (warp + 1) / kSampleWarps);
 
   // 1. The maximum.
+  const bool by_count = top_k > 0 && top_k < a.vocab, by_mass = top_p < 1.f;
   float top = -INFINITY;
   bool bad = false;
   x.template each<true>(from, to, [&](const float (&v)[G], int) {
 #pragma unroll
     for (int i = 0; i < G; ++i) top = fmaxf(top, v[i]), bad |= !(v[i] <= FLT_MAX);
   });
+  const float mine_top = top;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (threadIdx.x == 0) sh.listed = 0, sh.token = a.vocab;
   for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0, sh.low[i] = 0, sh.high[i] = 0;
   if (lane == 0) sh.warp_count[warp] = __float_as_uint(top);
   bad = __syncthreads_or(bad);
+  // 2. A value that so many threads' maxima reach that all CTAs together have top-k of them: the upper 20 bits of it.
+  const bool few = by_count && top_k <= kFewTopK && temperature > 0.f;
+  if (few) {
+    const uint32_t o = order_of(mine_top);
+    const int want = (top_k + a.ctas - 1) / a.ctas;
+    uint32_t reached = 0;
+    for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1)
+      if (__syncthreads_count(o >= (reached | bit)) >= want) reached |= bit;
+    if (threadIdx.x == 0) sh.own_reached = reached;
+  }
   if (warp == 0) {
     float m = lane < kSampleWarps ? __uint_as_float(sh.warp_count[lane]) : -INFINITY;
 #pragma unroll
@@ -334,9 +353,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (lane == 0) sh.own_max = m, sh.own_bad = bad;
   }
   cluster.sync();
+  uint32_t reached = 0xffffffffu;
   for (int r = 0; r < a.ctas; ++r) {
     const SampleShared* his = cluster.map_shared_rank(&sh, r);
     top = fmaxf(top, his->own_max), bad |= his->own_bad != 0;
+    reached = min(reached, his->own_reached);
   }
   bad |= top == -INFINITY || isnan(temperature) || isnan(top_p) || isnan(min_p) || isnan(uniform);
   if (bad) {
@@ -369,7 +390,91 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   w.cl = w.ch > 0.f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-w.ch, t, kLog), kLogRest), t) : 0.f;
   const float u = fminf(fmaxf(uniform, 0.f), 0.99999994f);
   const uint64_t least = min_p >= 1.f ? uint64_t(1) << kOne : min_p > 0.f ? part_of(min_p, uint64_t(1) << kOne, true) : 1;
-  const bool by_count = top_k > 0 && top_k < a.vocab, by_mass = top_p < 1.f;
+  // 4a. The first CTA collects all lists, up to kListed tokens in all, and sorts them by falling values,
+  // equal ones by their place; returns how many (0 where there are more: all CTAs get it, one sorts).
+  const auto collect = [&]() {
+    cluster.sync();
+    int n = 0;
+    for (int r = 0; r < a.ctas; ++r) n += cluster.map_shared_rank(&sh, r)->listed;
+    if (n > kListed || rank != 0) return n > kListed ? 0 : n;
+    n = 0;
+    for (int r = 0; r < a.ctas; ++r) {
+      const SampleShared* his = cluster.map_shared_rank(&sh, r);
+      const int count = his->listed;
+      for (int i = threadIdx.x; i < count; i += kSampleThreads) sh.sorted[n + i] = his->list[i];
+      n += count;
+    }
+    int padded = 2;
+    while (padded < n) padded <<= 1;
+    for (int i = n + threadIdx.x; i < padded; i += kSampleThreads) sh.sorted[i] = ~uint64_t(0);
+    sort(sh.sorted, padded);
+    return n;
+  };
+  const auto list = [&](float v, int place) {
+    const int i = atomicAdd(&sh.listed, 1);
+    if (i < kListed) sh.list[i] = uint64_t(~order_of(v)) << 32 | uint32_t(place);
+  };
+  const auto entry_weight = [&](uint32_t upside_down) { return weight_of(w, of_order(~upside_down)); };
+  constexpr int kEach = kListed / kSampleThreads;
+  // The token, where all that may stay is among the n tokens sorted: the first `count` of them, then by mass
+  // (need 0: top_p of their own).
+  const auto finish = [&](int n, int count, uint64_t need) {
+    uint64_t weight[kEach], sum = 0, all;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = threadIdx.x * kEach + k;
+      weight[k] = i < min(n, count) ? entry_weight(uint32_t(sh.sorted[i] >> 32)) : 0;
+      sum += weight[k];
+    }
+    uint64_t before = block_prefix(sh, sum, all) - sum;
+    if (by_mass && need == 0) need = max(part_of(fmaxf(top_p, 0.f), all, true), uint64_t(1));
+    uint64_t entry[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = threadIdx.x * kEach + k;
+      const bool stays = weight[k] >= least && (!by_mass || before < need);
+      before += weight[k];
+      entry[k] = stays ? sh.sorted[i] << 32 | sh.sorted[i] >> 32 : ~uint64_t(0);
+    }
+    // In the vocabulary's order: the sums of the weights there.
+    __syncthreads();
+    int padded = 2;
+    while (padded < n) padded <<= 1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (threadIdx.x * kEach + k < padded) sh.sorted[threadIdx.x * kEach + k] = entry[k];
+    sort(sh.sorted, padded);
+    sum = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = threadIdx.x * kEach + k;
+      entry[k] = i < padded ? sh.sorted[i] : ~uint64_t(0);
+      weight[k] = entry[k] != ~uint64_t(0) ? entry_weight(uint32_t(entry[k])) : 0;
+      sum += weight[k];
+    }
+    before = block_prefix(sh, sum, all) - sum;
+    const uint64_t drawn = part_of(u, all, false);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (drawn >= before && drawn < before + weight[k]) a.out[row] = int32_t(entry[k] >> 32);
+      before += weight[k];
+    }
+  };
+  if (few) {
+    const float from_value = of_order(max(reached, 0x00800000u));  // (-inf and what lies below it: none)
+    x.template each<false>(from, to, [&](const float (&v)[G], int e) {
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (v[i] >= from_value) list(v[i], e + i);
+    });
+    if (const int n = collect()) {
+      if (rank == 0) finish(n, top_k, 0);
+      cluster.sync();  // the lists have been read
+      return;
+    }
+    cluster.sync();
+    if (threadIdx.x == 0) sh.listed = 0;
+  }
 
   // The histogram of this CTA (`which`: its bin of a value, -1 for none) becomes the row's, in every CTA.
   const auto histogram = [&](auto&& which) {
@@ -405,7 +510,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 
   uint32_t limit = 0;            // tokens above it (in order_of) stay,
   uint64_t ties = 0;             // and as many of those at it, the first ones
-  uint64_t tie_weight = 0;
+  uint64_t tie_weight = 0, kept = 0;  // kept: the sum of what top-k leaves
   if (by_count || by_mass) {
     const auto whole_row = [&](float v) { return bin_of(w, v); };
     histogram(whole_row);
@@ -418,75 +523,82 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     bool mass = !by_count;  // what is searched for
     Found f = search(sh, mass, need, 0, 0);
     for (bool first = true;; first = false) {
-      if (f.above + f.in <= kListed) {
-        // 3a. All tokens of these bins (from the second search on the count was dealt with).
-        const int last_bin = f.bin;
+      const bool all_few = f.above + f.in <= kListed;
+      if (f.in <= kListed) {
+        // 4a. All tokens down to this bin, or those of this bin alone.  (From the second search on top-k was dealt with.)
+        const int bin = f.bin;
         x.template each<false>(from, to, [&](const float (&v)[G], int e) {
 #pragma unroll
-          for (int i = 0; i < G; ++i)
-            if (exponent_of(w, v[i]) > kLeast && bin_of(w, v[i]) <= last_bin && weight_of(w, v[i]))
-              sh.list[atomicAdd(&sh.listed, 1)] = uint64_t(~order_of(v[i])) << 32 | uint32_t(e + i);
+          for (int i = 0; i < G; ++i) {
+            if (!(exponent_of(w, v[i]) > kLeast)) continue;
+            const int b = bin_of(w, v[i]);
+            if ((b == bin || (all_few && b < bin)) && weight_of(w, v[i])) list(v[i], e + i);
+          }
         });
-        cluster.sync();
-        if (rank == 0) {
-          int n = 0;
-          for (int r = 0; r < a.ctas; ++r) {
-            const SampleShared* his = cluster.map_shared_rank(&sh, r);
-            const int count = his->listed;
-            for (int i = threadIdx.x; i < count; i += kSampleThreads) sh.sorted[n + i] = his->list[i];
-            n += count;
-          }
-          int padded = 2;
-          while (padded < n) padded <<= 1;
-          for (int i = n + threadIdx.x; i < padded; i += kSampleThreads) sh.sorted[i] = ~uint64_t(0);
-          sort(sh.sorted, padded);
-          const int i = threadIdx.x;
-          const uint64_t entry = i < n ? sh.sorted[i] : 0;
-          const bool counted = i < n && (!by_count || !first || i < top_k);
-          uint64_t weight = counted ? weight_of(w, of_order(~uint32_t(entry >> 32))) : 0, all;
-          const uint64_t with = block_prefix(sh, weight, all);
-          if (by_mass) {
-            // What top-p leaves of the tokens that top-k left: `need` where that was known before.
-            const uint64_t enough = first && by_count ? max(part_of(fmaxf(top_p, 0.f), all, true), uint64_t(1)) : need;
-            if (with - weight >= enough) weight = 0;
-          }
-          if (weight < least) weight = 0;
-          // In the vocabulary's order: the sums of the weights there.
-          __syncthreads();
-          if (i < padded) sh.sorted[i] = weight ? entry << 32 | entry >> 32 : ~uint64_t(0);
-          sort(sh.sorted, padded);
-          const uint64_t back = i < padded ? sh.sorted[i] : ~uint64_t(0);
-          weight = back != ~uint64_t(0) ? weight_of(w, of_order(~uint32_t(back))) : 0;
-          const uint64_t sums = block_prefix(sh, weight, all), drawn = part_of(u, all, false);
-          if (sums > drawn && sums - weight <= drawn) a.out[row] = int32_t(back >> 32);
+        const int n = collect();
+        if (all_few) {
+          if (rank == 0) finish(n, by_count && first ? top_k : n, first && by_count ? 0 : need);
+          cluster.sync();  // the lists have been read
+          return;
         }
-        cluster.sync();  // the lists have been read
-        return;
-      }
-      // 3b. The threshold within the bin, ten bits of its values at a time (of 16-bit types the first 20 differ).
-      const int bin = f.bin;
-      uint32_t prefix = 0, known = 0;  // the bits found
-      Found at = f;
+        // The threshold is the first entry at which the count or the sum is reached: it, and those of its value before it.
+        if (rank == 0) {
+          uint64_t weight[kEach], sum = 0, all;
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x * kEach + k;
+            weight[k] = i < n ? entry_weight(uint32_t(sh.sorted[i] >> 32)) : 0;
+            sum += weight[k];
+          }
+          uint64_t before = f.mass_above + block_prefix(sh, sum, all) - sum;
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x * kEach + k;
+            const bool is = mass ? before < need && before + weight[k] >= need : uint64_t(f.above) + i + 1 == need;
+            if (i < n && (is || (i == n - 1 && (mass ? before + weight[k] : uint64_t(f.above) + n) < need))) {
+              const uint32_t value = uint32_t(sh.sorted[i] >> 32);
+              int same = 1;
+              while (i - same >= 0 && uint32_t(sh.sorted[i - same] >> 32) == value) ++same;
+              sh.cut = ~value, sh.cut_ties = same;
+              sh.own_mass = before + weight[k];  // of all that stays
+            }
+            before += weight[k];
+          }
+        }
+        cluster.sync();
+        const SampleShared* his = cluster.map_shared_rank(&sh, 0);
+        limit = his->cut, ties = his->cut_ties, tie_weight = weight_of(w, of_order(limit));
+        kept = his->own_mass;
+        cluster.sync();
+        if (threadIdx.x == 0) sh.listed = 0;
+        __syncthreads();
+      } else {
+        // The threshold within the bin, ten bits of its values at a time (of 16-bit types the first 20 differ).
+        const int bin = f.bin;
+        uint32_t prefix = 0, known = 0;  // the bits found
+        Found at = f;
 #pragma unroll 1
-      for (int shift = 22;; shift = max(0, shift - 10)) {
-        const uint32_t width = known ? min(10, __ffs(int(known)) - 1 - shift) : 10;
-        const uint32_t most = (1u << width) - 1;
-        histogram([&](float v) {
-          const uint32_t o = order_of(v);
-          return bin_of(w, v) == bin && (o & known) == prefix ? int(most - ((o >> shift) & most)) : -1;
-        });
-        at = search(sh, mass, need, at.above, at.mass_above);
-        prefix |= (most - uint32_t(at.bin)) << shift, known |= most << shift;
-        if (shift == 0 || (G == 8 && shift <= 12)) break;
+        for (int shift = 22;; shift = max(0, shift - 10)) {
+          const uint32_t width = known ? min(10, __ffs(int(known)) - 1 - shift) : 10;
+          const uint32_t most = (1u << width) - 1;
+          histogram([&](float v) {
+            const uint32_t o = order_of(v);
+            return bin_of(w, v) == bin && (o & known) == prefix ? int(most - ((o >> shift) & most)) : -1;
+          });
+          at = search(sh, mass, need, at.above, at.mass_above);
+          prefix |= (most - uint32_t(at.bin)) << shift, known |= most << shift;
+          if (shift == 0 || (G == 8 && shift <= 12)) break;
+        }
+        if (G == 8) prefix |= prefix >> 31 ? 0 : 0xfffu;  // the bits that 16-bit types do not have
+        limit = prefix, tie_weight = at.mass_in / at.in;
+        ties = mass ? (need - at.mass_above + tie_weight - 1) / tie_weight : need - at.above;
+        ties = min(ties, uint64_t(at.in));
+        kept = at.mass_above + ties * tie_weight;
       }
-      if (G == 8) prefix |= prefix >> 31 ? 0 : 0xfffu;  // the bits that 16-bit types do not have
-      limit = prefix, tie_weight = at.mass_in / at.in;
-      ties = mass ? (need - at.mass_above + tie_weight - 1) / tie_weight : need - at.above;
-      ties = min(ties, uint64_t(at.in));
       if (mass || !by_mass) break;
       // top-p of what top-k left: the same histogram, made once more.
       mass = true;
-      need = max(part_of(top_p > 0.f ? top_p : 0.f, at.mass_above + ties * tie_weight, true), uint64_t(1));
+      need = max(part_of(top_p > 0.f ? top_p : 0.f, kept, true), uint64_t(1));
       histogram(whole_row);
       f = search(sh, true, need, 0, 0);
     }
@@ -494,16 +606,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   }
 
   // 4. Sums of what stays, by warp: weights above the limit, and values at it.
+  const float border = limit ? of_order(limit) : -INFINITY;
   const auto sums_of = [&](int a0, int b0, uint64_t& sum, uint32_t& at_limit) {
     sum = 0, at_limit = 0;
     x.template each<false>(a0, b0, [&](const float (&v)[G], int) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const uint32_t o = order_of(v[i]);
-        if (o < limit) continue;
-        if (o == limit) {
-          ++at_limit;
-        } else {
+        at_limit += v[i] == border;
+        if (v[i] > border) {
           const uint64_t m = weight_of(w, v[i]);
           sum += m >= least ? m : 0;
         }
@@ -571,16 +681,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         uint64_t m[G], lane_sum = 0;
         uint32_t lane_ties = 0;
 #pragma unroll
-        for (int k = 0; k < G; ++k) lane_ties += order_of(v[k]) == limit;
+        for (int k = 0; k < G; ++k) lane_ties += v[k] == border;
         uint64_t tie = before_ties + warp_prefix(lane_ties) - lane_ties;
         before_ties += __reduce_add_sync(0xffffffffu, lane_ties);
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-          const uint32_t o = order_of(v[k]);
           m[k] = 0;
-          if (o == limit) {
+          if (v[k] == border) {
             m[k] = tied(tie, 1), ++tie;
-          } else if (o > limit) {
+          } else if (v[k] > border) {
             m[k] = weight_of(w, v[k]);
             if (m[k] < least) m[k] = 0;
           }
