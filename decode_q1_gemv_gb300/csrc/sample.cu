@@ -149,7 +149,7 @@ struct SampleShared {
   uint32_t warp_count[kSampleWarps];
   Found found;
   float own_max;
-  uint32_t own_reached;
+  float own_reached;       // what at least its part of top-k tokens reach
   int own_bad, listed, token;
   uint64_t own_mass;
   uint32_t own_ties;
@@ -266,12 +266,32 @@ __device__ __forceinline__ Found search(SampleShared& sh, bool by_mass, uint64_t
   return sh.found;
 }
 
-// Sorts the first `n` (a power of two up to kListed) of v, rising.
-__device__ __forceinline__ void sort(uint64_t* v, int n) {
-  for (int size = 2; size <= n; size <<= 1)
+// Sorts the n (up to kListed) different entries of sh.sorted, rising; ~0 follows them up to a power of two.
+// Every thread of the CTA calls.
+constexpr int kByRank = 256;
+__device__ __forceinline__ void sort(SampleShared& sh, int n) {
+  uint64_t* v = sh.sorted;
+  __syncthreads();
+  if (n <= kByRank) {  // each entry goes where it belongs: two threads count the entries below it (two barriers, not 28 to 36)
+    const int i = threadIdx.x >> 1, half = threadIdx.x & 1, mid = (n + 1) / 2;
+    const uint64_t mine = i < n ? v[i] : 0;
+    int below = 0;
+    if (i < n)
+#pragma unroll 4
+      for (int k = half ? mid : 0; k < (half ? n : mid); ++k) below += v[k] < mine;
+    below += __shfl_xor_sync(0xffffffffu, below, 1);
+    __syncthreads();
+    if (i < n && half == 0) v[below] = mine;
+    __syncthreads();
+    return;
+  }
+  int padded = 2;
+  while (padded < n) padded <<= 1;
+  for (int i = n + threadIdx.x; i < padded; i += kSampleThreads) v[i] = ~uint64_t(0);
+  for (int size = 2; size <= padded; size <<= 1)
     for (int step = size >> 1; step > 0; step >>= 1) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kSampleThreads) {
+      for (int i = threadIdx.x; i < padded / 2; i += kSampleThreads) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const uint64_t a = v[lo], b = v[hi];
         if ((a > b) == ((lo & size) == 0)) v[lo] = b, v[hi] = a;
@@ -283,16 +303,13 @@ __device__ __forceinline__ void sort(uint64_t* v, int n) {
 // The sums of v over the CTA's threads up to each (its own among them), and of all.
 __device__ __forceinline__ uint64_t block_prefix(SampleShared& sh, uint64_t v, uint64_t& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t p = warp_prefix(v);
+  const uint64_t p = warp_prefix(v);
   __syncthreads();
   if (lane == 31) sh.warp_mass[warp] = p;
   __syncthreads();
-  all = 0;
-  for (int w = 0; w < kSampleWarps; ++w) {
-    if (w < warp) p += sh.warp_mass[w];
-    all += sh.warp_mass[w];
-  }
-  return p;
+  const uint64_t warps = warp_prefix(lane < kSampleWarps ? sh.warp_mass[lane] : 0);
+  all = __shfl_sync(0xffffffffu, warps, 31);
+  return p + (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0);
 }
 
 template <class T>
@@ -336,15 +353,26 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0, sh.low[i] = 0, sh.high[i] = 0;
   if (lane == 0) sh.warp_count[warp] = __float_as_uint(top);
   bad = __syncthreads_or(bad);
-  // 2. A value that so many threads' maxima reach that all CTAs together have top-k of them: the upper 20 bits of it.
+  // 2. A value that so many threads' maxima reach that all CTAs together have top-k of them, to a 2^-10th of their range.
   const bool few = by_count && top_k <= kFewTopK && temperature > 0.f;
   if (few) {
-    const uint32_t o = order_of(mine_top);
+    float lo = mine_top == -INFINITY ? INFINITY : mine_top;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    if (lane == 0) sh.warp_mass[warp] = __float_as_uint(lo);
     const int want = (top_k + a.ctas - 1) / a.ctas;
-    uint32_t reached = 0;
-    for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1)
-      if (__syncthreads_count(o >= (reached | bit)) >= want) reached |= bit;
-    if (threadIdx.x == 0) sh.own_reached = reached;
+    const bool enough = __syncthreads_count(mine_top > -INFINITY) >= want;
+    lo = __uint_as_float(uint32_t(sh.warp_mass[lane % kSampleWarps]));
+    float hi = __uint_as_float(sh.warp_count[lane % kSampleWarps]);
+#pragma unroll
+    for (int off = kSampleWarps / 2; off > 0; off >>= 1)
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off)), hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    if (enough)
+      for (int i = 0; i < 10; ++i) {
+        const float mid = 0.5f * lo + 0.5f * hi;
+        (__syncthreads_count(mine_top >= mid) >= want ? lo : hi) = mid;
+      }
+    if (threadIdx.x == 0) sh.own_reached = enough ? lo : -FLT_MAX;
   }
   if (warp == 0) {
     float m = lane < kSampleWarps ? __uint_as_float(sh.warp_count[lane]) : -INFINITY;
@@ -353,11 +381,16 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (lane == 0) sh.own_max = m, sh.own_bad = bad;
   }
   cluster.sync();
-  uint32_t reached = 0xffffffffu;
-  for (int r = 0; r < a.ctas; ++r) {
-    const SampleShared* his = cluster.map_shared_rank(&sh, r);
-    top = fmaxf(top, his->own_max), bad |= his->own_bad != 0;
-    reached = min(reached, his->own_reached);
+  float reached = INFINITY;
+  {
+    const SampleShared* his = cluster.map_shared_rank(&sh, lane < a.ctas ? lane : 0);
+    top = his->own_max, reached = his->own_reached, bad = his->own_bad != 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      reached = fminf(reached, __shfl_xor_sync(0xffffffffu, reached, off));
+    }
+    bad = __any_sync(0xffffffffu, bad);
   }
   bad |= top == -INFINITY || isnan(temperature) || isnan(top_p) || isnan(min_p) || isnan(uniform);
   if (bad) {
@@ -394,20 +427,18 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   // equal ones by their place; returns how many (0 where there are more: all CTAs get it, one sorts).
   const auto collect = [&]() {
     cluster.sync();
-    int n = 0;
-    for (int r = 0; r < a.ctas; ++r) n += cluster.map_shared_rank(&sh, r)->listed;
+    const uint32_t upto = uint32_t(warp_prefix(lane < a.ctas ? cluster.map_shared_rank(&sh, lane)->listed : 0));
+    const int n = int(__shfl_sync(0xffffffffu, upto, 31));
     if (n > kListed || rank != 0) return n > kListed ? 0 : n;
-    n = 0;
-    for (int r = 0; r < a.ctas; ++r) {
-      const SampleShared* his = cluster.map_shared_rank(&sh, r);
-      const int count = his->listed;
-      for (int i = threadIdx.x; i < count; i += kSampleThreads) sh.sorted[n + i] = his->list[i];
-      n += count;
+    for (int i = threadIdx.x; i - lane < n; i += kSampleThreads) {
+      int r = 0, first = 0;  // the CTA whose list holds entry i, and where that list begins
+      for (int k = 0; k < a.ctas; ++k) {
+        const int end = int(__shfl_sync(0xffffffffu, upto, k));
+        if (i >= end) r = k + 1, first = end;
+      }
+      if (i < n) sh.sorted[i] = cluster.map_shared_rank(&sh, r)->list[i - first];
     }
-    int padded = 2;
-    while (padded < n) padded <<= 1;
-    for (int i = n + threadIdx.x; i < padded; i += kSampleThreads) sh.sorted[i] = ~uint64_t(0);
-    sort(sh.sorted, padded);
+    sort(sh, n);
     return n;
   };
   const auto list = [&](float v, int place) {
@@ -434,22 +465,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       const int i = threadIdx.x * kEach + k;
       const bool stays = weight[k] >= least && (!by_mass || before < need);
       before += weight[k];
-      entry[k] = stays ? sh.sorted[i] << 32 | sh.sorted[i] >> 32 : ~uint64_t(0);
+      if (i < n) entry[k] = sh.sorted[i] << 32 | sh.sorted[i] >> 32 | (stays ? 0 : uint64_t(1) << 63);  // (the others behind)
     }
     // In the vocabulary's order: the sums of the weights there.
     __syncthreads();
-    int padded = 2;
-    while (padded < n) padded <<= 1;
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
-      if (threadIdx.x * kEach + k < padded) sh.sorted[threadIdx.x * kEach + k] = entry[k];
-    sort(sh.sorted, padded);
+      if (threadIdx.x * kEach + k < n) sh.sorted[threadIdx.x * kEach + k] = entry[k];
+    sort(sh, n);
     sum = 0;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int i = threadIdx.x * kEach + k;
-      entry[k] = i < padded ? sh.sorted[i] : ~uint64_t(0);
-      weight[k] = entry[k] != ~uint64_t(0) ? entry_weight(uint32_t(entry[k])) : 0;
+      entry[k] = i < n ? sh.sorted[i] : 0;
+      weight[k] = i < n && !(entry[k] >> 63) ? entry_weight(uint32_t(entry[k])) : 0;
       sum += weight[k];
     }
     before = block_prefix(sh, sum, all) - sum;
@@ -461,11 +490,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     }
   };
   if (few) {
-    const float from_value = of_order(max(reached, 0x00800000u));  // (-inf and what lies below it: none)
     x.template each<false>(from, to, [&](const float (&v)[G], int e) {
 #pragma unroll
       for (int i = 0; i < G; ++i)
-        if (v[i] >= from_value) list(v[i], e + i);
+        if (v[i] >= reached) list(v[i], e + i);
     });
     if (const int n = collect()) {
       if (rank == 0) finish(n, top_k, 0);
@@ -490,19 +518,21 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       }
     });
     cluster.sync();
-    const int share = kBins / a.ctas;
-    for (int i = threadIdx.x; i < share; i += kSampleThreads) {
-      const int b = rank * share + i;
-      uint32_t n = 0;
-      uint64_t m = 0;
-      for (int r = 0; r < a.ctas; ++r) {
-        const SampleShared* his = cluster.map_shared_rank(&sh, r);
-        n += his->count[b], m += uint64_t(his->high[b]) << 32 | his->low[b];
-      }
-      for (int r = 0; r < a.ctas; ++r) {
-        SampleShared* his = cluster.map_shared_rank(&sh, r);
-        his->all_count[b] = n, his->all_mass[b] = m;
-      }
+    if (a.ctas == 1) {
+      for (int b = threadIdx.x; b < kBins; b += kSampleThreads)
+        sh.all_count[b] = sh.count[b], sh.all_mass[b] = uint64_t(sh.high[b]) << 32 | sh.low[b];
+    } else {
+      // A CTA sums a share of the bins: ctas / 2 threads a bin take two CTAs each, join, and give the sum to those two.
+      const int share = kBins / a.ctas, part = int(threadIdx.x) / share, b = rank * share + int(threadIdx.x) % share;
+      SampleShared *one = cluster.map_shared_rank(&sh, 2 * part), *other = cluster.map_shared_rank(&sh, 2 * part + 1);
+      uint32_t n = one->count[b] + other->count[b];
+      uint64_t m = (uint64_t(one->high[b]) << 32 | one->low[b]) + (uint64_t(other->high[b]) << 32 | other->low[b]);
+      sh.list[threadIdx.x] = m, sh.list[kSampleThreads + threadIdx.x] = n;
+      __syncthreads();
+      n = 0, m = 0;
+      for (int i = int(threadIdx.x) % share; i < kSampleThreads; i += share) m += sh.list[i], n += uint32_t(sh.list[kSampleThreads + i]);
+      one->all_count[b] = n, one->all_mass[b] = m;
+      other->all_count[b] = n, other->all_mass[b] = m;
     }
     cluster.sync();
     for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0, sh.low[i] = 0, sh.high[i] = 0;
@@ -637,14 +667,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     sh.own_mass = m, sh.own_ties = n;
   }
   cluster.sync();
-  uint64_t before = 0, before_ties = 0, all = 0, all_ties = 0;  // of the row's CTAs, and those before this one
-  for (int r = 0; r < a.ctas; ++r) {
-    const SampleShared* his = cluster.map_shared_rank(&sh, r);
-    const uint64_t m = his->own_mass;
-    const uint32_t n = his->own_ties;
-    const uint64_t with = m + tied(all_ties, n);
-    if (r < rank) before += with, before_ties += n;
-    all += with, all_ties += n;
+  uint64_t before, before_ties, all;  // what stays in the row's CTAs before this one, the ties there, and what stays in all
+  {
+    const SampleShared* his = cluster.map_shared_rank(&sh, lane < a.ctas ? lane : 0);
+    const uint64_t m = lane < a.ctas ? his->own_mass : 0, n = lane < a.ctas ? his->own_ties : 0;
+    const uint64_t first = warp_prefix(n) - n, with = m + tied(first, n), upto = warp_prefix(with);
+    before_ties = __shfl_sync(0xffffffffu, first, rank);
+    before = __shfl_sync(0xffffffffu, upto - with, rank);
+    all = __shfl_sync(0xffffffffu, upto, 31);
   }
   const uint64_t drawn = part_of(u, all, false);
   const uint64_t own = sh.own_mass + tied(before_ties, sh.own_ties);
