@@ -18,7 +18,9 @@ struct GateArgs {
 };
 
 constexpr int kGateThreads = 256;
+constexpr int kGateValues = 8;  // consecutive ones a thread: four lanes a block
 
+// The same operations as torch's silu and multiplication of f32 tensors, bit for bit.
 template <int kAct>
 __device__ __forceinline__ float activation(float x) {
   float e = -x;
@@ -27,84 +29,77 @@ __device__ __forceinline__ float activation(float x) {
   return __fdiv_rn(x, __fadd_rn(1.0f, expf(e)));
 }
 
-// Group g (16 bytes) of a row.
-template <class T, int kAct, bool kVec>
-__device__ __forceinline__ void gate_group(const GateArgs& a, int64_t row, int g, const float (&x)[Elem<T>::kGroup],
-                                           const float (&u)[Elem<T>::kGroup]) {
+// Values e .. e+7 of a row of n; past it: zeros.
+template <class T, bool kVec>
+__device__ __forceinline__ void load8(const T* row, int e, int n, float (&v)[kGateValues]) {
   constexpr int G = Elem<T>::kGroup;
-  const int e = g * G;
-  float y[G];
+  if constexpr (kVec) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) y[i] = __fmul_rn(activation<kAct>(x[i]), u[i]);
-  if (a.y && e < a.n) {
-    T* to = static_cast<T*>(a.y) + row * a.ldy + e;
-    if constexpr (kVec) {
-      *reinterpret_cast<uint4*>(to) = Elem<T>::pack(y);
-    } else {
+    for (int i = 0; i < kGateValues; i += G) {
+      uint4 r = make_uint4(0u, 0u, 0u, 0u);
+      if (e + i < n) r = *reinterpret_cast<const uint4*>(row + e + i);
+      float part[G];
+      Elem<T>::unpack(r, part);
 #pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (e + i < a.n) to[i] = Elem<T>::from(y[i]);
+      for (int j = 0; j < G; ++j) v[i + j] = part[j];
     }
-  }
-  if (a.q) {  // the whole warp calls
-    uint32_t code[G / 4];
-    const float d = q8_block<G>(y, 0xffffffffu, code);
-    if (e >= a.n) return;
-    int8_t* to = a.q + row * a.n + e;
-    if constexpr (G == 4)
-      *reinterpret_cast<uint32_t*>(to) = code[0];
-    else
-      *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
-    if (e % kSub == 0) a.d[row * (a.n / kSub) + e / kSub] = __half_as_ushort(__float2half_rn(d));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kGateValues; ++i) v[i] = e + i < n ? Elem<T>::to(row[e + i]) : 0.f;
   }
 }
 
-// kGroups groups a thread, their loads side by side.
-template <class T, int kAct, bool kVec, int kGroups>
+template <class T, int kAct, bool kVec>
 __global__ void __launch_bounds__(kGateThreads) k_gated_act(GateArgs a) {
   constexpr int G = Elem<T>::kGroup;
   pdl_launch_dependents();
   pdl_wait();
   const int64_t row = blockIdx.x / unsigned(a.parts);
-  const int g0 = int(blockIdx.x - unsigned(row) * unsigned(a.parts)) * (kGateThreads * kGroups) + threadIdx.x;
-  const T* gate = static_cast<const T*>(a.gate) + row * a.ldg;
-  const T* up = static_cast<const T*>(a.up) + row * a.ldu;
-  float x[kGroups][G], u[kGroups][G];
+  const int e = (int(blockIdx.x - unsigned(row) * unsigned(a.parts)) * kGateThreads + int(threadIdx.x)) * kGateValues;
+  float x[kGateValues], u[kGateValues];
+  load8<T, kVec>(static_cast<const T*>(a.gate) + row * a.ldg, e, a.n, x);
+  load8<T, kVec>(static_cast<const T*>(a.up) + row * a.ldu, e, a.n, u);
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const int e = (g0 + k * kGateThreads) * G;
+  for (int i = 0; i < kGateValues; ++i) x[i] = __fmul_rn(activation<kAct>(x[i]), u[i]);
+  if (a.y) {
+    T* to = static_cast<T*>(a.y) + row * a.ldy + e;
     if constexpr (kVec) {
-      uint4 r = make_uint4(0u, 0u, 0u, 0u), s = r;
-      if (e < a.n) r = *reinterpret_cast<const uint4*>(gate + e), s = *reinterpret_cast<const uint4*>(up + e);
-      Elem<T>::unpack(r, x[k]);
-      Elem<T>::unpack(s, u[k]);
+#pragma unroll
+      for (int i = 0; i < kGateValues; i += G) {
+        float part[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) part[j] = x[i + j];
+        if (e + i < a.n) *reinterpret_cast<uint4*>(to + i) = Elem<T>::pack(part);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        x[k][i] = e + i < a.n ? Elem<T>::to(gate[e + i]) : 0.f;
-        u[k][i] = e + i < a.n ? Elem<T>::to(up[e + i]) : 0.f;
-      }
+      for (int i = 0; i < kGateValues; ++i)
+        if (e + i < a.n) to[i] = Elem<T>::from(x[i]);
     }
   }
-#pragma unroll
-  for (int k = 0; k < kGroups; ++k) gate_group<T, kAct, kVec>(a, row, g0 + k * kGateThreads, x[k], u[k]);
+  if (a.q) {  // the whole warp is here
+    uint32_t code[kGateValues / 4];
+    const float d = q8_block<kGateValues>(x, 0xffffffffu, code);
+    if (e >= a.n) return;  // (n is a multiple of 32)
+    *reinterpret_cast<uint2*>(a.q + row * a.n + e) = make_uint2(code[0], code[1]);
+    if (e % kSub == 0) a.d[row * (a.n / kSub) + e / kSub] = __half_as_ushort(__float2half_rn(d));
+  }
 }
 
-template <class T, int kAct, bool kVec, int kGroups>
+template <class T, int kAct, bool kVec>
 static int launch_gate_as(GateArgs& a, int64_t nvec, cudaStream_t s) {
-  constexpr int kPart = kGateThreads * kGroups * Elem<T>::kGroup;
+  constexpr int kPart = kGateThreads * kGateValues;
   a.parts = (a.n + kPart - 1) / kPart;
   // (2^24 rows of 2^24 values are more bytes than any device has; parts of them fit 31 bits
   // for all that does.)
   if (nvec * a.parts >= (int64_t(1) << 31)) return fail(Q1_ERR_ARG, "q8_gated_act: too many values");
-  return launch_op(k_gated_act<T, kAct, kVec, kGroups>, dim3(unsigned(nvec * a.parts)), kGateThreads, 0, 1, s,
-                   "q8_gated_act launch", a);
+  return launch_op(k_gated_act<T, kAct, kVec>, dim3(unsigned(nvec * a.parts)), kGateThreads, 0, 1, s, "q8_gated_act launch", a);
 }
 
 template <class T>
 static int launch_gate(GateArgs& a, int64_t nvec, int act, bool vec, cudaStream_t s) {
-  if (!vec) return act == Q1_ACT_SILU ? launch_gate_as<T, Q1_ACT_SILU, false, 1>(a, nvec, s) : launch_gate_as<T, Q1_ACT_GELU, false, 1>(a, nvec, s);
-  return act == Q1_ACT_SILU ? launch_gate_as<T, Q1_ACT_SILU, true, 1>(a, nvec, s) : launch_gate_as<T, Q1_ACT_GELU, true, 1>(a, nvec, s);
+  if (!vec) return act == Q1_ACT_SILU ? launch_gate_as<T, Q1_ACT_SILU, false>(a, nvec, s) : launch_gate_as<T, Q1_ACT_GELU, false>(a, nvec, s);
+  return act == Q1_ACT_SILU ? launch_gate_as<T, Q1_ACT_SILU, true>(a, nvec, s) : launch_gate_as<T, Q1_ACT_GELU, true>(a, nvec, s);
 }
 
 }  // namespace q1

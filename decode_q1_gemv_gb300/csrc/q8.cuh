@@ -2,9 +2,20 @@
 // quant.cu defines them, and quants back to numbers; the paged q8_0 cache.
 #pragma once
 
+#include <cfloat>
+
 #include "paged.cuh"
 
 namespace q1 {
+
+// roundf(t), halves away from zero, in the last byte, |t| < 2^22: |t| + 1/2 and then the sum with
+// 2^23, whose last bits are the whole part, both rounded toward zero, which keeps the whole
+// part where |t| + 1/2 is no float.
+__device__ __forceinline__ uint32_t q8_code(float t) {
+  const uint32_t k = __float_as_uint(__fadd_rz(__fadd_rz(fabsf(t), 0.5f), 8388608.0f));
+  const uint32_t sign = uint32_t(__float_as_int(t) >> 31);
+  return (k ^ sign) - sign;
+}
 
 // Quants of `kCount` values of a block of 32 that 32 / kCount neighbouring lanes
 // hold (`lanes`: the mask of those that call), four to a word, and the block's
@@ -19,13 +30,22 @@ __device__ __forceinline__ float q8_block(const float (&x)[kCount], unsigned lan
   const float amax = __uint_as_float(top >= 0x7f800000u ? 0x7fc00000u : top);
   const float d = __fdiv_rn(amax, 127.0f);
   const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+  if (id <= FLT_MAX) {
 #pragma unroll
-  for (int i = 0; i < kCount; i += 4) {
-    uint32_t c = 0;
+    for (int i = 0; i < kCount; i += 4) {
+      uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c |= uint32_t(uint8_t(static_cast<int8_t>(static_cast<int>(roundf(__fmul_rn(x[i + j], id)))))) << (8 * j);
-    code[i / 4] = c;
+      for (int j = 0; j < 4; ++j) c[j] = q8_code(__fmul_rn(x[i + j], id));
+      code[i / 4] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+  } else {  // d is NaN, or so small (a scale of zero) that its inverse is infinite
+#pragma unroll
+    for (int i = 0; i < kCount; i += 4) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c |= uint32_t(uint8_t(static_cast<int8_t>(static_cast<int>(roundf(__fmul_rn(x[i + j], id)))))) << (8 * j);
+      code[i / 4] = c;
+    }
   }
   return d;
 }
