@@ -20,14 +20,14 @@
 //   2  (small top-k) a value that top-k tokens at least reach: of the threads' own
 //      maxima the one with k / CTAs - 1 others above it in each CTA, the least of these;
 //      what reaches it is listed: 4a;
-//   3  (top-p, large top-k, or a list that is too long) a histogram over the exponent, 1024
-//      bins, of counts and sums, joined through distributed shared memory: the
-//      bin where the threshold lies.  The tokens down to that bin are listed if they are few: 4a;
-//      else those of the bin alone are, for the threshold; else (many equal ones) it is found by
-//      histograms of their bits, ten at a time: 4b;
-//   4a one CTA sorts the list, cuts, and draws;
-//   4b (and without top-k and top-p) sums by warp, whose one holds the token, and the
-//      token in it.
+//   3  (top-p, large top-k, or a list that is too long) how many tokens there are in each of
+//      2048 bins of the exponent, joined through distributed shared memory.  Counts
+//      times the weights of bins' middles tell to some 10^-3 where the sum crosses its border:
+//      a few bins around that are listed, while the weights of all tokens are summed;
+//   4  one CTA sorts the list and draws, if it is all that can stay, or finds the last token
+//      that stays (where it does not lie in the list after all, or there are too many equal tokens:
+//      by exact histograms of the values' bits, ten at a time);
+//   5  sums by warp, whose one holds the drawn token, and the token in it.
 // Bytes bound the largest calls, a few barriers of the cluster the smallest ones.
 #include <algorithm>
 #include <cfloat>
@@ -42,7 +42,8 @@ namespace q1 {
 namespace cg = cooperative_groups;
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024;
+constexpr int kBins = 2048;          // of exponents
+constexpr int kDigits = 1024;        // of ten bits of a value
 constexpr int kListed = 1024;        // tokens that one CTA sorts
 constexpr int kFewTopK = 256;        // top-k by the threads' maxima
 constexpr int kSteps = 512;          // parts of an exponent
@@ -82,21 +83,24 @@ __device__ __forceinline__ float exponent_of(const Weigh& w, float x) { return _
 
 // The weight of x, 2^44 for the maximum.
 __device__ __forceinline__ uint64_t weight_of(const Weigh& w, float x) {
-  const float d = __fsub_rn(x, w.max), y = __fmul_rn(d, w.ch);
-  if (!(y > kLeast)) return 0;  // -inf - max among them, and its product with a factor of zero
+  const float d = __fsub_rn(x, w.max);
+  const float y = fmaxf(__fmul_rn(d, w.ch), kLeast - 16.f);  // far below: zero whatever the rest is (-inf times 0 too)
   const float back = __fsub_rn(d, x);
   const float lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(w.max, back));  // x - max - d
   const float rest = __fmaf_rn(lost, w.ch, __fmaf_rn(d, w.cl, __fmaf_rn(d, w.ch, -y)));
   // y = n + k / 512 + r: rounded by adding 1.5 2^23 (|y| 512 < 2^22)
   const float z = __fmaf_rn(y, float(kSteps), kMagic);
-  const int whole = int(__float_as_uint(z) - kMagicBits);
+  const uint32_t whole = __float_as_uint(z);  // n 512 + k, and kMagicBits
   const float r = __fadd_rn(__fmaf_rn(__fsub_rn(z, kMagic), -1.0f / kSteps, y), rest);
   const float p = __fmul_rn(r, __fmaf_rn(r, 0.24022651f, 0.69314718f));  // 2^r - 1
   const uint32_t t = w.powers[whole & (kSteps - 1)];
   // t p < 2^22, rounded by the same addition; t as a float (truncated) by its bits
   const float tf = __uint_as_float((t >> 8) + (157u << 23));
   const uint32_t bits = t + (__float_as_uint(__fmaf_rn(tf, p, kMagic)) - kMagicBits);
-  return (uint64_t(bits) << 32) >> (32 + 31 - kOne - (whole >> 9));
+  // bits 2^(13 + n): 2^32 bits, moved right by 19 - n (up to 79; from 64 on nothing is left)
+  const uint32_t by = 32 + 31 - kOne + (kMagicBits >> 9) - (whole >> 9);
+  const uint32_t low = __funnelshift_rc(__funnelshift_rc(0u, bits, by), 0u, uint32_t(max(int(by) - 32, 0)));
+  return uint64_t(__funnelshift_rc(bits, 0u, by)) << 32 | low;
 }
 static_assert(kSteps == 512, "the shift above");
 
@@ -106,9 +110,15 @@ __device__ __forceinline__ uint32_t order_of(float x) {  // rises with x; -0 as 
 }
 __device__ __forceinline__ float of_order(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
 
-__device__ __forceinline__ int bin_of(const Weigh& w, float x) {  // of a weight above zero
-  return min(int(__fmul_rn(exponent_of(w, x), kBins / kLeast)), kBins - 1);
+// The bin of an exponent in (kLeast, 0], which rises where the exponent falls, and the exponent in its middle.
+__device__ __forceinline__ int bin_of(float y) {
+  return int(__float_as_uint(__fmaf_rn(y, (kBins - 1) / kLeast, kMagic)) - kMagicBits);
 }
+__device__ __forceinline__ float middle_of(int bin) { return float(bin) * (kLeast / (kBins - 1)); }
+// What part of itself the sum by middles may be off by for the bins around a border to hold it.  f32 logits
+// spread over the bins: it is off by some 10^-5; those of 16 bits lie anywhere in theirs.
+template <class T>
+constexpr uint64_t kMiddles = sizeof(T) == 4 ? 8192 : 2048;
 
 // f * v, f in [0, 1), rounded down or up.
 __device__ __forceinline__ uint64_t part_of(float f, uint64_t v, bool up) {
@@ -129,32 +139,34 @@ __device__ __forceinline__ uint64_t part_of(float f, uint64_t v, bool up) {
   return r + (up && rest);
 }
 
-// What a histogram's search gives: the bin, what lies before it and in it.
+// What a histogram's search gives: the digit, what lies before it and in it.
 struct Found {
-  int bin;
+  int digit;
   uint32_t above, in;
   uint64_t mass_above, mass_in;
 };
 
 struct SampleShared {
   uint32_t powers[kSteps];
-  uint32_t count[kBins], low[kBins], high[kBins];        // of this CTA
-  uint32_t all_count[kBins];                             // of the row
+  // This CTA's bins and the row's; or the counts, low and high halves of the sums of this CTA's digits and the row's counts.
+  uint32_t count[kBins], all_count[kBins];
   union {
-    uint64_t all_mass[kBins];
-    uint64_t sorted[kListed];  // (once the bins have been searched)
+    uint64_t all_mass[kDigits];
+    uint64_t sorted[kListed];
   };
   uint64_t list[kListed];
-  uint64_t warp_mass[kSampleWarps];
+  uint64_t warp_mass[kSampleWarps], warp_base[kSampleWarps], warp_above[kSampleWarps];
   uint32_t warp_count[kSampleWarps];
   Found found;
   float own_max;
   float own_reached;       // what at least its part of top-k tokens reach
   int own_bad, listed, token;
-  uint64_t own_mass;
-  uint32_t own_ties;
-  uint32_t cut;            // of the leader: what a list's threshold is
-  uint64_t cut_ties;
+  uint64_t own_mass, own_base, own_above;
+  int border[4];           // of the search of bins: see there
+  uint32_t border_count[2];
+  bool cut_found;          // of the leader: the last token that stays
+  uint32_t cut_value;
+  int cut_place;
 };
 
 template <class T>
@@ -176,7 +188,9 @@ struct Row {
   // Group i (of 16 aligned bytes): elements i G - skew on; -inf where there are none.
   __device__ __forceinline__ uint4 load(int i) const {
     const int e = i * G - skew;
-    if (e >= 0 && e + G <= vocab) return *reinterpret_cast<const uint4*>(row + e);
+    return e >= 0 && e + G <= vocab ? *reinterpret_cast<const uint4*>(row + e) : load_edge(row, e, vocab);
+  }
+  static __device__ __noinline__ uint4 load_edge(const T* row, int e, int vocab) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = masked_bits<T>();
@@ -190,18 +204,15 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // f(group's values, its first element) over groups [a, b) of a warp, lane by lane.
+  // f(group's values, its first element) over groups [a, b) of a warp, lane by lane; the first time (kFirst) they
+  // come from global memory and go to the cache.
+  // Light work: four groups loaded at a time.
   template <bool kFirst, class F>
   __device__ __forceinline__ void each(int a, int b, F&& f) const {
-    const int lane = threadIdx.x & 31;
-    for (int i0 = a + lane; i0 < b; i0 += 128) {
+    for (int i0 = a + int(threadIdx.x & 31); i0 < b; i0 += 128) {
       uint4 r[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + 32 * k;
-        r[k] = make_uint4(masked_bits<T>(), masked_bits<T>(), masked_bits<T>(), masked_bits<T>());
-        if (i < b) r[k] = kFirst || !cache ? load(i) : cache[i - first];
-      }
+      for (int k = 0; k < 4; ++k) r[k] = i0 + 32 * k < b ? kFirst || !cache ? load(i0 + 32 * k) : cache[i0 + 32 * k - first] : nothing();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = i0 + 32 * k;
@@ -211,6 +222,30 @@ struct Row {
         f(v, i * G - skew);
       }
     }
+  }
+  // Weights: a group at a time, three ahead under way.  (Fewer instructions to fetch: 256 rows 204 us, 211 with four at a
+  // time; the maximum alone 29000 cycles this way and 17000 the other.)
+  template <class F>
+  __device__ __forceinline__ void each_heavy(int a, int b, F&& f) const {
+    constexpr int kAhead = 3;
+    const auto get = [&](int i) { return i >= b ? nothing() : cache ? cache[i - first] : load(i); };
+    uint4 r[kAhead];
+    int i = a + int(threadIdx.x & 31);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) r[k] = get(i + 32 * k);
+#pragma unroll 1
+    for (; i < b; i += 32) {
+      const uint4 now = r[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) r[k] = r[k + 1];
+      r[kAhead - 1] = get(i + 32 * kAhead);
+      float v[G];
+      Elem<T>::unpack(now, v);
+      f(v, i * G - skew);
+    }
+  }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(masked_bits<T>(), masked_bits<T>(), masked_bits<T>(), masked_bits<T>());
   }
 };
 
@@ -229,11 +264,11 @@ __device__ __forceinline__ uint64_t warp_prefix(uint64_t v) {  // with its own
   return v;
 }
 
-// The first bin up to which the counts reach `need` (by mass: the sums), after
-// `above` and `mass_above` before the histogram; its last bin with anything in it
+// The first digit up to which the counts reach `need` (by mass: the sums), after
+// `above` and `mass_above` before the histogram; its last one with anything in it
 // where none does.  Every thread of the CTA calls and gets it.
 __device__ __forceinline__ Found search(SampleShared& sh, bool by_mass, uint64_t need, uint32_t above, uint64_t mass_above) {
-  constexpr int kEach = kBins / kSampleThreads;
+  constexpr int kEach = kDigits / kSampleThreads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t n[kEach], ns = 0;
   uint64_t m[kEach], ms = 0;
@@ -246,19 +281,18 @@ __device__ __forceinline__ Found search(SampleShared& sh, bool by_mass, uint64_t
   const uint32_t nincl = uint32_t(warp_prefix(ns));
   const uint64_t mincl = warp_prefix(ms);
   if (lane == 31) sh.warp_count[warp] = nincl, sh.warp_mass[warp] = mincl;
-  if (threadIdx.x == 0) sh.found.bin = -1;
   __syncthreads();
   uint32_t nb = above + nincl - ns;
   uint64_t mb = mass_above + mincl - ms;
-  for (int w = 0; w < warp; ++w) nb += sh.warp_count[w], mb += sh.warp_mass[w];
-  uint32_t last = 0;  // counts before and with the bins, for the one that is last of all
   uint32_t total = above;
-  for (int w = 0; w < kSampleWarps; ++w) total += sh.warp_count[w];
+  for (int w = 0; w < kSampleWarps; ++w) {
+    if (w < warp) nb += sh.warp_count[w], mb += sh.warp_mass[w];
+    total += sh.warp_count[w];
+  }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const uint64_t before = by_mass ? mb : nb, after = by_mass ? mb + m[i] : uint64_t(nb) + n[i];
-    last = nb + n[i];
-    if (n[i] && ((before < need && after >= need) || (after < need && last == total)))
+    if (n[i] && ((before < need && after >= need) || (after < need && nb + n[i] == total)))
       sh.found = {int(threadIdx.x) * kEach + i, nb, n[i], mb, m[i]};
     nb += n[i], mb += m[i];
   }
@@ -266,7 +300,43 @@ __device__ __forceinline__ Found search(SampleShared& sh, bool by_mass, uint64_t
   return sh.found;
 }
 
-// Sorts the n (up to kListed) different entries of sh.sorted, rising; ~0 follows them up to a power of two.
+// Bitonic, kEach (1 or 2) entries a thread; exchanges within a warp's entries by shuffles.
+template <int kEach>
+__device__ __forceinline__ void sort_bitonic(uint64_t* v, int n) {
+  const int lane = threadIdx.x & 31, first = int(threadIdx.x >> 5) * 32 * kEach + lane;
+  uint64_t mine[kEach];  // entries first and (two of them) first + 32
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) mine[k] = first + 32 * k < n ? v[first + 32 * k] : ~uint64_t(0);
+  const auto keep = [&](uint64_t& x, uint64_t other, int at, int step, int size) {
+    if ((other < x) == (((at & step) == 0) == ((at & size) == 0))) x = other;
+  };
+  for (int size = 2; size <= kSampleThreads * kEach; size <<= 1)
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      if (step >= 32 * kEach) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) v[first + 32 * k] = mine[k];
+        __syncthreads();
+        uint64_t other[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) other[k] = v[(first + 32 * k) ^ step];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) keep(mine[k], other[k], first + 32 * k, step, size);
+        __syncthreads();
+      } else if (step == 32) {
+        const uint64_t lo = min(mine[0], mine[kEach - 1]), hi = max(mine[0], mine[kEach - 1]);
+        const bool rising = (first & size) == 0;
+        mine[0] = rising ? lo : hi, mine[kEach - 1] = rising ? hi : lo;
+      } else {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) keep(mine[k], __shfl_xor_sync(0xffffffffu, mine[k], step), first + 32 * k, step, size);
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) v[first + 32 * k] = mine[k];
+  __syncthreads();
+}
+
+// Sorts the n (up to kListed) different entries of sh.sorted, rising.
 // Every thread of the CTA calls.
 constexpr int kByRank = 256;
 __device__ __forceinline__ void sort(SampleShared& sh, int n) {
@@ -285,19 +355,11 @@ __device__ __forceinline__ void sort(SampleShared& sh, int n) {
     __syncthreads();
     return;
   }
-  int padded = 2;
-  while (padded < n) padded <<= 1;
-  for (int i = n + threadIdx.x; i < padded; i += kSampleThreads) v[i] = ~uint64_t(0);
-  for (int size = 2; size <= padded; size <<= 1)
-    for (int step = size >> 1; step > 0; step >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < padded / 2; i += kSampleThreads) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const uint64_t a = v[lo], b = v[hi];
-        if ((a > b) == ((lo & size) == 0)) v[lo] = b, v[hi] = a;
-      }
-    }
-  __syncthreads();
+  static_assert(kListed == 2 * kSampleThreads, "");
+  if (n <= kSampleThreads)
+    sort_bitonic<1>(v, n);
+  else
+    sort_bitonic<2>(v, n);
 }
 
 // The sums of v over the CTA's threads up to each (its own among them), and of all.
@@ -350,7 +412,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (threadIdx.x == 0) sh.listed = 0, sh.token = a.vocab;
-  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0, sh.low[i] = 0, sh.high[i] = 0;
+  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0;
   if (lane == 0) sh.warp_count[warp] = __float_as_uint(top);
   bad = __syncthreads_or(bad);
   // 2. A value that so many threads' maxima reach that all CTAs together have top-k of them, to a 2^-10th of their range.
@@ -423,7 +485,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   w.cl = w.ch > 0.f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-w.ch, t, kLog), kLogRest), t) : 0.f;
   const float u = fminf(fmaxf(uniform, 0.f), 0.99999994f);
   const uint64_t least = min_p >= 1.f ? uint64_t(1) << kOne : min_p > 0.f ? part_of(min_p, uint64_t(1) << kOne, true) : 1;
-  // 4a. The first CTA collects all lists, up to kListed tokens in all, and sorts them by falling values,
+  // 4. The first CTA collects all lists, up to kListed tokens in all, and sorts them by falling values,
   // equal ones by their place; returns how many (0 where there are more: all CTAs get it, one sorts).
   const auto collect = [&]() {
     cluster.sync();
@@ -446,10 +508,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (i < kListed) sh.list[i] = uint64_t(~order_of(v)) << 32 | uint32_t(place);
   };
   const auto entry_weight = [&](uint32_t upside_down) { return weight_of(w, of_order(~upside_down)); };
+  const auto enough_of = [&](uint64_t mass) { return max(part_of(fmaxf(top_p, 0.f), mass, true), uint64_t(1)); };
   constexpr int kEach = kListed / kSampleThreads;
-  // The token, where all that may stay is among the n tokens sorted: the first `count` of them, then by mass
-  // (need 0: top_p of their own).
-  const auto finish = [&](int n, int count, uint64_t need) {
+  // The token, where all that may stay is among the n tokens sorted: the first `count` of them, then by mass.
+  const auto finish = [&](int n, int count, uint64_t base) {  // base: the sum that top-p is of, 0 for that of those
     uint64_t weight[kEach], sum = 0, all;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -458,7 +520,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       sum += weight[k];
     }
     uint64_t before = block_prefix(sh, sum, all) - sum;
-    if (by_mass && need == 0) need = max(part_of(fmaxf(top_p, 0.f), all, true), uint64_t(1));
+    const uint64_t need = by_mass ? enough_of(base ? base : all) : 0;
     uint64_t entry[kEach];
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -504,238 +566,364 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (threadIdx.x == 0) sh.listed = 0;
   }
 
-  // The histogram of this CTA (`which`: its bin of a value, -1 for none) becomes the row's, in every CTA.
-  const auto histogram = [&](auto&& which) {
-    x.template each<false>(from, to, [&](const float (&v)[G], int) {
+  // Of this CTA's slice, in the vocabulary's order, the token at which the sum of value(x, token) exceeds pick(sum of the row);
+  // -1 in all CTAs but the one that has it.  `summed`: sh.warp_mass holds the warps' sums.
+  const auto locate = [&](bool summed, auto&& value, auto&& pick) {
+    const auto sum_of = [&](int a0, int b0) {
+      uint64_t sum = 0;
+      x.each_heavy(a0, b0, [&](const float (&v)[G], int e) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const uint64_t m = weight_of(w, v[i]);
-        const int b = m ? which(v[i]) : -1;
-        if (b < 0) continue;
-        atomicAdd(&sh.count[b], 1u);
-        const uint32_t old = atomicAdd(&sh.low[b], uint32_t(m));
-        atomicAdd(&sh.high[b], uint32_t(m >> 32) + (old + uint32_t(m) < old));
-      }
-    });
-    cluster.sync();
-    if (a.ctas == 1) {
-      for (int b = threadIdx.x; b < kBins; b += kSampleThreads)
-        sh.all_count[b] = sh.count[b], sh.all_mass[b] = uint64_t(sh.high[b]) << 32 | sh.low[b];
-    } else {
-      // A CTA sums a share of the bins: ctas / 2 threads a bin take two CTAs each, join, and give the sum to those two.
-      const int share = kBins / a.ctas, part = int(threadIdx.x) / share, b = rank * share + int(threadIdx.x) % share;
-      SampleShared *one = cluster.map_shared_rank(&sh, 2 * part), *other = cluster.map_shared_rank(&sh, 2 * part + 1);
-      uint32_t n = one->count[b] + other->count[b];
-      uint64_t m = (uint64_t(one->high[b]) << 32 | one->low[b]) + (uint64_t(other->high[b]) << 32 | other->low[b]);
-      sh.list[threadIdx.x] = m, sh.list[kSampleThreads + threadIdx.x] = n;
+        for (int i = 0; i < G; ++i) sum += value(v[i], e + i);
+      });
+      sum = warp_sum(sum);
       __syncthreads();
-      n = 0, m = 0;
-      for (int i = int(threadIdx.x) % share; i < kSampleThreads; i += share) m += sh.list[i], n += uint32_t(sh.list[kSampleThreads + i]);
-      one->all_count[b] = n, one->all_mass[b] = m;
-      other->all_count[b] = n, other->all_mass[b] = m;
+      if (lane == 0) sh.warp_mass[warp] = sum;
+      __syncthreads();
+    };
+    if (!summed) sum_of(from, to);
+    if (threadIdx.x == 0) {
+      uint64_t m = 0;
+      for (int i = 0; i < kSampleWarps; ++i) m += sh.warp_mass[i];
+      sh.own_mass = m;
     }
     cluster.sync();
-    for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.count[i] = 0, sh.low[i] = 0, sh.high[i] = 0;
-  };
-
-  uint32_t limit = 0;            // tokens above it (in order_of) stay,
-  uint64_t ties = 0;             // and as many of those at it, the first ones
-  uint64_t tie_weight = 0, kept = 0;  // kept: the sum of what top-k leaves
-  if (by_count || by_mass) {
-    const auto whole_row = [&](float v) { return bin_of(w, v); };
-    histogram(whole_row);
-    uint64_t need = by_count ? uint64_t(top_k) : 0;
-    if (!by_count) {
-      uint64_t all = 0;
-      (void)block_prefix(sh, sh.all_mass[threadIdx.x] + sh.all_mass[threadIdx.x + kSampleThreads], all);
-      need = max(part_of(fmaxf(top_p, 0.f), all, true), uint64_t(1));
-    }
-    bool mass = !by_count;  // what is searched for
-    Found f = search(sh, mass, need, 0, 0);
-    for (bool first = true;; first = false) {
-      const bool all_few = f.above + f.in <= kListed;
-      if (f.in <= kListed) {
-        // 4a. All tokens down to this bin, or those of this bin alone.  (From the second search on top-k was dealt with.)
-        const int bin = f.bin;
-        x.template each<false>(from, to, [&](const float (&v)[G], int e) {
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            if (!(exponent_of(w, v[i]) > kLeast)) continue;
-            const int b = bin_of(w, v[i]);
-            if ((b == bin || (all_few && b < bin)) && weight_of(w, v[i])) list(v[i], e + i);
-          }
-        });
-        const int n = collect();
-        if (all_few) {
-          if (rank == 0) finish(n, by_count && first ? top_k : n, first && by_count ? 0 : need);
-          cluster.sync();  // the lists have been read
-          return;
-        }
-        // The threshold is the first entry at which the count or the sum is reached: it, and those of its value before it.
-        if (rank == 0) {
-          uint64_t weight[kEach], sum = 0, all;
-#pragma unroll
-          for (int k = 0; k < kEach; ++k) {
-            const int i = threadIdx.x * kEach + k;
-            weight[k] = i < n ? entry_weight(uint32_t(sh.sorted[i] >> 32)) : 0;
-            sum += weight[k];
-          }
-          uint64_t before = f.mass_above + block_prefix(sh, sum, all) - sum;
-#pragma unroll
-          for (int k = 0; k < kEach; ++k) {
-            const int i = threadIdx.x * kEach + k;
-            const bool is = mass ? before < need && before + weight[k] >= need : uint64_t(f.above) + i + 1 == need;
-            if (i < n && (is || (i == n - 1 && (mass ? before + weight[k] : uint64_t(f.above) + n) < need))) {
-              const uint32_t value = uint32_t(sh.sorted[i] >> 32);
-              int same = 1;
-              while (i - same >= 0 && uint32_t(sh.sorted[i - same] >> 32) == value) ++same;
-              sh.cut = ~value, sh.cut_ties = same;
-              sh.own_mass = before + weight[k];  // of all that stays
-            }
-            before += weight[k];
-          }
-        }
-        cluster.sync();
-        const SampleShared* his = cluster.map_shared_rank(&sh, 0);
-        limit = his->cut, ties = his->cut_ties, tie_weight = weight_of(w, of_order(limit));
-        kept = his->own_mass;
-        cluster.sync();
-        if (threadIdx.x == 0) sh.listed = 0;
-        __syncthreads();
-      } else {
-        // The threshold within the bin, ten bits of its values at a time (of 16-bit types the first 20 differ).
-        const int bin = f.bin;
-        uint32_t prefix = 0, known = 0;  // the bits found
-        Found at = f;
-#pragma unroll 1
-        for (int shift = 22;; shift = max(0, shift - 10)) {
-          const uint32_t width = known ? min(10, __ffs(int(known)) - 1 - shift) : 10;
-          const uint32_t most = (1u << width) - 1;
-          histogram([&](float v) {
-            const uint32_t o = order_of(v);
-            return bin_of(w, v) == bin && (o & known) == prefix ? int(most - ((o >> shift) & most)) : -1;
-          });
-          at = search(sh, mass, need, at.above, at.mass_above);
-          prefix |= (most - uint32_t(at.bin)) << shift, known |= most << shift;
-          if (shift == 0 || (G == 8 && shift <= 12)) break;
-        }
-        if (G == 8) prefix |= prefix >> 31 ? 0 : 0xfffu;  // the bits that 16-bit types do not have
-        limit = prefix, tie_weight = at.mass_in / at.in;
-        ties = mass ? (need - at.mass_above + tie_weight - 1) / tie_weight : need - at.above;
-        ties = min(ties, uint64_t(at.in));
-        kept = at.mass_above + ties * tie_weight;
-      }
-      if (mass || !by_mass) break;
-      // top-p of what top-k left: the same histogram, made once more.
-      mass = true;
-      need = max(part_of(top_p > 0.f ? top_p : 0.f, kept, true), uint64_t(1));
-      histogram(whole_row);
-      f = search(sh, true, need, 0, 0);
-    }
-    if (tie_weight < least) ties = 0;
-  }
-
-  // 4. Sums of what stays, by warp: weights above the limit, and values at it.
-  const float border = limit ? of_order(limit) : -INFINITY;
-  const auto sums_of = [&](int a0, int b0, uint64_t& sum, uint32_t& at_limit) {
-    sum = 0, at_limit = 0;
-    x.template each<false>(a0, b0, [&](const float (&v)[G], int) {
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        at_limit += v[i] == border;
-        if (v[i] > border) {
-          const uint64_t m = weight_of(w, v[i]);
-          sum += m >= least ? m : 0;
-        }
-      }
-    });
-    sum = warp_sum(sum);
-    at_limit = __reduce_add_sync(0xffffffffu, at_limit);
-  };
-  // Of `n` values at the limit after `before` others: the sum of those that stay.
-  const auto tied = [&](uint64_t before, uint64_t n) { return (before >= ties ? 0 : min(n, ties - before)) * tie_weight; };
-  uint64_t sum;
-  uint32_t at_limit;
-  sums_of(from, to, sum, at_limit);
-  __syncthreads();
-  if (lane == 0) sh.warp_mass[warp] = sum, sh.warp_count[warp] = at_limit;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint64_t m = 0;
-    uint32_t n = 0;
-    for (int i = 0; i < kSampleWarps; ++i) m += sh.warp_mass[i], n += sh.warp_count[i];
-    sh.own_mass = m, sh.own_ties = n;
-  }
-  cluster.sync();
-  uint64_t before, before_ties, all;  // what stays in the row's CTAs before this one, the ties there, and what stays in all
-  {
-    const SampleShared* his = cluster.map_shared_rank(&sh, lane < a.ctas ? lane : 0);
-    const uint64_t m = lane < a.ctas ? his->own_mass : 0, n = lane < a.ctas ? his->own_ties : 0;
-    const uint64_t first = warp_prefix(n) - n, with = m + tied(first, n), upto = warp_prefix(with);
-    before_ties = __shfl_sync(0xffffffffu, first, rank);
-    before = __shfl_sync(0xffffffffu, upto - with, rank);
-    all = __shfl_sync(0xffffffffu, upto, 31);
-  }
-  const uint64_t drawn = part_of(u, all, false);
-  const uint64_t own = sh.own_mass + tied(before_ties, sh.own_ties);
-  if (drawn >= before && drawn < before + own) {
-    // The warp's part that holds the token, then its sixteenth, then the token.
+    const uint64_t own = lane < a.ctas ? cluster.map_shared_rank(&sh, lane)->own_mass : 0, upto = warp_prefix(own);
+    const uint64_t target = pick(__shfl_sync(0xffffffffu, upto, 31));
+    uint64_t before = __shfl_sync(0xffffffffu, upto - own, rank);
+    if (target < before || target >= before + __shfl_sync(0xffffffffu, own, rank)) return -1;
+    // The warp's part that holds it, then its sixteenth, then the token.
     int a0 = x.first, b0 = x.last;
     for (int round = 0; round < 2; ++round) {
-      if (round) {
-        const int n = b0 - a0;
-        uint64_t m;
-        uint32_t t;
-        sums_of(a0 + n * warp / kSampleWarps, a0 + n * (warp + 1) / kSampleWarps, m, t);
-        __syncthreads();
-        if (lane == 0) sh.warp_mass[warp] = m, sh.warp_count[warp] = t;
-        __syncthreads();
-      }
-      int i = 0;
-      for (; i < kSampleWarps - 1; ++i) {
-        const uint64_t with = sh.warp_mass[i] + tied(before_ties, sh.warp_count[i]);
-        if (drawn < before + with) break;
-        before += with, before_ties += sh.warp_count[i];
-      }
-      const int64_t n = b0 - a0;
-      b0 = a0 + int(n * (i + 1) / kSampleWarps), a0 += int(n * i / kSampleWarps);
+      const int n = b0 - a0;
+      if (round) sum_of(a0 + int(int64_t(n) * warp / kSampleWarps), a0 + int(int64_t(n) * (warp + 1) / kSampleWarps));
+      const uint64_t m = lane < kSampleWarps ? sh.warp_mass[lane] : 0, to_here = before + warp_prefix(m);
+      const int i = __ffs(int(__ballot_sync(0xffffffffu, lane < kSampleWarps && target < to_here))) - 1;  // (there is one)
+      before = __shfl_sync(0xffffffffu, to_here - m, i);
+      b0 = a0 + int(int64_t(n) * (i + 1) / kSampleWarps), a0 += int(int64_t(n) * i / kSampleWarps);
     }
     if (warp == 0) {
-      bool done = false;
-      for (int i0 = a0; i0 < b0 && !done; i0 += 32) {
+      for (int i0 = a0; i0 < b0; i0 += 32) {
         const int i = i0 + lane;
         uint4 r = make_uint4(masked_bits<T>(), masked_bits<T>(), masked_bits<T>(), masked_bits<T>());
         if (i < b0) r = x.cache ? x.cache[i - x.first] : x.load(i);
         float v[G];
         Elem<T>::unpack(r, v);
-        uint64_t m[G], lane_sum = 0;
-        uint32_t lane_ties = 0;
+        uint64_t m[G], sum = 0;
 #pragma unroll
-        for (int k = 0; k < G; ++k) lane_ties += v[k] == border;
-        uint64_t tie = before_ties + warp_prefix(lane_ties) - lane_ties;
-        before_ties += __reduce_add_sync(0xffffffffu, lane_ties);
+        for (int k = 0; k < G; ++k) m[k] = value(v[k], i * G - x.skew + k), sum += m[k];
+        uint64_t upto = before + warp_prefix(sum) - sum;
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-          m[k] = 0;
-          if (v[k] == border) {
-            m[k] = tied(tie, 1), ++tie;
-          } else if (v[k] > border) {
-            m[k] = weight_of(w, v[k]);
-            if (m[k] < least) m[k] = 0;
+          if (target >= upto && target < upto + m[k]) sh.token = i * G - x.skew + k;
+          upto += m[k];
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+        if (target < before) break;
+      }
+    }
+    __syncthreads();
+    return sh.token;
+  };
+
+  float border = -INFINITY;  // tokens above it stay, and those at it up to this place
+  int place = -1;
+  bool summed = false;       // the warps' sums of what stays are known
+  const auto stays = [&](float v, int e) { return v > border || (v == border && e <= place); };
+  const auto kept_weight = [&](float v, int e) -> uint64_t {
+    if (!stays(v, e)) return 0;
+    const uint64_t m = weight_of(w, v);
+    return m >= least ? m : 0;
+  };
+  if (by_count || by_mass) {
+    // 3. Counts by exponents.
+    x.each_heavy(from, to, [&](const float (&v)[G], int) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float y = exponent_of(w, v[i]);
+        if (y > kLeast) atomicAdd(&sh.count[bin_of(y)], 1u);
+      }
+    });
+    cluster.sync();
+    {
+      const int share = kBins / a.ctas;
+      if (a.ctas >= 4) {  // ctas / 4 threads a bin take four CTAs each, join, and give the sum to those four
+        const int part = int(threadIdx.x) / share, b = rank * share + int(threadIdx.x) % share;
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += cluster.map_shared_rank(&sh, 4 * part + i)->count[b];
+        sh.list[threadIdx.x] = n;
+        __syncthreads();
+        n = 0;
+        for (int i = int(threadIdx.x) % share; i < kSampleThreads; i += share) n += uint32_t(sh.list[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cluster.map_shared_rank(&sh, 4 * part + i)->all_count[b] = n;
+      } else {
+        for (int b = rank * share + int(threadIdx.x); b < (rank + 1) * share; b += kSampleThreads) {
+          uint32_t n = 0;
+          for (int r = 0; r < a.ctas; ++r) n += cluster.map_shared_rank(&sh, r)->count[b];
+          for (int r = 0; r < a.ctas; ++r) cluster.map_shared_rank(&sh, r)->all_count[b] = n;
+        }
+      }
+    }
+    cluster.sync();
+    // The bins to look at: [lo, hi] around top-p's border, `end` the last one that top-k reaches into (if it leaves
+    // any out: `cut`), with counts before and in them.
+    int lo, hi, end;
+    bool cut;
+    uint32_t before_lo, upto_hi, before_end = 0, in_end = 0;
+    {
+      constexpr int kBinsEach = kBins / kSampleThreads;
+      const int b0 = int(threadIdx.x) * kBinsEach;
+      uint32_t n[kBinsEach], ns = 0;
+      uint64_t m[kBinsEach], ms = 0;
+      constexpr float kNext = 0.98521119f;  // 2^(-44 / 2047)
+      static_assert(kBins == 2048 && kLeast == -44.f, "");
+      float middle = exp2f(middle_of(b0)) * float(uint64_t(1) << kOne);
+#pragma unroll
+      for (int i = 0; i < kBinsEach; ++i) {
+        n[i] = sh.all_count[b0 + i];
+        m[i] = n[i] * __float2ull_rn(middle);
+        middle *= kNext;
+        ns += n[i], ms += m[i];
+      }
+      uint64_t total, of;
+      const uint32_t nb = uint32_t(block_prefix(sh, ns, total)) - ns;
+      const uint64_t mb = block_prefix(sh, ms, of) - ms;
+      if (threadIdx.x < 3) sh.border[threadIdx.x] = -1;
+      __syncthreads();
+      // f(bin, counts and sums before and with it) for this thread's bins.
+      const auto bins = [&](auto&& f) {
+        uint32_t count = nb;
+        uint64_t mass = mb;
+#pragma unroll
+        for (int i = 0; i < kBinsEach; ++i) {
+          f(b0 + i, count, count + n[i], mass, mass + m[i]);
+          count += n[i], mass += m[i];
+        }
+      };
+      cut = by_count && uint64_t(top_k) < total;
+      if (cut) {
+        bins([&](int b, uint32_t count, uint32_t with, uint64_t mass, uint64_t) {
+          if (count >= uint32_t(top_k) || with < uint32_t(top_k)) return;
+          sh.border[2] = b, sh.border_count[0] = count, sh.border_count[1] = with - count;
+          sh.own_mass = mass + (uint32_t(top_k) - count) * __float2ull_rn(exp2f(middle_of(b)) * float(uint64_t(1) << kOne));
+        });
+        __syncthreads();
+        before_end = sh.border_count[0], in_end = sh.border_count[1], of = sh.own_mass;
+      }
+      end = cut ? sh.border[2] : kBins - 1;
+      lo = hi = end;
+      if (by_mass) {
+        const uint64_t border_sum = enough_of(of), least_sum = max(border_sum - border_sum / kMiddles<T>, uint64_t(1)),
+                       most_sum = border_sum + border_sum / kMiddles<T>;
+        bins([&](int b, uint32_t, uint32_t, uint64_t mass, uint64_t with) {
+          if (mass < least_sum && with >= least_sum) sh.border[0] = b;
+          if (mass < most_sum && with >= most_sum) sh.border[1] = b;
+        });
+        __syncthreads();
+        if (sh.border[0] >= 0) lo = min(lo, sh.border[0]);
+        if (sh.border[1] >= 0) hi = min(hi, sh.border[1]);
+      }
+      bins([&](int b, uint32_t count, uint32_t with, uint64_t, uint64_t) {
+        if (b == lo) sh.border_count[0] = count;
+        if (b == hi) sh.border_count[1] = with;
+      });
+      __syncthreads();
+      before_lo = sh.border_count[0], upto_hi = sh.border_count[1];
+    }
+    const bool whole = max(upto_hi, before_end + in_end) <= kListed;  // all that may stay can be listed
+    const bool apart = cut && end > hi;
+    bool found = !cut && !by_mass;  // nothing is left out
+    if (!found && (whole || upto_hi - before_lo + (apart ? in_end : 0) <= kListed)) {
+      // The sums: of all that top-p is of but for the bin `end` (base), of what lies before lo (above), of what stays of it (kept).
+      const int list_from = whole ? 0 : lo, list_to = whole && cut ? end : hi;
+      const bool weigh = !whole || (by_mass && !cut);
+      uint64_t base = 0, above = 0, kept = 0;
+      const int base_to = cut ? end : kBins + 1, apart_at = cut ? end : -1;
+      const bool any_weight = least == 1;
+      x.each_heavy(from, to, [&](const float (&v)[G], int e) {
+#pragma unroll
+        for (int i0 = 0; i0 < G; i0 += 4) {  // four side by side, what is rare behind them
+          int b[4];
+          bool some = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float y = exponent_of(w, v[i0 + i]);
+            b[i] = y > kLeast ? bin_of(y) : kBins;
+            some |= (b[i] >= list_from && b[i] <= list_to) || b[i] == apart_at;
           }
-          lane_sum += m[k];
-        }
-        uint64_t sums = before + warp_prefix(lane_sum) - lane_sum;
-        before += warp_sum(lane_sum);
+          if (weigh) {
+            uint64_t m[4];
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-          if (drawn >= sums && drawn < sums + m[k]) a.out[row] = i * G - x.skew + k;
-          sums += m[k];
+            for (int i = 0; i < 4; ++i) m[i] = weight_of(w, v[i0 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              base += b[i] < base_to ? m[i] : 0;
+              above += b[i] < list_from ? m[i] : 0;
+            }
+            if (!any_weight) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) kept += b[i] < list_from && m[i] >= least ? m[i] : 0;
+            }
+          }
+          if (some) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((b[i] >= list_from && b[i] <= list_to) || b[i] == apart_at) list(v[i0 + i], e + i0 + i);
+          }
         }
-        done = drawn < before;
+      });
+      if (any_weight) kept = above;
+      base = warp_sum(base), above = warp_sum(above), kept = warp_sum(kept);
+      if (lane == 0) sh.warp_base[warp] = base, sh.warp_above[warp] = above;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        base = above = 0;
+        for (int i = 0; i < kSampleWarps; ++i) base += sh.warp_base[i], above += sh.warp_above[i];
+        sh.own_base = base, sh.own_above = above;
+      }
+      const int n = collect();  // (as many as the counts say: none are left out)
+      if (rank == 0) {
+        const SampleShared* his = cluster.map_shared_rank(&sh, lane < a.ctas ? lane : 0);
+        base = warp_sum(lane < a.ctas ? his->own_base : 0), above = warp_sum(lane < a.ctas ? his->own_above : 0);
+        uint64_t weight[kEach], sum = 0, all;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int i = threadIdx.x * kEach + k;
+          weight[k] = i < n ? entry_weight(uint32_t(sh.sorted[i] >> 32)) : 0;
+          sum += weight[k];
+        }
+        const uint64_t first = block_prefix(sh, sum, all) - sum;
+        const int left = cut ? n - int(in_end) + top_k - int(before_end) : n;  // entries that top-k leaves
+        if (whole) {
+          // (top-p's border lies beyond the list where the middles were too far off)
+          const bool reaches = cut || !by_mass || all >= enough_of(base);
+          if (threadIdx.x == 0) sh.cut_found = reaches;
+          if (reaches) finish(n, left, cut ? 0 : base);
+        } else {
+          if (threadIdx.x == 0) sh.cut_found = false;
+          __syncthreads();
+          uint64_t before = above + first;
+          uint64_t need = 0;
+          if (by_mass) {
+            if (cut) {  // and of the bin `end`, what top-k leaves
+              sum = 0;
+#pragma unroll
+              for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x * kEach + k;
+                if (i >= n - int(in_end) && i < left) sum += weight[k];
+              }
+              (void)block_prefix(sh, sum, all);
+              base += all;
+            }
+            need = enough_of(base);
+          }
+          const int together = apart ? n - int(in_end) : left;  // entries that follow what lies before lo without a gap
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x * kEach + k;
+            const bool is = by_mass ? i < together && before < need && before + weight[k] >= need : i == left - 1;
+            if (is) sh.cut_found = true, sh.cut_value = ~uint32_t(sh.sorted[i] >> 32), sh.cut_place = int(uint32_t(sh.sorted[i]));
+            before += weight[k];
+          }
+        }
+      }
+      cluster.sync();
+      const SampleShared* his = cluster.map_shared_rank(&sh, 0);
+      found = his->cut_found;
+      if (found && !whole) {
+        border = of_order(his->cut_value), place = his->cut_place;
+        // What stays of this CTA's list joins its warps' sums.
+        if (lane == 0) sh.warp_mass[warp] = kept;
+        __syncthreads();
+        for (int i = threadIdx.x; i < sh.listed; i += kSampleThreads) {
+          const float v = of_order(~uint32_t(sh.list[i] >> 32));
+          const int e = int(uint32_t(sh.list[i]));
+          const uint64_t m = kept_weight(v, e);
+          if (!m) continue;
+          const int g = (e + x.skew) / G - x.first;
+          int k = int(int64_t(g) * kSampleWarps / mine);
+          while (k + 1 < kSampleWarps && g >= int(int64_t(mine) * (k + 1) / kSampleWarps)) ++k;
+          atomicAdd(reinterpret_cast<unsigned long long*>(&sh.warp_mass[k]), static_cast<unsigned long long>(m));
+        }
+        summed = true;
+      }
+      cluster.sync();
+      if (found && whole) return;
+    }
+    if (!found) {
+      // Exact histograms of the values' bits: the token at which the count, then the sum is reached.
+      uint64_t need = cut ? uint64_t(top_k) : 0, kept = 0;
+      uint32_t *counts = sh.count, *low = sh.count + kDigits, *high = sh.all_count + kDigits;
+      for (bool mass = !cut;; mass = true) {
+        uint32_t prefix = 0, known = 0;  // the bits found
+        Found at = {0, 0, 0, 0, 0};
+#pragma unroll 1
+        for (int shift = 22;; shift = max(0, shift - 10)) {
+          const uint32_t width = known ? min(10, __ffs(int(known)) - 1 - shift) : 10;
+          const uint32_t most = (1u << width) - 1;
+          __syncthreads();
+          for (int i = threadIdx.x; i < kDigits; i += kSampleThreads) counts[i] = low[i] = high[i] = 0;
+          __syncthreads();
+          x.each_heavy(from, to, [&](const float (&v)[G], int) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              const uint32_t o = order_of(v[i]);
+              if ((o & known) != prefix) continue;
+              const uint64_t m = weight_of(w, v[i]);
+              if (!m) continue;
+              const uint32_t b = most - ((o >> shift) & most);
+              atomicAdd(&counts[b], 1u);
+              const uint32_t old = atomicAdd(&low[b], uint32_t(m));
+              atomicAdd(&high[b], uint32_t(m >> 32) + (old + uint32_t(m) < old));
+            }
+          });
+          cluster.sync();
+          const int share = kDigits / a.ctas;
+          for (int b = rank * share + int(threadIdx.x); b < (rank + 1) * share; b += kSampleThreads) {
+            uint32_t n = 0;
+            uint64_t m = 0;
+            for (int r = 0; r < a.ctas; ++r) {
+              const SampleShared* his = cluster.map_shared_rank(&sh, r);
+              n += his->count[b], m += uint64_t(his->all_count[kDigits + b]) << 32 | his->count[kDigits + b];
+            }
+            for (int r = 0; r < a.ctas; ++r) {
+              SampleShared* his = cluster.map_shared_rank(&sh, r);
+              his->all_count[b] = n, his->all_mass[b] = m;
+            }
+          }
+          cluster.sync();
+          if (mass && need == 0) {
+            uint64_t all;
+            (void)block_prefix(sh, sh.all_mass[threadIdx.x] + sh.all_mass[threadIdx.x + kSampleThreads], all);
+            need = enough_of(cut ? kept : all);
+          }
+          at = search(sh, mass, need, at.above, at.mass_above);
+          prefix |= (most - uint32_t(at.digit)) << shift, known |= most << shift;
+          if (shift == 0 || (G == 8 && shift <= 12)) break;
+        }
+        if (G == 8) prefix |= prefix >> 31 ? 0 : 0xfffu;  // the bits that 16-bit types do not have
+        // Of the tokens of this value as many as it takes, the first ones.
+        const uint64_t each = at.mass_in / at.in;
+        const uint64_t ties = min(mass ? (need - at.mass_above + each - 1) / each : need - at.above, uint64_t(at.in));
+        border = of_order(prefix), kept = at.mass_above + ties * each;
+        if (mass || !by_mass) {
+          const int last = locate(false, [&](float v, int) { return uint64_t(v == border); }, [&](uint64_t) { return ties - 1; });
+          if (last >= 0 && threadIdx.x < a.ctas) cluster.map_shared_rank(&sh, threadIdx.x)->cut_place = last;
+          cluster.sync();
+          place = sh.cut_place;
+          break;
+        }
+        need = 0;
       }
     }
   }
+
+  // 5. The token.
+  const auto pick = [&](uint64_t all) { return part_of(u, all, false); };
+  const int token = border == -INFINITY && least == 1 ? locate(false, [&](float v, int) { return weight_of(w, v); }, pick)
+                                                      : locate(summed, kept_weight, pick);
+  if (token >= 0 && threadIdx.x == 0) a.out[row] = token;
   cluster.sync();  // the sums have been read
 }
 
