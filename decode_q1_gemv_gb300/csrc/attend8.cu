@@ -14,16 +14,17 @@
 //     divided by a power of two near their largest value, which f16's 11 bits hold exactly
 //     down to 2^-14 of it.  The sums of 32 products are multiplied with the block's scale in f32.
 //   Values: a block's scale depends on the key and the block, so it goes into
-//     the weight: p d, rounded to bf16 (which has f32's range, so the size of scales
-//     does not matter) and, for f16 q, the remainder as a second bf16; quants are exact in bf16
-//     (0x4300 | 7 bits is 128 + them; the sign takes 128 or 256 off).
+//     the weight: p d, rounded to f16.  So that its size does not matter, p is
+//     relative not to the row's maximum alone but to that times a power of two that no scale
+//     of the values so far exceeds: p d then is at most 2^8, off by 2^-11 of itself or, below 2^-14,
+//     2^-25; the sum of p is f32, relative to the same.
 // ldmatrix moves pairs of bytes as 16-bit elements: a lane gets four dims of a
 // key, or (transposed) two dims of two keys; taking the even and the odd bytes of
 // a word apart puts dims in the order 0 2 1 3 in both operands.
 //
-// Maxima are looked at by a vote: weights are relative to a maximum in use,
-// which moves only when a score is 2^8 times beyond it (they are at most 2^8, which
-// f32 sums and bf16 hold), so most chunks have no exchange between lanes for it.
+// Maxima (of scores, and of the values' scales) are looked at by a vote: the ones in
+// use move only when a score is 2^8 times beyond, or a scale beyond, so most
+// chunks have no exchange between lanes for it.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -39,8 +40,8 @@ namespace q1 {
 
 namespace cg = cooperative_groups;
 
-constexpr int kKeys8 = 64;   // keys of a unit: 16 for each warp
 constexpr int kWarps8 = 4;
+constexpr int kKeys8 = 16 * kWarps8;  // keys of a unit: 16 for each warp
 constexpr int kWhole8 = 2;   // units of an item that is not split
 constexpr float kGrow8 = 8.f;  // log2 units a maximum may be behind
 
@@ -50,15 +51,15 @@ struct Attend8Args {
   int64_t s_page, s_slot, s_head;
 };
 
-template <int D, int NT>
+template <int D, int NT, int kWarps = kWarps8>
 struct Shape8 {
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = D, kChunkBytes = 16 * D, kScaleBytes = D / 16;  // a key's quants, 16 keys', a key's scales
   static constexpr int kStageBytes = 2 * kChunkBytes + 2 * 16 * kScaleBytes;
-  static constexpr int kCtas = NT == 1 ? 4 : 3;  // an SM
+  static constexpr int kCtas = kWarps == 2 * kWarps8 ? 1 : NT == 1 ? 4 : 3;  // an SM
   static constexpr int kStages = D == 64 ? 5 : NT == 1 ? 3 : 4;
-  static constexpr int kSmem = kWarps8 * kStages * kStageBytes;
-  static_assert(kSmem >= kWarps8 * kRows * (D + 4) * 4, "the warps' outputs go over the ring");
+  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static_assert(kSmem >= kWarps * kRows * (D + 4) * 4, "the warps' outputs go over the ring");
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "");
 };
 
@@ -68,67 +69,61 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, ui
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes, std::integral_constant<int, 4>) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// c += a b, of f16 or bf16.
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+// c += a b, and a b alone.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {  // of an 8x8 matrix of 16-bit elements
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// Quants b0 and b2 of a word as f16 and as bf16; b1 and b3 those of the word shifted by a byte.
-__device__ __forceinline__ uint32_t quants_f16(uint32_t w) {
+// Quants b0 and b2 of a word as f16; b1 and b3 those of the word shifted by a byte.
+__device__ __forceinline__ uint32_t quants(uint32_t w) {
   const uint32_t biased = (w & 0x00ff00ffu) ^ 0x64806480u, bias = 0x64806480u;
   const __half2 r = __hsub2(reinterpret_cast<const __half2&>(biased), reinterpret_cast<const __half2&>(bias));
   return reinterpret_cast<const uint32_t&>(r);
 }
-__device__ __forceinline__ uint32_t quants_bf16(uint32_t w) {
-  const uint32_t low = (w & 0x007f007fu) | 0x43004300u, sign = (w & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(low), reinterpret_cast<const __nv_bfloat162&>(sign));
-  return reinterpret_cast<const uint32_t&>(r);
-}
-// Scales of one key, `kBlocks` of them, from shared memory.  For keys (kSum) an infinite one
-// is NaN, as the sum of the block's values is: the scale only meets the sum of the quants.
-template <int kBlocks, bool kSum>
-__device__ __forceinline__ void scales_of(const unsigned char* at, float (&d)[kBlocks]) {
-  uint32_t w[kBlocks / 2];
-  if constexpr (kBlocks == 4) {
+// Scales of one key, kWords pairs of them, from shared memory; as f32.
+template <int kWords>
+__device__ __forceinline__ void scales_of(const unsigned char* at, uint32_t (&w)[kWords]) {
+  if constexpr (kWords == 2) {
     const uint2 v = *reinterpret_cast<const uint2*>(at);
     w[0] = v.x, w[1] = v.y;
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(at);
   }
-#pragma unroll
-  for (int i = 0; i < kBlocks / 2; ++i) {
-    if constexpr (kSum) {  // d * 0 + d
-      const uint32_t zero = 0u;
-      const __half2 r = __hfma2(reinterpret_cast<const __half2&>(w[i]), reinterpret_cast<const __half2&>(zero), reinterpret_cast<const __half2&>(w[i]));
-      w[i] = reinterpret_cast<const uint32_t&>(r);
-    }
-    Elem<__half>::unpack2(w[i], d[2 * i], d[2 * i + 1]);
-  }
+}
+// For keys an infinite scale is NaN, as the sum of the block's values is: the scale only meets the sum of the quants.
+__device__ __forceinline__ uint32_t no_infinity(uint32_t w) {  // w * 0 + w
+  const uint32_t zero = 0u;
+  const __half2 r = __hfma2(reinterpret_cast<const __half2&>(w), reinterpret_cast<const __half2&>(zero), reinterpret_cast<const __half2&>(w));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of numbers, where there are some
+  const __half2 r = __hmax2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
+  return reinterpret_cast<const uint32_t&>(r);
 }
 
 // kCluster: not shares of the axis but a cluster of a.ctas CTAs for each
 // sequence, key head and tile, which joins its own parts, as in attend.cu.
-template <class T, int D, int NT, bool kCluster>
-__global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q8(const __grid_constant__ Attend8Args args) {
-  using Shape = Shape8<D, NT>;
-  using Tile = Tiling<Shape::kRows, kKeys8>;
-  constexpr int kRows = Shape::kRows, kStages = Shape::kStages, kPieces = D / 16, kBlocks = D / 32;
-  constexpr bool kSplit = std::is_same<T, __half>::value;  // weights as two bf16
+template <class T, int D, int NT, bool kCluster, int kWarps = kWarps8>
+__global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_attend_q8(const __grid_constant__ Attend8Args args) {
+  constexpr int kUnit = 16 * kWarps;  // keys
+  using Shape = Shape8<D, NT, kWarps>;
+  using Tile = Tiling<Shape::kRows, kUnit>;
+  constexpr int kRows = Shape::kRows, kStages = Shape::kStages, kPieces = D / 16, kBlocks = D / 32, kWords = D / 64;
   const AttendArgs& a = args.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ LocateScratch scratch;
-  __shared__ float ml[kWarps8][kRows][2];
+  __shared__ float ml[kWarps][kRows][2];
   __shared__ float2 own[kRows];  // kCluster: the CTA's maxima and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
@@ -164,42 +159,58 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
     }
     const int keys = Tile::keys(a, cur.s, cur.m), of_all = Tile::keys_of_all(a, cur.s, cur.m);
     const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
+
+    // Chunk i of this warp: keys j0 + 64 i .. +15, which begin on a multiple of 16: in one page of 16 slots or more,
+    // which all lanes look up well before it is needed (of 8: each lane for row lane % 16).  A lane copies piece
+    // lane % kPieces of rows lane / kPieces and on; lane r the scales of row r's key, r + 16 of its value.
+    constexpr int kRowsOnce = 32 / kPieces;
+    const bool one_page = a.kv.page_shift >= 4;
+    const int j0 = cur.unit * kUnit + warp * 16, row0 = lane / kPieces;
+    const int64_t rows_on = kRowsOnce * a.kv.slot_stride;
     const int8_t* kbase = static_cast<const int8_t*>(a.kv.k) + cur.h * a.kv.head_stride + lane % kPieces * 16;
     const int8_t* vbase = static_cast<const int8_t*>(a.kv.v) + cur.h * a.kv.head_stride + lane % kPieces * 16;
     const uint16_t* sbase = (lane < 16 ? args.ks : args.vs) + cur.h * args.s_head;
-
-    // Chunk i of this warp: keys j0 + 64 i .. +15.  Lanes r and r + 16 find row r's place (its page well
-    // before it is needed); lane r copies the scales of its key, r + 16 those of its value.
-    const int j0 = cur.unit * kKeys8 + warp * 16;
-    const auto page_of = [&](int i) {  // of this lane's row; -1 past the keys
-      const int j = j0 + i * kKeys8 + (lane & 15);
+    const auto page_of = [&](int i) {  // -1 past the keys
+      const int j = j0 + i * kUnit + (one_page ? 0 : lane & 15);
       return i < take && j < keys ? table[j >> a.kv.page_shift] : -1;
     };
-    const auto fill = [&](int i, int page) {
+    const auto fill = [&](int i, int stage, int page) {
       if (i < take) {
-        const int j = j0 + i * kKeys8 + (lane & 15);
-        int64_t off = -1, soff = 0;
-        if (j < keys) {
-          if (page >= 0 && page < a.kv.pages) {
-            off = int64_t(page) * a.kv.page_stride + int64_t(j & page_mask) * a.kv.slot_stride;
-            soff = int64_t(page) * args.s_page + int64_t(j & page_mask) * args.s_slot;
-          } else {
-            atomicOr(a.status, kStatusBadIndex);
-          }
-        }
-        const uint32_t at = ring + (i % kStages) * Shape::kStageBytes;
-        // rows that are not there read as zeros
-        cp_async_small(at + 2 * Shape::kChunkBytes + lane * Shape::kScaleBytes, sbase + soff, off < 0 ? 0 : Shape::kScaleBytes,
-                       std::integral_constant<int, Shape::kScaleBytes>());
-        constexpr int kRowsOnce = 32 / kPieces;
+        const int j = j0 + i * kUnit;
+        const uint32_t at = ring + stage * Shape::kStageBytes;
+        const uint32_t sdst = at + 2 * Shape::kChunkBytes + lane * Shape::kScaleBytes, dst = at + row0 * Shape::kRowBytes;
+        const std::integral_constant<int, Shape::kScaleBytes> small;
+        if (one_page && j + 16 <= keys && page >= 0 && page < a.kv.pages) {
+          const int slot = j & page_mask;
+          const int64_t off = int64_t(page) * a.kv.page_stride + int64_t(slot + row0) * a.kv.slot_stride;
+          cp_async_small(sdst, sbase + int64_t(page) * args.s_page + int64_t(slot + (lane & 15)) * args.s_slot, Shape::kScaleBytes, small);
+          const int8_t *k = kbase + off, *v = vbase + off;
 #pragma unroll
-        for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
-          const int r = r0 + lane / kPieces;
-          const int64_t o = __shfl_sync(0xffffffffu, off, r);
-          const uint32_t dst = at + r * Shape::kRowBytes + (place(lane % kPieces, r) << 4);
-          const int64_t e = o < 0 ? 0 : o;
-          cp_async16(dst, kbase + e, o < 0 ? 0 : 16);
-          cp_async16(dst + Shape::kChunkBytes, vbase + e, o < 0 ? 0 : 16);
+          for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
+            const uint32_t to = dst + r0 * Shape::kRowBytes + (place(lane % kPieces, r0 + row0) << 4);
+            cp_async16(to, k, 16);
+            cp_async16(to + Shape::kChunkBytes, v, 16);
+            k += rows_on, v += rows_on;
+          }
+        } else {  // the last chunk, or two pages, or none; rows that are not there read as zeros
+          const int mine = j + (lane & 15);
+          int64_t off = -1, soff = 0;
+          if (mine < keys) {
+            if (page >= 0 && page < a.kv.pages) {
+              off = int64_t(page) * a.kv.page_stride + int64_t(mine & page_mask) * a.kv.slot_stride;
+              soff = int64_t(page) * args.s_page + int64_t(mine & page_mask) * args.s_slot;
+            } else {
+              atomicOr(a.status, kStatusBadIndex);
+            }
+          }
+          cp_async_small(sdst, sbase + soff, off < 0 ? 0 : Shape::kScaleBytes, small);
+#pragma unroll 1
+          for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, r0 + row0);
+            const uint32_t to = dst + r0 * Shape::kRowBytes + (place(lane % kPieces, r0 + row0) << 4);
+            cp_async16(to, kbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+            cp_async16(to + Shape::kChunkBytes, vbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+          }
         }
       }
       cp_commit();
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
     for (int i = 0; i < kStages; ++i) page[i] = page_of(i);
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-      fill(i, page[i]);
+      fill(i, i, page[i]);
       page[i] = page_of(i + kStages);
     }
 
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) w[p] = live ? *reinterpret_cast<const uint2*>(row + p * 16) : make_uint2(0u, 0u);
       float scale = a.scale_log2;
-      if constexpr (kSplit) {
+      if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) qb[t][p][0] = __byte_perm(w[p].x, w[p].y, 0x5410), qb[t][p][1] = __byte_perm(w[p].x, w[p].y, 0x7632);
       } else {
@@ -255,8 +266,9 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
         limit[t][e] = __shfl_sync(0xffffffffu, sees, (2 * c + e) * 4);
       }
     }
-    // o: dims 16 p + 2 g (0, 1) and + 1 (2, 3) of rows 2c (0, 2) and 2c + 1 (1, 3).  base: the maximum in use.
-    float o[NT][kPieces][4], base[NT][2], sum[NT][2];
+    // o: dims 16 p + 2 g (0, 1) and + 1 (2, 3) of rows 2c (0, 2) and 2c + 1 (1, 3).  base: what weights are
+    // relative to, the maximum in use and the power of two 2^most that the values' scales do not exceed.
+    float o[NT][kPieces][4], base[NT][2], sum[NT][2], most = -25.f, top_scale = 0.f;  // top_scale: 2^most
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -266,57 +278,76 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
       base[t][0] = base[t][1] = -FLT_MAX, sum[t][0] = sum[t][1] = 0.f;
     }
 
+    // matrices of ldmatrix: keys 0-7 and 8-15, of a block's two pieces
+    const int r = (lane & 7) + (lane & 8), second = lane >> 4;
+    int stage = 0;
     for (int i = 0; i < take; ++i) {
       cp_wait<kStages - 1>();
       __syncwarp();
-      const unsigned char* stage = my_ring + (i % kStages) * Shape::kStageBytes;
-      const uint32_t kt = ring + (i % kStages) * Shape::kStageBytes, vt = kt + Shape::kChunkBytes;
+      const unsigned char* scales = my_ring + stage * Shape::kStageBytes + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes;
+      const uint32_t kt = ring + stage * Shape::kStageBytes + r * Shape::kRowBytes, vt = kt + Shape::kChunkBytes;
       // s: keys g (0, 1) and g + 8 (2, 3) by rows 2c (0, 2) and 2c + 1 (1, 3)
       float s[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-      // matrices of ldmatrix: keys 0-7 and 8-15, of the block's two pieces
-      const int r = (lane & 7) + (lane & 8), second = lane >> 4;
       {
-        float d0[kBlocks], d8[kBlocks];
-        scales_of<kBlocks, true>(stage + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes, d0);
-        scales_of<kBlocks, true>(stage + 2 * Shape::kChunkBytes + (g + 8) * Shape::kScaleBytes, d8);
+        uint32_t d0[kWords], d8[kWords];
+        scales_of(scales, d0);
+        scales_of(scales + 8 * Shape::kScaleBytes, d8);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           uint32_t w[4];
-          ldsm4(kt + r * Shape::kRowBytes + (place(2 * b + second, r) << 4), w);
+          ldsm4(kt + (place(2 * b + second, r) << 4), w);
           float part[NT][4];
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[t][e] = 0.f;
-#pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const uint32_t k[4] = {quants_f16(w[2 * p]), quants_f16(w[2 * p + 1]), quants_f16(w[2 * p] >> 8), quants_f16(w[2 * p + 1] >> 8)};
+            const uint32_t k[4] = {quants(w[2 * p]), quants(w[2 * p + 1]), quants(w[2 * p] >> 8), quants(w[2 * p + 1] >> 8)};
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(part[t], k, qb[t][2 * b + p]);
+            for (int t = 0; t < NT; ++t) {
+              if (p == 0)
+                mma_f16_new(part[t], k, qb[t][2 * b][0], qb[t][2 * b][1]);
+              else
+                mma_f16(part[t], k, qb[t][2 * b + 1][0], qb[t][2 * b + 1][1]);
+            }
           }
+          if (b % 2 == 0) d0[b / 2] = no_infinity(d0[b / 2]), d8[b / 2] = no_infinity(d8[b / 2]);
+          float e0, e8, unused;
+          if (b % 2 == 0)
+            Elem<__half>::unpack2(d0[b / 2], e0, unused), Elem<__half>::unpack2(d8[b / 2], e8, unused);
+          else
+            Elem<__half>::unpack2(d0[b / 2], unused, e0), Elem<__half>::unpack2(d8[b / 2], unused, e8);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] = __fmaf_rn(part[t][e], e < 2 ? d0[b] : d8[b], s[t][e]);
+            for (int e = 0; e < 4; ++e) s[t][e] = b == 0 ? part[t][e] * (e < 2 ? e0 : e8) : __fmaf_rn(part[t][e], e < 2 ? e0 : e8, s[t][e]);
         }
       }
+      uint32_t d0[kWords], d8[kWords];
+      scales_of(scales + 16 * Shape::kScaleBytes, d0);
+      scales_of(scales + 24 * Shape::kScaleBytes, d8);
+      uint32_t tops = max2(no_infinity(d0[0]), no_infinity(d8[0]));  // (a NaN is passed over)
+      if constexpr (kWords == 2) tops = max2(tops, max2(no_infinity(d0[1]), no_infinity(d8[1])));
+      float top, other;
+      Elem<__half>::unpack2(tops, top, other);
+      top = fmaxf(top, other);
       // Scores to log2 units; keys a row may not see drop out by selection.
-      const int j = j0 + i * kKeys8 + g;
+      const int j = j0 + i * kUnit + g;
       const bool partial_view = j - g + 16 > of_all;
-      bool grown = false;
+      bool grown = top > top_scale;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[t][e] *= row_scale[t][e & 1];
           if (partial_view && j + (e >> 1) * 8 >= limit[t][e & 1]) s[t][e] = -INFINITY;
-          grown |= s[t][e] - base[t][e & 1] > kGrow8;
+          grown |= s[t][e] - base[t][e & 1] > kGrow8 - most;
         }
       if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float old = most;
+        if (top > top_scale) {  // the next power of two (2^-24 at least)
+          const uint32_t bits = (__float_as_uint(top) + 0x7fffffu) & 0x7f800000u;
+          top_scale = __uint_as_float(bits), most = float(int(bits >> 23) - 127);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float f[2];
@@ -325,9 +356,9 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
             float m = fmaxf(s[t][e], s[t][e + 2]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            m = fmaxf(m, base[t][e]);
-            f[e] = ex2(base[t][e] - m);
-            base[t][e] = m;
+            const float to = fmaxf(m, base[t][e] - old) + most;
+            f[e] = ex2(base[t][e] - to);
+            base[t][e] = to;
             sum[t][e] *= f[e];
           }
 #pragma unroll
@@ -341,52 +372,44 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
           s[t][e] = ex2(s[t][e] - base[t][e & 1]);
           sum[t][e & 1] += s[t][e];
         }
-      float d0[kBlocks], d8[kBlocks];
-      scales_of<kBlocks, false>(stage + 2 * Shape::kChunkBytes + (16 + g) * Shape::kScaleBytes, d0);
-      scales_of<kBlocks, false>(stage + 2 * Shape::kChunkBytes + (24 + g) * Shape::kScaleBytes, d8);
       // A scale that is no number must not reach, as 0 * inf, the rows that may not see its key.
       bool careful = false;
       if (partial_view) {
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) careful |= !(fabsf(d0[b]) <= FLT_MAX) || !(fabsf(d8[b]) <= FLT_MAX);
+        for (int k = 0; k < kWords; ++k) careful |= no_number<__half>(d0[k]) || no_number<__half>(d0[k] >> 16) || no_number<__half>(d8[k]) || no_number<__half>(d8[k] >> 16);
         careful = __any_sync(0xffffffffu, careful);
       }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
         uint32_t w[4];
-        ldsm4t(vt + r * Shape::kRowBytes + (place(2 * b + second, r) << 4), w);
-        uint32_t hi[NT][2], lo[NT][2];
+        ldsm4t(vt + (place(2 * b + second, r) << 4), w);
+        float e0, e8, unused;
+        if (b % 2 == 0)
+          Elem<__half>::unpack2(d0[b / 2], e0, unused), Elem<__half>::unpack2(d8[b / 2], e8, unused);
+        else
+          Elem<__half>::unpack2(d0[b / 2], unused, e0), Elem<__half>::unpack2(d8[b / 2], unused, e8);
+        uint32_t pt[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float p[4] = {s[t][0] * d0[b], s[t][1] * d0[b], s[t][2] * d8[b], s[t][3] * d8[b]};
+          float p[4] = {s[t][0] * e0, s[t][1] * e0, s[t][2] * e8, s[t][3] * e8};
           if (careful) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (j + (e >> 1) * 8 >= limit[t][e & 1]) p[e] = 0.f;
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t v = Elem<__nv_bfloat16>::pack2(p[2 * h], p[2 * h + 1]);
-            hi[t][h] = transposed(v);
-            if constexpr (kSplit) {
-              float x, y;
-              Elem<__nv_bfloat16>::unpack2(v, x, y);
-              lo[t][h] = transposed(Elem<__nv_bfloat16>::pack2(p[2 * h] - x, p[2 * h + 1] - y));
-            }
-          }
+          pt[t][0] = transposed(Elem<__half>::pack2(p[0], p[1]));
+          pt[t][1] = transposed(Elem<__half>::pack2(p[2], p[3]));
         }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint32_t v[4] = {quants_bf16(w[2 * p]), quants_bf16(w[2 * p] >> 8), quants_bf16(w[2 * p + 1]), quants_bf16(w[2 * p + 1] >> 8)};
+          const uint32_t v[4] = {quants(w[2 * p]), quants(w[2 * p] >> 8), quants(w[2 * p + 1]), quants(w[2 * p + 1] >> 8)};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma_bf16(o[t][2 * b + p], v, hi[t][0], hi[t][1]);
-            if constexpr (kSplit) mma_bf16(o[t][2 * b + p], v, lo[t][0], lo[t][1]);
-          }
+          for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * b + p], v, pt[t][0], pt[t][1]);
         }
       }
       __syncwarp();
-      fill(i + kStages, page[0]);
+      fill(i + kStages, stage, page[0]);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
       for (int k = 0; k < kStages - 1; ++k) page[k] = page[k + 1];
       page[kStages - 1] = page_of(i + 2 * kStages);
@@ -413,7 +436,7 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
         const int row = t * 8 + 2 * c + e;
         float m = ml[0][row][0];
 #pragma unroll
-        for (int w = 1; w < kWarps8; ++w) m = fmaxf(m, ml[w][row][0]);
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[w][row][0]);
         const float f = ex2(base[t][e] - m);
 #pragma unroll
         for (int p = 0; p < kPieces; ++p)
@@ -423,20 +446,20 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
     const bool whole = cur.unit == 0 && take == cur.units;
     if (!kCluster && threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
     float* part = partial<kRows, D>(a, blockIdx.x, cur.unit == 0);
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += kWarps8 * 32) {
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kWarps * 32) {
       const int row = i / (D / 4), col = i % (D / 4) * 4;
       int token, head;
       if (!row_of(a, cur, cur.m * kRows + row, token, head)) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       float m = -FLT_MAX, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps8; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float4 t = *reinterpret_cast<const float4*>(joined + (w * kRows + row) * kLd + col);
         v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
         m = fmaxf(m, ml[w][row][0]);
       }
 #pragma unroll
-      for (int w = 0; w < kWarps8; ++w)
+      for (int w = 0; w < kWarps; ++w)
         if (ml[w][row][1] != 0.f) l += ml[w][row][1] * ex2(ml[w][row][0] - m);
       if (kCluster) {  // in place: no other thread reads these
         *reinterpret_cast<float4*>(joined + row * kLd + col) = v;
@@ -455,8 +478,8 @@ __global__ void __launch_bounds__(kWarps8 * 32, Shape8<D, NT>::kCtas) k_attend_q
       cg::cluster_group cluster = cg::this_cluster();
       cluster.sync();
       const int rows = min(kRows, cur.s.count * a.group - cur.m * kRows), values = rows * (D / 4);
-      const int p = int(threadIdx.x) % ctas, per = kWarps8 * 32 / ctas;
-      for (int e0 = int(blockIdx.x) % ctas * per; e0 < values; e0 += kWarps8 * 32) {
+      const int p = int(threadIdx.x) % ctas, per = kWarps * 32 / ctas;
+      for (int e0 = int(blockIdx.x) % ctas * per; e0 < values; e0 += kWarps * 32) {
         const int e = e0 + int(threadIdx.x) / ctas, row = e / (D / 4), col = e % (D / 4) * 4;
         float2 his = make_float2(-FLT_MAX, 0.f);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -500,33 +523,46 @@ static int attend8_ctas() { return (NT == 1 ? 4 : 3) * num_sms(); }
 static int64_t few_workspace8(int dim) { return std::max(attend_workspace(attend8_ctas<1>(), 8, dim), attend_workspace(attend8_ctas<2>(), 16, dim)); }
 
 // The CTAs of a cluster for each sequence, key head and tile, which joins its
-// own parts; 0: shares of the axis and a join, or the tensor-core kernel.
+// own parts; 0: shares of the axis and a join, or the tensor-core kernel.  As in
+// attend.cu: all clusters run at once, CTAs a cluster until each has two units at most, then as many as fit, up to
+// ten units each (32 heads over 8 of 128, one token over 8191 keys: 11.8 us with 16, 13.7
+// by shares; over 16384: 18.5 and 17.0; 4 sequences of 8191: 17.5 and 18.9).
+constexpr int kMostUnits8 = 10;
 template <class T, int D, int NT>
-static int attend8_cluster(Attend8Args& g, int64_t max_new, int dev, const char* who, int& ctas) {
+static int attend8_cluster(Attend8Args& g, int64_t max_new, int dev, const char* who, int& ctas, int& warps) {
   AttendArgs& a = g.a;
   constexpr int kRows = 8 * NT;
-  ctas = 0;
+  ctas = 0, warps = kWarps8;
   const int units = (a.kv.table_tokens + kKeys8 - 1) / kKeys8;
   a.tiles = int(std::min<int64_t>((max_new * a.group + kRows - 1) / kRows, 1024));
-  if (units > 7 * 16 || (units <= kWhole8 && !many_rows8(max_new, a.group, a.kv.batch == 1))) return Q1_OK;
-  static int most[64][3] = {};  // clusters of 4, 8, 16 CTAs that run at once
-  for (int i = 0; i < 3; ++i) {
+  const int64_t clusters = int64_t(a.kv.batch) * a.kv.kv_heads * a.tiles;
+  if (units <= kWhole8 && !many_rows8(max_new, a.group, a.kv.batch == 1)) return Q1_OK;
+  static int most[64][4] = {};  // clusters of 4, 8, 16 CTAs that run at once, and of 16 with twice the warps
+  for (int i = 0; i < 4; ++i) {
     int once = dev >= 0 && dev < 64 ? most[dev][i] : 0;
     if (!once) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr = {};
+      const int size = i < 3 ? 4 << i : 16;
       attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = unsigned(4 << i), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.gridDim = dim3(unsigned(4 << i)), cfg.blockDim = dim3(kWarps8 * 32), cfg.dynamicSmemBytes = Shape8<D, NT>::kSmem;
+      attr.val.clusterDim.x = unsigned(size), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(unsigned(size)), cfg.blockDim = dim3((i < 3 ? 1 : 2) * kWarps8 * 32);
+      cfg.dynamicSmemBytes = i < 3 ? Shape8<D, NT>::kSmem : Shape8<D, NT, 2 * kWarps8>::kSmem;
       cfg.attrs = &attr, cfg.numAttrs = 1;
-      if (int e = cuda_status(cudaOccupancyMaxActiveClusters(&once, k_attend_q8<T, D, NT, true>, &cfg), who)) return e;
+      const cudaError_t e = i < 3 ? cudaOccupancyMaxActiveClusters(&once, k_attend_q8<T, D, NT, true>, &cfg)
+                                  : cudaOccupancyMaxActiveClusters(&once, k_attend_q8<T, D, NT, true, 2 * kWarps8>, &cfg);
+      if (int r = cuda_status(e, who)) return r;
       if (dev >= 0 && dev < 64) most[dev][i] = once;
     }
-    if (int64_t(a.kv.batch) * a.kv.kv_heads * a.tiles > once) break;
+    if (clusters > once) break;
+    if (i == 3) {
+      warps = 2 * kWarps8;
+      break;
+    }
     ctas = 4 << i;
     if (units <= 2 * ctas) break;
   }
-  if (units > 7 * ctas) ctas = 0;
+  if (units > kMostUnits8 * ctas * (warps / kWarps8)) ctas = 0;
   return Q1_OK;
 }
 
@@ -534,6 +570,7 @@ template <class T, int D, int NT>
 static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, void* workspace, cudaStream_t s, bool& ran,
                           const AttendArgs* many) {
   using Shape = Shape8<D, NT>;
+  using Wide = Shape8<D, NT, 2 * kWarps8>;
   const char* who = "q1_paged_attention_q8 launch";
   AttendArgs& a = g.a;
   static bool set[64] = {};
@@ -545,17 +582,23 @@ static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, v
     if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true>, most, Shape::kSmem), who)) return e;
     if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
       return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true, 2 * kWarps8>, most, Wide::kSmem), who)) return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true, 2 * kWarps8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
+      return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  int ctas = 0;
+  int ctas = 0, warps = kWarps8;
   if (only_clusters)
-    if (int e = attend8_cluster<T, D, NT>(g, max_new, dev, who, ctas)) return e;
+    if (int e = attend8_cluster<T, D, NT>(g, max_new, dev, who, ctas, warps)) return e;
   ran = ctas || !only_clusters;
   if (!ran) return Q1_OK;
   a.ctas = ctas;
-  if (ctas)
-    return launch_op<Attend8Args>(k_attend_q8<T, D, NT, true>, dim3(unsigned(a.kv.batch * a.kv.kv_heads * a.tiles * ctas)), kWarps8 * 32,
-                                  Shape::kSmem, ctas, s, who, g);
+  if (ctas) {
+    const dim3 grid(unsigned(a.kv.batch * a.kv.kv_heads * a.tiles * ctas));
+    if (warps > kWarps8)
+      return launch_op<Attend8Args>(k_attend_q8<T, D, NT, true, 2 * kWarps8>, grid, 2 * kWarps8 * 32, Wide::kSmem, ctas, s, who, g);
+    return launch_op<Attend8Args>(k_attend_q8<T, D, NT, true>, grid, kWarps8 * 32, Shape::kSmem, ctas, s, who, g);
+  }
   a.ctas = attend8_ctas<NT>();
   place_workspace(a, workspace);
   if (int e = launch_op<Attend8Args>(k_attend_q8<T, D, NT, false>, dim3(unsigned(a.ctas)), kWarps8 * 32, Shape::kSmem, 1, s, who, g)) return e;

@@ -533,8 +533,8 @@ int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t heads, int64_t 
 /* q1_paged_attention over a q8_0 cache; q and out are of `dtype` (Q1_BF16 or
  * Q1_F16).  Up to some tens of rows a key head (new tokens times the group) the
  * quants are multiplied as they are, which is exact, and scales are applied to
- * sums (keys) and weights (values, whose product with the scale is rounded to
- * bf16, with f16 q to the sum of two bf16).  More rows take the tensor-core kernel
+ * sums (keys) and weights (values: a weight's product with the scale is rounded to f16, off
+ * by 2^-11 of itself or by 2^-25 of the largest there is).  More rows take the tensor-core kernel
  * over a copy of the sequence that the call makes in the workspace: each value quant *
  * scale, divided by a power of two for its sequence and head (so its size does not
  * matter), rounded to f16, and with f16 q the remainder as a second f16.  As many sequences
