@@ -63,11 +63,16 @@ struct Shape8 {
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "");
 };
 
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes, std::integral_constant<int, 8>) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+template <int kBytes>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes, std::integral_constant<int, 4>) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+template <int kBytes>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {  // zeros past `bytes`
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_whole(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // c += a b, and a b alone.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -174,23 +179,33 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
       const int j = j0 + i * kUnit + (one_page ? 0 : lane & 15);
       return i < take && j < keys ? table[j >> a.kv.page_shift] : -1;
     };
-    const auto fill = [&](int i, int stage, int page) {
+    const int64_t row_off = int64_t(row0) * a.kv.slot_stride, scale_off = int64_t(lane & 15) * args.s_slot;
+    const bool dense = a.kv.slot_stride == D;  // a head's slots side by side: rows at constant distances
+    uint32_t to[16 / kRowsOnce];               // where this lane's pieces go in a stage
+#pragma unroll
+    for (int k = 0; k < 16 / kRowsOnce; ++k)
+      to[k] = ring + (k * kRowsOnce + row0) * Shape::kRowBytes + (place(lane % kPieces, k * kRowsOnce + row0) << 4);
+    const uint32_t scale_to = ring + 2 * Shape::kChunkBytes + lane * Shape::kScaleBytes;
+    const auto fill = [&](int i, uint32_t stage, int page) {  // stage: its offset
       if (i < take) {
         const int j = j0 + i * kUnit;
-        const uint32_t at = ring + stage * Shape::kStageBytes;
-        const uint32_t sdst = at + 2 * Shape::kChunkBytes + lane * Shape::kScaleBytes, dst = at + row0 * Shape::kRowBytes;
-        const std::integral_constant<int, Shape::kScaleBytes> small;
         if (one_page && j + 16 <= keys && page >= 0 && page < a.kv.pages) {
           const int slot = j & page_mask;
-          const int64_t off = int64_t(page) * a.kv.page_stride + int64_t(slot + row0) * a.kv.slot_stride;
-          cp_async_small(sdst, sbase + int64_t(page) * args.s_page + int64_t(slot + (lane & 15)) * args.s_slot, Shape::kScaleBytes, small);
+          const int64_t off = int64_t(page) * a.kv.page_stride + int64_t(slot) * a.kv.slot_stride + row_off;
+          cp_async_scales<Shape::kScaleBytes>(scale_to + stage, sbase + (int64_t(page) * args.s_page + int64_t(slot) * args.s_slot + scale_off));
           const int8_t *k = kbase + off, *v = vbase + off;
+          if (dense) {
 #pragma unroll
-          for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
-            const uint32_t to = dst + r0 * Shape::kRowBytes + (place(lane % kPieces, r0 + row0) << 4);
-            cp_async16(to, k, 16);
-            cp_async16(to + Shape::kChunkBytes, v, 16);
-            k += rows_on, v += rows_on;
+            for (int n = 0; n < 16 / kRowsOnce; ++n) {
+              cp_async_whole(to[n] + stage, k + n * kRowsOnce * D);
+              cp_async_whole(to[n] + stage + Shape::kChunkBytes, v + n * kRowsOnce * D);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 16 / kRowsOnce; ++n, k += rows_on, v += rows_on) {
+              cp_async_whole(to[n] + stage, k);
+              cp_async_whole(to[n] + stage + Shape::kChunkBytes, v);
+            }
           }
         } else {  // the last chunk, or two pages, or none; rows that are not there read as zeros
           const int mine = j + (lane & 15);
@@ -203,13 +218,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
               atomicOr(a.status, kStatusBadIndex);
             }
           }
-          cp_async_small(sdst, sbase + soff, off < 0 ? 0 : Shape::kScaleBytes, small);
-#pragma unroll 1
-          for (int r0 = 0; r0 < 16; r0 += kRowsOnce) {
-            const int64_t o = __shfl_sync(0xffffffffu, off, r0 + row0);
-            const uint32_t to = dst + r0 * Shape::kRowBytes + (place(lane % kPieces, r0 + row0) << 4);
-            cp_async16(to, kbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
-            cp_async16(to + Shape::kChunkBytes, vbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+          cp_async_scales<Shape::kScaleBytes>(scale_to + stage, sbase + soff, off < 0 ? 0 : Shape::kScaleBytes);
+#pragma unroll
+          for (int n = 0; n < 16 / kRowsOnce; ++n) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, n * kRowsOnce + row0);
+            cp_async16(to[n] + stage, kbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+            cp_async16(to[n] + stage + Shape::kChunkBytes, vbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
           }
         }
       }
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
     for (int i = 0; i < kStages; ++i) page[i] = page_of(i);
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-      fill(i, i, page[i]);
+      fill(i, i * Shape::kStageBytes, page[i]);
       page[i] = page_of(i + kStages);
     }
 
@@ -280,12 +294,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 
     // matrices of ldmatrix: keys 0-7 and 8-15, of a block's two pieces
     const int r = (lane & 7) + (lane & 8), second = lane >> 4;
-    int stage = 0;
+    uint32_t stage = 0;  // its offset
+    uint32_t at_k[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) at_k[b] = ring + r * Shape::kRowBytes + (place(2 * b + second, r) << 4);
+    const unsigned char* my_scales = my_ring + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes;
     for (int i = 0; i < take; ++i) {
       cp_wait<kStages - 1>();
       __syncwarp();
-      const unsigned char* scales = my_ring + stage * Shape::kStageBytes + 2 * Shape::kChunkBytes + g * Shape::kScaleBytes;
-      const uint32_t kt = ring + stage * Shape::kStageBytes + r * Shape::kRowBytes, vt = kt + Shape::kChunkBytes;
+      const unsigned char* scales = my_scales + stage;
       // s: keys g (0, 1) and g + 8 (2, 3) by rows 2c (0, 2) and 2c + 1 (1, 3)
       float s[NT][4];
       {
@@ -295,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           uint32_t w[4];
-          ldsm4(kt + (place(2 * b + second, r) << 4), w);
+          ldsm4(at_k[b] + stage, w);
           float part[NT][4];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -335,11 +352,19 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[t][e] *= row_scale[t][e & 1];
-          if (partial_view && j + (e >> 1) * 8 >= limit[t][e & 1]) s[t][e] = -INFINITY;
-          grown |= s[t][e] - base[t][e & 1] > kGrow8 - most;
-        }
+        for (int e = 0; e < 4; ++e) s[t][e] *= row_scale[t][e & 1];
+      if (partial_view) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + (e >> 1) * 8 >= limit[t][e & 1]) s[t][e] = -INFINITY;
+      }
+      const float beyond = kGrow8 - most;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) grown |= s[t][e] - base[t][e & 1] > beyond;
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -382,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
         uint32_t w[4];
-        ldsm4t(vt + (place(2 * b + second, r) << 4), w);
+        ldsm4t(at_k[b] + stage + Shape::kChunkBytes, w);
         float e0, e8, unused;
         if (b % 2 == 0)
           Elem<__half>::unpack2(d0[b / 2], e0, unused), Elem<__half>::unpack2(d8[b / 2], e8, unused);
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
       }
       __syncwarp();
       fill(i + kStages, stage, page[0]);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = stage == (kStages - 1) * Shape::kStageBytes ? 0 : stage + Shape::kStageBytes;
 #pragma unroll
       for (int k = 0; k < kStages - 1; ++k) page[k] = page[k + 1];
       page[kStages - 1] = page_of(i + 2 * kStages);
