@@ -20,13 +20,20 @@ struct GateArgs {
 constexpr int kGateThreads = 256;
 constexpr int kGateValues = 8;  // consecutive ones a thread: four lanes a block
 
-// The same operations as torch's silu and multiplication of f32 tensors, bit for bit.
+// silu: the same operations as torch's silu of f32 tensors, bit for bit.  gelu: x / (1 + e^-2u) with the
+// exponential and the reciprocal of the special-function unit, off by some 2^-22 of itself each.
 template <int kAct>
 __device__ __forceinline__ float activation(float x) {
-  float e = -x;
-  if constexpr (kAct == Q1_ACT_GELU)
-    e = __fmul_rn(-1.5957691216057308f, __fmaf_rn(__fmul_rn(__fmul_rn(x, x), x), 0.044715f, x));  // -2 sqrt(2/pi)
-  return __fdiv_rn(x, __fadd_rn(1.0f, expf(e)));
+  if constexpr (kAct == Q1_ACT_SILU) {
+    return __fdiv_rn(x, __fadd_rn(1.0f, expf(-x)));
+  } else {
+    // -2 sqrt(2/pi) log2(e) x (1 + 0.044715 x^2)
+    const float t = __fmul_rn(__fmul_rn(x, -2.3022082f), __fmaf_rn(__fmul_rn(x, x), 0.044715f, 1.0f));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return __fmul_rn(x, r);
+  }
 }
 
 // Values e .. e+7 of a row of n; past it: zeros.
