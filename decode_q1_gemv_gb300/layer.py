@@ -1,18 +1,20 @@
 """One decoder layer around the 1-bit products: prompts, then tokens one by one.
 
-    python -m decode_q1_gemv_gb300.layer [--prompt 300] [--sequences 4] [--steps 16]
+    python -m decode_q1_gemv_gb300.layer [--prompt 300] [--sequences 4] [--steps 16] [--cache bf16|q8_0] [--vocab 32000]
 
 The path of a layer of a 1-bit decoder, every step of it a call of the binding:
 residual and norm with the q8_0 activation (add_rms_norm), the q, k and v
 products (gemv_multi or gemm_small) with their requests' low-rank adapters
 (lora_add), rotary positions and the cache's new entries (rope_append),
 attention over the paged cache (paged_attention), the o product, the second
-norm, gate and up, and down.  silu(gate) * up is plain torch.
+norm, gate and up, silu(gate) * up with its q8_0 form (gated_act), and down.
 
 ``PagedCache`` hands out pages and keeps the index tensors of the current call
-on the device; ``DecoderLayer`` holds the packed weights.  The command builds
-one layer of the Llama-3-8B shape from seeded synthetic weights (no checkpoint
-is read) and times it.
+on the device; of type int8 it holds keys and values as q8_0 (rope_append_q8,
+paged_attention_q8, cache_read_q8).  ``DecoderLayer`` holds the packed weights,
+``Head`` those of the output product, from whose logits it draws the next
+tokens (sample).  The command builds one layer of the Llama-3-8B shape and a
+head from seeded synthetic weights (no checkpoint is read) and times them.
 """
 from __future__ import annotations
 
@@ -27,13 +29,26 @@ MAX_ADAPTED = 65535  # of one lora_add
 
 
 class PagedCache:
-    """Keys and values of `sequences` sequences in pages of `page_size` tokens."""
+    """Keys and values of `sequences` sequences in pages of `page_size` tokens, of
+    `dtype` bf16 or f16, or int8: q8_0 quants with the f16 scales `ks` and `vs`,
+    a head's tokens of a page side by side."""
 
     def __init__(self, sequences: int, pages: int, page_size: int, kv_heads: int, dim: int, max_tokens: int,
                  dtype=torch.bfloat16, device="cuda"):
         self.page_size = page_size
-        self.k = torch.empty((pages, page_size, kv_heads, dim), dtype=dtype, device=device)
-        self.v = torch.empty_like(self.k)
+        self.quantized = dtype == torch.int8
+        if self.quantized:
+            if dim % 32:
+                raise ValueError("a q8_0 cache's dim is a multiple of 32")
+
+            def storage(last, dtype):
+                return torch.empty((pages, kv_heads, page_size, last), dtype=dtype, device=device).transpose(1, 2)
+
+            self.k, self.v = storage(dim, torch.int8), storage(dim, torch.int8)
+            self.ks, self.vs = storage(dim // 32, torch.float16), storage(dim // 32, torch.float16)
+        else:
+            self.k = torch.empty((pages, page_size, kv_heads, dim), dtype=dtype, device=device)
+            self.v = torch.empty_like(self.k)
         width = -(-max_tokens // page_size)
         self.table = torch.zeros((sequences, width), dtype=torch.int32, device=device)
         self.kv_len = torch.zeros(sequences, dtype=torch.int32, device=device)
@@ -79,7 +94,22 @@ class PagedCache:
         self.max_new = 0
 
     def args(self):
+        """The cache's tensors as rope_append and paged_attention take them, or their q8_0 forms."""
+        if self.quantized:
+            return self.k, self.v, self.ks, self.vs, self.table, self.kv_len, self.new_start
         return self.k, self.v, self.table, self.kv_len, self.new_start
+
+    def read(self, sequence: int, dtype=torch.float32):
+        """Keys and values [tokens, kv_heads, dim] of a sequence, a copy of type `dtype`."""
+        n = self.lengths[sequence]
+        if n == 0:
+            return tuple(torch.empty((0, *self.k.shape[2:]), dtype=dtype, device=self.k.device) for _ in range(2))
+        row = slice(sequence, sequence + 1)
+        if self.quantized:
+            whole = torch.tensor([0, n], dtype=torch.int32, device=self.k.device)
+            return binding.cache_read_q8(self.k, self.v, self.ks, self.vs, self.table[row], self.kv_len[row], whole, n, dtype=dtype)
+        pages = self.table[sequence, :len(self.pages[sequence])].long()
+        return tuple(t[pages].flatten(0, 1)[:n].to(dtype) for t in (self.k, self.v))
 
 
 class DecoderLayer:
@@ -129,8 +159,12 @@ class DecoderLayer:
         q, k, v = self._products(("q", "k", "v"), n.q, n.d)
         for name, out in (("q", q), ("k", k), ("v", v)):
             self._adapt(name, n.y, out, index)
-        heads = binding.rope_append(q, k, v, self.cos_sin, *cache.args())
-        a = binding.paged_attention(heads, *cache.args(), max_new=cache.max_new)
+        if cache.quantized:
+            heads = binding.rope_append_q8(q, k, v, self.cos_sin, *cache.args())
+            a = binding.paged_attention_q8(heads, *cache.args(), max_new=cache.max_new)
+        else:
+            heads = binding.rope_append(q, k, v, self.cos_sin, *cache.args())
+            a = binding.paged_attention(heads, *cache.args(), max_new=cache.max_new)
         a = a.view(a.shape[0], -1).float()
         out, = self._products(("o",), *binding.quantize(a))
         self._adapt("o", a, out, index)
@@ -138,9 +172,33 @@ class DecoderLayer:
         gate, up = self._products(("gate", "up"), n.q, n.d)
         self._adapt("gate", n.y, gate, index)
         self._adapt("up", n.y, up, index)
-        h = torch.nn.functional.silu(gate).mul_(up)
-        out, = self._products(("down",), *binding.quantize(h))
-        return self._adapt("down", h, out, index), n.residual
+        h = binding.gated_act(gate, up, out="both" if adapted and "down" in self.adapters else "q8")
+        out, = self._products(("down",), h.q, h.d)
+        return self._adapt("down", h.y, out, index), n.residual
+
+
+class Head:
+    """blocks: Q1_0 blocks (uint8 [vocab, n/128, 18]) of the output product; norm: f32 [n]."""
+
+    def __init__(self, blocks: torch.Tensor, norm: torch.Tensor, eps: float = 1e-5):
+        self.vocab, self.n = blocks.shape[0], blocks.shape[1] * 128
+        self.packed, self.norm, self.eps = binding.pack(blocks, self.vocab, self.n), norm, eps
+
+    def logits(self, x: torch.Tensor, residual: torch.Tensor | None) -> torch.Tensor:
+        """f32 [tokens, vocab] of the last layer's output and residual [tokens, n]."""
+        n = binding.add_rms_norm(x, self.norm, self.eps, residual=residual)
+        out = torch.empty((x.shape[0], self.vocab), dtype=torch.float32, device=x.device)
+        if x.shape[0] == 1:
+            binding.gemv(self.packed, self.vocab, self.n, n.q[0], n.d[0], out[0])
+            return out
+        for t in range(0, x.shape[0], MAX_VECTORS):
+            e = min(x.shape[0], t + MAX_VECTORS)
+            binding.gemm_small(self.packed, self.vocab, self.n, n.q[t:e], n.d[t:e], out[t:e])
+        return out
+
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor | None, uniform: torch.Tensor, **settings) -> torch.Tensor:
+        """The next token (int32) of each row of x, drawn with uniform f32 [rows]; settings as of sample."""
+        return binding.sample(self.logits(x, residual), uniform, **settings)
 
 
 def rope_table(positions: int, dim: int, theta: float = 500000.0, device="cuda") -> torch.Tensor:
@@ -172,32 +230,49 @@ def synthetic_layer(shapes=synth.LLAMA3_8B_LAYER, dim: int = 128, positions: int
     return DecoderLayer(blocks, [1 + normal(hidden, std=0.1) for _ in range(2)], rope_table(positions, dim), dim, low)
 
 
+def synthetic_head(vocab: int, hidden: int, seed: int = 6) -> Head:
+    """A head of seeded synthetic weights."""
+    b = synth.weight_blocks(synth.rng_for(seed, 0), vocab, hidden, "ones")
+    b[:, :, :2] = synth.fp16_bits([2 * hidden ** -0.5]).view("uint8")
+    return Head(torch.from_numpy(b).cuda(), torch.ones(hidden, device="cuda"))
+
+
 def main() -> None:
-    ap = argparse.ArgumentParser(description="One decoder layer: prompts, then tokens one by one.")
+    ap = argparse.ArgumentParser(description="One decoder layer and a head: prompts, then tokens one by one.")
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--sequences", type=int, default=4)
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--cache", choices=("bf16", "q8_0"), default="bf16")
+    ap.add_argument("--vocab", type=int, default=32000)
     args = ap.parse_args()
     layer = synthetic_layer(adapters=3)
     hidden, dim = layer.shape["q"][1], layer.dim
+    head = synthetic_head(args.vocab, hidden)
     most = args.prompt + args.steps
-    cache = PagedCache(args.sequences, args.sequences * (-(-most // 16)), 16, layer.shape["k"][0] // dim, dim, most)
+    cache = PagedCache(args.sequences, args.sequences * (-(-most // 16)), 16, layer.shape["k"][0] // dim, dim, most,
+                       torch.int8 if args.cache == "q8_0" else torch.bfloat16)
     of = torch.arange(args.sequences, dtype=torch.int32, device="cuda") % 4 - 1  # one sequence in four has no adapter
 
     def run(new):
         cache.extend([new] * args.sequences)
         x = torch.randn(new * args.sequences, hidden, device="cuda")
-        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start, end, drawn = (torch.cuda.Event(enable_timing=True) for _ in range(3))
         start.record()
         out, residual = layer(x, None, cache, of.repeat_interleave(new))
         end.record()
+        last = slice(new - 1, None, new)  # of each sequence
+        tokens = head(out[last], residual[last], torch.rand(args.sequences, device="cuda"), temperature=0.8, top_k=50, top_p=0.95)
+        drawn.record()
         torch.cuda.synchronize()
         assert torch.isfinite(out).all() and torch.isfinite(residual).all() and binding.device_status() == 0
-        return start.elapsed_time(end)
+        assert ((tokens >= 0) & (tokens < args.vocab)).all()
+        return start.elapsed_time(end), end.elapsed_time(drawn), tokens.tolist()
 
-    print(f"prompt: {args.sequences} x {args.prompt} tokens, {run(args.prompt):.3f} ms (first call)")
-    times = sorted(run(1) for _ in range(args.steps))
-    print(f"steps: {args.sequences} tokens each, median {times[len(times) // 2]:.3f} ms of {args.steps}")
+    layer_ms, head_ms, tokens = run(args.prompt)
+    print(f"prompt: {args.sequences} x {args.prompt} tokens, {layer_ms:.3f} ms, head {head_ms:.3f} ms (first call), next {tokens}")
+    times = [run(1)[:2] for _ in range(args.steps)]
+    layer_ms, head_ms = (sorted(t)[len(times) // 2] for t in zip(*times))
+    print(f"steps: {args.sequences} tokens each, median {layer_ms:.3f} ms, head {head_ms:.3f} ms of {args.steps}")
 
 
 if __name__ == "__main__":

@@ -261,6 +261,37 @@ def test_read_into_given_tensors_on_a_stream_and_bad_pages():
     assert (bad[16:32] == 0).all() and torch.equal(bad[:16], want[0][:16]) and torch.equal(bad[32:], want[0][32:])
 
 
+def test_what_the_binding_refuses():
+    c = Cache8([(1, 20)], 1, 64, 16)
+    x, table = normal(1, 1, 64), rope_table(20, 64)
+    with pytest.raises(TypeError, match="bfloat16, float16"):
+        binding.rope_append_q8(x, x, x, table, *c.args(), dtype=torch.float32)
+    with pytest.raises(TypeError, match="q_out has dtype"):
+        binding.rope_append_q8(x, x, x, table, *c.args(), q_out=torch.empty(1, 1, 64, device="cuda"))
+    for i, text in ((0, "cache_k has dtype"), (1, "cache_v has dtype"), (2, "scale_k has dtype"), (3, "scale_v has dtype")):
+        bad = list(c.args())
+        bad[i] = bad[i].to(torch.float32)
+        with pytest.raises(TypeError, match=text):
+            binding.cache_read_q8(*bad, 1)
+    bad = list(c.args())
+    bad[3] = torch.empty(*bad[3].shape[:3], 3, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="scale_v has shape"):
+        binding.cache_read_q8(*bad, 1)
+    bad[3] = torch.empty(*c.vs.shape[:3], 4, dtype=torch.float16, device="cuda")[..., :2]
+    with pytest.raises(ValueError, match="same strides"):
+        binding.cache_read_q8(*bad, 1)
+    with pytest.raises(ValueError, match="positive"):
+        binding.cache_read_q8(*c.args(), 0)
+    q = normal(2, 1, 2, 64, dtype=torch.float16)
+    with pytest.raises(binding.Q1Error, match="workspace holds"):
+        binding.paged_attention_q8(q, *c.args(), max_new=1, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="q has dim 128, the cache 64"):
+        binding.paged_attention_q8(q.view(1, 1, 128), *c.args(), max_new=1)
+    with pytest.raises(TypeError, match="q has dtype"):
+        binding.paged_attention_q8(q.float(), *c.args(), max_new=1)
+    assert binding.device_status() == 0
+
+
 # -------------------------------------------------------------- attention --
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim", [64, 128])
