@@ -51,13 +51,14 @@ struct Attend8Args {
   int64_t s_page, s_slot, s_head;
 };
 
-template <int D, int NT, int kWarps = kWarps8>
+// kWarps warps take chunks of 16 kHalves keys each.
+template <int D, int NT, int kWarps = kWarps8, int kHalves = 1>
 struct Shape8 {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kRowBytes = D, kChunkBytes = 16 * D, kScaleBytes = D / 16;  // a key's quants, 16 keys', a key's scales
-  static constexpr int kStageBytes = 2 * kChunkBytes + 2 * 16 * kScaleBytes;
-  static constexpr int kCtas = kWarps == 2 * kWarps8 ? 1 : NT == 1 ? 4 : 3;  // an SM
-  static constexpr int kStages = D == 64 ? 5 : NT == 1 ? 3 : 4;
+  static constexpr int kRows = 8 * NT, kChunk = 16 * kHalves, kUnit = kChunk * kWarps;
+  static constexpr int kRowBytes = D, kChunkBytes = kChunk * D, kScaleBytes = D / 16;  // a key's quants, a chunk's, a key's scales
+  static constexpr int kStageBytes = 2 * kChunkBytes + 2 * kChunk * kScaleBytes;
+  static constexpr int kCtas = kWarps == 2 * kWarps8 ? 1 : kHalves == 1 ? (NT == 1 ? 4 : 3) : D == 64 ? 4 - NT + 1 : 4 - NT;  // an SM
+  static constexpr int kStages = (D == 64 ? 5 : NT == 1 ? 3 : 4) / kHalves + (kHalves == 2);
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
   static_assert(kSmem >= kWarps * kRows * (D + 4) * 4, "the warps' outputs go over the ring");
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "");
@@ -119,10 +120,10 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of number
 
 // kCluster: not shares of the axis but a cluster of a.ctas CTAs for each
 // sequence, key head and tile, which joins its own parts, as in attend.cu.
-template <class T, int D, int NT, bool kCluster, int kWarps = kWarps8>
-__global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_attend_q8(const __grid_constant__ Attend8Args args) {
-  constexpr int kUnit = 16 * kWarps;  // keys
-  using Shape = Shape8<D, NT, kWarps>;
+template <class T, int D, int NT, bool kCluster, int kWarps = kWarps8, int kHalves = 1>
+__global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps, kHalves>::kCtas) k_attend_q8(const __grid_constant__ Attend8Args args) {
+  using Shape = Shape8<D, NT, kWarps, kHalves>;
+  constexpr int kUnit = Shape::kUnit, kChunk = Shape::kChunk;  // keys
   using Tile = Tiling<Shape::kRows, kUnit>;
   constexpr int kRows = Shape::kRows, kStages = Shape::kStages, kPieces = D / 16, kBlocks = D / 32, kWords = D / 64;
   const AttendArgs& a = args.a;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
     if (bad && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
     u0 = item - head * a.tiles, u1 = Tile::tiles(a, cur.s);  // tiles, here
   } else {
-    total = locate<Tile, kWhole8>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
+    total = locate<Tile, kWhole8 / kHalves>(a, blockIdx.x, ctas, scratch, cur, u0, u1);
     if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
   }
   unsigned char* my_ring = smem + warp * (kStages * Shape::kStageBytes);
@@ -165,50 +166,60 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
     const int keys = Tile::keys(a, cur.s, cur.m), of_all = Tile::keys_of_all(a, cur.s, cur.m);
     const int32_t* table = a.kv.table + cur.b * a.kv.table_stride;
 
-    // Chunk i of this warp: keys j0 + 64 i .. +15, which begin on a multiple of 16: in one page of 16 slots or more,
-    // which all lanes look up well before it is needed (of 8: each lane for row lane % 16).  A lane copies piece
-    // lane % kPieces of rows lane / kPieces and on; lane r the scales of row r's key, r + 16 of its value.
-    constexpr int kRowsOnce = 32 / kPieces;
-    const bool one_page = a.kv.page_shift >= 4;
-    const int j0 = cur.unit * kUnit + warp * 16, row0 = lane / kPieces;
+    // Chunk i of this warp: kChunk keys from j0 + kUnit i on, a multiple of 16.  16 of them lie in one page of 16
+    // slots or more, which their lanes look up well before it is needed (of 8: each lane for row lane % kChunk).  A
+    // lane copies piece lane % kPieces of rows lane / kPieces and on, and the scales of row lane % kChunk (of 16
+    // rows: lanes from 16 on those of the values).
+    constexpr int kRowsOnce = 32 / kPieces, kTimes = kChunk / kRowsOnce, kPlaces = 8 / kRowsOnce;
+    const bool one_page = a.kv.page_shift >= 4;  // for 16
+    const int j0 = cur.unit * kUnit + warp * kChunk, row0 = lane / kPieces, my_row = lane % kChunk;
     const int64_t rows_on = kRowsOnce * a.kv.slot_stride;
     const int8_t* kbase = static_cast<const int8_t*>(a.kv.k) + cur.h * a.kv.head_stride + lane % kPieces * 16;
     const int8_t* vbase = static_cast<const int8_t*>(a.kv.v) + cur.h * a.kv.head_stride + lane % kPieces * 16;
-    const uint16_t* sbase = (lane < 16 ? args.ks : args.vs) + cur.h * args.s_head;
+    const uint16_t* sbase = (lane < 16 || kHalves == 2 ? args.ks : args.vs) + cur.h * args.s_head;
+    const uint16_t* sbase_v = args.vs + cur.h * args.s_head;  // kHalves == 2
     const auto page_of = [&](int i) {  // -1 past the keys
-      const int j = j0 + i * kUnit + (one_page ? 0 : lane & 15);
+      const int j = j0 + i * kUnit + (one_page ? my_row & 16 : my_row);
       return i < take && j < keys ? table[j >> a.kv.page_shift] : -1;
     };
-    const int64_t row_off = int64_t(row0) * a.kv.slot_stride, scale_off = int64_t(lane & 15) * args.s_slot;
+    const int64_t row_off = int64_t(row0) * a.kv.slot_stride;
     const bool dense = a.kv.slot_stride == D;  // a head's slots side by side: rows at constant distances
-    uint32_t to[16 / kRowsOnce];               // where this lane's pieces go in a stage
+    uint32_t to[kPlaces];  // where this lane's pieces go in a stage: of its first rows, repeated every 8
 #pragma unroll
-    for (int k = 0; k < 16 / kRowsOnce; ++k)
+    for (int k = 0; k < kPlaces; ++k)
       to[k] = ring + (k * kRowsOnce + row0) * Shape::kRowBytes + (place(lane % kPieces, k * kRowsOnce + row0) << 4);
+    const auto dst_of = [&](int n) { return to[n % kPlaces] + n / kPlaces * 8 * Shape::kRowBytes; };
     const uint32_t scale_to = ring + 2 * Shape::kChunkBytes + lane * Shape::kScaleBytes;
+    constexpr int kScaleV = kChunk * Shape::kScaleBytes;
     const auto fill = [&](int i, uint32_t stage, int page) {  // stage: its offset
       if (i < take) {
         const int j = j0 + i * kUnit;
-        if (one_page && j + 16 <= keys && page >= 0 && page < a.kv.pages) {
-          const int slot = j & page_mask;
-          const int64_t off = int64_t(page) * a.kv.page_stride + int64_t(slot) * a.kv.slot_stride + row_off;
-          cp_async_scales<Shape::kScaleBytes>(scale_to + stage, sbase + (int64_t(page) * args.s_page + int64_t(slot) * args.s_slot + scale_off));
-          const int8_t *k = kbase + off, *v = vbase + off;
-          if (dense) {
+        const bool usual = one_page && j + kChunk <= keys && page >= 0 && page < a.kv.pages;
+        if (kHalves == 1 ? usual : __all_sync(0xffffffffu, usual)) {
+          const int64_t soff = int64_t(page) * args.s_page + int64_t((j + my_row) & page_mask) * args.s_slot;
+          cp_async_scales<Shape::kScaleBytes>(scale_to + stage, sbase + soff);
+          if constexpr (kHalves == 2) cp_async_scales<Shape::kScaleBytes>(scale_to + stage + kScaleV, sbase_v + soff);
 #pragma unroll
-            for (int n = 0; n < 16 / kRowsOnce; ++n) {
-              cp_async_whole(to[n] + stage, k + n * kRowsOnce * D);
-              cp_async_whole(to[n] + stage + Shape::kChunkBytes, v + n * kRowsOnce * D);
-            }
-          } else {
+          for (int h = 0; h < kHalves; ++h) {
+            const int its_page = kHalves == 1 ? page : __shfl_sync(0xffffffffu, page, h * 16);
+            const int64_t off = int64_t(its_page) * a.kv.page_stride + int64_t((j + h * 16) & page_mask) * a.kv.slot_stride + row_off;
+            const int8_t *k = kbase + off, *v = vbase + off;
+            if (dense) {
 #pragma unroll
-            for (int n = 0; n < 16 / kRowsOnce; ++n, k += rows_on, v += rows_on) {
-              cp_async_whole(to[n] + stage, k);
-              cp_async_whole(to[n] + stage + Shape::kChunkBytes, v);
+              for (int n = 0; n < 16 / kRowsOnce; ++n) {
+                cp_async_whole(dst_of(h * 16 / kRowsOnce + n) + stage, k + n * kRowsOnce * D);
+                cp_async_whole(dst_of(h * 16 / kRowsOnce + n) + stage + Shape::kChunkBytes, v + n * kRowsOnce * D);
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < 16 / kRowsOnce; ++n, k += rows_on, v += rows_on) {
+                cp_async_whole(dst_of(h * 16 / kRowsOnce + n) + stage, k);
+                cp_async_whole(dst_of(h * 16 / kRowsOnce + n) + stage + Shape::kChunkBytes, v);
+              }
             }
           }
-        } else {  // the last chunk, or two pages, or none; rows that are not there read as zeros
-          const int mine = j + (lane & 15);
+        } else {  // the last chunk, or several pages, or none; rows that are not there read as zeros
+          const int mine = j + my_row;
           int64_t off = -1, soff = 0;
           if (mine < keys) {
             if (page >= 0 && page < a.kv.pages) {
@@ -219,11 +230,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
             }
           }
           cp_async_scales<Shape::kScaleBytes>(scale_to + stage, sbase + soff, off < 0 ? 0 : Shape::kScaleBytes);
+          if constexpr (kHalves == 2) cp_async_scales<Shape::kScaleBytes>(scale_to + stage + kScaleV, sbase_v + soff, off < 0 ? 0 : Shape::kScaleBytes);
 #pragma unroll
-          for (int n = 0; n < 16 / kRowsOnce; ++n) {
+          for (int n = 0; n < kTimes; ++n) {
             const int64_t o = __shfl_sync(0xffffffffu, off, n * kRowsOnce + row0);
-            cp_async16(to[n] + stage, kbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
-            cp_async16(to[n] + stage + Shape::kChunkBytes, vbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+            cp_async16(dst_of(n) + stage, kbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+            cp_async16(dst_of(n) + stage + Shape::kChunkBytes, vbase + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
           }
         }
       }
@@ -303,16 +315,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
       cp_wait<kStages - 1>();
       __syncwarp();
       const unsigned char* scales = my_scales + stage;
-      // s: keys g (0, 1) and g + 8 (2, 3) by rows 2c (0, 2) and 2c + 1 (1, 3)
-      float s[NT][4];
-      {
+      // s: keys g (0, 1) and g + 8 (2, 3) of each 16 by rows 2c (0, 2) and 2c + 1 (1, 3)
+      float s[kHalves][NT][4];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
         uint32_t d0[kWords], d8[kWords];
-        scales_of(scales, d0);
-        scales_of(scales + 8 * Shape::kScaleBytes, d8);
+        scales_of(scales + h * 16 * Shape::kScaleBytes, d0);
+        scales_of(scales + (h * 16 + 8) * Shape::kScaleBytes, d8);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           uint32_t w[4];
-          ldsm4(at_k[b] + stage, w);
+          ldsm4(at_k[b] + stage + h * 16 * Shape::kRowBytes, w);
           float part[NT][4];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -334,37 +347,47 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] = b == 0 ? part[t][e] * (e < 2 ? e0 : e8) : __fmaf_rn(part[t][e], e < 2 ? e0 : e8, s[t][e]);
+            for (int e = 0; e < 4; ++e)
+              s[h][t][e] = b == 0 ? part[t][e] * (e < 2 ? e0 : e8) : __fmaf_rn(part[t][e], e < 2 ? e0 : e8, s[h][t][e]);
         }
       }
-      uint32_t d0[kWords], d8[kWords];
-      scales_of(scales + 16 * Shape::kScaleBytes, d0);
-      scales_of(scales + 24 * Shape::kScaleBytes, d8);
-      uint32_t tops = max2(no_infinity(d0[0]), no_infinity(d8[0]));  // (a NaN is passed over)
-      if constexpr (kWords == 2) tops = max2(tops, max2(no_infinity(d0[1]), no_infinity(d8[1])));
+      uint32_t d0[kHalves][kWords], d8[kHalves][kWords], tops = 0u;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        scales_of(scales + kScaleV + h * 16 * Shape::kScaleBytes, d0[h]);
+        scales_of(scales + kScaleV + (h * 16 + 8) * Shape::kScaleBytes, d8[h]);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) tops = max2(tops, max2(no_infinity(d0[h][k]), no_infinity(d8[h][k])));  // (a NaN is passed over)
+      }
       float top, other;
       Elem<__half>::unpack2(tops, top, other);
       top = fmaxf(top, other);
       // Scores to log2 units; keys a row may not see drop out by selection.
       const int j = j0 + i * kUnit + g;
-      const bool partial_view = j - g + 16 > of_all;
+      const bool partial_view = j - g + kChunk > of_all;
       bool grown = top > top_scale;
+      const float beyond = kGrow8 - most;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] *= row_scale[t][e & 1];
-      if (partial_view) {
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + (e >> 1) * 8 >= limit[t][e & 1]) s[t][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) s[h][t][e] *= row_scale[t][e & 1];
+      if (partial_view) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j + h * 16 + (e >> 1) * 8 >= limit[t][e & 1]) s[h][t][e] = -INFINITY;
       }
-      const float beyond = kGrow8 - most;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) grown |= s[t][e] - base[t][e & 1] > beyond;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) grown |= s[h][t][e] - base[t][e & 1] > beyond;
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -378,7 +401,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(s[t][e], s[t][e + 2]);
+            float m = fmaxf(s[0][t][e], s[0][t][e + 2]);
+            if constexpr (kHalves == 2) m = fmaxf(m, fmaxf(s[kHalves - 1][t][e], s[kHalves - 1][t][e + 2]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
             const float to = fmaxf(m, base[t][e] - old) + most;
@@ -391,47 +415,54 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
         }
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[t][e] = ex2(s[t][e] - base[t][e & 1]);
-          sum[t][e & 1] += s[t][e];
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[h][t][e] = ex2(s[h][t][e] - base[t][e & 1]);
+            sum[t][e & 1] += s[h][t][e];
+          }
       // A scale that is no number must not reach, as 0 * inf, the rows that may not see its key.
       bool careful = false;
       if (partial_view) {
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) careful |= no_number<__half>(d0[k]) || no_number<__half>(d0[k] >> 16) || no_number<__half>(d8[k]) || no_number<__half>(d8[k] >> 16);
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < kWords; ++k)
+            careful |= no_number<__half>(d0[h][k]) || no_number<__half>(d0[h][k] >> 16) || no_number<__half>(d8[h][k]) || no_number<__half>(d8[h][k] >> 16);
         careful = __any_sync(0xffffffffu, careful);
       }
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        uint32_t w[4];
-        ldsm4t(at_k[b] + stage + Shape::kChunkBytes, w);
-        float e0, e8, unused;
-        if (b % 2 == 0)
-          Elem<__half>::unpack2(d0[b / 2], e0, unused), Elem<__half>::unpack2(d8[b / 2], e8, unused);
-        else
-          Elem<__half>::unpack2(d0[b / 2], unused, e0), Elem<__half>::unpack2(d8[b / 2], unused, e8);
-        uint32_t pt[NT][2];
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float p[4] = {s[t][0] * e0, s[t][1] * e0, s[t][2] * e8, s[t][3] * e8};
-          if (careful) {
+        for (int b = 0; b < kBlocks; ++b) {
+          uint32_t w[4];
+          ldsm4t(at_k[b] + stage + Shape::kChunkBytes + h * 16 * Shape::kRowBytes, w);
+          float e0, e8, unused;
+          if (b % 2 == 0)
+            Elem<__half>::unpack2(d0[h][b / 2], e0, unused), Elem<__half>::unpack2(d8[h][b / 2], e8, unused);
+          else
+            Elem<__half>::unpack2(d0[h][b / 2], unused, e0), Elem<__half>::unpack2(d8[h][b / 2], unused, e8);
+          uint32_t pt[NT][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j + (e >> 1) * 8 >= limit[t][e & 1]) p[e] = 0.f;
+          for (int t = 0; t < NT; ++t) {
+            float p[4] = {s[h][t][0] * e0, s[h][t][1] * e0, s[h][t][2] * e8, s[h][t][3] * e8};
+            if (careful) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (j + h * 16 + (e >> 1) * 8 >= limit[t][e & 1]) p[e] = 0.f;
+            }
+            pt[t][0] = transposed(Elem<__half>::pack2(p[0], p[1]));
+            pt[t][1] = transposed(Elem<__half>::pack2(p[2], p[3]));
           }
-          pt[t][0] = transposed(Elem<__half>::pack2(p[0], p[1]));
-          pt[t][1] = transposed(Elem<__half>::pack2(p[2], p[3]));
-        }
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint32_t v[4] = {quants(w[2 * p]), quants(w[2 * p] >> 8), quants(w[2 * p + 1]), quants(w[2 * p + 1] >> 8)};
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t v[4] = {quants(w[2 * p]), quants(w[2 * p] >> 8), quants(w[2 * p + 1]), quants(w[2 * p + 1] >> 8)};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * b + p], v, pt[t][0], pt[t][1]);
+            for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * b + p], v, pt[t][0], pt[t][1]);
+          }
         }
-      }
       __syncwarp();
       fill(i + kStages, stage, page[0]);
       stage = stage == (kStages - 1) * Shape::kStageBytes ? 0 : stage + Shape::kStageBytes;
@@ -543,9 +574,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps>::kCtas) k_a
 // Which kernel, from the rows a key head at most (new tokens times the group), where clusters do not take the call.
 static bool many_rows8(int64_t max_new, int64_t group, bool one) { return max_new > (one ? 32 : 64) / group; }
 
-template <int NT>
-static int attend8_ctas() { return (NT == 1 ? 4 : 3) * num_sms(); }
-static int64_t few_workspace8(int dim) { return std::max(attend_workspace(attend8_ctas<1>(), 8, dim), attend_workspace(attend8_ctas<2>(), 16, dim)); }
+// Where the work is split by shares of the axis, chunks are of 32 keys: two independent streams of
+// instructions, and half the votes and waits (64 sequences of 8 heads of 64, 8000 keys at most: 61 us, 68 with 16;
+// 16 x 64 heads over 8 of 128, 4000: 25.7 and 29.2; 64 x 32 over 8, 16384: 178 and 177).
+template <int D, int NT>
+using ShareShape = Shape8<D, NT, kWarps8, 2>;
+template <int D>
+static int64_t few_workspace8() {
+  return std::max(attend_workspace(ShareShape<D, 1>::kCtas * num_sms(), 8, D), attend_workspace(ShareShape<D, 2>::kCtas * num_sms(), 16, D));
+}
+static int64_t few_workspace8(int dim) { return dim == 64 ? few_workspace8<64>() : few_workspace8<128>(); }
 
 // The CTAs of a cluster for each sequence, key head and tile, which joins its
 // own parts; 0: shares of the axis and a join, or the tensor-core kernel.  As in
@@ -596,6 +634,8 @@ static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, v
                           const AttendArgs* many) {
   using Shape = Shape8<D, NT>;
   using Wide = Shape8<D, NT, 2 * kWarps8>;
+  using Share = ShareShape<D, NT>;
+  const auto by_shares = k_attend_q8<T, D, NT, false, kWarps8, 2>;
   const char* who = "q1_paged_attention_q8 launch";
   AttendArgs& a = g.a;
   static bool set[64] = {};
@@ -603,7 +643,7 @@ static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, v
   if (int e = cuda_status(cudaGetDevice(&dev), who)) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
     const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, false>, most, Shape::kSmem), who)) return e;
+    if (int e = cuda_status(cudaFuncSetAttribute(by_shares, most, Share::kSmem), who)) return e;
     if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true>, most, Shape::kSmem), who)) return e;
     if (int e = cuda_status(cudaFuncSetAttribute(k_attend_q8<T, D, NT, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who))
       return e;
@@ -624,9 +664,9 @@ static int launch_attend8(Attend8Args& g, int64_t max_new, bool only_clusters, v
       return launch_op<Attend8Args>(k_attend_q8<T, D, NT, true, 2 * kWarps8>, grid, 2 * kWarps8 * 32, Wide::kSmem, ctas, s, who, g);
     return launch_op<Attend8Args>(k_attend_q8<T, D, NT, true>, grid, kWarps8 * 32, Shape::kSmem, ctas, s, who, g);
   }
-  a.ctas = attend8_ctas<NT>();
+  a.ctas = Share::kCtas * num_sms();
   place_workspace(a, workspace);
-  if (int e = launch_op<Attend8Args>(k_attend_q8<T, D, NT, false>, dim3(unsigned(a.ctas)), kWarps8 * 32, Shape::kSmem, 1, s, who, g)) return e;
+  if (int e = launch_op<Attend8Args>(by_shares, dim3(unsigned(a.ctas)), kWarps8 * 32, Share::kSmem, 1, s, who, g)) return e;
   // No item has more units than stay whole: nothing to join.
   if (a.kv.table_tokens <= kWhole8 * kKeys8) return Q1_OK;
   if (many && many->ctas)

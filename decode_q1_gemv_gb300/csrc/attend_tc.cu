@@ -288,12 +288,17 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             atomicOr(a.status, kStatusBadIndex);
             page = kParts * a.kv.pages;  // past the map's end: the box reads as zeros
           }
+          int c[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page;
 #pragma unroll
           for (int kv = 0; kv < 2 * kParts; ++kv) {
-            int c[3];
+            if constexpr (kParts > 1) {
+              const int step = kv == 0 ? 0 : kv % 2 ? a.kv.pages : -a.kv.pages;  // to the second part, and back
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-              c[i] = g.axis_head == i + 1 ? cur.h : g.axis_slot == i + 1 ? (j & page_mask) : page + kv % kParts * a.kv.pages;
+              for (int i = 0; i < 3; ++i) c[i] += g.axis_page == i + 1 ? step : 0;
+            }
             if (!wait(empty(pos.stage), pos.parity ^ 1)) {
               ok = false;
               break;
@@ -349,10 +354,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         hand_on(hand);
       };
       const auto parts_full = [&]() {  // from pos on
-        RingPos at = pos;
-        bool done = wait(full(at.stage), at.parity);
-#pragma unroll
-        for (int part = 1; part < kParts; ++part) {
+        bool done = wait(full(pos.stage), pos.parity);
+        if constexpr (kParts > 1) {
+          RingPos at = pos;
           at.next<kStages>();
           done = done && wait(full(at.stage), at.parity);
         }
@@ -480,9 +484,14 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
       return done;
     };
     bool ok = true;
-    float scale = a.scale_log2, v_factor = 1.f;
-    uint64_t scale2 = f32x2(scale, scale);
-    int q_load = 0, q_use = 0;  // parities of the items whose Q is loaded, and of the one at work
+    uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+    uint32_t q_parity = 0;  // of the item whose Q is loaded (bit 0), and of the one at work (bit 1)
+    const auto scale_of = [&]() {  // of this item's scores
+      float x = a.scale_log2, y;
+      if constexpr (kNormed) split2(scale2, x, y);
+      return x;
+    };
+    const auto factors_of = [&](const Cursor& it) { return g.factors + 2 * (it.b * a.kv.kv_heads + it.h); };
     // Q of an item, if this tile has rows of it that see keys: this warp's 16
     // rows, 16 (8) lanes a row; rows past the last are zero.
     const auto load_q = [&](const Cursor& it) {
@@ -511,13 +520,13 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] *= __uint_as_float((254u - e) << 23);
           v = Elem<T>::pack(x);
-          if (piece == 0) q_factor[q_load][w][r] = __uint_as_float(e << 23);
+          if (piece == 0) q_factor[q_parity & 1][w][r] = __uint_as_float(e << 23);
         }
         *reinterpret_cast<uint4*>(q + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(qfull + 8 * w);
-      q_load ^= 1;
+      q_parity ^= 1;
     };
     if (u0 < u1) load_q(cur);
     for (int64_t u = u0; u < u1 && ok;) {
@@ -549,10 +558,9 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             tc_fence_after();
             if constexpr (kNormed) {
               if (t == 0) {  // (the row's factor was written before its Q, which these scores come from)
-                const float* f = g.factors + 2 * (cur.b * a.kv.kv_heads + cur.h);
-                scale = a.scale_log2 * f[0], v_factor = f[1];
-                if constexpr (kTurned) scale *= q_factor[q_use][w][row];
-                q_use ^= 1;
+                float scale = a.scale_log2 * factors_of(cur)[0];
+                if constexpr (kTurned) scale *= q_factor[q_parity >> 1][w][row];
+                q_parity ^= 2;
                 scale = fminf(fmaxf(scale, FLT_MIN), FLT_MAX);
                 scale2 = f32x2(scale, scale);
               }
@@ -601,7 +609,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
             }
             ok = fetch(other);
             if (!ok) break;
-            const float top = fmaxf(mine, other) * scale;
+            const float top = fmaxf(mine, other) * scale_of();
             const bool grown = top > used + kTcGrow || (used == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, grown)) {
               float f = 1.f;
@@ -649,6 +657,7 @@ __global__ void __launch_bounds__(kTcAThreads, 1) k_attend_tc(const __grid_const
         }
         const bool whole = cur.unit == 0 && take == cur.units;
         const int sees = live ? keys_seen(cur.s, token - cur.s.first) : 0;
+        const float v_factor = kNormed ? factors_of(cur)[1] : 1.f;
         const float inv = kNormed ? inverse(sum, sees) * v_factor : inverse(sum, sees);
         if (threadIdx.x == 0 && cur.unit == 0 && !whole) leave_join(a, cur, u, total, ctas);
         float* part = partial<kTcItem, D>(a, blockIdx.x, cur.unit == 0) + w * kTcM + row;
