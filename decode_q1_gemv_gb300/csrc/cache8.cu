@@ -111,9 +111,7 @@ __global__ void __launch_bounds__(kCacheThreads) k_rope_append_q8(const __grid_c
 }
 
 // 16 values of a block: quants times the scale.
-__device__ __forceinline__ void read16(const int8_t* q, const uint16_t* d, float (&v)[16]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(q);
-  const float s = __half2float(__ushort_as_half(*d));
+__device__ __forceinline__ void values16(const uint4& w, float s, float (&v)[16]) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -160,8 +158,8 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache_read_q8(const __grid_co
     if (!out) continue;
     float x[16] = {};
     if (at.good)
-      read16(static_cast<const int8_t*>(second ? kv.v : kv.k) + slot + head * kv.head_stride + e,
-             (second ? a.p.vs : a.p.ks) + scale + head * a.p.s_head + e / kSub, x);
+      values16(*reinterpret_cast<const uint4*>(static_cast<const int8_t*>(second ? kv.v : kv.k) + slot + head * kv.head_stride + e),
+               __half2float(__ushort_as_half((second ? a.p.vs : a.p.ks)[scale + head * a.p.s_head + e / kSub])), x);
     write16(out + (int64_t(token) * kv.kv_heads + head) * a.dim + e, x);
   }
 }
@@ -242,28 +240,42 @@ __global__ void __launch_bounds__(kCopyThreads) k_copy_q8(const __grid_constant_
   const int e = int(threadIdx.x) % units * 16;
   const int32_t* table = kv.table + b * kv.table_stride;
   const int64_t part = int64_t(kv.batch) * a.pages * kv.kv_heads * 128 * a.dim;
-  for (int j = blockIdx.x * step + int(threadIdx.x) / units; j < s.len; j += gridDim.x * step) {
-    const int page = table[j >> kv.page_shift];
-    const bool good = page >= 0 && page < kv.pages;
-    if (!good) atomicOr(a.status, kStatusBadIndex);
-    const int64_t from = value_offset(a.p, page, j & page_mask) + head * kv.head_stride + e;
-    const int64_t scale = scale_offset(a.p, page, j & page_mask) + head * a.p.s_head + e / kSub;
-    const int64_t to = (((int64_t(b) * a.pages + j / 128) * kv.kv_heads + head) * 128 + j % 128) * a.dim + e;
-    float x[2][16] = {};
-    if (good) {
-      read16(static_cast<const int8_t*>(kv.k) + from, a.p.ks + scale, x[0]);
-      read16(static_cast<const int8_t*>(kv.v) + from, a.p.vs + scale, x[1]);
+  // kAtOnce tokens' loads side by side.
+  constexpr int kAtOnce = 2;
+  for (int j0 = blockIdx.x * step + int(threadIdx.x) / units; j0 < s.len; j0 += kAtOnce * gridDim.x * step) {
+    uint4 q[kAtOnce][2];
+    uint16_t d[kAtOnce][2];
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      const int j = j0 + n * int(gridDim.x) * step;
+      q[n][0] = q[n][1] = make_uint4(0u, 0u, 0u, 0u), d[n][0] = d[n][1] = 0;
+      if (j >= s.len) continue;
+      const int page = table[j >> kv.page_shift];
+      if (page < 0 || page >= kv.pages) {  // zeros
+        atomicOr(a.status, kStatusBadIndex);
+        continue;
+      }
+      const int64_t from = value_offset(a.p, page, j & page_mask) + head * kv.head_stride + e;
+      const int64_t scale = scale_offset(a.p, page, j & page_mask) + head * a.p.s_head + e / kSub;
+      q[n][0] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(kv.k) + from), d[n][0] = a.p.ks[scale];
+      q[n][1] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(kv.v) + from), d[n][1] = a.p.vs[scale];
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      __half* out = (i ? a.v : a.k) + to;
+    for (int n = 0; n < kAtOnce; ++n) {
+      const int j = j0 + n * int(gridDim.x) * step;
+      if (j >= s.len) break;
+      const int64_t to = (((int64_t(b) * a.pages + j / 128) * kv.kv_heads + head) * 128 + j % 128) * a.dim + e;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) x[i][n] = __fmul_rn(x[i][n], inverse[i]);
-      write16(out, x[i]);
-      if constexpr (kParts == 2) {
+      for (int i = 0; i < 2; ++i) {
+        float x[16];
+        values16(q[n][i], __fmul_rn(__half2float(__ushort_as_half(d[n][i])), inverse[i]), x);
+        __half* out = (i ? a.v : a.k) + to;
+        write16(out, x);
+        if constexpr (kParts == 2) {
 #pragma unroll
-        for (int n = 0; n < 16; ++n) x[i][n] = __fsub_rn(x[i][n], __half2float(__float2half_rn(x[i][n])));
-        write16(out + part, x[i]);
+          for (int k = 0; k < 16; ++k) x[k] = __fsub_rn(x[k], __half2float(__float2half_rn(x[k])));
+          write16(out + part, x);
+        }
       }
     }
   }
