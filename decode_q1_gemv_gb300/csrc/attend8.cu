@@ -25,6 +25,13 @@
 // Maxima (of scores, and of the values' scales) are looked at by a vote: the ones in
 // use move only when a score is 2^8 times beyond, or a scale beyond, so most
 // chunks have no exchange between lanes for it.
+//
+// Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64 sequences, 1.08 GB of keys and
+// values, 177 us: 6.1 TB/s, 0.90 of the copy bandwidth (the 16-bit cache's kernel takes 313 us for 2.04 GB); one token over
+// 8191 keys 12.1 us, over 1000 6.0.  A chunk of 16 keys is some 520 instructions of a warp, 96 of them masks and shifts
+// that take quants out of words, on a pipe with half the lanes: issue is active 60 % of the cycles there, that pipe
+// 50 %, and with rows past eight (16 sequences of 4 tokens, 157 MB, 62 us) these bound it.
+// 2048 tokens over 16001 keys take 412 us, 30 of them the copy.
 #include <algorithm>
 #include <cfloat>
 #include <climits>

@@ -6,6 +6,11 @@
 // when there are many tokens (4 in and 1.06 out a key or value on append, 1.06
 // in and 2 or 4 out on reading), and the chain of small loads (which sequence,
 // its length, its page) when there are few, as in rope.cu.
+//
+// Measured: 5751 tokens of seven prompts (32 + 8 + 8 heads of 64) appended in 18.1 us (102 MB, 0.83 of the copy
+// bandwidth) and read back in 6.5; 64 single tokens (heads of 128) in 3.2 and 2.1 us a launch.  The copy of
+// 16001 tokens of 8 heads of 128 to f16 with its scales' maxima takes some 30 us (101 MB, most of it in L2), of 27000 tokens of 16
+// heads of 64 in two parts 55 (283 MB); CTAs from 4 to 200 an SM and one to four tokens' loads at once change it by 10 %.
 #include "q8.cuh"
 
 namespace q1 {

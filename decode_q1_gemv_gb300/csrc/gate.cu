@@ -1,9 +1,13 @@
 // gate.cu -- q8_gated_act: y = act(gate) * up, and the q8_0 form of y.
 //
-// Elementwise but for a block's maximum: a value costs some forty instructions
-// (the exponential, three divisions' worth of it a fourth each) and 9 bytes (f32 in,
-// a quant out), so bytes bound it.  A thread takes 16-byte groups of gate and up;
-// the lanes of a block exchange its maximum, as in norm.cu.
+// Elementwise but for a block's maximum: a value costs some thirty-five instructions (silu's exponential and
+// division seventeen of them) and 9 bytes (f32 in, a quant out), so bytes bound it, by little: with one
+// 16-byte group a thread, eight lanes a block, the block's two divisions made it 109 us where eight values a
+// thread, four lanes a block, take 84.
+//
+// Measured: 4095 rows of 14336 f32 values to q8_0, 532 MB, 84 us: 6.3 TB/s, 0.94 of the copy
+// bandwidth; 2000 x 11008 bf16, gelu, 132 MB, 20.6 us (0.95; 31.5 with an exact exponential and division);
+// one row of 14336 1.9 us a launch in a chain of them.
 #include "q8.cuh"
 
 namespace q1 {
