@@ -28,10 +28,10 @@
 //
 // Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64 sequences, 1.08 GB of keys and
 // values, 177 us: 6.1 TB/s, 0.90 of the copy bandwidth (the 16-bit cache's kernel takes 313 us for 2.04 GB); one token over
-// 8191 keys 12.1 us, over 1000 6.0.  A chunk of 16 keys is some 520 instructions of a warp, 96 of them masks and shifts
-// that take quants out of words, on a pipe with half the lanes: issue is active 60 % of the cycles there, that pipe
-// 50 %, and with rows past eight (16 sequences of 4 tokens, 157 MB, 62 us) these bound it.
-// 2048 tokens over 16001 keys take 412 us, 30 of them the copy.
+// 8191 keys 12.1 us, over 1000 6.0.  Profiled with 16 of those sequences, instructions are issued
+// in 57 % of the cycles and the pipe of masks and shifts, which take quants out of words, is 51 % active.  Rows past
+// eight are further from their bytes (16 sequences of 4 tokens: 61 us, floor 21).
+// 2048 tokens over 16001 keys take 412 to 420 us (profiled: 37 of them the maxima and the copy).
 #include <algorithm>
 #include <cfloat>
 #include <climits>

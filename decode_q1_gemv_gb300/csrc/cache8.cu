@@ -9,7 +9,7 @@
 //
 // Measured: 5751 tokens of seven prompts (32 + 8 + 8 heads of 64) appended in 18.1 us (102 MB, 0.83 of the copy
 // bandwidth) and read back in 6.5; 64 single tokens (heads of 128) in 3.2 and 2.1 us a launch.  The copy of
-// 16001 tokens of 8 heads of 128 to f16 with its scales' maxima takes some 30 us (101 MB, most of it in L2), of 27000 tokens of 16
+// 16001 tokens of 8 heads of 128 to f16 with its scales' maxima takes 37 us in profiled launches (101 MB, most of it in L2), of 27000 tokens of 16
 // heads of 64 in two parts 55 (283 MB); CTAs from 4 to 200 an SM and one to four tokens' loads at once change it by 10 %.
 #include "q8.cuh"
 

@@ -29,8 +29,8 @@
 //      by exact histograms of the values' bits, ten at a time);
 //   5  sums by warp, whose one holds the drawn token, and the token in it.
 // Bytes would bound it (33 MB, 5 us, for 64 rows of 128256 f32 logits); what does is, for one row, the chain
-// of barriers (two to seven of the cluster, some 1000 cycles each), and for many rows with a large nucleus the weights'
-// instructions: some 34 a value, 13 of them on the pipe of shifts and masks, which has half the lanes.
+// of steps between barriers (profiled: the first stall reason), and for many rows with a large nucleus the weights'
+// instructions (256 rows: issued in 70 % of the cycles, the pipe of shifts and masks 54 % active).
 // (The arithmetic two values an instruction is 3 % faster for 256 rows and up to 5 % slower else; histograms of
 // exact sums instead of counts took 3 shared atomics a value: 404 us for 256 rows.)
 //
@@ -53,8 +53,8 @@ constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 2048;          // of exponents
 constexpr int kDigits = 1024;        // of ten bits of a value
 constexpr int kListed = 1024;        // tokens that one CTA sorts
-// Top-k by the threads' maxima, else by counts (64 rows of 128256 f32 logits: k = 20 15.9 us and 32.3, 256 20.5 and 38,
-// 400 30.5 and 37.3; one row: 400 20.4 and 19.2; beyond, lists of more than kListed are likely).
+// Top-k by the threads' maxima, else by counts.  (64 rows of 128256 f32 logits: k = 20 15.9 us and 32.3, 256 20.5 and 38,
+// 400 30.5 and 37.3; one row: 400 20.4 and 19.2.  Larger k were not compared.)
 constexpr int kFewTopK = 400;
 constexpr int kSteps = 512;          // parts of an exponent
 constexpr int kOne = 44;             // bits behind the point
