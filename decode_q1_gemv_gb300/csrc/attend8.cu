@@ -595,8 +595,8 @@ static int64_t few_workspace8(int dim) { return dim == 64 ? few_workspace8<64>()
 // The CTAs of a cluster for each sequence, key head and tile, which joins its
 // own parts; 0: shares of the axis and a join, or the tensor-core kernel.  As in
 // attend.cu: all clusters run at once, CTAs a cluster until each has two units at most, then as many as fit, up to
-// ten units each (32 heads over 8 of 128, one token over 8191 keys: 11.8 us with 16, 13.7
-// by shares; over 16384: 18.5 and 17.0; 4 sequences of 8191: 17.5 and 18.9).
+// ten units each (32 heads over 8 of 128, one token over 8191 keys: 12.1 us with clusters, 12.8
+// by shares; over 16384: 18.5 and 15.7; 4 sequences of 4000: 12.9 and 14.4, of 8191: 17.2 and 17.0).
 constexpr int kMostUnits8 = 10;
 template <class T, int D, int NT>
 static int attend8_cluster(Attend8Args& g, int64_t max_new, int dev, const char* who, int& ctas, int& warps) {
