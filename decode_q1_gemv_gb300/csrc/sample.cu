@@ -173,7 +173,7 @@ struct SampleShared {
   int own_bad, listed, token;
   uint64_t own_mass, own_base, own_above;
   int border[4];           // of the search of bins: see there
-  uint32_t border_count[2];
+  uint32_t border_count[4];  // of the bin that top-k reaches into; of the bins to look at
   bool cut_found;          // of the leader: the last token that stays
   uint32_t cut_value;
   int cut_place;
@@ -735,11 +735,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         if (sh.border[1] >= 0) hi = min(hi, sh.border[1]);
       }
       bins([&](int b, uint32_t count, uint32_t with, uint64_t, uint64_t) {
-        if (b == lo) sh.border_count[0] = count;
-        if (b == hi) sh.border_count[1] = with;
+        // (not the words above: without top-p no barrier lies between their last reader and here)
+        if (b == lo) sh.border_count[2] = count;
+        if (b == hi) sh.border_count[3] = with;
       });
       __syncthreads();
-      before_lo = sh.border_count[0], upto_hi = sh.border_count[1];
+      before_lo = sh.border_count[2], upto_hi = sh.border_count[3];
     }
     const bool whole = max(upto_hi, before_end + in_end) <= kListed;  // all that may stay can be listed
     const bool apart = cut && end > hi;
