@@ -15,16 +15,16 @@
 //     down to 2^-14 of it.  The sums of 32 products are multiplied with the block's scale in f32.
 //   Values: a block's scale depends on the key and the block, so it goes into
 //     the weight: p d, rounded to f16.  So that its size does not matter, p is
-//     relative not to the row's maximum alone but to that times a power of two that no scale
-//     of the values so far exceeds: p d then is at most 2^8, off by 2^-11 of itself or, below 2^-14,
-//     2^-25; the sum of p is f32, relative to the same.
+//     relative not to the row's largest weight but to its largest product of a weight and
+//     a key's largest scale: p d then is at most 2^8, off by 2^-11 of itself or, below 2^-14,
+//     2^-25; the sum of p is f32, relative to the same.  (Relative to the largest scale of any key, a key
+//     that weighs nothing in the row, or that it may not see, took bits from all others.)
 // ldmatrix moves pairs of bytes as 16-bit elements: a lane gets four dims of a
 // key, or (transposed) two dims of two keys; taking the even and the odd bytes of
 // a word apart puts dims in the order 0 2 1 3 in both operands.
 //
-// Maxima (of scores, and of the values' scales) are looked at by a vote: the ones in
-// use move only when a score is 2^8 times beyond, or a scale beyond, so most
-// chunks have no exchange between lanes for it.
+// Maxima are looked at by a vote: the ones in use move only when a product is 2^8 times
+// beyond, so most chunks have no exchange between lanes for it.
 //
 // Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64 sequences, 1.08 GB of keys and
 // values, 177 us: 6.1 TB/s, 0.90 of the copy bandwidth (the 16-bit cache's kernel takes 313 us for 2.04 GB); one token over
@@ -51,6 +51,9 @@ constexpr int kWarps8 = 4;
 constexpr int kKeys8 = 16 * kWarps8;  // keys of a unit: 16 for each warp
 constexpr int kWhole8 = 2;   // units of an item that is not split
 constexpr float kGrow8 = 8.f;  // log2 units a maximum may be behind
+// The log2 that a key's largest scale counts with at least: those of scales of zero have to be some number.  (Sums
+// of weights are up to 2^(8 - this) times the number of keys.)
+constexpr float kLeastScale8 = -40.f;
 
 struct Attend8Args {
   AttendArgs a;        // kv.k and kv.v are quants
@@ -123,6 +126,17 @@ __device__ __forceinline__ uint32_t no_infinity(uint32_t w) {  // w * 0 + w
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of numbers, where there are some
   const __half2 r = __hmax2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
   return reinterpret_cast<const uint32_t&>(r);
+}
+// log2 of the largest of a key's scales that are numbers, kLeastScale8 at least.
+template <int kWords>
+__device__ __forceinline__ float log2_largest(const uint32_t (&w)[kWords]) {
+  uint32_t tops = 0u;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) tops = max2(tops, no_infinity(w[k]));  // (a NaN is passed over)
+  float a, b, r;
+  Elem<__half>::unpack2(tops, a, b);
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(a, b)));  // -inf of zero
+  return fmaxf(r, kLeastScale8);
 }
 
 // kCluster: not shares of the axis but a cluster of a.ctas CTAs for each
@@ -300,8 +314,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps, kHalves>::k
       }
     }
     // o: dims 16 p + 2 g (0, 1) and + 1 (2, 3) of rows 2c (0, 2) and 2c + 1 (1, 3).  base: what weights are
-    // relative to, the maximum in use and the power of two 2^most that the values' scales do not exceed.
-    float o[NT][kPieces][4], base[NT][2], sum[NT][2], most = -25.f, top_scale = 0.f;  // top_scale: 2^most
+    // relative to, the maximum in use of a visible key's score and its largest scale's logarithm.
+    float o[NT][kPieces][4], base[NT][2], sum[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -358,22 +372,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps, kHalves>::k
               s[h][t][e] = b == 0 ? part[t][e] * (e < 2 ? e0 : e8) : __fmaf_rn(part[t][e], e < 2 ? e0 : e8, s[h][t][e]);
         }
       }
-      uint32_t d0[kHalves][kWords], d8[kHalves][kWords], tops = 0u;
+      uint32_t d0[kHalves][kWords], d8[kHalves][kWords];
+      float up[kHalves][2];  // log2 of the largest scales of keys g and g + 8
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         scales_of(scales + kScaleV + h * 16 * Shape::kScaleBytes, d0[h]);
         scales_of(scales + kScaleV + (h * 16 + 8) * Shape::kScaleBytes, d8[h]);
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) tops = max2(tops, max2(no_infinity(d0[h][k]), no_infinity(d8[h][k])));  // (a NaN is passed over)
+        up[h][0] = log2_largest(d0[h]), up[h][1] = log2_largest(d8[h]);
       }
-      float top, other;
-      Elem<__half>::unpack2(tops, top, other);
-      top = fmaxf(top, other);
       // Scores to log2 units; keys a row may not see drop out by selection.
       const int j = j0 + i * kUnit + g;
       const bool partial_view = j - g + kChunk > of_all;
-      bool grown = top > top_scale;
-      const float beyond = kGrow8 - most;
+      bool grown = false;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -394,25 +404,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps, kHalves>::k
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) grown |= s[h][t][e] - base[t][e & 1] > beyond;
+          for (int e = 0; e < 4; ++e) grown |= s[h][t][e] - base[t][e & 1] > kGrow8 - up[h][e >> 1];
       if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float old = most;
-        if (top > top_scale) {  // the next power of two (2^-24 at least)
-          const uint32_t bits = (__float_as_uint(top) + 0x7fffffu) & 0x7f800000u;
-          top_scale = __uint_as_float(bits), most = float(int(bits >> 23) - 127);
-        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(s[0][t][e], s[0][t][e + 2]);
-            if constexpr (kHalves == 2) m = fmaxf(m, fmaxf(s[kHalves - 1][t][e], s[kHalves - 1][t][e + 2]));
+            float m = fmaxf(s[0][t][e] + up[0][0], s[0][t][e + 2] + up[0][1]);
+            if constexpr (kHalves == 2) m = fmaxf(m, fmaxf(s[kHalves - 1][t][e] + up[kHalves - 1][0], s[kHalves - 1][t][e + 2] + up[kHalves - 1][1]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            const float to = fmaxf(m, base[t][e] - old) + most;
+            const float to = fmaxf(m, base[t][e]);
             f[e] = ex2(base[t][e] - to);
             base[t][e] = to;
             sum[t][e] *= f[e];

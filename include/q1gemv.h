@@ -534,10 +534,11 @@ int64_t q1_paged_attention_q8_workspace(int64_t max_new, int64_t heads, int64_t 
  * Q1_F16).  Up to some tens of rows a key head (new tokens times the group) the
  * quants are multiplied as they are, which is exact, and scales are applied to
  * sums (keys) and weights (values: a weight's product with the scale is rounded to f16, off
- * by 2^-11 of itself or by 2^-25 of the largest there is).  More rows take the tensor-core kernel
+ * by 2^-11 of itself or by 2^-25 of the row's largest).  More rows take the tensor-core kernel
  * over a copy of the sequence that the call makes in the workspace: each value quant *
  * scale, divided by a power of two for its sequence and head (so its size does not
- * matter), rounded to f16, and with f16 q the remainder as a second f16.  As many sequences
+ * matter; values 2^-28 of the head's largest and below are off by 2^-39 of it), rounded
+ * to f16, and with f16 q the remainder as a second f16.  As many sequences
  * are copied at a time as the workspace holds: at least q1_paged_attention_q8_workspace(...,
  * 1) bytes are needed, and more make fewer launches for several such sequences.
  * All else as q1_paged_attention; a value is no number where its scale is none. */
