@@ -127,12 +127,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of number
   const __half2 r = __hmax2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
   return reinterpret_cast<const uint32_t&>(r);
 }
-// log2 of the largest of a key's scales that are numbers, kLeastScale8 at least.
+// log2 of the largest magnitude of a key's scales that are numbers, kLeastScale8 at least.
 template <int kWords>
 __device__ __forceinline__ float log2_largest(const uint32_t (&w)[kWords]) {
   uint32_t tops = 0u;
 #pragma unroll
-  for (int k = 0; k < kWords; ++k) tops = max2(tops, no_infinity(w[k]));  // (a NaN is passed over)
+  for (int k = 0; k < kWords; ++k) tops = max2(tops, no_infinity(w[k] & 0x7fff7fffu));  // (a NaN is passed over)
   float a, b, r;
   Elem<__half>::unpack2(tops, a, b);
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(a, b)));  // -inf of zero

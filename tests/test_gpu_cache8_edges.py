@@ -118,6 +118,21 @@ def test_zeros_and_small_scales_among_the_values(dtype, new, width):
 
 
 @pytest.mark.parametrize("width", [None, 500])
+@pytest.mark.parametrize("new", [1, 5, 16, 90])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+def test_scales_below_zero(which, new, width):
+    """Quants and scales of the other sign are the same values."""
+    c = Cache8([(new, 300), (1, 70)], 2, 128, 16, width=width)
+    q = normal(70, c.total, 4, 128, dtype=torch.bfloat16)
+    for name in ("k", "v"):
+        if which in (name, "both"):
+            quants, scales = getattr(c, name), getattr(c, name + "s")
+            quants.copy_(-quants)
+            scales.copy_(-scales)
+    check_rows(c, 4, torch.bfloat16, q=q)
+
+
+@pytest.mark.parametrize("width", [None, 500])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 128), (2, 2, 64), (5, 1, 128), (8, 1, 64), (3, 1, 64)])
 @pytest.mark.parametrize("new,length", [(2, 2), (3, 50), (8, 300), (15, 200), (32, 1500), (64, 64)])
