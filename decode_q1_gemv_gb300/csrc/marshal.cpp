@@ -237,6 +237,7 @@ q1_paged_kv paged_kv(PyObject* const* a, int64_t total_new) {
   const at::Tensor &k = tensor(a[0], "cache_k"), &v = tensor(a[1], "cache_v"), &table = tensor(a[2], "table");
   if (k.dim() != 4) refuse(PyExc_ValueError, "cache_k must be [pages, page_size, kv_heads, dim]");
   if (table.dim() != 2) refuse(PyExc_ValueError, "table must be [batch, width]");
+  if (k.size(3) < 1) refuse(PyExc_ValueError, "the cache's dim is 0");  // (callers divide by it)
   q1_paged_kv p = {};
   p.k = pointer(k, "cache_k", kBf16 | kF16, k.sizes());
   p.v = pointer(v, "cache_v", type_bit(k.scalar_type()), k.sizes());
@@ -317,6 +318,7 @@ q1_paged_q8 paged_q8(PyObject* const* a, int64_t total_new) {
   if (table.dim() != 2) refuse(PyExc_ValueError, "table must be [batch, width]");
   q1_paged_q8 p = {};
   p.pages = k.size(0), p.page_size = k.size(1), p.kv_heads = k.size(2), p.dim = k.size(3);
+  if (p.dim < 1) refuse(PyExc_ValueError, "the cache's dim is 0");  // (callers divide by it)
   if (p.dim % 32) refuse(PyExc_ValueError, "the cache's dim %lld is no multiple of 32", (long long)p.dim);
   const Sizes<4> scales = {p.pages, p.page_size, p.kv_heads, p.dim / 32};
   p.k = static_cast<int8_t*>(pointer(k, "cache_k", kI8, k.sizes()));
