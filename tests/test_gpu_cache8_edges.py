@@ -159,3 +159,41 @@ def test_any_size_of_values_within_the_bounds_of_few_rows(kstd, vstd, qstd, new,
     for i, n in enumerate(c.len):
         c.put(i, normal(8 + i, n, 2, 64, std=kstd), normal(18 + i, n, 2, 64, std=vstd))
     check_rows(c, 4, dtype, scale=0.1, q=normal(73, c.total, 4, 64, std=qstd, dtype=dtype))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("seqs,max_new", [([(1, 700), (1, 90), (1, 1)], 1), ([(90, 400), (1, 700), (3, 90), (2, 2)], 90), ([(70, 300)], 70)])
+def test_appended_over_and_over_between_calls(seqs, max_new, dtype, dim):
+    """The new tokens' slots are written again before every call of a graph: each call sees what was written last, in
+    the launches that do not wait for the one before them too."""
+    heads, kv_heads, calls = 8, 2, 6
+    c = Cache8(seqs, kv_heads, dim, 16, width=70)
+    rows = [normal(60 + i, c.total, (heads + 2 * kv_heads) * dim) for i in range(calls)]
+    cs = torch.zeros(700, dim, device="cuda")
+    cs[:, :dim // 2] = 1  # no turn
+    ws = torch.empty(binding.paged_attention_q8_workspace(max_new, heads, kv_heads, dim, 70 * 16, 4, dtype), dtype=torch.uint8, device="cuda")
+
+    def step(i):
+        q, k, v = rows[i].split([heads * dim, kv_heads * dim, kv_heads * dim], 1)
+        turned = binding.rope_append_q8(q, k, v, cs, *c.args(), dtype=dtype)
+        return binding.paged_attention_q8(turned, *c.args(), max_new=max_new, workspace=ws)
+
+    want = []
+    for i in range(calls):
+        want.append(step(i))
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [step(i) for i in range(calls)]
+    for _ in range(20):
+        for o in outs:
+            o.fill_(7.0)
+        g.replay()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    for _ in range(20):
+        for o, w in zip([step(i) for i in range(calls)], want):
+            assert torch.equal(o, w)
+    assert binding.device_status() == 0
