@@ -702,7 +702,8 @@ def paged_attention_q8(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Te
     """q1_paged_attention_q8: paged_attention over a q8_0 cache (as in
     rope_append_q8), q [tokens, heads, dim] bf16 or f16.  A given workspace
     (uint8) must hold paged_attention_q8_workspace(...) bytes of one
-    sequence; the call's own has room for the copies of a gigabyte of sequences."""
+    sequence; the call's own has room for the copies of a gigabyte of sequences (of the
+    table's width each: a table far wider than its sequences makes prompts slow)."""
     call = (_marshal or _native()).paged_attention_q8
     if stream is not None:
         return _on_stream(call, stream, q, cache_k, cache_v, scale_k, scale_v, table, kv_len, new_start, max_new, scale, out,

@@ -27,11 +27,11 @@
 // beyond, so most chunks have no exchange between lanes for it.
 //
 // Measured (32 heads over 8 key heads of 128, bf16): one token of each of 64 sequences, 1.08 GB of keys and
-// values, 177 us: 6.1 TB/s, 0.90 of the copy bandwidth (the 16-bit cache's kernel takes 313 us for 2.04 GB); one token over
-// 8191 keys 12.1 us, over 1000 6.0.  Profiled with 16 of those sequences, instructions are issued
-// in 57 % of the cycles and the pipe of masks and shifts, which take quants out of words, is 51 % active.  Rows past
-// eight are further from their bytes (16 sequences of 4 tokens: 61 us, floor 21).
-// 2048 tokens over 16001 keys take 412 to 420 us (profiled: 37 of them the maxima and the copy).
+// values, 177 us: 6.1 TB/s, 0.90 of the copy bandwidth (the 16-bit cache's kernel takes 312 us for 2.04 GB); one token over
+// 8191 keys 11.8 us, over 1000 6.0 (16-bit: 11.9, 6.1).  Profiled with 16 of those sequences, instructions are issued
+// in 59 % of the cycles and the pipe of masks and shifts, which take quants out of words, is 51 % active.  Rows past
+// eight are further from their bytes (16 sequences of 4 tokens: 62 us, floor 21; of up to 12, f16: 50, floor 11).
+// 2048 tokens over 16001 keys take 412 to 422 us (profiled: 37 of them the maxima and the copy).
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -585,8 +585,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape8<D, NT, kWarps, kHalves>::k
 static bool many_rows8(int64_t max_new, int64_t group, bool one) { return max_new > (one ? 32 : 64) / group; }
 
 // Where the work is split by shares of the axis, chunks are of 32 keys: two independent streams of
-// instructions, and half the votes and waits (64 sequences of 8 heads of 64, 8000 keys at most: 61 us, 68 with 16;
-// 16 x 64 heads over 8 of 128, 4000: 25.7 and 29.2; 64 x 32 over 8, 16384: 178 and 177).
+// instructions, and half the votes and waits (64 sequences of 16 heads over 8 of 64, 8000 keys at most: 61 us, 68 with 16;
+// 16 x 64 heads over 8 of 128, 4000: 25.8 and 29.2; 64 x 32 over 8, 16384: 176 and 178; 16 x 12 tokens of 32 over 8, f16,
+// 4000: 50 and 55).
 template <int D, int NT>
 using ShareShape = Shape8<D, NT, kWarps8, 2>;
 template <int D>
@@ -598,8 +599,8 @@ static int64_t few_workspace8(int dim) { return dim == 64 ? few_workspace8<64>()
 // The CTAs of a cluster for each sequence, key head and tile, which joins its
 // own parts; 0: shares of the axis and a join, or the tensor-core kernel.  As in
 // attend.cu: all clusters run at once, CTAs a cluster until each has two units at most, then as many as fit, up to
-// ten units each (32 heads over 8 of 128, one token over 8191 keys: 12.1 us with clusters, 12.8
-// by shares; over 16384: 18.5 and 15.7; 4 sequences of 4000: 12.9 and 14.4, of 8191: 17.2 and 17.0).
+// ten units each (32 heads over 8 of 128, one token over 8191 keys: 11.8 us with clusters, 12.7
+// by shares; over 16384: 18.3 and 15.7; 4 sequences of 4000: 13.0 and 14.5, of 8191: 17.0 and 16.9).
 constexpr int kMostUnits8 = 10;
 template <class T, int D, int NT>
 static int attend8_cluster(Attend8Args& g, int64_t max_new, int dev, const char* who, int& ctas, int& warps) {
