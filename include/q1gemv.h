@@ -594,8 +594,9 @@ typedef struct q1_sampling {
  *   uniform : f32 [rows], in [0, 1) (held within it).
  *   out : int32 [rows].
  * The weights are fixed-point numbers of 44 bits behind the point, off by 2^-30 of
- * themselves or the last bit; their sums are whole numbers, so a row's token does not
- * depend on the order of anything, nor on the other rows.  -inf masks a token.  A row with a NaN or
+ * themselves or the last bit (below 2^-44 of the largest: zero); their sums are whole numbers, so a row's token
+ * does not depend on the order of anything, nor on the other rows.  Where a border lies within that of a sum, they
+ * decide: of two equal maxima and nothing else above 2^-44, top_p 0.5 keeps one.  -inf masks a token.  A row with a NaN or
  * +inf, one whose logits are all -inf, and one with a setting or a uniform that is NaN give -1.
  * 1 <= rows <= 65535, 1 <= vocab <= 2^19. */
 int q1_sample(const void *logits, int64_t ld, int64_t rows, int64_t vocab, int dtype, const float *uniform,

@@ -43,3 +43,14 @@ def test_small_top_k_among_many_equal_tokens(settings, rows, dtype):
     outs = [binding.sample(x, u, **settings) for _ in range(40)]
     for o in outs:
         assert o.tolist() == want
+
+
+@pytest.mark.parametrize("rest,kept", [(-20.0, 2), (-30.0, 2), (-31.0, 1), (-50.0, 1)])
+def test_two_equal_maxima_and_half_of_the_sum(rest, kept):
+    """top_p 0.5 of two equal maxima is the first one alone, unless others weigh something: e^-30 is 2^-43.3, e^-31 2^-44.7,
+    which is below the last bit of the weights."""
+    x = torch.full((2, 100), -torch.inf, device="cuda")
+    x[:, [40, 70]] = 3.0
+    x[:, 90] = 3.0 + rest
+    u = torch.tensor([0.25, 0.75], device="cuda")
+    assert binding.sample(x, u, top_p=0.5).tolist() == [40, 70 if kept == 2 else 40]
